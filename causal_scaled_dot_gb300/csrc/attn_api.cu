@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "kernel_simple.cuh"
 #include "kernel_ws.cuh"
+#include "cache_index.h"
 #include "fwd_schedule.h"
 #include "tmap_cache.h"
 
@@ -494,7 +495,8 @@ extern "C" int attn_sync_status(void* stream) {
     if (cudaMemcpy(&word, dev->status_word, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemcpy(dev->status_word, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
         return ATTN_ERR_DEVICE;
-    return (word & ptx::kStatusTimeout) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+    if (word & ptx::kStatusTimeout) return ATTN_ERR_TIMEOUT;
+    return (word & kStatusBadCache) ? ATTN_ERR_BAD_CACHE : ATTN_OK;
 }
 
 extern "C" int attn_selftest_wait_timeout(int limit_us, void* stream) {
@@ -516,6 +518,7 @@ extern "C" const char* attn_status_string(int status) {
         case ATTN_ERR_DEVICE: return "ATTN_ERR_DEVICE: CUDA device query failed";
         case ATTN_ERR_LAUNCH: return "ATTN_ERR_LAUNCH: kernel launch failed";
         case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT: a device-side wait ran out";
+        case ATTN_ERR_BAD_CACHE: return "ATTN_ERR_BAD_CACHE: a block number or length outside the cache";
         default: return "unknown attn status";
     }
 }
@@ -558,6 +561,12 @@ int encode_bf16_box(CUtensorMap* map, int device, const void* ptr, int D, int S,
                     int box_rows) {
     if (box_rows < 1 || box_rows > 256) return ATTN_ERR_INVALID_ARG;
     return encode_3d(map, device, ptr, 2, D, S, outer, box_rows);
+}
+
+int encode_byte_box(CUtensorMap* map, int device, const void* ptr, int D, int S, long long outer,
+                    int box_rows) {
+    if (box_rows < 1 || box_rows > 256) return ATTN_ERR_INVALID_ARG;
+    return encode_3d(map, device, ptr, 1, D, S, outer, box_rows);
 }
 
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {

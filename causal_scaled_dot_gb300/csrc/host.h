@@ -22,6 +22,10 @@ int encode_bf16_tiles(CUtensorMap* map, int device, const void* ptr, int D, int 
 // The same view with a box of `box_rows` rows (at most 256).
 int encode_bf16_box(CUtensorMap* map, int device, const void* ptr, int D, int S, long long outer,
                     int box_rows);
+// The view [outer, S, D] of one-byte elements with a box of 128 bytes x
+// `box_rows` rows; bytes of the box past column D read as zero.
+int encode_byte_box(CUtensorMap* map, int device, const void* ptr, int D, int S, long long outer,
+                    int box_rows);
 
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb);
 

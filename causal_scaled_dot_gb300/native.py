@@ -20,6 +20,7 @@ ATTN_ERR_MISALIGNED = 3
 ATTN_ERR_DEVICE = 4
 ATTN_ERR_LAUNCH = 5
 ATTN_ERR_TIMEOUT = 6
+ATTN_ERR_BAD_CACHE = 7
 
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
@@ -88,6 +89,15 @@ def load() -> ctypes.CDLL:
         u16p = ctypes.POINTER(ctypes.c_ushort)
         lib.attn_fwd_schedule.argtypes = [ci, ci, ci, ci, u16p, u16p]
         lib.attn_fwd_schedule.restype = ci
+        cache_p, ll3_p = ctypes.POINTER(AttnCache), ctypes.POINTER(ctypes.c_longlong)
+        lib.attn_cache_write.argtypes = [cache_p, vp, ll3_p, vp, ll3_p, vp, ci, vp]
+        lib.attn_cache_write.restype = ci
+        lib.attn_cache_read.argtypes = [cache_p, vp, vp, ci, ci, vp]
+        lib.attn_cache_read.restype = ci
+        lib.attn_cache_fwd.argtypes = [cache_p, vp, ll3_p, vp, vp, vp, ci, ci, cf, ci, vp, u64, vp]
+        lib.attn_cache_fwd.restype = ci
+        lib.attn_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(u64)]
+        lib.attn_cache_workspace.restype = ci
         _lib = lib
         return lib
 
@@ -104,6 +114,16 @@ class AttnOptions(ctypes.Structure):
                 ("keep_bits", ctypes.c_void_p), ("keep_heads", ctypes.c_int),
                 ("dropout_p", ctypes.c_float), ("seed", ctypes.c_ulonglong),
                 ("offset", ctypes.c_ulonglong)]
+
+
+class AttnCache(ctypes.Structure):
+    """The C struct attn_cache_t (include/attn.h), field for field; ``kv_cache.KVCache``
+    fills one from tensors."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("num_blocks", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("max_blocks", ctypes.c_int), ("B", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 ATTN_INPUT_BF16, ATTN_INPUT_E4M3 = 0, 1
@@ -389,6 +409,16 @@ def attn_fwd_fp8(q, k, v, q_descale: float, k_descale: float, v_descale: float, 
     if check and rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_fp8")
     return rc
+
+
+def attn_cache_workspace(Hq: int, Hkv: int, Sq: int, D: int) -> int:
+    """The C entry point ``attn_cache_workspace``: bytes that ``attn_cache_fwd`` needs
+    on the current device for these sizes."""
+    n = ctypes.c_ulonglong(0)
+    rc = load().attn_cache_workspace(int(Hq), int(Hkv), int(Sq), int(D), ctypes.byref(n))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_workspace")
+    return n.value
 
 
 def attn_sync_status(stream=None, check: bool = True) -> int:

@@ -7,7 +7,9 @@
  * the weights attn_fwd_dropout; their combinations attn_fwd_ex), the matching
  * gradients (attn_bwd, attn_bwd_block_masked, attn_bwd_elem_masked,
  * attn_bwd_dropout, attn_bwd_ex), the output
- * projection of the attention output (attn_out_proj), status helpers
+ * projection of the attention output (attn_out_proj), an 8-bit key/value cache
+ * (attn_cache_write, attn_cache_read, and attention over it,
+ * attn_cache_fwd with attn_cache_workspace), status helpers
  * (attn_sync_status, attn_selftest_wait_timeout, attn_status_string,
  * attn_version), and the forward's work order for inspection
  * (attn_fwd_schedule).
@@ -43,7 +45,8 @@
  * context is bound to the thread on entry, so a thread that has made no CUDA
  * call yet (an autograd engine's worker, say) can call too.
  *
- * Device status word: kernels whose bounded waits run out record it in one
+ * Device status word: kernels whose bounded waits run out, and cache kernels
+ * that meet a block number or length outside the cache, record it in one
  * word per device (read and cleared by attn_sync_status).  It is shared by
  * every stream and caller on that device.
  */
@@ -62,7 +65,9 @@ typedef enum {
     ATTN_ERR_MISALIGNED = 3,  /* a tensor pointer not 16-byte aligned (TMA requirement) */
     ATTN_ERR_DEVICE = 4,      /* a CUDA runtime/driver query failed */
     ATTN_ERR_LAUNCH = 5,      /* the kernel launch itself failed */
-    ATTN_ERR_TIMEOUT = 6      /* a device-side wait ran past its limit (read by attn_sync_status) */
+    ATTN_ERR_TIMEOUT = 6,     /* a device-side wait ran past its limit (read by attn_sync_status) */
+    ATTN_ERR_BAD_CACHE = 7    /* a cache call met a block number or length outside the cache
+                                 (read by attn_sync_status) */
 } attn_status_t;
 
 /* Input formats of attn_options_t. */
@@ -338,14 +343,135 @@ int attn_out_proj(const void *out, const void *w, const float *bias, void *y, in
                   int D, int E, void *stream);
 
 /*
+ * attn_cache_t -- a paged key/value cache in 8 bits, as attn_cache_write,
+ * attn_cache_read and attn_cache_fwd take it.  A block (page) holds
+ * block_size tokens of every key/value head as E4M3 codes (the OCP "fn"
+ * encoding, one byte each) with one fp32 scale per block and head, for K and V
+ * each: element value = decoded code * scale.  All pointers are device memory
+ * of the current device, owned by the caller.
+ *   k, v              codes [num_blocks, Hkv, block_size, D], contiguous, 16-byte aligned.
+ *   k_scale, v_scale  fp32 [num_blocks, Hkv]; finite and > 0 for written blocks.
+ *   block_table       int32 [B, max_blocks]: the block that holds tokens
+ *                     i*block_size .. of sequence b at [b][i].  Entries past a
+ *                     sequence's last token are not read.
+ *   seq_lens          int32 [B]: tokens each sequence holds, those of the
+ *                     current step included: write the step's lengths first,
+ *                     then call attn_cache_write and attn_cache_fwd for every
+ *                     layer with them.  0: an idle slot of the batch.
+ *   num_blocks, max_blocks, B, Hkv   >= 1.
+ *   block_size        16, 32, 64 or 128;  D  64 or 128 (else ATTN_ERR_UNSUPPORTED).
+ * The k and v of a step's n_b new tokens (and the queries) of sequence b stand
+ * for positions seq_lens[b] - n_b .. seq_lens[b] - 1.
+ *
+ * Block numbers and lengths live on the device, so the kernels check them: a
+ * length outside 0 .. max_blocks*block_size is taken as the nearer of the two,
+ * a token whose block number is outside 0 .. num_blocks-1 is neither written
+ * nor read and no query sees it, and either sets the device status word
+ * (attn_sync_status then returns ATTN_ERR_BAD_CACHE).
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    const int *block_table;
+    const int *seq_lens;
+    int num_blocks, block_size, max_blocks;
+    int B, Hkv, D;
+} attn_cache_t;
+
+/*
+ * attn_cache_write -- quantise the step's new tokens into the cache.
+ *   k, v      bf16 [B, Hkv, S, D], 16-byte aligned, D contiguous.
+ *   k_strides, v_strides   {batch, head, token} strides in elements, each >= 0
+ *             and a multiple of 8; NULL: contiguous [B, Hkv, S, D].
+ *   new_lens  int32 [B] in device memory: sequence b has new_lens[b] new
+ *             tokens, k[b, :, 0 .. new_lens[b]-1] (0 .. S; values outside are
+ *             taken as the nearer bound and set the status word); rows past it
+ *             are not read.  NULL: S new tokens in every sequence.
+ *   S         >= 1.
+ * The scale s of a block and head is the smallest power of two (at least
+ * 2^-126) with max|x| <= 448 s over its tokens, and code = x / s rounded to
+ * nearest even: the division is exact, so codes do not depend on how the
+ * tokens were split over calls beyond what moving a block to a larger scale
+ * costs.  A block that held tokens before this call keeps its scale unless a
+ * new token needs a larger one; its earlier codes are then multiplied by
+ * (old scale / new scale) and rounded again, which is exact but for values
+ * that fall below 2^-6 (E4M3's smallest normal).  Earlier tokens must have been
+ * written (their scale is read).  NaN and infinities are stored as NaN (E4M3
+ * has no infinity) and do not enter the scale.  Values of 2^127 and above may
+ * round to a code whose value overflows fp32.
+ * New tokens at a position < 0 (seq_lens[b] < n_b) are dropped.  Nothing but
+ * the new tokens' codes, their blocks' scales and those blocks' earlier codes
+ * is written.  A block that is written must belong to one sequence (one table
+ * entry) of the call; blocks that are only read may be shared.
+ * One kernel on `stream`, asynchronous; allocates nothing.  k and v may not
+ * overlap the cache.  Errors as attn_fwd.
+ */
+int attn_cache_write(const attn_cache_t *cache, const void *k, const long long *k_strides,
+                     const void *v, const long long *v_strides, const int *new_lens, int S,
+                     void *stream);
+
+/*
+ * attn_cache_read -- positions first .. first+S-1 of every sequence back as bf16:
+ *   k, v   bf16 [B, Hkv, S, D], contiguous, 16-byte aligned, written; either
+ *          may be NULL to skip it, not both.  Row i of sequence b is position
+ *          first + i: code * scale in fp32, rounded to bf16 (exact for scales
+ *          that attn_cache_write made, within bf16's range).  Rows at or past
+ *          seq_lens[b] are left as they were.
+ *   first  >= 0;  S >= 1 (first + S may pass the cache's end).
+ * k and v may overlap neither the cache nor each other.  One kernel on
+ * `stream`, asynchronous; allocates nothing.  Errors as attn_fwd.
+ */
+int attn_cache_read(const attn_cache_t *cache, void *k, void *v, int first, int S, void *stream);
+
+/*
+ * attn_cache_fwd -- attention of the step's queries over the cache:
+ * O_i = sum_j softmax_j(scale * q_i . k_j) v_j and LSE_i, j over the visible keys.
+ *   q         bf16 [B, Hq, Sq, D], 16-byte aligned, D contiguous; q_strides as
+ *             k_strides above (NULL: contiguous).
+ *   out       bf16 [B, Hq, Sq, D] contiguous, 16-byte aligned; lse fp32
+ *             [B, Hq, Sq] contiguous or NULL.  Written for the valid queries only.
+ *   q_lens    int32 [B] in device memory: sequence b has q_lens[b] queries,
+ *             rows 0 .. q_lens[b]-1 (0 .. Sq, as new_lens above); rows past
+ *             it are left as they were.  NULL: Sq queries in every sequence.
+ *   Hq        a multiple of Hkv; query head h reads key/value head h / (Hq / Hkv).
+ *   causal    non-zero: the query at position p (see attn_cache_t) sees keys
+ *             0 .. p; zero: all keys 0 .. seq_lens[b]-1.
+ *   workspace  device memory, 16-byte aligned, of at least the bytes that
+ *             attn_cache_workspace gives; contents before and after are
+ *             unspecified.  Calls that may run at the same time (other streams,
+ *             graphs replayed side by side) need a workspace each.
+ * A query that sees no key (an idle slot, or a position < 0) gets O = 0 and
+ * LSE = -inf.  Keys that no query row may see (past seq_lens[b], after the
+ * position) do not affect it whatever their codes.  Scores accumulate in fp32
+ * from q rounded to 2^-18 of its row's largest element; the probabilities that
+ * multiply V keep 8 bits or 2^-16 of the row's largest weight, whichever is
+ * coarser; sums and LSE are fp32.
+ * Results are deterministic.  Asynchronous on `stream`; allocates nothing.
+ * out and lse may overlap neither each other nor any input.  Other errors as
+ * attn_fwd (scale finite and > 0).
+ */
+int attn_cache_fwd(const attn_cache_t *cache, const void *q, const long long *q_strides, void *out,
+                   float *lse, const int *q_lens, int Hq, int Sq, float scale, int causal,
+                   void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/*
+ * attn_cache_workspace -- *bytes receives the workspace that attn_cache_fwd
+ * needs on the current device for these sizes; it does not depend on the batch
+ * or on the sequence lengths.  Errors: ATTN_ERR_INVALID_ARG for a size < 1, Hq
+ * not a multiple of Hkv or a NULL bytes; ATTN_ERR_UNSUPPORTED as attn_fwd.
+ */
+int attn_cache_workspace(int Hq, int Hkv, int Sq, int D, unsigned long long *bytes);
+
+/*
  * attn_sync_status -- synchronise `stream` and report device-side failures of
  * the attention kernels enqueued on this device since the last call.
  *
  * Every wait inside the kernels is bounded in time; a wait that runs out sets
  * a per-device status word and makes the kernel exit cleanly (it never traps).
  * This call waits for `stream`, reads and clears that word, and returns
- * ATTN_OK, ATTN_ERR_TIMEOUT, or ATTN_ERR_DEVICE if the synchronisation itself
- * failed.  The word is one per device, not per stream: a timeout left by a
+ * ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_CACHE (a cache call met a block
+ * number or a length outside the cache; see attn_cache_t), or ATTN_ERR_DEVICE
+ * if the synchronisation itself failed.  The word is one per device, not per stream: a timeout left by a
  * kernel on another stream of the same device is reported (and cleared) here
  * too, and outputs of a kernel that timed out are only partly written.
  */
