@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/attn.h"
 #include "cache_index.h"
@@ -80,6 +81,63 @@ CacheView view_of(const attn_cache_t* c, unsigned int* status) {
     v.D = c->D;
     v.status = status;
     return v;
+}
+
+// Query rows of a unit: the smallest of 8, 16, 32 and 64 that holds all rows of
+// a key/value head, else 64.  A tile's products take the same time whatever R
+// is (A is the cache's side) until R = 64, while the softmax works on all R
+// rows, used or not.
+int rows_per_unit(long long group, long long Sq) {
+    const long long rows = group * Sq;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+int ctas_per_sm(int R) { return R == 8 ? CacheLayout<8>::kCtas : R == 16 ? CacheLayout<16>::kCtas
+                                     : R == 32 ? CacheLayout<32>::kCtas : CacheLayout<64>::kCtas; }
+unsigned long long workspace_bytes_of(int R, int sms) {
+    // two partial units per CTA: R rows of 128 sums, and (M, l)
+    return (unsigned long long)sms * ctas_per_sm(R) * 2 * R * (128 * 4 + 8);
+}
+
+constexpr int kMaxDevices = 64;
+std::mutex g_cache_mutex;
+int g_cache_ready[kMaxDevices];  // 0 not yet, 1 ready, else an ATTN_ERR code
+
+template <int R>
+bool allow_smem() {
+    return cudaFuncSetAttribute(attn_cache_fwd_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)CacheLayout<R>::kDynamicSmem) == cudaSuccess;
+}
+int setup_cache_kernels(int dev) {
+    if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
+    std::lock_guard<std::mutex> lock(g_cache_mutex);
+    if (g_cache_ready[dev] == 0)
+        g_cache_ready[dev] = allow_smem<8>() && allow_smem<16>() && allow_smem<32>() && allow_smem<64>() ? 1 : ATTN_ERR_DEVICE;
+    return g_cache_ready[dev] == 1 ? ATTN_OK : g_cache_ready[dev];
+}
+
+template <int R>
+int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, int sms, void* workspace, cudaStream_t st) {
+    using L = CacheLayout<R>;
+    const long long tiles = (p.plan.capacity + kCacheTile - 1) / kCacheTile;  // of one unit, at most
+    const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads;
+    const long long most = (long long)sms * L::kCtas;
+    const int grid = (int)(units >= most || units * tiles >= most ? most : units * tiles);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)most * 2 * R * 128);
+    attn_cache_fwd_kernel<R><<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+    if (tiles == 1) return ATTN_OK;  // no unit can cross CTAs
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, R / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<R>, (const CacheFwdParams)p, grid) == cudaSuccess ? ATTN_OK
+                                                                                                             : ATTN_ERR_LAUNCH;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH; }
@@ -163,7 +221,11 @@ extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int 
 extern "C" int attn_cache_workspace(int Hq, int Hkv, int Sq, int D, unsigned long long* bytes) {
     if (!bytes || Hq < 1 || Hkv < 1 || Sq < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
-    *bytes = 16;
+    int sms = 0, device = -1;
+    unsigned int* status = nullptr;
+    const int rc = host::current_device(&sms, &status, &device);
+    if (rc != ATTN_OK) return rc;
+    *bytes = workspace_bytes_of(rows_per_unit(Hq / Hkv, Sq), sms);
     return ATTN_OK;
 }
 
@@ -196,22 +258,39 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     int sms = 0, device = -1;
     unsigned int* status = nullptr;
     if ((rc = host::current_device(&sms, &status, &device)) != ATTN_OK) return rc;
+    if ((rc = setup_cache_kernels(device)) != ATTN_OK) return rc;
+    const int group = Hq / cache->Hkv, R = rows_per_unit(group, Sq);
+    if (workspace_bytes < workspace_bytes_of(R, sms)) return ATTN_ERR_INVALID_ARG;
+    alignas(64) CUtensorMap tk, tv;
+    const long long outer = (long long)cache->num_blocks * cache->Hkv;
+    if (host::encode_byte_box(&tk, device, cache->k, cache->D, cache->block_size, outer, cache->block_size) != ATTN_OK ||
+        host::encode_byte_box(&tv, device, cache->v, cache->D, cache->block_size, outer, cache->block_size) != ATTN_OK)
+        return ATTN_ERR_INVALID_ARG;
     p.c = view_of(cache, status);
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
-    p.q_lens = q_lens;
     p.Hq = Hq;
     p.Sq = Sq;
-    p.group = Hq / cache->Hkv;
-    p.causal = causal ? 1 : 0;
+    p.group = group;
+    p.hper = group < R ? group : R;
+    p.hgroups = (group + p.hper - 1) / p.hper;
     p.scale_log2 = scale * kLog2e;
-    const long long grid = ((long long)rows + 3) / 4;
-    if (grid > (1ll << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    p.wait_limit_ns = host::wait_limit_ns();
+    p.plan.seq_lens = cache->seq_lens;
+    p.plan.q_lens = q_lens;
+    p.plan.B = cache->B;
+    p.plan.Sq = Sq;
+    p.plan.capacity = cache->max_blocks * cache->block_size;
+    p.plan.causal = causal ? 1 : 0;
+    p.plan.qper = R / p.hper;
+    p.plan.q_tiles = (Sq + p.plan.qper - 1) / p.plan.qper;
+    p.plan.heads = cache->Hkv * p.hgroups;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache->D == 64)
-        attn_cache_fwd_row_kernel<64><<<(unsigned)grid, 128, 0, st>>>(p);
-    else
-        attn_cache_fwd_row_kernel<128><<<(unsigned)grid, 128, 0, st>>>(p);
-    return launched();
+    switch (R) {
+        case 8: return launch_fwd<8>(tk, tv, p, sms, workspace, st);
+        case 16: return launch_fwd<16>(tk, tv, p, sms, workspace, st);
+        case 32: return launch_fwd<32>(tk, tv, p, sms, workspace, st);
+        default: return launch_fwd<64>(tk, tv, p, sms, workspace, st);
+    }
 }

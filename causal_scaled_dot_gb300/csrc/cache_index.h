@@ -67,4 +67,145 @@ ATTN_HD unsigned long long cache_offset(int block, int head, int slot, int Hkv, 
     return (((unsigned long long)block * Hkv + head) * block_size + slot) * D;
 }
 
+// ---------------------------------------------------------------- work of the attention
+// A unit is one sequence, one tile of query rows and one group of query heads
+// that share a key/value head; it takes the key tiles (128 keys) 0 .. tiles-1.
+// All units' tiles stand in one row, by sequence, query tile, head, key tile,
+// and CTA c of G takes tiles [c T / G, (c + 1) T / G) of it, so CTAs get equal
+// work whatever the lengths; units that cross a border are joined afterwards.
+// Lengths are device data, so this runs on the device.
+constexpr int kCacheTile = 128;  // keys per tile
+
+struct CachePlan {
+    const int *seq_lens, *q_lens;  // q_lens may be null: Sq each
+    int B, Sq, capacity, causal;
+    int qper;     // queries per query tile
+    int q_tiles;  // query tiles of Sq queries
+    int heads;    // head groups per sequence and query tile
+};
+
+ATTN_HD CacheSpan plan_span(const CachePlan& p, int b, bool* bad) {
+    return cache_span(p.seq_lens[b], p.q_lens ? p.q_lens[b] : p.Sq, p.capacity, p.Sq, bad);
+}
+ATTN_HD int plan_q_tiles(const CachePlan& p, const CacheSpan& s) { return (s.count + p.qper - 1) / p.qper; }
+// Keys that some row of the query tile sees, and its key tiles: at least one,
+// so that rows without a key have an owner too.
+ATTN_HD int plan_keys(const CachePlan& p, const CacheSpan& s, int qt) {
+    const int last = (qt + 1) * p.qper < s.count ? (qt + 1) * p.qper : s.count;
+    const int n = p.causal ? s.first + last : s.len;
+    return n < 0 ? 0 : n;
+}
+ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
+    const int n = plan_keys(p, s, qt);
+    return n <= kCacheTile ? 1 : (n + kCacheTile - 1) / kCacheTile;
+}
+
+// Tiles of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
+ATTN_HD long long plan_chunk(const CachePlan& p, long long first, long long last, bool* bad) {
+    if (first >= last) return 0;
+    long long sum = 0;
+    int b = (int)(first / p.q_tiles), qt = (int)(first - (long long)b * p.q_tiles);
+    CacheSpan s = plan_span(p, b, bad);
+    for (long long i = first; i < last; ++i) {
+        if (qt == p.q_tiles) {
+            qt = 0;
+            s = plan_span(p, ++b, bad);
+        }
+        if (qt < plan_q_tiles(p, s)) sum += (long long)plan_tiles(p, s, qt) * p.heads;
+        ++qt;
+    }
+    return sum;
+}
+
+struct CachePlace {
+    int b, qt, h, t;
+};
+// The place of the tile `offset` tiles after the start of pair `first`
+// (offset < the tiles of the pairs from there on).
+ATTN_HD CachePlace plan_find(const CachePlan& p, long long first, long long offset) {
+    bool bad = false;
+    CachePlace x{(int)(first / p.q_tiles), (int)(first % p.q_tiles), 0, 0};
+    CacheSpan s = plan_span(p, x.b, &bad);
+    for (;;) {
+        if (x.qt == p.q_tiles) {
+            x.qt = 0;
+            if (++x.b >= p.B) return CachePlace{p.B, 0, 0, 0};
+            s = plan_span(p, x.b, &bad);
+        }
+        if (x.qt < plan_q_tiles(p, s)) {
+            const int tiles = plan_tiles(p, s, x.qt);
+            const long long all = (long long)tiles * p.heads;
+            if (offset < all) {
+                x.h = (int)(offset / tiles);
+                x.t = (int)(offset - (long long)x.h * tiles);
+                return x;
+            }
+            offset -= all;
+        }
+        ++x.qt;
+    }
+}
+
+// The CTAs that share `total` tiles: all, or one per tile, so that none
+// between the first and the last piece of a unit is without a tile.
+ATTN_HD int plan_ctas(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
+// First tile of CTA `cta` of plan_ctas() many (the total for those past them).
+ATTN_HD long long plan_begin(long long total, int cta, int ctas) { return cta < ctas ? total * cta / ctas : total; }
+// The last CTA with a piece of a unit that begins in `cta` and ends before tile `unit_end`.
+ATTN_HD int plan_last(long long total, int cta, int ctas, long long unit_end) {
+    while (plan_begin(total, cta + 1, ctas) < unit_end) ++cta;
+    return cta;
+}
+
+// A CTA's share of one unit: key tiles t .. t + n - 1 of its `tiles`.
+struct CacheUnit {
+    int b, qt, h, t, n, tiles, keys;
+    CacheSpan s;
+};
+// Walks the units of a run of `left` tiles from a place on.
+struct CacheCursor {
+    CachePlace at;
+    long long left;
+    CacheSpan s;
+    int tiles;
+};
+ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, long long left) {
+    bool bad = false;
+    CacheCursor c{at, at.b < p.B ? left : 0, {}, 0};
+    if (c.left > 0) {
+        c.s = plan_span(p, at.b, &bad);
+        c.tiles = plan_tiles(p, c.s, at.qt);
+    }
+    return c;
+}
+ATTN_HD bool cursor_next(const CachePlan& p, CacheCursor& c, CacheUnit& u) {
+    if (c.left <= 0) return false;
+    u.b = c.at.b;
+    u.qt = c.at.qt;
+    u.h = c.at.h;
+    u.t = c.at.t;
+    u.tiles = c.tiles;
+    u.n = c.tiles - c.at.t < c.left ? c.tiles - c.at.t : (int)c.left;
+    u.s = c.s;
+    u.keys = plan_keys(p, c.s, c.at.qt);
+    c.left -= u.n;
+    c.at.t = 0;
+    if (++c.at.h == p.heads) {
+        c.at.h = 0;
+        bool bad = false;
+        if (++c.at.qt >= plan_q_tiles(p, c.s)) {
+            c.at.qt = 0;
+            do {
+                if (++c.at.b >= p.B) {
+                    c.left = 0;
+                    return true;
+                }
+                c.s = plan_span(p, c.at.b, &bad);
+            } while (c.s.count == 0);
+        }
+        c.tiles = plan_tiles(p, c.s, c.at.qt);
+    }
+    return true;
+}
+
 }  // namespace attn

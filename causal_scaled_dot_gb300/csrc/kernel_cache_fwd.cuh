@@ -1,6 +1,38 @@
-// kernel_cache_fwd.cuh -- attention over the 8-bit cache, the plain form: one
-// warp per query row walks the row's keys with the running maximum and sum of
-// an online softmax.
+// kernel_cache_fwd.cuh -- attention over the 8-bit cache on sm_103a.
+//
+// The codes go from the cache to the tensor cores as they are: TMA copies whole
+// pages into shared memory and tcgen05.mma kind::f8f6f4 multiplies E4M3 by
+// E4M3, so no byte of K or V is ever widened.  What must not be rounded to
+// E4M3's 4 significant bits, q and the softmax weights, enters as two E4M3
+// pieces, x = hi + lo with hi the nearest code and lo the nearest code to the
+// rest: 8 significant bits, which is all of a bf16 q (down to 2^-18 of its row's
+// largest element, where lo underflows) and bf16's precision for the weights.
+//
+// Both products are computed transposed, so that the few query rows of a
+// decoding step are the narrow N side of the instruction and not its M = 128:
+//     S^T [128 keys x 2R] = K [128 x D] * Qp^T,   Qp = R rows hi, R rows lo
+//     O^T [D x 2R]       += V^T [D x 128 keys] * Pp^T
+// with R = 8, 16, 32 or 64 query rows (the queries of a tile times the query
+// heads of one key/value head).  In S^T a thread owns one key, so a block's
+// scales are one factor per thread: s = (S_hi + S_lo) * ks * (row factor).
+// V's scale joins the weight, w = e * vs * c_r with e = 2^(s - M_r); c_r keeps
+// the row's largest w near 2^6, so that lo's underflow (2^-10) is 2^-16 of it
+// whatever the scales.  M_r and c_r move only when some w or e passes 448
+// (E4M3's largest): then the warpgroup finds the tile's maxima and rescales O^T
+// in tensor memory; otherwise a tile needs one vote of the warpgroup and no
+// reduction.  The sum of e is kept per thread (per key) and reduced at the end.
+//
+// Roles (384 threads): warp 0 copies pages (lane i takes page i of a tile) with
+// the tables and scales of the next 32 pages already in registers; warp 1
+// issues the products; warps 2-3 split the next unit's q rows into pieces;
+// warps 4-7 and 8-11 are two softmax warpgroups, each with half of the R rows.
+// CTAs take equal runs of key tiles of all units (cache_index.h); a unit that
+// crosses into the next CTA leaves partial (O, M, l), which a second kernel
+// joins, already resident when the first one ends.
+//
+// What bounds it: one token over a long cache moves 2 bytes per (key, d) pair
+// and is bound by HBM; with R = 64 the softmax's issue slots (about 15
+// instructions a score) come before the tensor cores.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,58 +41,778 @@
 #include "common.cuh"
 #include "kernel_cache_rw.cuh"
 #include "ptx.cuh"
+#include "ptx_cache.cuh"
 
 namespace attn {
 
 struct CacheFwdParams {
     CacheView c;
+    CachePlan plan;
     const __nv_bfloat16* q;
     long long q_stride[3];  // batch, head, token, in elements
     __nv_bfloat16* out;
     float* lse;             // may be null
-    const int* q_lens;      // may be null: Sq each
-    int Hq, Sq, group, causal;
+    int Hq, Sq, group;
+    int hper;               // query heads of a unit
+    int hgroups;            // units that share a key/value head: ceil(group / hper)
     float scale_log2;       // scale * log2(e)
+    float* part_o;          // [G][2][R][128] partial sums of w V / c
+    float2* part_ml;        // [G][2][R] their M and l
+    unsigned long long wait_limit_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) attn_cache_fwd_row_kernel(const CacheFwdParams p) {
-    constexpr int E = D / 32;  // elements per lane: d = lane * E ..
-    const CacheView& c = p.c;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)c.B * p.Hq * p.Sq) return;
-    const int i = (int)(row % p.Sq), hq = (int)(row / p.Sq % p.Hq), b = (int)(row / p.Sq / p.Hq);
-    const int h = hq / p.group;
+template <int R>
+struct CacheLayout {
+    static constexpr int kThreads = 384;
+    static constexpr int kN = 2 * R;               // columns of S^T and O^T: hi and lo pieces
+    static constexpr int kH = R / 2;               // rows of one softmax warpgroup
+    static constexpr int kCtas = R == 8 ? 2 : 1;   // per SM
+    static constexpr int kStages = R == 8 ? 3 : R == 16 ? 6 : R == 32 ? 5 : 4;
+    static constexpr uint32_t kTileBytes = 128 * 128;       // 128 keys x 128 bytes
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes; // K, V
+    static constexpr uint32_t kQ = kStages * kStageBytes;   // 2 x [2R x 128 bytes]
+    static constexpr uint32_t kP = kQ + 2 * kN * 128;       // 2 x [2R x 128 keys]
+    static constexpr uint32_t kInfo = kP + 2 * kN * 128;    // per stage: 8 K scales, 8 V scales, bad pages
+    static constexpr uint32_t kInfoBytes = 80;
+    static constexpr uint32_t kRows = kInfo + kStages * kInfoBytes;  // 2 x [R] CacheRow
+    static constexpr uint32_t kUnit = kRows + 2 * R * 16;            // 2 x CacheWork
+    static constexpr uint32_t kTab = kUnit + 2 * 48;                 // [R] float4 {factor, -M, c, -}
+    static constexpr uint32_t kMv = kTab + R * 16;                   // [R] float2 {M, max of s + log2 vs}
+    static constexpr uint32_t kFac = kMv + R * 8;                    // [R] float2: what l and O are multiplied by
+    static constexpr uint32_t kRed = kFac + R * 8;                   // [2][4 warps][H] float2
+    static constexpr uint32_t kNanAt = kRed + 4 * R * 8;             // [128] first key with NaN in V's column
+    static constexpr uint32_t kScan = kNanAt + 512;                  // 12 long long + 6 int
+    static constexpr uint32_t kBars = kScan + 128;
+    static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kQEmpty = kQFull + 2,
+                         kSFull = kQEmpty + 2, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2,
+                         kOFull = kPvDone + 2, kOFree = kOFull + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1;
+    static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kUnset = kAbort + 4;    // [2] some row of the warpgroup has no maximum yet
+    static constexpr uint32_t kNanSeen = kUnset + 8;
+    static constexpr uint32_t kDynamicSmem = kNanSeen + 4 + 1024;
+    static_assert(kInfo % 16 == 0 && kRows % 16 == 0 && kUnit % 16 == 0 && kTab % 16 == 0 && kScan % 8 == 0 && kBars % 8 == 0,
+                  "alignment");
+    static_assert(kCtas * (kDynamicSmem + 1024) <= 228 * 1024, "shared memory budget");
+    static constexpr uint32_t kTmemCols = 4 * kN;     // S^T twice, O^T twice
+    static_assert(kCtas * kTmemCols <= 512, "tensor memory budget");
+    static constexpr uint32_t kS = 0, kO = 2 * kN;
+};
+
+// A query row of a unit in shared memory: the factor of its scores, the keys it
+// sees, and its place in out and lse (-1: padding).
+struct CacheRow {
+    float factor;
+    int keys;
+    long long at;
+};
+// A unit in shared memory, for the roles that follow the query warps.
+struct CacheWork {
+    int t, n;        // key tiles t .. t + n - 1; n = 0: no more units
+    int keys;        // keys that some row sees
+    int keys_all;    // keys that every row of the unit sees
+    int slot;        // -1: the whole unit; else the partial slot (0: begun elsewhere, 1: begun here)
+    int rows;        // rows in use
+    int pad[6];
+};
+static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48, "shared memory layout");
+
+template <int R>
+__device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
+    return base + CacheLayout<R>::kBars + 8u * (uint32_t)i;
+}
+
+// Sums the plan over the block and finds this CTA's run of tiles; every thread
+// of the block calls it, `scan` is shared memory (12 long long, then an int4).
+// Returns the CTAs that share the tiles.
+template <int kThreads>
+__device__ int cache_locate(const CachePlan& p, long long* scan, int cta, int ctas, unsigned int* status,
+                            long long* begin, long long* end, long long* total, CachePlace* place, bool at_end) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long pairs = (long long)p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
+    const long long first = min(tid * per, pairs), last = min(first + per, pairs);
     bool bad = false;
-    const CacheSpan s = cache_span(c.seq_lens[b], p.q_lens ? p.q_lens[b] : p.Sq, c.max_blocks * c.block_size, p.Sq, &bad);
-    if (i >= s.count) return;
-    const int n = min(s.len, p.causal ? max(s.first + i + 1, 0) : s.len);
-    const __nv_bfloat16* q = p.q + b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2] + lane * E;
-    float qf[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        qf[e] = __bfloat162float(q[e]);
-        o[e] = 0.f;
+    const long long mine = plan_chunk(p, first, last, &bad);
+    if (bad && cta == 0) atomicOr(status, kStatusBadCache);
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
-        const int block = cache_block(c.block_table[(long long)b * c.max_blocks + (j >> c.block_shift)], c.num_blocks, &bad);
-        if (block < 0) continue;
-        const size_t at = cache_offset(block, h, j & (c.block_size - 1), c.Hkv, c.block_size, D) + lane * E;
-        const float ks = c.k_scale[(long long)block * c.Hkv + h], vs = c.v_scale[(long long)block * c.Hkv + h];
-        float dot = 0.f;
-        for (int e = 0; e < E; ++e) dot += qf[e] * e4m3_unpair(c.k[at + e]).x;
-        for (int w = 16; w > 0; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
-        const float x = dot * ks * p.scale_log2, top = fmaxf(m, x);
-        const float keep = top == -INFINITY ? 1.f : ptx::ex2(m - top), w = top == -INFINITY ? (x == x ? 0.f : x) : ptx::ex2(x - top);
-        l = l * keep + w;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * vs * e4m3_unpair(c.v[at + e]).x;
-        m = top;
+    if (lane == 31) scan[warp] = sum;
+    __syncthreads();
+    long long before = sum - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
     }
-    if (bad && lane == 0) atomicOr(c.status, kStatusBadCache);
+    *total = all;
+    ctas = plan_ctas(all, ctas);
+    *begin = plan_begin(all, cta, ctas);
+    *end = plan_begin(all, cta + 1, ctas);
+    const long long want = at_end ? *end : *begin;
+    int* out = reinterpret_cast<int*>(scan + 12);
+    if (want >= before && want < before + mine) {
+        const CachePlace x = plan_find(p, first, want - before);
+        out[0] = x.b;
+        out[1] = x.qt;
+        out[2] = x.h;
+        out[3] = x.t;
+    }
+    __syncthreads();
+    *place = want < all ? CachePlace{out[0], out[1], out[2], out[3]} : CachePlace{p.B, 0, 0, 0};
+    return ctas;
+}
+
+// Row r of a unit: its query, head, and whether it is in use.
+__device__ __forceinline__ bool cache_row(const CacheFwdParams& p, const CacheUnit& u, int r, int* i, int* hq) {
+    const int iq = r / p.hper, g = u.h % p.hgroups * p.hper + (r - iq * p.hper);
+    *i = u.qt * p.plan.qper + iq;
+    *hq = u.h / p.hgroups * p.group + g;
+    return iq < p.plan.qper && *i < u.s.count && g < p.group;
+}
+
+// ---------------------------------------------------------------- warp 0: pages
+template <int R>
+__device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur,
+                                uint32_t base, uint8_t* smem, volatile int* abort_flag) {
+    using L = CacheLayout<R>;
+    const CacheView& c = p.c;
+    const int lane = threadIdx.x & 31;
+    const int pages = kCacheTile >> c.block_shift;  // of one tile
+    const uint64_t lim = p.wait_limit_ns;
+    int stage = 0;
+    uint32_t phase = 0, pend = 0, pend_par = 0;
+    bool bad = false;
+    CacheUnit u;
+    while (cursor_next(p.plan, cur, u)) {
+        const int hk = u.h / p.hgroups;
+        const int* table = c.block_table + (long long)u.b * c.max_blocks;
+        const int last_page = (u.keys + c.block_size - 1) >> c.block_shift;  // pages with a key that some row sees
+        // This lane's page of a window of 32: its block (-1: none), scales.  The next window's scales and
+        // the one after that's table entries are under way meanwhile.
+        const int page0 = u.t * pages;
+        auto entry = [&](int page) { return page < last_page ? __ldg(table + page) : -1; };
+        auto block_of = [&](int page, int e) { return page < last_page ? cache_block(e, c.num_blocks, &bad) : -1; };
+        auto scales = [&](int block) {
+            const long long at = (long long)block * c.Hkv + hk;
+            return block < 0 ? make_float2(0.f, 0.f) : make_float2(__ldg(c.k_scale + at), __ldg(c.v_scale + at));
+        };
+        int window = page0 + lane;
+        int block = block_of(window, entry(window)), next = block_of(window + 32, entry(window + 32));
+        float2 sc = scales(block), next_sc = scales(next);
+        int ahead = entry(window + 64);
+        int at = 0;  // the tile's first page in the window
+        for (int t = u.t; t < u.t + u.n; ++t) {
+            if (at == 32) {
+                at = 0;
+                window += 32;
+                block = next;
+                sc = next_sc;
+                next = block_of(window + 32, ahead);
+                next_sc = scales(next);
+                ahead = entry(window + 64);
+            }
+            bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
+            if (!__all_sync(0xffffffffu, ok)) goto drain;
+            const int i = lane - at;
+            const bool mine = i >= 0 && i < pages;
+            // pages that some row should see but that the table places outside the cache
+            const uint32_t missing = __ballot_sync(0xffffffffu, mine && block < 0 && window < last_page) >> at;
+            float* info = reinterpret_cast<float*>(smem + L::kInfo + stage * L::kInfoBytes);
+            if (mine) {
+                info[i] = sc.x;
+                info[8 + i] = sc.y;
+            }
+            if (lane == 0) reinterpret_cast<int*>(info)[16] = (int)missing;
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kKFull + stage), L::kTileBytes);
+                ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kVFull + stage), L::kTileBytes);
+            }
+            __syncwarp();
+            if (mine) {
+                // A page that is not there is read past the last block, where TMA fills zeros.
+                const int row = block < 0 ? c.num_blocks * c.Hkv : block * c.Hkv + hk;
+                const uint32_t dst = base + (uint32_t)stage * L::kStageBytes + (uint32_t)(i << c.block_shift) * 128u;
+                ptx::tma_load_3d(dst, tm_k, cache_bar<R>(base, L::kKFull + stage), 0, 0, row);
+                ptx::tma_load_3d(dst + L::kTileBytes, tm_v, cache_bar<R>(base, L::kVFull + stage), 0, 0, row);
+            }
+            pend |= 1u << stage;
+            pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+            at += pages;
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (bad) atomicOr(p.c.status, kStatusBadCache);
+    return;
+drain:
+    for (int s = 0; s < L::kStages; ++s)
+        if (pend & (1u << s)) {
+            ptx::drain_wait(cache_bar<R>(base, L::kKFull + s), (pend_par >> s) & 1u, lim);
+            ptx::drain_wait(cache_bar<R>(base, L::kVFull + s), (pend_par >> s) & 1u, lim);
+        }
+}
+
+// ---------------------------------------------------------------- warp 1: products
+template <int R>
+__device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
+                               volatile int* abort_flag) {
+    using L = CacheLayout<R>;
+    constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, L::kN, false);
+    constexpr uint32_t kIdescO = ptx::idesc_e4m3_a_mn(128, L::kN);
+    const uint64_t lim = p.wait_limit_ns;
+    const int k_steps = p.c.D / 32;
+    auto wait = [&](int bar, uint32_t par) {
+        return ptx::mbar_wait_spin(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim);
+    };
+    int stage = 0, g = 0;       // stage and number of the tile whose S^T is next
+    uint32_t phase = 0;
+    int prev_stage = -1, prev_unit = 0, prev_phase = 0;  // the tile whose O^T step is still to come
+    bool prev_first = false, prev_last = false;
+    auto issue_pv = [&]() -> bool {  // of tile g - 1
+        const int pb = (g - 1) & 1, ub = prev_unit & 1;
+        if (!wait(L::kVFull + prev_stage, prev_phase)) return false;
+        if (prev_first && !wait(L::kOFree + ub, ((prev_unit >> 1) & 1) ^ 1)) return false;
+        if (!wait(L::kPFull + pb, ((g - 1) >> 1) & 1)) return false;
+        ptx::tc_fence_after();
+        ptx::mma_ss_f8_a_mn_k128(tmem + L::kO + (uint32_t)ub * L::kN,
+                                 ptx::sdesc_sw128(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes, 16, 1024),
+                                 ptx::sdesc_sw128(base + L::kP + (uint32_t)pb * L::kN * 128, 16, 1024), kIdescO,
+                                 prev_first ? 0u : 1u);
+        ptx::mma_commit(cache_bar<R>(base, L::kEmpty + prev_stage));
+        ptx::mma_commit(cache_bar<R>(base, L::kPvDone + pb));
+        if (prev_last) ptx::mma_commit(cache_bar<R>(base, L::kOFull + ub));
+        prev_stage = -1;
+        return true;
+    };
+    for (int unit = 0;; ++unit) {
+        const int ub = unit & 1;
+        if (!wait(L::kQFull + ub, (unit >> 1) & 1)) goto done;
+        const int n = reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub].n;
+        if (n == 0) break;
+        for (int k = 0; k < n; ++k, ++g) {
+            const int sb = g & 1;
+            // While this tile's K is still on its way, the last tile's O^T goes first.
+            if (prev_stage >= 0 && !ptx::mbar_test_wait(cache_bar<R>(base, L::kKFull + stage), phase) && !issue_pv())
+                goto done;
+            if (!wait(L::kKFull + stage, phase) || !wait(L::kSFree + sb, ((g >> 1) & 1) ^ 1)) goto done;
+            ptx::tc_fence_after();
+            {
+                const uint64_t a = ptx::sdesc_sw128(base + (uint32_t)stage * L::kStageBytes, 16, 1024);
+                const uint64_t b = ptx::sdesc_sw128(base + L::kQ + (uint32_t)ub * L::kN * 128, 16, 1024);
+                for (int s = 0; s < k_steps; ++s)
+                    ptx::mma_ss_f8(tmem + L::kS + (uint32_t)sb * L::kN, a + 2 * s, b + 2 * s, kIdescS, s > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(cache_bar<R>(base, L::kSFull + sb));
+            if (k == n - 1) ptx::mma_commit(cache_bar<R>(base, L::kQEmpty + ub));
+            if (prev_stage >= 0 && !issue_pv()) goto done;
+            prev_stage = stage;
+            prev_phase = (int)phase;
+            prev_unit = unit;
+            prev_first = k == 0;
+            prev_last = k == n - 1;
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (prev_stage >= 0) issue_pv();
+done:
+    ptx::mma_commit(cache_bar<R>(base, L::kDrain));
+    ptx::drain_wait(cache_bar<R>(base, L::kDrain), 0u, lim);
+}
+
+// ---------------------------------------------------------------- warps 2-3: query rows
+template <int R>
+__device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint32_t base, uint8_t* smem,
+                                 volatile int* abort_flag) {
+    using L = CacheLayout<R>;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
+    const int D = p.c.D;
+    CacheUnit u;
+    for (int unit = 0;; ++unit) {
+        const int ub = unit & 1;
+        const bool more = cursor_next(p.plan, cur, u);
+        const bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
+                                       p.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        CacheWork* work = reinterpret_cast<CacheWork*>(smem + L::kUnit) + ub;
+        if (more) {
+            CacheRow* rows = reinterpret_cast<CacheRow*>(smem + L::kRows) + ub * R;
+            constexpr int kBatch = 4;
+#pragma unroll 1
+            for (int r0 = w; r0 < R; r0 += 2 * kBatch) {
+                uint2 x[kBatch];  // 4 elements a lane (2 for D = 64)
+                bool used[kBatch];
+                long long at[kBatch];
+                int seen[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    int i, hq;
+                    used[k] = cache_row(p, u, r0 + 2 * k, &i, &hq);
+                    at[k] = used[k] ? ((long long)u.b * p.Hq + hq) * p.Sq + i : -1;
+                    seen[k] = !used[k] ? 0 : p.plan.causal ? max(u.s.first + i + 1, 0) : u.s.len;
+                    x[k] = make_uint2(0, 0);
+                    if (used[k]) {
+                        const __nv_bfloat16* src = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2];
+                        if (D == 128)
+                            x[k] = *reinterpret_cast<const uint2*>(src + lane * 4);
+                        else
+                            x[k].x = *reinterpret_cast<const uint32_t*>(src + lane * 2);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + 2 * k;
+                    // the largest magnitude, by bit pattern; not finite: the whole row is NaN
+                    const uint32_t m0 = __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0 & 0xffffu, m0 >> 16));
+                    const float scale = e4m3_pow2_scale(__uint_as_float(top << 16));
+                    const float inv = top >= 0x7f80u ? NAN : 1.f / scale;
+                    float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xffff0000u),
+                                  __uint_as_float(x[k].y << 16), __uint_as_float(x[k].y & 0xffff0000u)};
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float a = f[2 * e] * inv, b = f[2 * e + 1] * inv;
+                        hi[e] = e4m3_pair(a, b);
+                        const float2 h = e4m3_unpair(hi[e]);
+                        lo[e] = e4m3_pair(a - h.x, b - h.y);
+                    }
+                    // hi and lo rows of the warpgroup that owns row r: n = wg * R + (r mod H) and + H
+                    const int n = (r / L::kH) * R + r % L::kH;
+                    auto put = [&](int row, const uint32_t* v) {
+                        const uint32_t line = base + L::kQ + (uint32_t)ub * L::kN * 128 + (uint32_t)row * 128u;
+                        if (D == 128)
+                            ptx::st_shared_u32(line + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4, v[0] | v[1] << 16);
+                        else
+                            ptx::st_shared_u16(line + (((lane >> 3) ^ (row & 7)) << 4) + (lane & 7) * 2, v[0]);
+                    };
+                    put(n, hi);
+                    put(n + L::kH, lo);
+                    if (lane == 0) rows[r] = CacheRow{used[k] ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
+                }
+            }
+            if (w == 0 && lane == 0) {
+                const int q0 = u.qt * p.plan.qper;
+                work->t = u.t;
+                work->n = u.n;
+                work->keys = u.keys;
+                work->keys_all = p.plan.causal ? max(u.s.first + q0 + 1, 0) : u.s.len;
+                work->slot = u.n == u.tiles ? -1 : u.t > 0 ? 0 : 1;
+                work->rows = min(p.plan.qper, u.s.count - q0) * p.hper;
+            }
+        } else if (w == 0 && lane == 0) {
+            work->n = 0;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(cache_bar<R>(base, L::kQFull + ub));
+        if (!more) return;
+    }
+}
+
+// ---------------------------------------------------------------- warps 4-11: softmax
+template <int R>
+__device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
+                                   volatile int* abort_flag) {
+    using L = CacheLayout<R>;
+    constexpr int H = L::kH;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wg = (warp - 4) >> 2, wq = warp & 3;
+    const int j = wq * 32 + lane;  // this thread's key of a tile (lane of S^T) and its d (lane of O^T)
+    const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * R);
+    const uint64_t lim = p.wait_limit_ns;
+    float4* tab = reinterpret_cast<float4*>(smem + L::kTab) + wg * H;
+    float2* mv = reinterpret_cast<float2*>(smem + L::kMv) + wg * H;
+    float2* fac = reinterpret_cast<float2*>(smem + L::kFac) + wg * H;
+    float2* red = reinterpret_cast<float2*>(smem + L::kRed) + wg * 4 * H;
+    int* nan_at = reinterpret_cast<int*>(smem + L::kNanAt);
+    volatile int* unset = reinterpret_cast<volatile int*>(smem + L::kUnset) + wg;
+    volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kNanSeen);
+    const int bar = 1 + wg;  // the warpgroup's barrier
+    // A wait that ran out leaves this false: the warp goes on without waiting and without writing
+    // results, so that it meets its warpgroup at every barrier and nobody is left there.
+    bool alive = true;
+    auto wait = [&](int which, uint32_t par) {
+        if (alive) alive = ptx::mbar_wait(cache_bar<R>(base, which), par, abort_flag, p.c.status, lim);
+        alive = __all_sync(0xffffffffu, alive);
+    };
+    auto arrive = [&](int which) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(cache_bar<R>(base, which));
+    };
+    const int page = j >> p.c.block_shift;  // of a tile
+    int g = 0, stage = 0;                   // number and stage of the current tile
+    uint32_t phase = 0;
+    uint32_t s[R];  // S^T: hi columns, then lo columns; then e, then w
+    float l[H];     // this thread's keys' part of the rows' sums
+    for (int unit = 0;; ++unit) {
+        const int ub = unit & 1;
+        wait(L::kQFull + ub, (unit >> 1) & 1);
+        const CacheWork work = reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub];
+        if (ptx::bar_any(3, 256, !alive) || work.n == 0) break;  // all eight warps go on together or not at all
+        const CacheRow* rows = reinterpret_cast<const CacheRow*>(smem + L::kRows) + ub * R + wg * H;
+        const bool idle = work.rows <= wg * H;
+        if (j < H) {
+            mv[j] = make_float2(-INFINITY, -INFINITY);
+            tab[j] = make_float4(rows[j].factor, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int r = 0; r < H; ++r) l[r] = 0.f;
+        bool todo = true;  // some row has no maximum yet
+        // Some tile of the share holds keys that not every row sees.  Like all that decides about
+        // barriers, it follows from `work` alone, which every warp has read the same.
+        const bool borders = (work.t + work.n) * kCacheTile > work.keys_all;
+
+        for (int k = 0; k < work.n; ++k, ++g) {
+            const int t = work.t + k, sb = g & 1;
+            wait(L::kKFull + stage, phase);  // the scales beside the tile
+            wait(L::kSFull + sb, (g >> 1) & 1);
+            ptx::tc_fence_after();
+            const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
+            const float ks = info[page];
+            const int missing = reinterpret_cast<const int*>(info)[16];
+            const int key = t * kCacheTile + j;
+            const bool full = (t + 1) * kCacheTile <= work.keys_all && missing == 0;
+            const bool here = key < work.keys && !((missing >> page) & 1);
+            const float vs = here ? info[8 + page] : 0.f;
+            if ((t + 1) * kCacheTile > work.keys_all && wg == 0) {
+                // A weight of 0 times NaN is NaN: keys that nobody sees become 0 in V, and NaN that only
+                // some rows see is taken out and noted by the first position that has it.
+                wait(L::kVFull + stage, phase);
+                const uint32_t line = base + (uint32_t)stage * L::kStageBytes + L::kTileBytes + (uint32_t)j * 128u;
+                if (alive && key >= work.keys) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) ptx::st_shared_v4(line + 16 * x, 0, 0, 0, 0);
+                } else if (alive && key >= work.keys_all) {
+                    for (int x = 0; x < 8; ++x) {
+                        const uint4 v = ptx::ld_shared_v4(line + 16 * x);
+                        uint32_t word[4] = {v.x, v.y, v.z, v.w};
+                        bool found = false;
+                        for (int y = 0; y < 4; ++y)
+                            for (int b = 0; b < 4; ++b)
+                                if ((word[y] >> (8 * b) & 0x7fu) == 0x7fu) {
+                                    found = true;
+                                    word[y] &= ~(0xffu << (8 * b));
+                                    atomicMin(nan_at + (x ^ (j & 7)) * 16 + y * 4 + b, key);
+                                }
+                        if (found) {
+                            *nan_seen = 1;
+                            ptx::st_shared_v4(line + 16 * x, word[0], word[1], word[2], word[3]);
+                        }
+                    }
+                }
+            }
+            if (!idle) {
+                const uint32_t s_addr = my_tmem + L::kS + (uint32_t)sb * L::kN;
+                auto sees = [&](int r) { return here && key < rows[r].keys; };
+                // e and w of this thread's key for every row; returns the largest of them.
+                auto weights = [&]() {
+                    float top = 0.f;
+#pragma unroll
+                    for (int r = 0; r < H; ++r) {
+                        const float4 f = tab[r];
+                        const float x = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks;
+                        float y = fmaf(x, f.x, f.y);
+                        if (!full) y = sees(r) ? y : -INFINITY;
+                        const float e = ptx::ex2(y), w = e * vs * f.z;
+                        s[r] = __float_as_uint(e);
+                        s[H + r] = __float_as_uint(w);
+                        top = ptx::max3(top, e, w);
+                    }
+                    return top;
+                };
+                float top = 0.f;
+                if (!todo) {
+                    ptx::tmem_load<R>(s_addr, s);
+                    top = weights();
+                }
+                if (ptx::bar_any(bar, 128, todo || top > 448.f)) {
+                    // The rows' maxima move: over the tile's scores, and over scores + log2 of V's scale.
+                    ptx::tmem_load<R>(s_addr, s);
+                    const float lvs = ptx::lg2(vs);
+                    auto warp_max = [](float x) {  // through the order of the bit patterns
+                        const int b = __float_as_int(x), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+                        return __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+                    };
+#pragma unroll
+                    for (int r = 0; r < H; ++r) {
+                        float y = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks * rows[r].factor;
+                        if (!full) y = sees(r) ? y : -INFINITY;
+                        const float a = warp_max(y), b = warp_max(y + lvs);
+                        if (lane == (r & 31)) red[wq * H + r] = make_float2(a, b);
+                    }
+                    ptx::bar_sync(bar, 128);
+                    if (wq == 0) {
+                        bool open = false;
+                        if (lane < H) {
+                            const CacheRow row = rows[lane];
+                            const float2 had = mv[lane];
+                            const float lc_had = tab[lane].w;
+                            float m = had.x, v = had.y;
+                            if (row.at >= 0) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    m = fmaxf(m, red[x * H + lane].x);
+                                    v = fmaxf(v, red[x * H + lane].y);
+                                }
+                            }
+                            const bool none = m == -INFINITY, had_none = had.x == -INFINITY;
+                            const float lc = none ? 0.f : fminf(m - v + 6.f, 100.f);
+                            fac[lane] = had_none ? make_float2(0.f, 0.f)
+                                                 : make_float2(ptx::ex2(had.x - m), ptx::ex2(had.x - m + lc - lc_had));
+                            mv[lane] = make_float2(m, v);
+                            tab[lane] = make_float4(row.factor, none ? 0.f : -m, none ? 0.f : ptx::ex2(lc), lc);
+                            open = none && row.at >= 0 && row.keys > 0;
+                        }
+                        open = __any_sync(0xffffffffu, open);
+                        if (lane == 0) *unset = open;
+                    }
+                    ptx::bar_sync(bar, 128);
+                    todo = *unset;
+                    if (k > 0) {
+                        wait(L::kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                        ptx::tc_fence_after();
+                        const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
+                        ptx::tmem_load<R>(o_addr, s);
+#pragma unroll
+                        for (int r = 0; r < H; ++r) {
+                            const float2 f = fac[r];
+                            l[r] *= f.x;
+                            s[r] = __float_as_uint(__uint_as_float(s[r]) * f.y);
+                            s[H + r] = __float_as_uint(__uint_as_float(s[H + r]) * f.y);
+                        }
+                        ptx::tmem_store<R>(o_addr, s);
+                        ptx::tmem_load<R>(s_addr, s);
+                    }
+                    weights();
+                }
+                ptx::tc_fence_before();
+                arrive(L::kSFree + sb);
+                wait(L::kPvDone + sb, ((g >> 1) & 1) ^ 1);  // the tile before last has left P's buffer
+                const uint32_t p_addr = base + L::kP + (uint32_t)sb * L::kN * 128u + (uint32_t)wg * R * 128u + (j & 15);
+                auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's part, a multiple of 8 rows apart
+                    ptx::st_shared_u8(p_addr + (uint32_t)n * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4), code);
+                };
+#pragma unroll
+                for (int r = 0; r < H; r += 2) {
+                    l[r] += __uint_as_float(s[r]);
+                    l[r + 1] += __uint_as_float(s[r + 1]);
+                    // hi: the weight at 4 significant bits, to nearest; lo: the rest
+                    const float w0 = __uint_as_float(s[H + r]), w1 = __uint_as_float(s[H + r + 1]);
+                    const float h0 = __uint_as_float((s[H + r] + 0x80000u) & 0xfff00000u);
+                    const float h1 = __uint_as_float((s[H + r + 1] + 0x80000u) & 0xfff00000u);
+                    const uint32_t hi = e4m3_pair(h0, h1), lo = e4m3_pair(w0 - h0, w1 - h1);
+                    put(r, hi);
+                    put(r + 1, hi >> 8);
+                    put(H + r, lo);
+                    put(H + r + 1, lo >> 8);
+                }
+            } else {
+                arrive(L::kSFree + sb);
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            arrive(L::kPFull + sb);
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+
+        // ---- the unit's rows leave
+        float2* sums = red;
+        if (!idle) {
+#pragma unroll
+            for (int r = 0; r < H; ++r) {
+                float x = l[r];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane == (r & 31)) sums[wq * H + r].x = x;
+            }
+        }
+        bool nan = false;
+        if (borders) {
+            ptx::bar_sync(3, 256);
+            nan = *nan_seen != 0;
+        } else {
+            ptx::bar_sync(bar, 128);
+        }
+        const long long slot = (long long)blockIdx.x * 2 + work.slot;
+        if (!idle && j < H) {
+            const float sum = sums[j].x + sums[H + j].x + sums[2 * H + j].x + sums[3 * H + j].x;
+            const float m = mv[j].x, c = tab[j].z;
+            float f = c == 0.f ? 0.f : 1.f / c;
+            if (sum != sum) f = sum;  // NaN, whatever O holds
+            if (work.slot < 0) {
+                f = sum == 0.f ? 0.f : f / sum;
+                if (alive && p.lse != nullptr && rows[j].at >= 0)
+                    p.lse[rows[j].at] = sum == 0.f ? -INFINITY : (m + ptx::lg2(sum)) * kLn2;
+            } else if (alive) {
+                p.part_ml[slot * R + wg * H + j] = make_float2(m, sum);
+            }
+            fac[j].x = f;
+        }
+        ptx::bar_sync(bar, 128);
+        wait(L::kOFull + ub, (unit >> 1) & 1);
+        ptx::tc_fence_after();
+        if (!idle) {
+            ptx::tmem_load<R>(my_tmem + L::kO + (uint32_t)ub * L::kN, s);
+            const int first_nan = nan ? nan_at[j] : 0x7fffffff;
+            if (alive && j < p.c.D) {
+#pragma unroll
+                for (int r = 0; r < H; ++r) {
+                    float o = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * fac[r].x;
+                    if (first_nan < rows[r].keys) o = NAN;
+                    if (work.slot >= 0)
+                        p.part_o[(slot * R + wg * H + r) * 128 + j] = o;
+                    else if (rows[r].at >= 0)
+                        p.out[rows[r].at * p.c.D + j] = __float2bfloat16(o);
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        arrive(L::kOFree + ub);
+        arrive(L::kQEmpty + ub);
+        if (nan) {  // put back for the next unit
+            ptx::bar_sync(3, 256);
+            if (wg == 0) nan_at[j] = 0x7fffffff;
+            if (wg == 0 && j == 0) *nan_seen = 0;
+            ptx::bar_sync(3, 256);
+        }
+    }
+}
+
+template <int R>
+__global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCtas)
+    attn_cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ CacheFwdParams p) {
+    using L = CacheLayout<R>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    ptx::launch_dependents();
+    long long begin, end, total;
+    CachePlace place;
+    cache_locate<L::kThreads>(p.plan, reinterpret_cast<long long*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
+                              &begin, &end, &total, &place, false);
+    if (begin == end) return;  // the whole block
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            ptx::mbar_init(cache_bar<R>(base, L::kKFull + s), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kVFull + s), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kEmpty + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(cache_bar<R>(base, L::kQFull + i), 2);    // the query warps
+            ptx::mbar_init(cache_bar<R>(base, L::kQEmpty + i), 9);   // the softmax warps and the last S^T product
+            ptx::mbar_init(cache_bar<R>(base, L::kSFull + i), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kSFree + i), 8);
+            ptx::mbar_init(cache_bar<R>(base, L::kPFull + i), 8);
+            ptx::mbar_init(cache_bar<R>(base, L::kPvDone + i), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kOFull + i), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kOFree + i), 8);
+        }
+        ptx::mbar_init(cache_bar<R>(base, L::kDrain), 1);
+        *abort_flag = 0;
+        *reinterpret_cast<volatile int*>(smem + L::kNanSeen) = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp >= 4 && warp < 8) reinterpret_cast<int*>(smem + L::kNanAt)[threadIdx.x - 128] = 0x7fffffff;
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), L::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        cache_load_role<R>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+    } else if (warp == 1) {
+        if (lane == 0) cache_mma_role<R>(p, base, smem, tmem, abort_flag);
+    } else if (warp < 4) {
+        cache_query_role<R>(p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+    } else {
+        cache_softmax_role<R>(p, base, smem, tmem, abort_flag);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+// Joins a unit's partial results: CTA x joins the unit that begins in CTA x of
+// the first kernel and ends in a later one (there is at most one), rows
+// blockIdx.y * 8 .. + 7, a warp each: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
+template <int R>
+__global__ void __launch_bounds__(256) attn_cache_join_kernel(const CacheFwdParams p, int ctas) {
+    __shared__ long long scan[12 + 4];
+    long long begin, end, total;
+    CachePlace at;
+    ctas = cache_locate<256>(p.plan, scan, blockIdx.x, ctas, p.c.status, &begin, &end, &total, &at, true);
+    CacheUnit u;
+    bool mine = false;
+    if (begin < end && at.b < p.plan.B && at.t > 0 && end - at.t >= begin) {
+        CachePlace start = at;
+        start.t = 0;
+        CacheCursor cur = cursor_at(p.plan, start, 0x7fffffff);
+        mine = cursor_next(p.plan, cur, u);
+    }
+    ptx::wait_prerequisites();
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    int i, hq;
+    if (!mine || !cache_row(p, u, r, &i, &hq)) return;
+    // Pieces: slot 1 of this CTA, slot 0 of the following ones up to the unit's end.
+    const int n = plan_last(total, blockIdx.x, ctas, end - at.t + u.tiles) - blockIdx.x + 1;
+    auto piece = [&](int x) { return ((long long)(blockIdx.x + x) * 2 + (x == 0 ? 1 : 0)) * R + r; };
+    float m = -INFINITY;
+    for (int x = lane; x < n; x += 32) m = fmaxf(m, p.part_ml[piece(x)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+        const float2 ml = p.part_ml[piece(x)];
+        const float f = ptx::ex2(ml.x - ref);
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + piece(x) * 128 + lane * 4);
+        l += f * ml.y;
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int e = 0; e < E; ++e) p.out[row * D + lane * E + e] = __float2bfloat16(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
+    const long long row = ((long long)u.b * p.Hq + hq) * p.Sq + i;
+    if (lane * 4 < p.c.D) {
+        uint2 w;
+        w.x = ptx::pack_bf16x2(o.x * inv, o.y * inv);
+        w.y = ptx::pack_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(p.out + row * p.c.D + lane * 4) = w;
+    }
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
 }
 
 }  // namespace attn

@@ -255,3 +255,109 @@ def test_checked_index_arithmetic(tmp_path):
                     str(tmp_path / "index"), str(src)], check=True)
     res = subprocess.run([str(tmp_path / "index")], capture_output=True, text=True)
     assert res.returncode == 0 and res.stdout.startswith("OK"), res.stdout
+
+
+PLAN_PROGRAM = r"""
+#include "cache_index.h"
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+using namespace attn;
+#define CHECK(c) do { if (!(c)) { std::printf("FAIL line %d: %s\n", __LINE__, #c); return 1; } } while (0)
+// Every unit's tiles are taken exactly once and in order, for each count of CTAs, with the plan summed
+// by `threads` threads in chunks as the kernel does it.
+int main() {
+    std::srand(7);
+    for (int round = 0; round < 400; ++round) {
+        CachePlan p{};
+        p.B = 1 + std::rand() % 9;
+        p.Sq = 1 + std::rand() % 40;
+        p.capacity = 128 * (1 + std::rand() % 8);
+        p.causal = std::rand() % 2;
+        p.qper = 1 + std::rand() % 16;
+        p.q_tiles = (p.Sq + p.qper - 1) / p.qper;
+        p.heads = 1 + std::rand() % 5;
+        std::vector<int> lens(p.B), counts(p.B);
+        for (int b = 0; b < p.B; ++b) {
+            lens[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (p.capacity + 1);
+            if (std::rand() % 9 == 0) lens[b] = -3;
+            if (std::rand() % 9 == 0) lens[b] = 2147483647;
+            counts[b] = std::rand() % (p.Sq + 1);
+        }
+        p.seq_lens = lens.data();
+        p.q_lens = std::rand() % 3 ? counts.data() : nullptr;
+        // the units, written down one by one
+        struct U { int b, qt, h, tiles, keys; };
+        std::vector<U> want;
+        long long total = 0;
+        for (int b = 0; b < p.B; ++b) {
+            const int len = lens[b] < 0 ? 0 : lens[b] > p.capacity ? p.capacity : lens[b];
+            const int count = p.q_lens ? counts[b] : p.Sq;
+            for (int qt = 0; qt * p.qper < count; ++qt) {
+                const int last = (qt + 1) * p.qper < count ? (qt + 1) * p.qper : count;
+                int keys = p.causal ? len - count + last : len;
+                if (keys < 0) keys = 0;
+                const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
+                for (int h = 0; h < p.heads; ++h) {
+                    want.push_back({b, qt, h, tiles, keys});
+                    total += tiles;
+                }
+            }
+        }
+        const long long pairs = (long long)p.B * p.q_tiles;
+        const int threads = 1 + std::rand() % 20;
+        const long long per = (pairs + threads - 1) / threads;
+        std::vector<long long> sum(threads);
+        long long all = 0;
+        bool bad = false;
+        for (int t = 0; t < threads; ++t) {
+            const long long a = t * per < pairs ? t * per : pairs, z = a + per < pairs ? a + per : pairs;
+            all += sum[t] = plan_chunk(p, a, z, &bad);
+        }
+        CHECK(all == total);
+        const int given = 1 + std::rand() % 70, ctas = plan_ctas(total, given);
+        size_t unit = 0;
+        int tile = 0, pieces = 0, expect_last = -1;
+        for (int c = 0; c < given; ++c) {
+            const long long begin = plan_begin(total, c, ctas), end = plan_begin(total, c + 1, ctas);
+            CHECK((begin == end) == (c >= ctas));  // no CTA without a tile among those that share them
+            if (begin == end) continue;
+            long long before = 0;
+            int t = 0;
+            while (begin >= before + sum[t]) before += sum[t++];
+            CacheCursor cur = cursor_at(p, plan_find(p, t * per, begin - before), end - begin);
+            CacheUnit u;
+            while (cursor_next(p, cur, u)) {
+                CHECK(unit < want.size());
+                const U& w = want[unit];
+                CHECK(u.b == w.b && u.qt == w.qt && u.h == w.h && u.tiles == w.tiles && u.keys == w.keys && u.t == tile && u.n > 0);
+                CHECK(u.t + u.n <= u.tiles);
+                tile += u.n;
+                ++pieces;
+                if (tile == u.tiles) {
+                    CHECK(pieces == 1 || expect_last == c);  // the piece that the join takes last
+                    tile = pieces = 0;
+                    ++unit;
+                } else if (pieces == 1) {
+                    CHECK(end - tile >= begin);  // it begins in this CTA
+                    expect_last = plan_last(total, c, ctas, end - tile + u.tiles);
+                }
+            }
+        }
+        CHECK(unit == want.size() && tile == 0);
+    }
+    std::printf("OK\n");
+    return 0;
+}
+"""
+
+
+def test_attention_work_is_split_exactly(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
+    src = tmp_path / "plan.cpp"
+    src.write_text(PLAN_PROGRAM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-fsanitize=address,undefined", "-I",
+                    os.path.join(ROOT, "causal_scaled_dot_gb300", "csrc"), "-o", str(tmp_path / "plan"), str(src)], check=True)
+    res = subprocess.run([str(tmp_path / "plan")], capture_output=True, text=True)
+    assert res.returncode == 0 and res.stdout.startswith("OK"), res.stdout + res.stderr
