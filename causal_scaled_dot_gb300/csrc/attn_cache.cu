@@ -274,6 +274,7 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     p.Sq = Sq;
     p.group = group;
     p.hper = group < R ? group : R;
+    p.hper_inv = (65536 + p.hper - 1) / p.hper;
     p.hgroups = (group + p.hper - 1) / p.hper;
     p.scale_log2 = scale * kLog2e;
     p.wait_limit_ns = host::wait_limit_ns();
@@ -285,6 +286,7 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     p.plan.causal = causal ? 1 : 0;
     p.plan.qper = R / p.hper;
     p.plan.q_tiles = (Sq + p.plan.qper - 1) / p.plan.qper;
+    if ((long long)cache->B * p.plan.q_tiles > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     p.plan.heads = cache->Hkv * p.hgroups;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (R) {

@@ -101,12 +101,12 @@ ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
 }
 
 // Tiles of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
-ATTN_HD long long plan_chunk(const CachePlan& p, long long first, long long last, bool* bad) {
+ATTN_HD long long plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
     if (first >= last) return 0;
     long long sum = 0;
-    int b = (int)(first / p.q_tiles), qt = (int)(first - (long long)b * p.q_tiles);
+    int b = p.q_tiles == 1 ? first : first / p.q_tiles, qt = first - b * p.q_tiles;
     CacheSpan s = plan_span(p, b, bad);
-    for (long long i = first; i < last; ++i) {
+    for (int i = first; i < last; ++i) {
         if (qt == p.q_tiles) {
             qt = 0;
             s = plan_span(p, ++b, bad);
@@ -122,9 +122,10 @@ struct CachePlace {
 };
 // The place of the tile `offset` tiles after the start of pair `first`
 // (offset < the tiles of the pairs from there on).
-ATTN_HD CachePlace plan_find(const CachePlan& p, long long first, long long offset) {
+ATTN_HD CachePlace plan_find(const CachePlan& p, int first, long long offset) {
     bool bad = false;
-    CachePlace x{(int)(first / p.q_tiles), (int)(first % p.q_tiles), 0, 0};
+    const int b = p.q_tiles == 1 ? first : first / p.q_tiles;
+    CachePlace x{b, first - b * p.q_tiles, 0, 0};
     CacheSpan s = plan_span(p, x.b, &bad);
     for (;;) {
         if (x.qt == p.q_tiles) {
@@ -136,7 +137,7 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, long long first, long long offs
             const int tiles = plan_tiles(p, s, x.qt);
             const long long all = (long long)tiles * p.heads;
             if (offset < all) {
-                x.h = (int)(offset / tiles);
+                x.h = offset < 0x7fffffff ? (int)offset / tiles : (int)(offset / tiles);
                 x.t = (int)(offset - (long long)x.h * tiles);
                 return x;
             }
@@ -150,7 +151,14 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, long long first, long long offs
 // between the first and the last piece of a unit is without a tile.
 ATTN_HD int plan_ctas(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
 // First tile of CTA `cta` of plan_ctas() many (the total for those past them).
-ATTN_HD long long plan_begin(long long total, int cta, int ctas) { return cta < ctas ? total * cta / ctas : total; }
+ATTN_HD long long plan_begin(long long total, int cta, int ctas) {
+    if (cta >= ctas) return total;
+    if (total < 0x7fffffff) {  // total * cta / ctas without a 64-bit division; ctas < 2^15
+        const int t = (int)total, q = t / ctas, r = t - q * ctas;
+        return (long long)q * cta + (r * cta) / ctas;
+    }
+    return total / ctas * cta + total % ctas * cta / ctas;
+}
 // The last CTA with a piece of a unit that begins in `cta` and ends before tile `unit_end`.
 ATTN_HD int plan_last(long long total, int cta, int ctas, long long unit_end) {
     while (plan_begin(total, cta + 1, ctas) < unit_end) ++cta;

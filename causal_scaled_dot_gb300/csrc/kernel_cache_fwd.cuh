@@ -14,16 +14,17 @@
 //     O^T [D x 2R]       += V^T [D x 128 keys] * Pp^T
 // with R = 8, 16, 32 or 64 query rows (the queries of a tile times the query
 // heads of one key/value head).  In S^T a thread owns one key, so a block's
-// scales are one factor per thread: s = (S_hi + S_lo) * ks * (row factor).
-// V's scale joins the weight, w = e * vs * c_r with e = 2^(s - M_r); c_r keeps
-// the row's largest w near 2^6, so that lo's underflow (2^-10) is 2^-16 of it
-// whatever the scales.  M_r and c_r move only when some w or e passes 448
-// (E4M3's largest): then the warpgroup finds the tile's maxima and rescales O^T
-// in tensor memory; otherwise a tile needs one vote of the warpgroup and no
-// reduction.  The sum of e is kept per thread (per key) and reduced at the end.
+// scales are one factor per thread.  V's scale vs joins the weight:
+//     w_j = 2^(s_j + log2 vs_j - M + 6),   M = max_j (s_j + log2 vs_j),
+//     O = (sum_j w_j code_j) / (sum_j w_j / vs_j),
+// so that a row's largest w is near 2^6 whatever the scales and lo's underflow
+// (2^-10) is 2^-16 of it.  M moves only when some w passes 448 (E4M3's largest):
+// then the warpgroup finds the tile's maxima and rescales O^T in tensor memory;
+// otherwise a tile needs one vote of the warpgroup and no reduction.  The sum of
+// w / vs is kept per thread (per key) and reduced at the end.
 //
 // Roles (384 threads): warp 0 copies pages (lane i takes page i of a tile) with
-// the tables and scales of the next 32 pages already in registers; warp 1
+// the tables and scales of the pages ahead already in registers; warp 1
 // issues the products; warps 2-3 split the next unit's q rows into pieces;
 // warps 4-7 and 8-11 are two softmax warpgroups, each with half of the R rows.
 // CTAs take equal runs of key tiles of all units (cache_index.h); a unit that
@@ -31,11 +32,14 @@
 // joins, already resident when the first one ends.
 //
 // What bounds it: one token over a long cache moves 2 bytes per (key, d) pair
-// and is bound by HBM; with R = 64 the softmax's issue slots (about 15
-// instructions a score) come before the tensor cores.
+// and is bound by HBM; with R = 64 the exponentials (16 a cycle and SM) and the
+// softmax's issue slots (about 8 instructions a score) come next to the tensor
+// cores.
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "cache_index.h"
 #include "common.cuh"
@@ -54,10 +58,11 @@ struct CacheFwdParams {
     float* lse;             // may be null
     int Hq, Sq, group;
     int hper;               // query heads of a unit
+    int hper_inv;           // ceil(2^16 / hper): r / hper = r * hper_inv >> 16 for r < 64
     int hgroups;            // units that share a key/value head: ceil(group / hper)
     float scale_log2;       // scale * log2(e)
-    float* part_o;          // [G][2][R][128] partial sums of w V / c
-    float2* part_ml;        // [G][2][R] their M and l
+    float* part_o;          // [G][2][R][128] partial sums of w code
+    float2* part_ml;        // [G][2][R] their M - 6 and sum of w / vs
     unsigned long long wait_limit_ns;
 };
 
@@ -76,27 +81,33 @@ struct CacheLayout {
     static constexpr uint32_t kInfoBytes = 80;
     static constexpr uint32_t kRows = kInfo + kStages * kInfoBytes;  // 2 x [R] CacheRow
     static constexpr uint32_t kUnit = kRows + 2 * R * 16;            // 2 x CacheWork
-    static constexpr uint32_t kTab = kUnit + 2 * 48;                 // [R] float4 {factor, -M, c, -}
-    static constexpr uint32_t kMv = kTab + R * 16;                   // [R] float2 {M, max of s + log2 vs}
-    static constexpr uint32_t kFac = kMv + R * 8;                    // [R] float2: what l and O are multiplied by
-    static constexpr uint32_t kRed = kFac + R * 8;                   // [2][4 warps][H] float2
-    static constexpr uint32_t kNanAt = kRed + 4 * R * 8;             // [128] first key with NaN in V's column
-    static constexpr uint32_t kScan = kNanAt + 512;                  // 12 long long + 6 int
+    static constexpr uint32_t kTab = kUnit + 2 * 48;                 // [R / 2] float4 {two rows' factors, their 6 - M}
+    static constexpr uint32_t kFac = kTab + R * 8;                   // [R] float: what l and O are multiplied by
+    static constexpr uint32_t kRed = kFac + R * 4;                   // [R][4 warps] float
+    static constexpr uint32_t kNanAt = kRed + R * 16;                // 2 x [128] first key with NaN in V's column
+    static constexpr uint32_t kScan = kNanAt + 1024;                 // 12 long long + 4 int
     static constexpr uint32_t kBars = kScan + 128;
     static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kQEmpty = kQFull + 2,
                          kSFull = kQEmpty + 2, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2,
-                         kOFull = kPvDone + 2, kOFree = kOFull + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1;
+                         kOFull = kPvDone + 2, kOFree = kOFull + 2, kNan = kOFree + 2, kDrain = kNan + 2,
+                         kNumBars = kDrain + 1;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
-    static constexpr uint32_t kUnset = kAbort + 4;    // [2] some row of the warpgroup has no maximum yet
-    static constexpr uint32_t kNanSeen = kUnset + 8;
-    static constexpr uint32_t kDynamicSmem = kNanSeen + 4 + 1024;
+    static constexpr uint32_t kNanSeen = kAbort + 4;  // [2]
+    static constexpr uint32_t kDynamicSmem = kNanSeen + 8 + 1024;
     static_assert(kInfo % 16 == 0 && kRows % 16 == 0 && kUnit % 16 == 0 && kTab % 16 == 0 && kScan % 8 == 0 && kBars % 8 == 0,
                   "alignment");
     static_assert(kCtas * (kDynamicSmem + 1024) <= 228 * 1024, "shared memory budget");
     static constexpr uint32_t kTmemCols = 4 * kN;     // S^T twice, O^T twice
     static_assert(kCtas * kTmemCols <= 512, "tensor memory budget");
     static constexpr uint32_t kS = 0, kO = 2 * kN;
+    // Rows go through the softmax C at a time; row r of a warpgroup has its hi piece in
+    // column column(r) of the warpgroup's R columns, and its lo piece C further.
+    static constexpr int kC = kH < 16 ? kH : 16;
+    __host__ __device__ static constexpr int column(int r) { return r / kC * 2 * kC + r % kC; }
+    // Pp^T: R = 8 keeps a row per column (K-major, 128 keys = 128 bytes); else a row per key (MN-major,
+    // 2R bytes), where a thread writes its key's codes 16 at a time.
+    static constexpr bool kPerKey = R > 8;
 };
 
 // A query row of a unit in shared memory: the factor of its scores, the keys it
@@ -129,18 +140,18 @@ template <int kThreads>
 __device__ int cache_locate(const CachePlan& p, long long* scan, int cta, int ctas, unsigned int* status,
                             long long* begin, long long* end, long long* total, CachePlace* place, bool at_end) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long pairs = (long long)p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
-    const long long first = min(tid * per, pairs), last = min(first + per, pairs);
+    const int pairs = p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
+    const int first = min(tid * per, pairs), last = min(first + per, pairs);
     bool bad = false;
     const long long mine = plan_chunk(p, first, last, &bad);
     if (bad && cta == 0) atomicOr(status, kStatusBadCache);
     long long sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    const int steps = pairs < 32 ? pairs : 32;  // lanes of a warp that have something
+    for (int o = 1; o < steps; o <<= 1) {
         const long long up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
     }
-    if (lane == 31) scan[warp] = sum;
+    if (lane == steps - 1) scan[warp] = sum;
     __syncthreads();
     long long before = sum - mine, all = 0;
 #pragma unroll
@@ -168,9 +179,10 @@ __device__ int cache_locate(const CachePlan& p, long long* scan, int cta, int ct
 
 // Row r of a unit: its query, head, and whether it is in use.
 __device__ __forceinline__ bool cache_row(const CacheFwdParams& p, const CacheUnit& u, int r, int* i, int* hq) {
-    const int iq = r / p.hper, g = u.h % p.hgroups * p.hper + (r - iq * p.hper);
+    const int iq = r * p.hper_inv >> 16;
+    const int hk = p.hgroups == 1 ? u.h : u.h / p.hgroups, g = (u.h - hk * p.hgroups) * p.hper + (r - iq * p.hper);
     *i = u.qt * p.plan.qper + iq;
-    *hq = u.h / p.hgroups * p.group + g;
+    *hq = hk * p.group + g;
     return iq < p.plan.qper && *i < u.s.count && g < p.group;
 }
 
@@ -186,24 +198,40 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
     int stage = 0;
     uint32_t phase = 0, pend = 0, pend_par = 0;
     bool bad = false;
-    CacheUnit u;
-    while (cursor_next(p.plan, cur, u)) {
-        const int hk = u.h / p.hgroups;
-        const int* table = c.block_table + (long long)u.b * c.max_blocks;
-        const int last_page = (u.keys + c.block_size - 1) >> c.block_shift;  // pages with a key that some row sees
-        // This lane's page of a window of 32: its block (-1: none), scales.  The next window's scales and
-        // the one after that's table entries are under way meanwhile.
-        const int page0 = u.t * pages;
-        auto entry = [&](int page) { return page < last_page ? __ldg(table + page) : -1; };
-        auto block_of = [&](int page, int e) { return page < last_page ? cache_block(e, c.num_blocks, &bad) : -1; };
-        auto scales = [&](int block) {
-            const long long at = (long long)block * c.Hkv + hk;
-            return block < 0 ? make_float2(0.f, 0.f) : make_float2(__ldg(c.k_scale + at), __ldg(c.v_scale + at));
-        };
-        int window = page0 + lane;
-        int block = block_of(window, entry(window)), next = block_of(window + 32, entry(window + 32));
-        float2 sc = scales(block), next_sc = scales(next);
-        int ahead = entry(window + 64);
+    // One sequence's table as far as some row of the unit sees.
+    struct Pages {
+        const int* table;
+        int last, hk;
+    };
+    auto pages_of = [&](const CacheUnit& u) {
+        return Pages{c.block_table + (long long)u.b * c.max_blocks, (u.keys + c.block_size - 1) >> c.block_shift,
+                     p.hgroups == 1 ? u.h : u.h / p.hgroups};
+    };
+    auto entry = [&](const Pages& g, int page) { return page < g.last ? __ldg(g.table + page) : -1; };
+    auto block_of = [&](const Pages& g, int page, int e) { return page < g.last ? cache_block(e, c.num_blocks, &bad) : -1; };
+    auto scales = [&](const Pages& g, int block) {
+        const long long at = (long long)block * c.Hkv + g.hk;
+        return block < 0 ? make_float2(0.f, 0.f) : make_float2(__ldg(c.k_scale + at), __ldg(c.v_scale + at));
+    };
+    // This lane's page of a window of 32: its block (-1: none) and scales.  What comes after it is under way
+    // meanwhile: of a long unit the next window's blocks and scales and the table entries of the one after
+    // that, and at a unit's start the first window of the next unit.
+    CacheUnit u, u2;
+    bool more = cursor_next(p.plan, cur, u);
+    Pages g = pages_of(u);
+    int e = entry(g, u.t * pages + lane), block = block_of(g, u.t * pages + lane, e);
+    float2 sc = scales(g, block);
+    while (more) {
+        const bool more2 = cursor_next(p.plan, cur, u2);
+        const Pages g2 = pages_of(u2);
+        const int e2 = more2 ? entry(g2, u2.t * pages + lane) : -1;
+        int block2 = -1;
+        float2 sc2 = make_float2(0.f, 0.f);
+        int window = u.t * pages + lane;
+        const bool wide = u.n * pages > 32;
+        int next = wide ? block_of(g, window + 32, entry(g, window + 32)) : -1;
+        float2 next_sc = scales(g, next);
+        int ahead = wide ? entry(g, window + 64) : -1;
         int at = 0;  // the tile's first page in the window
         for (int t = u.t; t < u.t + u.n; ++t) {
             if (at == 32) {
@@ -211,16 +239,27 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 window += 32;
                 block = next;
                 sc = next_sc;
-                next = block_of(window + 32, ahead);
-                next_sc = scales(next);
-                ahead = entry(window + 64);
+                next = block_of(g, window + 32, ahead);
+                next_sc = scales(g, next);
+                ahead = entry(g, window + 64);
             }
             bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
             if (!__all_sync(0xffffffffu, ok)) goto drain;
             const int i = lane - at;
             const bool mine = i >= 0 && i < pages;
+            if (mine) {
+                // A page that is not there is read past the last block, where TMA fills zeros.
+                const int row = block < 0 ? c.num_blocks * c.Hkv : block * c.Hkv + g.hk;
+                const uint32_t dst = base + (uint32_t)stage * L::kStageBytes + (uint32_t)(i << c.block_shift) * 128u;
+                ptx::tma_load_3d(dst, tm_k, cache_bar<R>(base, L::kKFull + stage), 0, 0, row);
+                ptx::tma_load_3d(dst + L::kTileBytes, tm_v, cache_bar<R>(base, L::kVFull + stage), 0, 0, row);
+            }
+            if (t == u.t) {
+                block2 = more2 ? block_of(g2, u2.t * pages + lane, e2) : -1;
+                sc2 = scales(g2, block2);
+            }
             // pages that some row should see but that the table places outside the cache
-            const uint32_t missing = __ballot_sync(0xffffffffu, mine && block < 0 && window < last_page) >> at;
+            const uint32_t missing = __ballot_sync(0xffffffffu, mine && block < 0 && window < g.last) >> at;
             float* info = reinterpret_cast<float*>(smem + L::kInfo + stage * L::kInfoBytes);
             if (mine) {
                 info[i] = sc.x;
@@ -228,17 +267,10 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
             }
             if (lane == 0) reinterpret_cast<int*>(info)[16] = (int)missing;
             __syncwarp();
+            // The copies' bytes may come in before they are announced: the phase ends with this arrival at the earliest.
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kKFull + stage), L::kTileBytes);
                 ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kVFull + stage), L::kTileBytes);
-            }
-            __syncwarp();
-            if (mine) {
-                // A page that is not there is read past the last block, where TMA fills zeros.
-                const int row = block < 0 ? c.num_blocks * c.Hkv : block * c.Hkv + hk;
-                const uint32_t dst = base + (uint32_t)stage * L::kStageBytes + (uint32_t)(i << c.block_shift) * 128u;
-                ptx::tma_load_3d(dst, tm_k, cache_bar<R>(base, L::kKFull + stage), 0, 0, row);
-                ptx::tma_load_3d(dst + L::kTileBytes, tm_v, cache_bar<R>(base, L::kVFull + stage), 0, 0, row);
             }
             pend |= 1u << stage;
             pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
@@ -248,6 +280,11 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 phase ^= 1u;
             }
         }
+        more = more2;
+        u = u2;
+        g = g2;
+        block = block2;
+        sc = sc2;
     }
     if (bad) atomicOr(p.c.status, kStatusBadCache);
     return;
@@ -264,10 +301,10 @@ template <int R>
 __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
                                volatile int* abort_flag) {
     using L = CacheLayout<R>;
-    constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, L::kN, false);
-    constexpr uint32_t kIdescO = ptx::idesc_e4m3_a_mn(128, L::kN);
+    constexpr uint32_t kIdescS = ptx::idesc_e4m3(128, L::kN, false, false);
+    constexpr uint32_t kIdescO = ptx::idesc_e4m3(128, L::kN, true, L::kPerKey);
     const uint64_t lim = p.wait_limit_ns;
-    const int k_steps = p.c.D / 32;
+    const bool wide = p.c.D == 128;
     auto wait = [&](int bar, uint32_t par) {
         return ptx::mbar_wait_spin(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim);
     };
@@ -281,10 +318,13 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
         if (prev_first && !wait(L::kOFree + ub, ((prev_unit >> 1) & 1) ^ 1)) return false;
         if (!wait(L::kPFull + pb, ((g - 1) >> 1) & 1)) return false;
         ptx::tc_fence_after();
-        ptx::mma_ss_f8_a_mn_k128(tmem + L::kO + (uint32_t)ub * L::kN,
-                                 ptx::sdesc_sw128(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes, 16, 1024),
-                                 ptx::sdesc_sw128(base + L::kP + (uint32_t)pb * L::kN * 128, 16, 1024), kIdescO,
-                                 prev_first ? 0u : 1u);
+        const uint32_t o = tmem + L::kO + (uint32_t)ub * L::kN, pp = base + L::kP + (uint32_t)pb * L::kN * 128;
+        // V: 32 keys = 32 rows of 128 bytes further per step.  Pp: 32 bytes, or 32 rows.
+        const uint64_t v = ptx::sdesc_rows<128>(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes);
+        if constexpr (L::kPerKey)
+            ptx::mma_ss_f8_x4<256, 2 * L::kN>(o, v, ptx::sdesc_rows<L::kN>(pp), kIdescO, prev_first ? 0u : 1u);
+        else
+            ptx::mma_ss_f8_x4<256, 2>(o, v, ptx::sdesc_rows<128>(pp), kIdescO, prev_first ? 0u : 1u);
         ptx::mma_commit(cache_bar<R>(base, L::kEmpty + prev_stage));
         ptx::mma_commit(cache_bar<R>(base, L::kPvDone + pb));
         if (prev_last) ptx::mma_commit(cache_bar<R>(base, L::kOFull + ub));
@@ -304,10 +344,15 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
             if (!wait(L::kKFull + stage, phase) || !wait(L::kSFree + sb, ((g >> 1) & 1) ^ 1)) goto done;
             ptx::tc_fence_after();
             {
-                const uint64_t a = ptx::sdesc_sw128(base + (uint32_t)stage * L::kStageBytes, 16, 1024);
-                const uint64_t b = ptx::sdesc_sw128(base + L::kQ + (uint32_t)ub * L::kN * 128, 16, 1024);
-                for (int s = 0; s < k_steps; ++s)
-                    ptx::mma_ss_f8(tmem + L::kS + (uint32_t)sb * L::kN, a + 2 * s, b + 2 * s, kIdescS, s > 0 ? 1u : 0u);
+                const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes);
+                const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
+                const uint32_t st = tmem + L::kS + (uint32_t)sb * L::kN;
+                if (wide) {
+                    ptx::mma_ss_f8_x4<2, 2>(st, a, b, kIdescS, 0u);
+                } else {  // D = 64: the other half of the rows is zero in K
+                    ptx::mma_ss_f8(st, a, b, kIdescS, 0u);
+                    ptx::mma_ss_f8(st, a + 2, b + 2, kIdescS, 1u);
+                }
             }
             ptx::mma_commit(cache_bar<R>(base, L::kSFull + sb));
             if (k == n - 1) ptx::mma_commit(cache_bar<R>(base, L::kQEmpty + ub));
@@ -334,40 +379,44 @@ template <int R>
 __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint32_t base, uint8_t* smem,
                                  volatile int* abort_flag) {
     using L = CacheLayout<R>;
+    constexpr int kBatch = L::kH < 8 ? L::kH : 8;  // rows of a warp under way at once
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
-    const int D = p.c.D;
+    const bool wide = p.c.D == 128;
+    // Warp w takes rows w, w + 2, ...; a lane takes 4 elements of a row (2 for D = 64).
+    uint2 x[kBatch];
+    long long at[kBatch];
+    int seen[kBatch];
+    auto load = [&](const CacheUnit& u, int r0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            int i, hq;
+            const bool used = cache_row(p, u, r0 + 2 * k, &i, &hq);
+            at[k] = used ? ((long long)u.b * p.Hq + hq) * p.Sq + i : -1;
+            seen[k] = !used ? 0 : p.plan.causal ? max(u.s.first + i + 1, 0) : u.s.len;
+            x[k] = make_uint2(0, 0);
+            if (used) {
+                const __nv_bfloat16* src = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2];
+                if (wide)
+                    x[k] = *reinterpret_cast<const uint2*>(src + lane * 4);
+                else
+                    x[k].x = *reinterpret_cast<const uint32_t*>(src + lane * 2);
+            }
+        }
+    };
     CacheUnit u;
     for (int unit = 0;; ++unit) {
         const int ub = unit & 1;
         const bool more = cursor_next(p.plan, cur, u);
+        if (more) load(u, w);
         const bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
                                        p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, ok)) return;
         CacheWork* work = reinterpret_cast<CacheWork*>(smem + L::kUnit) + ub;
         if (more) {
             CacheRow* rows = reinterpret_cast<CacheRow*>(smem + L::kRows) + ub * R;
-            constexpr int kBatch = 4;
 #pragma unroll 1
             for (int r0 = w; r0 < R; r0 += 2 * kBatch) {
-                uint2 x[kBatch];  // 4 elements a lane (2 for D = 64)
-                bool used[kBatch];
-                long long at[kBatch];
-                int seen[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    int i, hq;
-                    used[k] = cache_row(p, u, r0 + 2 * k, &i, &hq);
-                    at[k] = used[k] ? ((long long)u.b * p.Hq + hq) * p.Sq + i : -1;
-                    seen[k] = !used[k] ? 0 : p.plan.causal ? max(u.s.first + i + 1, 0) : u.s.len;
-                    x[k] = make_uint2(0, 0);
-                    if (used[k]) {
-                        const __nv_bfloat16* src = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2];
-                        if (D == 128)
-                            x[k] = *reinterpret_cast<const uint2*>(src + lane * 4);
-                        else
-                            x[k].x = *reinterpret_cast<const uint32_t*>(src + lane * 2);
-                    }
-                }
+                if (r0 != w) load(u, r0);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
                     const int r = r0 + 2 * k;
@@ -375,9 +424,10 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
                     const uint32_t m0 = __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
                     const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0 & 0xffffu, m0 >> 16));
                     const float scale = e4m3_pow2_scale(__uint_as_float(top << 16));
-                    const float inv = top >= 0x7f80u ? NAN : 1.f / scale;
-                    float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xffff0000u),
-                                  __uint_as_float(x[k].y << 16), __uint_as_float(x[k].y & 0xffff0000u)};
+                    // 1 / scale, by its exponent: scale is a power of two of at most 2^120
+                    const float inv = top >= 0x7f80u ? NAN : __uint_as_float((254u << 23) - __float_as_uint(scale));
+                    const float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xffff0000u),
+                                        __uint_as_float(x[k].y << 16), __uint_as_float(x[k].y & 0xffff0000u)};
                     uint32_t hi[2], lo[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -386,18 +436,17 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
                         const float2 h = e4m3_unpair(hi[e]);
                         lo[e] = e4m3_pair(a - h.x, b - h.y);
                     }
-                    // hi and lo rows of the warpgroup that owns row r: n = wg * R + (r mod H) and + H
-                    const int n = (r / L::kH) * R + r % L::kH;
+                    const int n = (r / L::kH) * R + L::column(r % L::kH);
                     auto put = [&](int row, const uint32_t* v) {
                         const uint32_t line = base + L::kQ + (uint32_t)ub * L::kN * 128 + (uint32_t)row * 128u;
-                        if (D == 128)
+                        if (wide)
                             ptx::st_shared_u32(line + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4, v[0] | v[1] << 16);
                         else
                             ptx::st_shared_u16(line + (((lane >> 3) ^ (row & 7)) << 4) + (lane & 7) * 2, v[0]);
                     };
                     put(n, hi);
-                    put(n + L::kH, lo);
-                    if (lane == 0) rows[r] = CacheRow{used[k] ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
+                    put(n + L::kC, lo);
+                    if (lane == 0) rows[r] = CacheRow{at[k] >= 0 ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
                 }
             }
             if (w == 0 && lane == 0) {
@@ -420,23 +469,42 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
 }
 
 // ---------------------------------------------------------------- warps 4-11: softmax
+// Adds each of a warp's H rows over its lanes; lane i returns the sum of row
+// i / (32 / H).  Half of the rows change hands in the first step, a quarter in the next.
+template <int H>
+__device__ __forceinline__ float cache_sum_rows(float* l) {
+    const int lane = threadIdx.x & 31;
+    int o = 16;
+#pragma unroll
+    for (int n = H; n > 1; n /= 2, o /= 2) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float give = upper ? l[i] : l[i + n / 2], keep = upper ? l[i + n / 2] : l[i];
+            l[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    float x = l[0];
+    for (; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
 template <int R>
 __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
                                    volatile int* abort_flag) {
     using L = CacheLayout<R>;
-    constexpr int H = L::kH;
+    constexpr int H = L::kH, C = L::kC;
+    constexpr float kTop = 448.f;        // E4M3's largest value
+    constexpr float kRoom = 6.f;         // log2 of a row's largest weight when its maximum is new
+    constexpr float kLeastScale = -80.f; // log2 of the least scale of V that a weight is computed for
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wg = (warp - 4) >> 2, wq = warp & 3;
     const int j = wq * 32 + lane;  // this thread's key of a tile (lane of S^T) and its d (lane of O^T)
     const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * R);
     const uint64_t lim = p.wait_limit_ns;
-    float4* tab = reinterpret_cast<float4*>(smem + L::kTab) + wg * H;
-    float2* mv = reinterpret_cast<float2*>(smem + L::kMv) + wg * H;
-    float2* fac = reinterpret_cast<float2*>(smem + L::kFac) + wg * H;
-    float2* red = reinterpret_cast<float2*>(smem + L::kRed) + wg * 4 * H;
-    int* nan_at = reinterpret_cast<int*>(smem + L::kNanAt);
-    volatile int* unset = reinterpret_cast<volatile int*>(smem + L::kUnset) + wg;
-    volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kNanSeen);
+    float4* tab = reinterpret_cast<float4*>(smem + L::kTab) + wg * (H / 2);
+    float* fac = reinterpret_cast<float*>(smem + L::kFac) + wg * H;
+    float* red = reinterpret_cast<float*>(smem + L::kRed) + wg * 4 * H;  // [H][4 warps]
     const int bar = 1 + wg;  // the warpgroup's barrier
     // A wait that ran out leaves this false: the warp goes on without waiting and without writing
     // results, so that it meets its warpgroup at every barrier and nobody is left there.
@@ -450,27 +518,35 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         if (lane == 0) ptx::mbar_arrive(cache_bar<R>(base, which));
     };
     const int page = j >> p.c.block_shift;  // of a tile
-    int g = 0, stage = 0;                   // number and stage of the current tile
+    int g = 0, stage = 0;   // number and stage of the current tile
+    uint32_t nan_phase = 0; // bit ub: phase of barrier kNan + ub
     uint32_t phase = 0;
-    uint32_t s[R];  // S^T: hi columns, then lo columns; then e, then w
-    float l[H];     // this thread's keys' part of the rows' sums
+    float l[H];  // this thread's keys' part of the rows' sums of w / vs
     for (int unit = 0;; ++unit) {
         const int ub = unit & 1;
+        int* nan_at = reinterpret_cast<int*>(smem + L::kNanAt) + ub * 128;
+        volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kNanSeen) + ub;
         wait(L::kQFull + ub, (unit >> 1) & 1);
         const CacheWork work = reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub];
-        if (ptx::bar_any(3, 256, !alive) || work.n == 0) break;  // all eight warps go on together or not at all
         const CacheRow* rows = reinterpret_cast<const CacheRow*>(smem + L::kRows) + ub * R + wg * H;
-        const bool idle = work.rows <= wg * H;
-        if (j < H) {
-            mv[j] = make_float2(-INFINITY, -INFINITY);
-            tab[j] = make_float4(rows[j].factor, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int r = 0; r < H; ++r) l[r] = 0.f;
-        bool todo = true;  // some row has no maximum yet
         // Some tile of the share holds keys that not every row sees.  Like all that decides about
         // barriers, it follows from `work` alone, which every warp has read the same.
         const bool borders = (work.t + work.n) * kCacheTile > work.keys_all;
+        if (borders && wg == 0) {
+            nan_at[j] = 0x7fffffff;
+            if (j == 0) *nan_seen = 0;
+        }
+        float row_max = -INFINITY;  // of row `lane`, the same in the four warps
+        if (j < H) {
+            float* t = reinterpret_cast<float*>(tab + j / 2) + (j & 1);
+            t[0] = rows[j].factor;
+            t[2] = -INFINITY;
+        }
+        if (ptx::bar_any(bar, 128, !alive) || work.n == 0) break;  // the four warps go on together or not at all
+        const bool idle = work.rows <= wg * H;
+#pragma unroll
+        for (int r = 0; r < H; ++r) l[r] = 0.f;
+        bool todo = true;  // some row that sees keys has no maximum yet
 
         for (int k = 0; k < work.n; ++k, ++g) {
             const int t = work.t + k, sb = g & 1;
@@ -478,12 +554,11 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
             wait(L::kSFull + sb, (g >> 1) & 1);
             ptx::tc_fence_after();
             const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
-            const float ks = info[page];
+            const float ks = info[page], lvs = fmaxf(ptx::lg2(info[8 + page]), kLeastScale), ivs = ptx::ex2(-lvs);
             const int missing = reinterpret_cast<const int*>(info)[16];
             const int key = t * kCacheTile + j;
             const bool full = (t + 1) * kCacheTile <= work.keys_all && missing == 0;
             const bool here = key < work.keys && !((missing >> page) & 1);
-            const float vs = here ? info[8 + page] : 0.f;
             if ((t + 1) * kCacheTile > work.keys_all && wg == 0) {
                 // A weight of 0 times NaN is NaN: keys that nobody sees become 0 in V, and NaN that only
                 // some rows see is taken out and noted by the first position that has it.
@@ -493,17 +568,23 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 #pragma unroll
                     for (int x = 0; x < 8; ++x) ptx::st_shared_v4(line + 16 * x, 0, 0, 0, 0);
                 } else if (alive && key >= work.keys_all) {
+#pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
                         const uint4 v = ptx::ld_shared_v4(line + 16 * x);
                         uint32_t word[4] = {v.x, v.y, v.z, v.w};
                         bool found = false;
-                        for (int y = 0; y < 4; ++y)
-                            for (int b = 0; b < 4; ++b)
-                                if ((word[y] >> (8 * b) & 0x7fu) == 0x7fu) {
-                                    found = true;
-                                    word[y] &= ~(0xffu << (8 * b));
-                                    atomicMin(nan_at + (x ^ (j & 7)) * 16 + y * 4 + b, key);
-                                }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            // 0x7f in a byte's low bits: adding 1 to them carries into its top bit
+                            uint32_t hit = ((word[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            if (hit) found = true;
+                            while (hit) {
+                                const int b = (__ffs(hit) - 1) >> 3;
+                                hit &= hit - 1;
+                                word[y] &= ~(0xffu << (8 * b));
+                                atomicMin(nan_at + (x ^ (j & 7)) * 16 + y * 4 + b, key);
+                            }
+                        }
                         if (found) {
                             *nan_seen = 1;
                             ptx::st_shared_v4(line + 16 * x, word[0], word[1], word[2], word[3]);
@@ -513,114 +594,144 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
             }
             if (!idle) {
                 const uint32_t s_addr = my_tmem + L::kS + (uint32_t)sb * L::kN;
+                const uint32_t p_line = base + L::kP + (uint32_t)sb * L::kN * 128u;
+                const uint64_t ks2 = ptx::f2(ks, ks), ivs2 = ptx::f2(ivs, ivs);
                 auto sees = [&](int r) { return here && key < rows[r].keys; };
-                // e and w of this thread's key for every row; returns the largest of them.
-                auto weights = [&]() {
+                // The weights of this thread's key for every row, into Pp; returns the largest.  `add`: the
+                // rows whose sum takes them.
+                auto pass = [&](auto masked, uint32_t add) {
                     float top = 0.f;
 #pragma unroll
-                    for (int r = 0; r < H; ++r) {
-                        const float4 f = tab[r];
-                        const float x = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks;
-                        float y = fmaf(x, f.x, f.y);
-                        if (!full) y = sees(r) ? y : -INFINITY;
-                        const float e = ptx::ex2(y), w = e * vs * f.z;
-                        s[r] = __float_as_uint(e);
-                        s[H + r] = __float_as_uint(w);
-                        top = ptx::max3(top, e, w);
+                    for (int c = 0; c < H; c += C) {
+                        uint32_t s[2 * C];
+                        ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
+                        uint32_t hi[C / 2], lo[C / 2];
+#pragma unroll
+                        for (int i = 0; i < C; i += 2) {
+                            const int r = c + i;
+                            const float4 f = tab[r / 2];
+                            const uint64_t x = ptx::mul2(ptx::add2(ptx::f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                                                   ptx::f2(__uint_as_float(s[C + i]), __uint_as_float(s[C + i + 1]))),
+                                                         ks2);
+                            const uint64_t y = ptx::fma2(x, ptx::f2(f.x, f.y), ptx::f2(f.z + lvs, f.w + lvs));
+                            float y0, y1;
+                            ptx::f2_split(y, y0, y1);
+                            if (decltype(masked)::value) {
+                                y0 = sees(r) ? y0 : -INFINITY;
+                                y1 = sees(r + 1) ? y1 : -INFINITY;
+                            }
+                            const float w0 = ptx::ex2(y0), w1 = ptx::ex2(y1);
+                            top = ptx::max3(top, w0, w1);
+                            const uint64_t w = ptx::f2(w0, w1);
+                            float l0 = l[r], l1 = l[r + 1];
+                            ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l0, l1)), l0, l1);
+                            if (!decltype(masked)::value || add == ~0u || (add >> r & 1)) l[r] = l0;
+                            if (!decltype(masked)::value || add == ~0u || (add >> (r + 1) & 1)) l[r + 1] = l1;
+                            // hi: w at 4 significant bits, to nearest (w (2^20 + 1) less its own excess over w)
+                            const uint64_t big = ptx::mul2(w, ptx::f2(1048577.f, 1048577.f));
+                            const uint64_t minus = ptx::f2(-1.f, -1.f);
+                            const uint64_t h = ptx::fma2(ptx::fma2(w, minus, big), minus, big);
+                            float h0, h1, r0, r1;
+                            ptx::f2_split(h, h0, h1);
+                            ptx::f2_split(ptx::fma2(h, minus, w), r0, r1);
+                            hi[i / 2] = e4m3_pair(h0, h1);
+                            lo[i / 2] = e4m3_pair(r0, r1);
+                        }
+                        if constexpr (L::kPerKey) {
+                            // 2C bytes of this key's row: C hi codes, then C lo codes
+                            constexpr uint32_t kTurn = L::kN == 128 ? 0 : L::kN == 64 ? 1 : 2;  // key bits that swizzle
+                            const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
+                            auto piece = [&](uint32_t i) { return p_line + (uint32_t)j * L::kN + ((i ^ turn) << 4); };
+                            const uint32_t i0 = (uint32_t)(wg * R + 2 * c) / 16;
+                            auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
+                            if constexpr (C == 16) {
+                                ptx::st_shared_v4(piece(i0), four(hi), four(hi + 2), four(hi + 4), four(hi + 6));
+                                ptx::st_shared_v4(piece(i0 + 1), four(lo), four(lo + 2), four(lo + 4), four(lo + 6));
+                            } else {
+                                ptx::st_shared_v4(piece(i0), four(hi), four(hi + 2), four(lo), four(lo + 2));
+                            }
+                        } else {
+                            auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's eight
+                                ptx::st_shared_u8(p_line + (uint32_t)(wg * R + n) * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4) +
+                                                      (uint32_t)(j & 15),
+                                                  code);
+                            };
+#pragma unroll
+                            for (int i = 0; i < C; i += 2) {
+                                put(i, hi[i / 2]);
+                                put(i + 1, hi[i / 2] >> 8);
+                                put(C + i, lo[i / 2]);
+                                put(C + i + 1, lo[i / 2] >> 8);
+                            }
+                        }
                     }
                     return top;
                 };
+                wait(L::kPvDone + sb, ((g >> 1) & 1) ^ 1);  // the tile before last has left Pp's buffer
                 float top = 0.f;
-                if (!todo) {
-                    ptx::tmem_load<R>(s_addr, s);
-                    top = weights();
-                }
-                if (ptx::bar_any(bar, 128, todo || top > 448.f)) {
-                    // The rows' maxima move: over the tile's scores, and over scores + log2 of V's scale.
-                    ptx::tmem_load<R>(s_addr, s);
-                    const float lvs = ptx::lg2(vs);
-                    auto warp_max = [](float x) {  // through the order of the bit patterns
-                        const int b = __float_as_int(x), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
-                        return __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-                    };
+                if (!todo) top = full ? pass(std::false_type(), ~0u) : pass(std::true_type(), ~0u);
+                if (ptx::bar_any(bar, 128, todo || top > kTop)) {
+                    // The rows' maxima move: of s + log2 vs over the tile, through the order of the bit patterns.
 #pragma unroll
-                    for (int r = 0; r < H; ++r) {
-                        float y = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks * rows[r].factor;
-                        if (!full) y = sees(r) ? y : -INFINITY;
-                        const float a = warp_max(y), b = warp_max(y + lvs);
-                        if (lane == (r & 31)) red[wq * H + r] = make_float2(a, b);
-                    }
-                    ptx::bar_sync(bar, 128);
-                    if (wq == 0) {
-                        bool open = false;
-                        if (lane < H) {
-                            const CacheRow row = rows[lane];
-                            const float2 had = mv[lane];
-                            const float lc_had = tab[lane].w;
-                            float m = had.x, v = had.y;
-                            if (row.at >= 0) {
+                    for (int c = 0; c < H; c += C) {
+                        uint32_t s[2 * C];
+                        ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    m = fmaxf(m, red[x * H + lane].x);
-                                    v = fmaxf(v, red[x * H + lane].y);
-                                }
-                            }
-                            const bool none = m == -INFINITY, had_none = had.x == -INFINITY;
-                            const float lc = none ? 0.f : fminf(m - v + 6.f, 100.f);
-                            fac[lane] = had_none ? make_float2(0.f, 0.f)
-                                                 : make_float2(ptx::ex2(had.x - m), ptx::ex2(had.x - m + lc - lc_had));
-                            mv[lane] = make_float2(m, v);
-                            tab[lane] = make_float4(row.factor, none ? 0.f : -m, none ? 0.f : ptx::ex2(lc), lc);
-                            open = none && row.at >= 0 && row.keys > 0;
+                        for (int i = 0; i < C; ++i) {
+                            float y = fmaf((__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * ks, rows[c + i].factor, lvs);
+                            if (!full) y = sees(c + i) ? y : -INFINITY;
+                            const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+                            if (lane == c + i) red[(c + i) * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
                         }
-                        open = __any_sync(0xffffffffu, open);
-                        if (lane == 0) *unset = open;
                     }
                     ptx::bar_sync(bar, 128);
-                    todo = *unset;
+                    // Every warp works out the same new maxima, a row per lane.
+                    float f = 1.f;
+                    bool open = false;
+                    float m = -INFINITY;
+                    if (lane < H) {
+                        const float had = row_max;
+                        const float4 x = reinterpret_cast<const float4*>(red)[lane];
+                        m = had;
+                        if (rows[lane].at >= 0) m = fmaxf(fmaxf(fmaxf(m, x.x), fmaxf(x.y, x.z)), x.w);
+                        f = had == -INFINITY ? 0.f : ptx::ex2(had - m);
+                        open = m == -INFINITY && rows[lane].at >= 0 && rows[lane].keys > 0;
+                    }
+                    // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
+                    const uint32_t anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
+                    const bool was_todo = todo;
+                    todo = __any_sync(0xffffffffu, open);
+                    row_max = m;
+                    if (wq == 0 && lane < H) {
+                        fac[lane] = f;
+                        reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kRoom - m;
+                    }
+                    ptx::bar_sync(bar, 128);
+#pragma unroll
+                    for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
                     if (k > 0) {
                         wait(L::kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                         ptx::tc_fence_after();
                         const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
-                        ptx::tmem_load<R>(o_addr, s);
 #pragma unroll
-                        for (int r = 0; r < H; ++r) {
-                            const float2 f = fac[r];
-                            l[r] *= f.x;
-                            s[r] = __float_as_uint(__uint_as_float(s[r]) * f.y);
-                            s[H + r] = __float_as_uint(__uint_as_float(s[H + r]) * f.y);
+                        for (int c = 0; c < H; c += C) {
+                            uint32_t s[2 * C];
+                            ptx::tmem_load<2 * C>(o_addr + 2 * c, s);
+#pragma unroll
+                            for (int i = 0; i < C; ++i) {
+                                const float x = fac[c + i];
+                                s[i] = __float_as_uint(__uint_as_float(s[i]) * x);
+                                s[C + i] = __float_as_uint(__uint_as_float(s[C + i]) * x);
+                            }
+                            ptx::tmem_store<2 * C>(o_addr + 2 * c, s);
                         }
-                        ptx::tmem_store<R>(o_addr, s);
-                        ptx::tmem_load<R>(s_addr, s);
                     }
-                    weights();
+                    pass(std::true_type(), was_todo ? ~0u : anew);
                 }
                 ptx::tc_fence_before();
-                arrive(L::kSFree + sb);
-                wait(L::kPvDone + sb, ((g >> 1) & 1) ^ 1);  // the tile before last has left P's buffer
-                const uint32_t p_addr = base + L::kP + (uint32_t)sb * L::kN * 128u + (uint32_t)wg * R * 128u + (j & 15);
-                auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's part, a multiple of 8 rows apart
-                    ptx::st_shared_u8(p_addr + (uint32_t)n * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4), code);
-                };
-#pragma unroll
-                for (int r = 0; r < H; r += 2) {
-                    l[r] += __uint_as_float(s[r]);
-                    l[r + 1] += __uint_as_float(s[r + 1]);
-                    // hi: the weight at 4 significant bits, to nearest; lo: the rest
-                    const float w0 = __uint_as_float(s[H + r]), w1 = __uint_as_float(s[H + r + 1]);
-                    const float h0 = __uint_as_float((s[H + r] + 0x80000u) & 0xfff00000u);
-                    const float h1 = __uint_as_float((s[H + r + 1] + 0x80000u) & 0xfff00000u);
-                    const uint32_t hi = e4m3_pair(h0, h1), lo = e4m3_pair(w0 - h0, w1 - h1);
-                    put(r, hi);
-                    put(r + 1, hi >> 8);
-                    put(H + r, lo);
-                    put(H + r + 1, lo >> 8);
-                }
-            } else {
-                arrive(L::kSFree + sb);
             }
+            arrive(L::kSFree + sb);
             ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
             arrive(L::kPFull + sb);
             if (++stage == L::kStages) {
                 stage = 0;
@@ -629,65 +740,62 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         }
 
         // ---- the unit's rows leave
-        float2* sums = red;
-        if (!idle) {
-#pragma unroll
-            for (int r = 0; r < H; ++r) {
-                float x = l[r];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane == (r & 31)) sums[wq * H + r].x = x;
-            }
-        }
         bool nan = false;
         if (borders) {
-            ptx::bar_sync(3, 256);
-            nan = *nan_seen != 0;
-        } else {
-            ptx::bar_sync(bar, 128);
+            // Warpgroup 0 has noted the NaN that it took out; warpgroup 1 waits for that.
+            if (wg == 0)
+                arrive(L::kNan + ub);
+            else
+                wait(L::kNan + ub, nan_phase >> ub & 1u);
+            nan_phase ^= 1u << ub;
         }
+        if (!idle) {
+            const float sum = cache_sum_rows<H>(l);
+            if (lane % (32 / H) == 0) red[lane / (32 / H) * 4 + wq] = sum;
+        }
+        ptx::bar_sync(bar, 128);
+        if (borders) nan = *nan_seen != 0;
         const long long slot = (long long)blockIdx.x * 2 + work.slot;
         if (!idle && j < H) {
-            const float sum = sums[j].x + sums[H + j].x + sums[2 * H + j].x + sums[3 * H + j].x;
-            const float m = mv[j].x, c = tab[j].z;
-            float f = c == 0.f ? 0.f : 1.f / c;
-            if (sum != sum) f = sum;  // NaN, whatever O holds
+            const float4 x = reinterpret_cast<const float4*>(red)[j];
+            const float sum = x.x + x.y + (x.z + x.w), m = row_max - kRoom;
+            float f = 1.f;
             if (work.slot < 0) {
-                f = sum == 0.f ? 0.f : f / sum;
+                f = sum == 0.f ? 0.f : ptx::rcp(sum);
                 if (alive && p.lse != nullptr && rows[j].at >= 0)
                     p.lse[rows[j].at] = sum == 0.f ? -INFINITY : (m + ptx::lg2(sum)) * kLn2;
             } else if (alive) {
                 p.part_ml[slot * R + wg * H + j] = make_float2(m, sum);
             }
-            fac[j].x = f;
+            fac[j] = f;
         }
         ptx::bar_sync(bar, 128);
         wait(L::kOFull + ub, (unit >> 1) & 1);
         ptx::tc_fence_after();
         if (!idle) {
-            ptx::tmem_load<R>(my_tmem + L::kO + (uint32_t)ub * L::kN, s);
             const int first_nan = nan ? nan_at[j] : 0x7fffffff;
-            if (alive && j < p.c.D) {
 #pragma unroll
-                for (int r = 0; r < H; ++r) {
-                    float o = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * fac[r].x;
-                    if (first_nan < rows[r].keys) o = NAN;
-                    if (work.slot >= 0)
-                        p.part_o[(slot * R + wg * H + r) * 128 + j] = o;
-                    else if (rows[r].at >= 0)
-                        p.out[rows[r].at * p.c.D + j] = __float2bfloat16(o);
+            for (int c = 0; c < H; c += C) {
+                uint32_t s[2 * C];
+                ptx::tmem_load<2 * C>(my_tmem + L::kO + (uint32_t)ub * L::kN + 2 * c, s);
+                if (alive && j < p.c.D) {
+#pragma unroll
+                    for (int i = 0; i < C; ++i) {
+                        const int r = c + i;
+                        const CacheRow row = rows[r];
+                        float o = (__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * fac[r];
+                        if (first_nan < row.keys) o = NAN;
+                        if (work.slot >= 0)
+                            p.part_o[(slot * R + wg * H + r) * 128 + j] = o;
+                        else if (row.at >= 0)
+                            p.out[row.at * p.c.D + j] = __float2bfloat16(o);
+                    }
                 }
             }
         }
         ptx::tc_fence_before();
         arrive(L::kOFree + ub);
         arrive(L::kQEmpty + ub);
-        if (nan) {  // put back for the next unit
-            ptx::bar_sync(3, 256);
-            if (wg == 0) nan_at[j] = 0x7fffffff;
-            if (wg == 0 && j == 0) *nan_seen = 0;
-            ptx::bar_sync(3, 256);
-        }
     }
 }
 
@@ -705,12 +813,6 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     ptx::launch_dependents();
-    long long begin, end, total;
-    CachePlace place;
-    cache_locate<L::kThreads>(p.plan, reinterpret_cast<long long*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
-                              &begin, &end, &total, &place, false);
-    if (begin == end) return;  // the whole block
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             ptx::mbar_init(cache_bar<R>(base, L::kKFull + s), 1);
@@ -726,25 +828,29 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
             ptx::mbar_init(cache_bar<R>(base, L::kPvDone + i), 1);
             ptx::mbar_init(cache_bar<R>(base, L::kOFull + i), 1);
             ptx::mbar_init(cache_bar<R>(base, L::kOFree + i), 8);
+            ptx::mbar_init(cache_bar<R>(base, L::kNan + i), 4);      // softmax warpgroup 0
         }
         ptx::mbar_init(cache_bar<R>(base, L::kDrain), 1);
         *abort_flag = 0;
-        *reinterpret_cast<volatile int*>(smem + L::kNanSeen) = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
     }
-    if (warp >= 4 && warp < 8) reinterpret_cast<int*>(smem + L::kNanAt)[threadIdx.x - 128] = 0x7fffffff;
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_addr(tmem_slot), L::kTmemCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    long long begin, end, total;
+    CachePlace place;
+    cache_locate<L::kThreads>(p.plan, reinterpret_cast<long long*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
+                              &begin, &end, &total, &place, false);  // barriers of the block within
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
+    if (begin == end) {
+        // no tile for this CTA
+    } else if (warp == 0) {
         cache_load_role<R>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
     } else if (warp == 1) {
         if (lane == 0) cache_mma_role<R>(p, base, smem, tmem, abort_flag);

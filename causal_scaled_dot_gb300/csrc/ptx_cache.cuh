@@ -60,26 +60,38 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// D (+)= A B^T over 128 keys in four K = 32 steps: A an MN-major SW128 tile
-// whose K rows advance 32 rows = 4096 bytes per step, B K-major, 32 bytes.
-__device__ __forceinline__ void mma_ss_f8_a_mn_k128(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                    uint32_t accumulate) {
+// Four steps over 128 keys, the operands' descriptors advancing by kA and kB
+// (in 16-byte units) each.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ss_f8_x4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-        "add.s64 a, %1, 256; add.s64 b, %2, 2;\n\t"
+        "add.s64 a, %1, %5; add.s64 b, %2, %6;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
-        "add.s64 a, %1, 512; add.s64 b, %2, 4;\n\t"
+        "add.s64 a, a, %5; add.s64 b, b, %6;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
-        "add.s64 a, %1, 768; add.s64 b, %2, 6;\n\t"
+        "add.s64 a, a, %5; add.s64 b, b, %6;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB)
         : "memory");
 }
-// Instruction descriptor for kind::f8f6f4, E4M3 A (MN-major: bit 15) and B (K-major), fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3_a_mn(int M, int N) {
-    return idesc_e4m3_f32(M, N, false) | (1u << 15);
+// Instruction descriptor for kind::f8f6f4, E4M3 A and B, fp32 D; bit 15: A is
+// MN-major, bit 16: B is.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+    return idesc_e4m3_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
+}
+// Shared-memory descriptor of an operand with rows of 128, 64 or 32 bytes in the
+// swizzle of that width (16-byte piece i of row k sits at i ^ (k mod 8), i ^
+// (k / 2 mod 4) or i ^ (k / 4 mod 2)), groups of eight rows next to each other;
+// fields as in sdesc_sw128, layout 2, 4 or 6.
+template <int kRowBytes>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
+    static_assert(kRowBytes == 128 || kRowBytes == 64 || kRowBytes == 32, "swizzled rows");
+    constexpr uint64_t layout = kRowBytes == 128 ? 2 : kRowBytes == 64 ? 4 : 6;
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(8 * kRowBytes >> 4) << 32) | (1ull << 46) |
+           (layout << 61);
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -113,6 +125,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Programmatic dependent launch: lets the next kernel of the stream, when it was

@@ -267,6 +267,10 @@ using namespace attn;
 // Every unit's tiles are taken exactly once and in order, for each count of CTAs, with the plan summed
 // by `threads` threads in chunks as the kernel does it.
 int main() {
+    for (long long total : {1ll, 303ll, 304ll, 70000ll, 0x7ffffffell, 0x7fffffffll, 0x123456789abll})
+        for (int ctas : {1, 152, 304})
+            for (int c = 0; c <= ctas; ++c)
+                CHECK(plan_begin(total, c, ctas) == (long long)((__int128)total * c / ctas));
     std::srand(7);
     for (int round = 0; round < 400; ++round) {
         CachePlan p{};
@@ -304,14 +308,12 @@ int main() {
                 }
             }
         }
-        const long long pairs = (long long)p.B * p.q_tiles;
-        const int threads = 1 + std::rand() % 20;
-        const long long per = (pairs + threads - 1) / threads;
+        const int pairs = p.B * p.q_tiles, threads = 1 + std::rand() % 20, per = (pairs + threads - 1) / threads;
         std::vector<long long> sum(threads);
         long long all = 0;
         bool bad = false;
         for (int t = 0; t < threads; ++t) {
-            const long long a = t * per < pairs ? t * per : pairs, z = a + per < pairs ? a + per : pairs;
+            const int a = t * per < pairs ? t * per : pairs, z = a + per < pairs ? a + per : pairs;
             all += sum[t] = plan_chunk(p, a, z, &bad);
         }
         CHECK(all == total);
