@@ -121,7 +121,8 @@ int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, i
     const long long tiles = (p.plan.capacity + kCacheTile - 1) / kCacheTile;  // of one unit, at most
     const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads;
     const long long most = (long long)sms * L::kCtas;
-    const int grid = (int)(units >= most || units * tiles >= most ? most : units * tiles);
+    if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
+    const int grid = (int)(units * tiles < most ? units * tiles : most);
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)most * 2 * R * 128);
     attn_cache_fwd_kernel<R><<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);

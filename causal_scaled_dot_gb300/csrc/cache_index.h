@@ -73,7 +73,8 @@ ATTN_HD unsigned long long cache_offset(int block, int head, int slot, int Hkv, 
 // All units' tiles stand in one row, by sequence, query tile, head, key tile,
 // and CTA c of G takes tiles [c T / G, (c + 1) T / G) of it, so CTAs get equal
 // work whatever the lengths; units that cross a border are joined afterwards.
-// Lengths are device data, so this runs on the device.
+// Lengths are device data, so this runs on the device.  The host makes sure
+// that T fits in 31 bits.
 constexpr int kCacheTile = 128;  // keys per tile
 
 struct CachePlan {
@@ -101,9 +102,9 @@ ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
 }
 
 // Tiles of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
-ATTN_HD long long plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
+ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
     if (first >= last) return 0;
-    long long sum = 0;
+    int sum = 0;
     int b = p.q_tiles == 1 ? first : first / p.q_tiles, qt = first - b * p.q_tiles;
     CacheSpan s = plan_span(p, b, bad);
     for (int i = first; i < last; ++i) {
@@ -111,7 +112,7 @@ ATTN_HD long long plan_chunk(const CachePlan& p, int first, int last, bool* bad)
             qt = 0;
             s = plan_span(p, ++b, bad);
         }
-        if (qt < plan_q_tiles(p, s)) sum += (long long)plan_tiles(p, s, qt) * p.heads;
+        if (qt < plan_q_tiles(p, s)) sum += plan_tiles(p, s, qt) * p.heads;
         ++qt;
     }
     return sum;
@@ -122,7 +123,7 @@ struct CachePlace {
 };
 // The place of the tile `offset` tiles after the start of pair `first`
 // (offset < the tiles of the pairs from there on).
-ATTN_HD CachePlace plan_find(const CachePlan& p, int first, long long offset) {
+ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
     bool bad = false;
     const int b = p.q_tiles == 1 ? first : first / p.q_tiles;
     CachePlace x{b, first - b * p.q_tiles, 0, 0};
@@ -135,13 +136,12 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, long long offset) {
         }
         if (x.qt < plan_q_tiles(p, s)) {
             const int tiles = plan_tiles(p, s, x.qt);
-            const long long all = (long long)tiles * p.heads;
-            if (offset < all) {
-                x.h = offset < 0x7fffffff ? (int)offset / tiles : (int)(offset / tiles);
-                x.t = (int)(offset - (long long)x.h * tiles);
+            if (offset < tiles * p.heads) {
+                x.h = offset / tiles;
+                x.t = offset - x.h * tiles;
                 return x;
             }
-            offset -= all;
+            offset -= tiles * p.heads;
         }
         ++x.qt;
     }
@@ -149,18 +149,16 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, long long offset) {
 
 // The CTAs that share `total` tiles: all, or one per tile, so that none
 // between the first and the last piece of a unit is without a tile.
-ATTN_HD int plan_ctas(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
-// First tile of CTA `cta` of plan_ctas() many (the total for those past them).
-ATTN_HD long long plan_begin(long long total, int cta, int ctas) {
+ATTN_HD int plan_ctas(int total, int ctas) { return total < ctas ? total : ctas; }
+// First tile of CTA `cta` of plan_ctas() many (the total for those past them):
+// total * cta / ctas, for fewer than 2^15 CTAs.
+ATTN_HD int plan_begin(int total, int cta, int ctas) {
     if (cta >= ctas) return total;
-    if (total < 0x7fffffff) {  // total * cta / ctas without a 64-bit division; ctas < 2^15
-        const int t = (int)total, q = t / ctas, r = t - q * ctas;
-        return (long long)q * cta + (r * cta) / ctas;
-    }
-    return total / ctas * cta + total % ctas * cta / ctas;
+    const int q = total / ctas, r = total - q * ctas;
+    return q * cta + (r * cta) / ctas;
 }
 // The last CTA with a piece of a unit that begins in `cta` and ends before tile `unit_end`.
-ATTN_HD int plan_last(long long total, int cta, int ctas, long long unit_end) {
+ATTN_HD int plan_last(int total, int cta, int ctas, int unit_end) {
     while (plan_begin(total, cta + 1, ctas) < unit_end) ++cta;
     return cta;
 }
@@ -173,11 +171,11 @@ struct CacheUnit {
 // Walks the units of a run of `left` tiles from a place on.
 struct CacheCursor {
     CachePlace at;
-    long long left;
+    int left;
     CacheSpan s;
     int tiles;
 };
-ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, long long left) {
+ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, int left) {
     bool bad = false;
     CacheCursor c{at, at.b < p.B ? left : 0, {}, 0};
     if (c.left > 0) {
@@ -193,7 +191,7 @@ ATTN_HD bool cursor_next(const CachePlan& p, CacheCursor& c, CacheUnit& u) {
     u.h = c.at.h;
     u.t = c.at.t;
     u.tiles = c.tiles;
-    u.n = c.tiles - c.at.t < c.left ? c.tiles - c.at.t : (int)c.left;
+    u.n = c.tiles - c.at.t < c.left ? c.tiles - c.at.t : c.left;
     u.s = c.s;
     u.keys = plan_keys(p, c.s, c.at.qt);
     c.left -= u.n;

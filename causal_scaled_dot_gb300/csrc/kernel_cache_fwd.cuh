@@ -85,8 +85,8 @@ struct CacheLayout {
     static constexpr uint32_t kFac = kTab + R * 8;                   // [R] float: what l and O are multiplied by
     static constexpr uint32_t kRed = kFac + R * 4;                   // [R][4 warps] float
     static constexpr uint32_t kNanAt = kRed + R * 16;                // 2 x [128] first key with NaN in V's column
-    static constexpr uint32_t kScan = kNanAt + 1024;                 // 12 long long + 4 int
-    static constexpr uint32_t kBars = kScan + 128;
+    static constexpr uint32_t kScan = kNanAt + 1024;                 // 12 int + 4 int
+    static constexpr uint32_t kBars = kScan + 64;
     static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kQEmpty = kQFull + 2,
                          kSFull = kQEmpty + 2, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2,
                          kOFull = kPvDone + 2, kOFree = kOFull + 2, kNan = kOFree + 2, kDrain = kNan + 2,
@@ -134,46 +134,41 @@ __device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
 }
 
 // Sums the plan over the block and finds this CTA's run of tiles; every thread
-// of the block calls it, `scan` is shared memory (12 long long, then an int4).
+// of the block calls it, `scan` is shared memory (12 int, then an int4).
 // Returns the CTAs that share the tiles.
 template <int kThreads>
-__device__ int cache_locate(const CachePlan& p, long long* scan, int cta, int ctas, unsigned int* status,
-                            long long* begin, long long* end, long long* total, CachePlace* place, bool at_end) {
+__device__ int cache_locate(const CachePlan& p, int* scan, int cta, int ctas, unsigned int* status, int* begin, int* end,
+                            int* total, CachePlace* place, bool at_end) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pairs = p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
     const int first = min(tid * per, pairs), last = min(first + per, pairs);
     bool bad = false;
-    const long long mine = plan_chunk(p, first, last, &bad);
+    const int mine = plan_chunk(p, first, last, &bad);
     if (bad && cta == 0) atomicOr(status, kStatusBadCache);
-    long long sum = mine;
+    int sum = mine;
     const int steps = pairs < 32 ? pairs : 32;  // lanes of a warp that have something
     for (int o = 1; o < steps; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
     }
     if (lane == steps - 1) scan[warp] = sum;
     __syncthreads();
-    long long before = sum - mine, all = 0;
+    int before = sum - mine, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        all += scan[w];
+        const int x = scan[w];
+        if (w < warp) before += x;
+        all += x;
     }
     *total = all;
     ctas = plan_ctas(all, ctas);
     *begin = plan_begin(all, cta, ctas);
     *end = plan_begin(all, cta + 1, ctas);
-    const long long want = at_end ? *end : *begin;
-    int* out = reinterpret_cast<int*>(scan + 12);
-    if (want >= before && want < before + mine) {
-        const CachePlace x = plan_find(p, first, want - before);
-        out[0] = x.b;
-        out[1] = x.qt;
-        out[2] = x.h;
-        out[3] = x.t;
-    }
+    const int want = at_end ? *end : *begin;
+    if (want >= before && want < before + mine)
+        *reinterpret_cast<CachePlace*>(scan + 12) = plan_find(p, first, want - before);
     __syncthreads();
-    *place = want < all ? CachePlace{out[0], out[1], out[2], out[3]} : CachePlace{p.B, 0, 0, 0};
+    *place = want < all ? *reinterpret_cast<const CachePlace*>(scan + 12) : CachePlace{p.B, 0, 0, 0};
     return ctas;
 }
 
@@ -243,7 +238,7 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 next_sc = scales(g, next);
                 ahead = entry(g, window + 64);
             }
-            bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
+            bool ok = ptx::mbar_wait_call(cache_bar<R>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
             if (!__all_sync(0xffffffffu, ok)) goto drain;
             const int i = lane - at;
             const bool mine = i >= 0 && i < pages;
@@ -306,7 +301,7 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
     const uint64_t lim = p.wait_limit_ns;
     const bool wide = p.c.D == 128;
     auto wait = [&](int bar, uint32_t par) {
-        return ptx::mbar_wait_spin(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim);
+        return ptx::mbar_wait_call(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim);
     };
     int stage = 0, g = 0;       // stage and number of the tile whose S^T is next
     uint32_t phase = 0;
@@ -379,74 +374,74 @@ template <int R>
 __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint32_t base, uint8_t* smem,
                                  volatile int* abort_flag) {
     using L = CacheLayout<R>;
-    constexpr int kBatch = L::kH < 8 ? L::kH : 8;  // rows of a warp under way at once
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
-    const bool wide = p.c.D == 128;
-    // Warp w takes rows w, w + 2, ...; a lane takes 4 elements of a row (2 for D = 64).
-    uint2 x[kBatch];
+    // A lane takes 8 elements of a row: D / 8 lanes a row, 2 or 4 rows a step; warp w takes every other step.
+    const int lanes = p.c.D / 8, part = lane & (lanes - 1), per = 32 / lanes;
+    const int row0 = w * per + lane / lanes;
+    constexpr int kBatch = R >= 32 ? 4 : R / 4 < 2 ? 1 : 2;  // steps under way at once
+    uint4 x[kBatch];
     long long at[kBatch];
     int seen[kBatch];
     auto load = [&](const CacheUnit& u, int r0) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             int i, hq;
-            const bool used = cache_row(p, u, r0 + 2 * k, &i, &hq);
+            const int r = r0 + k * 2 * per;
+            const bool used = r < R && cache_row(p, u, r, &i, &hq);
             at[k] = used ? ((long long)u.b * p.Hq + hq) * p.Sq + i : -1;
             seen[k] = !used ? 0 : p.plan.causal ? max(u.s.first + i + 1, 0) : u.s.len;
-            x[k] = make_uint2(0, 0);
-            if (used) {
-                const __nv_bfloat16* src = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2];
-                if (wide)
-                    x[k] = *reinterpret_cast<const uint2*>(src + lane * 4);
-                else
-                    x[k].x = *reinterpret_cast<const uint32_t*>(src + lane * 2);
-            }
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (used)
+                x[k] = *reinterpret_cast<const uint4*>(p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + i * p.q_stride[2] +
+                                                       part * 8);
         }
     };
     CacheUnit u;
     for (int unit = 0;; ++unit) {
         const int ub = unit & 1;
         const bool more = cursor_next(p.plan, cur, u);
-        if (more) load(u, w);
-        const bool ok = ptx::mbar_wait(cache_bar<R>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
+        if (more) load(u, row0);
+        const bool ok = ptx::mbar_wait_call(cache_bar<R>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
                                        p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, ok)) return;
         CacheWork* work = reinterpret_cast<CacheWork*>(smem + L::kUnit) + ub;
         if (more) {
             CacheRow* rows = reinterpret_cast<CacheRow*>(smem + L::kRows) + ub * R;
 #pragma unroll 1
-            for (int r0 = w; r0 < R; r0 += 2 * kBatch) {
-                if (r0 != w) load(u, r0);
+            for (int r0 = row0; r0 - row0 < R; r0 += kBatch * 2 * per) {
+                if (r0 != row0) load(u, r0);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    const int r = r0 + 2 * k;
+                    const int r = r0 + k * 2 * per;
+                    const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                     // the largest magnitude, by bit pattern; not finite: the whole row is NaN
-                    const uint32_t m0 = __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0 & 0xffffu, m0 >> 16));
-                    const float scale = e4m3_pow2_scale(__uint_as_float(top << 16));
+                    uint32_t m = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
+                                          __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+                    m = max(m & 0xffffu, m >> 16);
+                    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float scale = e4m3_pow2_scale(__uint_as_float(m << 16));
                     // 1 / scale, by its exponent: scale is a power of two of at most 2^120
-                    const float inv = top >= 0x7f80u ? NAN : __uint_as_float((254u << 23) - __float_as_uint(scale));
-                    const float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xffff0000u),
-                                        __uint_as_float(x[k].y << 16), __uint_as_float(x[k].y & 0xffff0000u)};
-                    uint32_t hi[2], lo[2];
+                    const float inv = m >= 0x7f80u ? NAN : __uint_as_float((254u << 23) - __float_as_uint(scale));
+                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float a = f[2 * e] * inv, b = f[2 * e + 1] * inv;
-                        hi[e] = e4m3_pair(a, b);
-                        const float2 h = e4m3_unpair(hi[e]);
-                        lo[e] = e4m3_pair(a - h.x, b - h.y);
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = __uint_as_float(v[e] << 16) * inv, b = __uint_as_float(v[e] & 0xffff0000u) * inv;
+                        const uint32_t h = e4m3_pair(a, b);
+                        const float2 hf = e4m3_unpair(h);
+                        hi[e >> 1] |= h << (16 * (e & 1));
+                        lo[e >> 1] |= e4m3_pair(a - hf.x, b - hf.y) << (16 * (e & 1));
                     }
-                    const int n = (r / L::kH) * R + L::column(r % L::kH);
-                    auto put = [&](int row, const uint32_t* v) {
-                        const uint32_t line = base + L::kQ + (uint32_t)ub * L::kN * 128 + (uint32_t)row * 128u;
-                        if (wide)
-                            ptx::st_shared_u32(line + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4, v[0] | v[1] << 16);
-                        else
-                            ptx::st_shared_u16(line + (((lane >> 3) ^ (row & 7)) << 4) + (lane & 7) * 2, v[0]);
-                    };
-                    put(n, hi);
-                    put(n + L::kC, lo);
-                    if (lane == 0) rows[r] = CacheRow{at[k] >= 0 ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
+                    if (r < R) {
+                        const int n = (r / L::kH) * R + L::column(r % L::kH);
+                        uint8_t* q8 = smem + L::kQ + ub * L::kN * 128;
+                        auto put = [&](int row, const uint32_t* c) {
+                            *reinterpret_cast<uint2*>(q8 + row * 128 + (((part >> 1) ^ (row & 7)) << 4) + (part & 1) * 8) =
+                                make_uint2(c[0], c[1]);
+                        };
+                        put(n, hi);
+                        put(n + L::kC, lo);
+                        if (part == 0) rows[r] = CacheRow{at[k] >= 0 ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
+                    }
                 }
             }
             if (w == 0 && lane == 0) {
@@ -510,7 +505,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
     // results, so that it meets its warpgroup at every barrier and nobody is left there.
     bool alive = true;
     auto wait = [&](int which, uint32_t par) {
-        if (alive) alive = ptx::mbar_wait(cache_bar<R>(base, which), par, abort_flag, p.c.status, lim);
+        if (alive) alive = ptx::mbar_wait_call(cache_bar<R>(base, which), par, abort_flag, p.c.status, lim);
         alive = __all_sync(0xffffffffu, alive);
     };
     auto arrive = [&](int which) {
@@ -668,65 +663,69 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                     return top;
                 };
                 wait(L::kPvDone + sb, ((g >> 1) & 1) ^ 1);  // the tile before last has left Pp's buffer
-                float top = 0.f;
-                if (!todo) top = full ? pass(std::false_type(), ~0u) : pass(std::true_type(), ~0u);
-                if (ptx::bar_any(bar, 128, todo || top > kTop)) {
-                    // The rows' maxima move: of s + log2 vs over the tile, through the order of the bit patterns.
-#pragma unroll
-                    for (int c = 0; c < H; c += C) {
-                        uint32_t s[2 * C];
-                        ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
-#pragma unroll
-                        for (int i = 0; i < C; ++i) {
-                            float y = fmaf((__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * ks, rows[c + i].factor, lvs);
-                            if (!full) y = sees(c + i) ? y : -INFINITY;
-                            const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
-                            if (lane == c + i) red[(c + i) * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-                        }
-                    }
-                    ptx::bar_sync(bar, 128);
-                    // Every warp works out the same new maxima, a row per lane.
-                    float f = 1.f;
-                    bool open = false;
-                    float m = -INFINITY;
-                    if (lane < H) {
-                        const float had = row_max;
-                        const float4 x = reinterpret_cast<const float4*>(red)[lane];
-                        m = had;
-                        if (rows[lane].at >= 0) m = fmaxf(fmaxf(fmaxf(m, x.x), fmaxf(x.y, x.z)), x.w);
-                        f = had == -INFINITY ? 0.f : ptx::ex2(had - m);
-                        open = m == -INFINITY && rows[lane].at >= 0 && rows[lane].keys > 0;
-                    }
-                    // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
-                    const uint32_t anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
-                    const bool was_todo = todo;
-                    todo = __any_sync(0xffffffffu, open);
-                    row_max = m;
-                    if (wq == 0 && lane < H) {
-                        fac[lane] = f;
-                        reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kRoom - m;
-                    }
-                    ptx::bar_sync(bar, 128);
-#pragma unroll
-                    for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
-                    if (k > 0) {
-                        wait(L::kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
-                        ptx::tc_fence_after();
-                        const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
-#pragma unroll
+                // First as it stands; once more when a maximum has to move, or only so while a row has none.
+                uint32_t add = ~0u;
+                for (bool move = todo;;) {
+                    if (move) {
+                        // The rows' maxima move: of s + log2 vs over the tile, through the order of the bit patterns.
+#pragma unroll 1
                         for (int c = 0; c < H; c += C) {
                             uint32_t s[2 * C];
-                            ptx::tmem_load<2 * C>(o_addr + 2 * c, s);
+                            ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
 #pragma unroll
                             for (int i = 0; i < C; ++i) {
-                                const float x = fac[c + i];
-                                s[i] = __float_as_uint(__uint_as_float(s[i]) * x);
-                                s[C + i] = __float_as_uint(__uint_as_float(s[C + i]) * x);
+                                float y = fmaf((__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * ks, rows[c + i].factor, lvs);
+                                if (!full) y = sees(c + i) ? y : -INFINITY;
+                                const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+                                if (lane == c + i) red[(c + i) * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
                             }
-                            ptx::tmem_store<2 * C>(o_addr + 2 * c, s);
+                        }
+                        ptx::bar_sync(bar, 128);
+                        // Every warp works out the same new maxima, a row per lane.
+                        float f = 1.f;
+                        bool open = false;
+                        float m = -INFINITY;
+                        if (lane < H) {
+                            const float had = row_max;
+                            const float4 x = reinterpret_cast<const float4*>(red)[lane];
+                            m = had;
+                            if (rows[lane].at >= 0) m = fmaxf(fmaxf(fmaxf(m, x.x), fmaxf(x.y, x.z)), x.w);
+                            f = had == -INFINITY ? 0.f : ptx::ex2(had - m);
+                            open = m == -INFINITY && rows[lane].at >= 0 && rows[lane].keys > 0;
+                        }
+                        // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
+                        const uint32_t anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
+                        if (!todo) add = anew;
+                        todo = __any_sync(0xffffffffu, open);
+                        row_max = m;
+                        if (wq == 0 && lane < H) {
+                            fac[lane] = f;
+                            reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kRoom - m;
+                        }
+                        ptx::bar_sync(bar, 128);
+#pragma unroll
+                        for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
+                        if (k > 0) {
+                            wait(L::kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                            ptx::tc_fence_after();
+                            const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
+#pragma unroll 1
+                            for (int c = 0; c < H; c += C) {
+                                uint32_t s[2 * C];
+                                ptx::tmem_load<2 * C>(o_addr + 2 * c, s);
+#pragma unroll
+                                for (int i = 0; i < C; ++i) {
+                                    const float x = fac[c + i];
+                                    s[i] = __float_as_uint(__uint_as_float(s[i]) * x);
+                                    s[C + i] = __float_as_uint(__uint_as_float(s[C + i]) * x);
+                                }
+                                ptx::tmem_store<2 * C>(o_addr + 2 * c, s);
+                            }
                         }
                     }
-                    pass(std::true_type(), was_todo ? ~0u : anew);
+                    const float top = move || !full ? pass(std::true_type(), add) : pass(std::false_type(), ~0u);
+                    if (move || !ptx::bar_any(bar, 128, top > kTop)) break;
+                    move = true;
                 }
                 ptx::tc_fence_before();
             }
@@ -774,7 +773,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         ptx::tc_fence_after();
         if (!idle) {
             const int first_nan = nan ? nan_at[j] : 0x7fffffff;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < H; c += C) {
                 uint32_t s[2 * C];
                 ptx::tmem_load<2 * C>(my_tmem + L::kO + (uint32_t)ub * L::kN + 2 * c, s);
@@ -841,9 +840,9 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    long long begin, end, total;
+    int begin, end, total;
     CachePlace place;
-    cache_locate<L::kThreads>(p.plan, reinterpret_cast<long long*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
+    cache_locate<L::kThreads>(p.plan, reinterpret_cast<int*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
                               &begin, &end, &total, &place, false);  // barriers of the block within
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -873,8 +872,8 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
 // blockIdx.y * 8 .. + 7, a warp each: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
 template <int R>
 __global__ void __launch_bounds__(256) attn_cache_join_kernel(const CacheFwdParams p, int ctas) {
-    __shared__ long long scan[12 + 4];
-    long long begin, end, total;
+    __shared__ __align__(16) int scan[12 + 4];
+    int begin, end, total;
     CachePlace at;
     ctas = cache_locate<256>(p.plan, scan, blockIdx.x, ctas, p.c.status, &begin, &end, &total, &at, true);
     CacheUnit u;

@@ -94,6 +94,32 @@ __device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
            (layout << 61);
 }
 
+// mbar_wait (ptx.cuh) as a first probe in place and a call for the rest: the
+// cache kernels wait in many places, and their roles share an instruction cache.
+// The clock is read only after many probes: a read of the global timer takes
+// longer than most waits.
+__device__ __noinline__ bool mbar_wait_rest(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            unsigned int* status, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicOr(status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               unsigned int* status, uint64_t limit_ns) {
+    return mbar_test_wait(bar, parity) || mbar_wait_rest(bar, parity, abort_flag, status, limit_ns);
+}
+
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

@@ -267,10 +267,10 @@ using namespace attn;
 // Every unit's tiles are taken exactly once and in order, for each count of CTAs, with the plan summed
 // by `threads` threads in chunks as the kernel does it.
 int main() {
-    for (long long total : {1ll, 303ll, 304ll, 70000ll, 0x7ffffffell, 0x7fffffffll, 0x123456789abll})
-        for (int ctas : {1, 152, 304})
+    for (int total : {1, 303, 304, 70000, 0x7ffffffe, 0x7fffffff})
+        for (int ctas : {1, 152, 304, 32767})
             for (int c = 0; c <= ctas; ++c)
-                CHECK(plan_begin(total, c, ctas) == (long long)((__int128)total * c / ctas));
+                CHECK(plan_begin(total, c, ctas) == (int)((long long)total * c / ctas));
     std::srand(7);
     for (int round = 0; round < 400; ++round) {
         CachePlan p{};
@@ -293,7 +293,7 @@ int main() {
         // the units, written down one by one
         struct U { int b, qt, h, tiles, keys; };
         std::vector<U> want;
-        long long total = 0;
+        int total = 0;
         for (int b = 0; b < p.B; ++b) {
             const int len = lens[b] < 0 ? 0 : lens[b] > p.capacity ? p.capacity : lens[b];
             const int count = p.q_lens ? counts[b] : p.Sq;
@@ -309,8 +309,8 @@ int main() {
             }
         }
         const int pairs = p.B * p.q_tiles, threads = 1 + std::rand() % 20, per = (pairs + threads - 1) / threads;
-        std::vector<long long> sum(threads);
-        long long all = 0;
+        std::vector<int> sum(threads);
+        int all = 0;
         bool bad = false;
         for (int t = 0; t < threads; ++t) {
             const int a = t * per < pairs ? t * per : pairs, z = a + per < pairs ? a + per : pairs;
@@ -321,10 +321,10 @@ int main() {
         size_t unit = 0;
         int tile = 0, pieces = 0, expect_last = -1;
         for (int c = 0; c < given; ++c) {
-            const long long begin = plan_begin(total, c, ctas), end = plan_begin(total, c + 1, ctas);
+            const int begin = plan_begin(total, c, ctas), end = plan_begin(total, c + 1, ctas);
             CHECK((begin == end) == (c >= ctas));  // no CTA without a tile among those that share them
             if (begin == end) continue;
-            long long before = 0;
+            int before = 0;
             int t = 0;
             while (begin >= before + sum[t]) before += sum[t++];
             CacheCursor cur = cursor_at(p, plan_find(p, t * per, begin - before), end - begin);
