@@ -23,10 +23,12 @@
 // otherwise a tile needs one vote of the warpgroup and no reduction.  The sum of
 // w / vs is kept per thread (per key) and reduced at the end.
 //
-// Roles (384 threads): warp 0 copies pages (lane i takes page i of a tile) with
+// Roles: warp 0 copies pages (lane i takes page i of a tile) with
 // the tables and scales of the pages ahead already in registers; warp 1
 // issues the products; warps 2-3 split the next unit's q rows into pieces;
-// warps 4-7 and 8-11 are two softmax warpgroups, each with half of the R rows.
+// the rest are two (R = 8, 16) or four softmax warpgroups, each with its part of
+// the R rows: four interleave better, since a vote makes the warps of one wait
+// for its slowest.
 // CTAs take equal runs of key tiles of all units (cache_index.h); a unit that
 // crosses into the next CTA leaves partial (O, M, l), which a second kernel
 // joins, already resident when the first one ends.
@@ -68,9 +70,10 @@ struct CacheFwdParams {
 
 template <int R>
 struct CacheLayout {
-    static constexpr int kThreads = 384;
+    static constexpr int kWgs = R >= 32 ? 4 : 2;   // softmax warpgroups
+    static constexpr int kThreads = 128 + 128 * kWgs;
     static constexpr int kN = 2 * R;               // columns of S^T and O^T: hi and lo pieces
-    static constexpr int kH = R / 2;               // rows of one softmax warpgroup
+    static constexpr int kH = R / kWgs;            // rows of one softmax warpgroup
     static constexpr int kCtas = R == 8 ? 2 : 1;   // per SM
     static constexpr int kStages = R == 8 ? 3 : R == 16 ? 6 : R == 32 ? 5 : 4;
     static constexpr uint32_t kTileBytes = 128 * 128;       // 128 keys x 128 bytes
@@ -85,11 +88,10 @@ struct CacheLayout {
     static constexpr uint32_t kFac = kTab + R * 8;                   // [R] float: what l and O are multiplied by
     static constexpr uint32_t kRed = kFac + R * 4;                   // [R][4 warps] float
     static constexpr uint32_t kNanAt = kRed + R * 16;                // 2 x [128] first key with NaN in V's column
-    static constexpr uint32_t kScan = kNanAt + 1024;                 // 12 int + 4 int
-    static constexpr uint32_t kBars = kScan + 64;
+    static constexpr uint32_t kScan = kNanAt + 1024;                 // 20 int + 4 int
+    static constexpr uint32_t kBars = kScan + 96;
     static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kQEmpty = kQFull + 2,
-                         kSFull = kQEmpty + 2, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2,
-                         kOFull = kPvDone + 2, kOFree = kOFull + 2, kNan = kOFree + 2, kDrain = kNan + 2,
+                         kSFull = kQEmpty + 2, kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2, kNan = kOFree + 2, kDrain = kNan + 2,
                          kNumBars = kDrain + 1;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
@@ -102,7 +104,7 @@ struct CacheLayout {
     static_assert(kCtas * kTmemCols <= 512, "tensor memory budget");
     static constexpr uint32_t kS = 0, kO = 2 * kN;
     // Rows go through the softmax C at a time; row r of a warpgroup has its hi piece in
-    // column column(r) of the warpgroup's R columns, and its lo piece C further.
+    // column column(r) of the warpgroup's 2H columns, and its lo piece C further.
     static constexpr int kC = kH < 16 ? kH : 16;
     __host__ __device__ static constexpr int column(int r) { return r / kC * 2 * kC + r % kC; }
     // Pp^T: R = 8 keeps a row per column (K-major, 128 keys = 128 bytes); else a row per key (MN-major,
@@ -134,7 +136,7 @@ __device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
 }
 
 // Sums the plan over the block and finds this CTA's run of tiles; every thread
-// of the block calls it, `scan` is shared memory (12 int, then an int4).
+// of the block calls it, `scan` is shared memory (20 int, then an int4).
 // Returns the CTAs that share the tiles.
 template <int kThreads>
 __device__ int cache_locate(const CachePlan& p, int* scan, int cta, int ctas, unsigned int* status, int* begin, int* end,
@@ -166,9 +168,9 @@ __device__ int cache_locate(const CachePlan& p, int* scan, int cta, int ctas, un
     *end = plan_begin(all, cta + 1, ctas);
     const int want = at_end ? *end : *begin;
     if (want >= before && want < before + mine)
-        *reinterpret_cast<CachePlace*>(scan + 12) = plan_find(p, first, want - before);
+        *reinterpret_cast<CachePlace*>(scan + 20) = plan_find(p, first, want - before);
     __syncthreads();
-    *place = want < all ? *reinterpret_cast<const CachePlace*>(scan + 12) : CachePlace{p.B, 0, 0, 0};
+    *place = want < all ? *reinterpret_cast<const CachePlace*>(scan + 20) : CachePlace{p.B, 0, 0, 0};
     return ctas;
 }
 
@@ -300,8 +302,12 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
     constexpr uint32_t kIdescO = ptx::idesc_e4m3(128, L::kN, true, L::kPerKey);
     const uint64_t lim = p.wait_limit_ns;
     const bool wide = p.c.D == 128;
+    // The whole warp waits and counts, so that what it hands to the tensor core is uniform; one lane issues.
+    const bool leader = (threadIdx.x & 31) == 0;
+    bool ok = true;
     auto wait = [&](int bar, uint32_t par) {
-        return ptx::mbar_wait_call(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim);
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim));
+        return ok;
     };
     int stage = 0, g = 0;       // stage and number of the tile whose S^T is next
     uint32_t phase = 0;
@@ -316,42 +322,45 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
         const uint32_t o = tmem + L::kO + (uint32_t)ub * L::kN, pp = base + L::kP + (uint32_t)pb * L::kN * 128;
         // V: 32 keys = 32 rows of 128 bytes further per step.  Pp: 32 bytes, or 32 rows.
         const uint64_t v = ptx::sdesc_rows<128>(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes);
-        if constexpr (L::kPerKey)
-            ptx::mma_ss_f8_x4<256, 2 * L::kN>(o, v, ptx::sdesc_rows<L::kN>(pp), kIdescO, prev_first ? 0u : 1u);
-        else
-            ptx::mma_ss_f8_x4<256, 2>(o, v, ptx::sdesc_rows<128>(pp), kIdescO, prev_first ? 0u : 1u);
-        ptx::mma_commit(cache_bar<R>(base, L::kEmpty + prev_stage));
-        ptx::mma_commit(cache_bar<R>(base, L::kPvDone + pb));
-        if (prev_last) ptx::mma_commit(cache_bar<R>(base, L::kOFull + ub));
+        if (leader) {
+            if constexpr (L::kPerKey)
+                ptx::mma_ss_f8_x4<256, 2 * L::kN>(o, v, ptx::sdesc_rows<L::kN>(pp), kIdescO, prev_first ? 0u : 1u);
+            else
+                ptx::mma_ss_f8_x4<256, 2>(o, v, ptx::sdesc_rows<128>(pp), kIdescO, prev_first ? 0u : 1u);
+            ptx::mma_commit(cache_bar<R>(base, L::kEmpty + prev_stage));
+            if (prev_last) ptx::mma_commit(cache_bar<R>(base, L::kOFull + ub));
+        }
         prev_stage = -1;
         return true;
     };
-    for (int unit = 0;; ++unit) {
+    for (int unit = 0; ok; ++unit) {
         const int ub = unit & 1;
-        if (!wait(L::kQFull + ub, (unit >> 1) & 1)) goto done;
+        if (!wait(L::kQFull + ub, (unit >> 1) & 1)) break;
         const int n = reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub].n;
         if (n == 0) break;
         for (int k = 0; k < n; ++k, ++g) {
             const int sb = g & 1;
             // While this tile's K is still on its way, the last tile's O^T goes first.
-            if (prev_stage >= 0 && !ptx::mbar_test_wait(cache_bar<R>(base, L::kKFull + stage), phase) && !issue_pv())
-                goto done;
-            if (!wait(L::kKFull + stage, phase) || !wait(L::kSFree + sb, ((g >> 1) & 1) ^ 1)) goto done;
+            if (prev_stage >= 0 && !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<R>(base, L::kKFull + stage), phase)) &&
+                !issue_pv())
+                break;
+            // The buffer of S^T is free: every warp has written the weights of tile g - 2, whose O^T step is issued.
+            if (!wait(L::kKFull + stage, phase)) break;
             ptx::tc_fence_after();
-            {
-                const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes);
-                const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
-                const uint32_t st = tmem + L::kS + (uint32_t)sb * L::kN;
+            const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes);
+            const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
+            const uint32_t st = tmem + L::kS + (uint32_t)sb * L::kN;
+            if (leader) {
                 if (wide) {
                     ptx::mma_ss_f8_x4<2, 2>(st, a, b, kIdescS, 0u);
                 } else {  // D = 64: the other half of the rows is zero in K
                     ptx::mma_ss_f8(st, a, b, kIdescS, 0u);
                     ptx::mma_ss_f8(st, a + 2, b + 2, kIdescS, 1u);
                 }
+                ptx::mma_commit(cache_bar<R>(base, L::kSFull + sb));
+                if (k == n - 1) ptx::mma_commit(cache_bar<R>(base, L::kQEmpty + ub));
             }
-            ptx::mma_commit(cache_bar<R>(base, L::kSFull + sb));
-            if (k == n - 1) ptx::mma_commit(cache_bar<R>(base, L::kQEmpty + ub));
-            if (prev_stage >= 0 && !issue_pv()) goto done;
+            if (prev_stage >= 0 && !issue_pv()) break;
             prev_stage = stage;
             prev_phase = (int)phase;
             prev_unit = unit;
@@ -363,10 +372,11 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
             }
         }
     }
-    if (prev_stage >= 0) issue_pv();
-done:
-    ptx::mma_commit(cache_bar<R>(base, L::kDrain));
-    ptx::drain_wait(cache_bar<R>(base, L::kDrain), 0u, lim);
+    if (ok && prev_stage >= 0) issue_pv();
+    if (leader) {
+        ptx::mma_commit(cache_bar<R>(base, L::kDrain));
+        ptx::drain_wait(cache_bar<R>(base, L::kDrain), 0u, lim);
+    }
 }
 
 // ---------------------------------------------------------------- warps 2-3: query rows
@@ -432,7 +442,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
                         lo[e >> 1] |= e4m3_pair(a - hf.x, b - hf.y) << (16 * (e & 1));
                     }
                     if (r < R) {
-                        const int n = (r / L::kH) * R + L::column(r % L::kH);
+                        const int n = (r / L::kH) * 2 * L::kH + L::column(r % L::kH);
                         uint8_t* q8 = smem + L::kQ + ub * L::kN * 128;
                         auto put = [&](int row, const uint32_t* c) {
                             *reinterpret_cast<uint2*>(q8 + row * 128 + (((part >> 1) ^ (row & 7)) << 4) + (part & 1) * 8) =
@@ -463,7 +473,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
     }
 }
 
-// ---------------------------------------------------------------- warps 4-11: softmax
+// ---------------------------------------------------------------- warps 4 on: softmax
 // Adds each of a warp's H rows over its lanes; lane i returns the sum of row
 // i / (32 / H).  Half of the rows change hands in the first step, a quarter in the next.
 template <int H>
@@ -495,18 +505,18 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wg = (warp - 4) >> 2, wq = warp & 3;
     const int j = wq * 32 + lane;  // this thread's key of a tile (lane of S^T) and its d (lane of O^T)
-    const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * R);
+    const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * 2 * H);
     const uint64_t lim = p.wait_limit_ns;
     float4* tab = reinterpret_cast<float4*>(smem + L::kTab) + wg * (H / 2);
     float* fac = reinterpret_cast<float*>(smem + L::kFac) + wg * H;
     float* red = reinterpret_cast<float*>(smem + L::kRed) + wg * 4 * H;  // [H][4 warps]
     const int bar = 1 + wg;  // the warpgroup's barrier
-    // A wait that ran out leaves this false: the warp goes on without waiting and without writing
+    // A wait that ran out leaves this false: the lane goes on without waiting and without writing
     // results, so that it meets its warpgroup at every barrier and nobody is left there.
     bool alive = true;
     auto wait = [&](int which, uint32_t par) {
         if (alive) alive = ptx::mbar_wait_call(cache_bar<R>(base, which), par, abort_flag, p.c.status, lim);
-        alive = __all_sync(0xffffffffu, alive);
+        __syncwarp();
     };
     auto arrive = [&](int which) {
         __syncwarp();
@@ -545,7 +555,8 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 
         for (int k = 0; k < work.n; ++k, ++g) {
             const int t = work.t + k, sb = g & 1;
-            wait(L::kKFull + stage, phase);  // the scales beside the tile
+            // S^T is there; so are the scales beside K, which were written before it, and the O^T step of
+            // tile g - 2 is done, which came before it: its buffer of Pp is free.
             wait(L::kSFull + sb, (g >> 1) & 1);
             ptx::tc_fence_after();
             const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
@@ -637,7 +648,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                             constexpr uint32_t kTurn = L::kN == 128 ? 0 : L::kN == 64 ? 1 : 2;  // key bits that swizzle
                             const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
                             auto piece = [&](uint32_t i) { return p_line + (uint32_t)j * L::kN + ((i ^ turn) << 4); };
-                            const uint32_t i0 = (uint32_t)(wg * R + 2 * c) / 16;
+                            const uint32_t i0 = (uint32_t)(wg * 2 * H + 2 * c) / 16;
                             auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
                             if constexpr (C == 16) {
                                 ptx::st_shared_v4(piece(i0), four(hi), four(hi + 2), four(hi + 4), four(hi + 6));
@@ -647,7 +658,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                             }
                         } else {
                             auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's eight
-                                ptx::st_shared_u8(p_line + (uint32_t)(wg * R + n) * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4) +
+                                ptx::st_shared_u8(p_line + (uint32_t)(wg * 2 * H + n) * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4) +
                                                       (uint32_t)(j & 15),
                                                   code);
                             };
@@ -662,7 +673,6 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                     }
                     return top;
                 };
-                wait(L::kPvDone + sb, ((g >> 1) & 1) ^ 1);  // the tile before last has left Pp's buffer
                 // First as it stands; once more when a maximum has to move, or only so while a row has none.
                 uint32_t add = ~0u;
                 for (bool move = todo;;) {
@@ -706,7 +716,8 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 #pragma unroll
                         for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
                         if (k > 0) {
-                            wait(L::kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                            // the O^T step of the tile before is done: its stage is empty
+                            wait(L::kEmpty + (stage == 0 ? L::kStages : stage) - 1, stage == 0 ? phase ^ 1u : phase);
                             ptx::tc_fence_after();
                             const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
 #pragma unroll 1
@@ -729,7 +740,6 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                 }
                 ptx::tc_fence_before();
             }
-            arrive(L::kSFree + sb);
             ptx::fence_proxy_async_smem();
             arrive(L::kPFull + sb);
             if (++stage == L::kStages) {
@@ -741,7 +751,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         // ---- the unit's rows leave
         bool nan = false;
         if (borders) {
-            // Warpgroup 0 has noted the NaN that it took out; warpgroup 1 waits for that.
+            // Warpgroup 0 has noted the NaN that it took out; the others wait for that.
             if (wg == 0)
                 arrive(L::kNan + ub);
             else
@@ -809,7 +819,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     uint8_t* smem = smem_raw + (base - raw);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
 
     ptx::launch_dependents();
     if (threadIdx.x == 0) {
@@ -820,13 +830,11 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(cache_bar<R>(base, L::kQFull + i), 2);    // the query warps
-            ptx::mbar_init(cache_bar<R>(base, L::kQEmpty + i), 9);   // the softmax warps and the last S^T product
+            ptx::mbar_init(cache_bar<R>(base, L::kQEmpty + i), 4 * L::kWgs + 1);  // the softmax warps and the last S^T product
             ptx::mbar_init(cache_bar<R>(base, L::kSFull + i), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kSFree + i), 8);
-            ptx::mbar_init(cache_bar<R>(base, L::kPFull + i), 8);
-            ptx::mbar_init(cache_bar<R>(base, L::kPvDone + i), 1);
+            ptx::mbar_init(cache_bar<R>(base, L::kPFull + i), 4 * L::kWgs);
             ptx::mbar_init(cache_bar<R>(base, L::kOFull + i), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kOFree + i), 8);
+            ptx::mbar_init(cache_bar<R>(base, L::kOFree + i), 4 * L::kWgs);
             ptx::mbar_init(cache_bar<R>(base, L::kNan + i), 4);      // softmax warpgroup 0
         }
         ptx::mbar_init(cache_bar<R>(base, L::kDrain), 1);
@@ -852,7 +860,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     } else if (warp == 0) {
         cache_load_role<R>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
     } else if (warp == 1) {
-        if (lane == 0) cache_mma_role<R>(p, base, smem, tmem, abort_flag);
+        cache_mma_role<R>(p, base, smem, tmem, abort_flag);
     } else if (warp < 4) {
         cache_query_role<R>(p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
     } else {
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
 // blockIdx.y * 8 .. + 7, a warp each: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
 template <int R>
 __global__ void __launch_bounds__(256) attn_cache_join_kernel(const CacheFwdParams p, int ctas) {
-    __shared__ __align__(16) int scan[12 + 4];
+    __shared__ __align__(16) int scan[20 + 4];
     int begin, end, total;
     CachePlace at;
     ctas = cache_locate<256>(p.plan, scan, blockIdx.x, ctas, p.c.status, &begin, &end, &total, &at, true);
