@@ -302,8 +302,9 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
     constexpr uint32_t kIdescO = ptx::idesc_e4m3(128, L::kN, true, L::kPerKey);
     const uint64_t lim = p.wait_limit_ns;
     const bool wide = p.c.D == 128;
-    // The whole warp waits and counts, so that what it hands to the tensor core is uniform; one lane issues.
-    const bool leader = (threadIdx.x & 31) == 0;
+    // The whole warp waits and counts, so that what it hands to the tensor core sits in uniform registers
+    // (a register apiece moved there costs more than the product's issue); one lane issues.
+    const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](int bar, uint32_t par) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim));
@@ -336,7 +337,7 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
     for (int unit = 0; ok; ++unit) {
         const int ub = unit & 1;
         if (!wait(L::kQFull + ub, (unit >> 1) & 1)) break;
-        const int n = reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub].n;
+        const int n = __shfl_sync(0xffffffffu, reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub].n, 0);
         if (n == 0) break;
         for (int k = 0; k < n; ++k, ++g) {
             const int sb = g & 1;
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     uint8_t* smem = smem_raw + (base - raw);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // uniform, also to the compiler
 
     ptx::launch_dependents();
     if (threadIdx.x == 0) {
@@ -853,7 +854,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     cache_locate<L::kThreads>(p.plan, reinterpret_cast<int*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
                               &begin, &end, &total, &place, false);  // barriers of the block within
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (begin == end) {
         // no tile for this CTA

@@ -138,6 +138,16 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool x) {
         : "memory");
     return any != 0;
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(x));
+    return x != 0;
+}
 __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
