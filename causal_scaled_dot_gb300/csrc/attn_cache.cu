@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -93,9 +94,34 @@ int rows_per_unit(long long group, long long Sq) {
 }
 int ctas_per_sm(int R) { return R == 8 ? CacheLayout<8>::kCtas : R == 16 ? CacheLayout<16>::kCtas
                                      : R == 32 ? CacheLayout<32>::kCtas : CacheLayout<64>::kCtas; }
-unsigned long long workspace_bytes_of(int R, int sms) {
-    // two partial units per CTA: R rows of 128 sums, and (M, l)
-    return (unsigned long long)sms * ctas_per_sm(R) * 2 * R * (128 * 4 + 8);
+// Key tiles that a unit may have, by the cache's capacity; up to 4 (512 tokens)
+// units are not split: joining two pieces takes about as long as three more
+// tiles in the same CTA.
+constexpr int kWholeTiles = 4;
+long long tiles_of(const attn_cache_t* c) {
+    return ((long long)c->max_blocks * c->block_size + kCacheTile - 1) / kCacheTile;
+}
+bool splits(const attn_cache_t* c) { return tiles_of(c) > kWholeTiles; }
+
+struct Workspace {  // offsets of its parts, and its size
+    unsigned long long ml, tickets, bytes;
+};
+Workspace workspace_of(const attn_cache_t* c, int R, int sms) {
+    // two partial units per CTA: R rows of 128 sums, and (M, l); a ticket per CTA
+    const unsigned long long ctas = (unsigned long long)sms * ctas_per_sm(R);
+    Workspace w{};
+    if (!splits(c)) return w;
+    w.ml = ctas * 2 * R * 128 * 4;
+    w.tickets = w.ml + ctas * 2 * R * 8;
+    w.bytes = w.tickets + ctas * 8;
+    return w;
+}
+
+// A number that no other launch of this process has, in the upper 48 bits, and
+// never 0: the low bits count pieces.
+unsigned long long next_ticket() {
+    static std::atomic<unsigned long long> count{1};
+    return (count.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4Bull + 1) << 16;
 }
 
 constexpr int kMaxDevices = 64;
@@ -116,29 +142,14 @@ int setup_cache_kernels(int dev) {
 }
 
 template <int R>
-int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, int sms, void* workspace, cudaStream_t st) {
+int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, int sms, long long tiles, cudaStream_t st) {
     using L = CacheLayout<R>;
-    const long long tiles = (p.plan.capacity + kCacheTile - 1) / kCacheTile;  // of one unit, at most
-    const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads;
-    const long long most = (long long)sms * L::kCtas;
+    const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads, most = (long long)sms * L::kCtas;
     if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
-    const int grid = (int)(units * tiles < most ? units * tiles : most);
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)most * 2 * R * 128);
+    const long long work = p.plan.whole ? units : units * tiles;  // of the plan, at most
+    const int grid = (int)(work < most ? work : most);
     attn_cache_fwd_kernel<R><<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
-    if (tiles == 1) return ATTN_OK;  // no unit can cross CTAs
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, R / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<R>, (const CacheFwdParams)p, grid) == cudaSuccess ? ATTN_OK
-                                                                                                             : ATTN_ERR_LAUNCH;
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH; }
@@ -219,14 +230,16 @@ extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int 
     return launched();
 }
 
-extern "C" int attn_cache_workspace(int Hq, int Hkv, int Sq, int D, unsigned long long* bytes) {
-    if (!bytes || Hq < 1 || Hkv < 1 || Sq < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
-    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+extern "C" int attn_cache_workspace(const attn_cache_t* cache, int Hq, int Sq, unsigned long long* bytes) {
+    int rc = check_cache(cache);
+    if (rc != ATTN_OK) return rc;
+    if (!bytes || Hq < 1 || Sq < 1 || Hq % cache->Hkv) return ATTN_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (!splits(cache)) return ATTN_OK;
     int sms = 0, device = -1;
     unsigned int* status = nullptr;
-    const int rc = host::current_device(&sms, &status, &device);
-    if (rc != ATTN_OK) return rc;
-    *bytes = workspace_bytes_of(rows_per_unit(Hq / Hkv, Sq), sms);
+    if ((rc = host::current_device(&sms, &status, &device)) != ATTN_OK) return rc;
+    *bytes = workspace_of(cache, rows_per_unit(Hq / cache->Hkv, Sq), sms).bytes;
     return ATTN_OK;
 }
 
@@ -235,7 +248,7 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
                               unsigned long long workspace_bytes, void* stream) {
     int rc = check_cache(cache);
     if (rc != ATTN_OK) return rc;
-    if (!q || !out || !workspace || Hq < 1 || Sq < 1 || Hq % cache->Hkv) return ATTN_ERR_INVALID_ARG;
+    if (!q || !out || Hq < 1 || Sq < 1 || Hq % cache->Hkv || (!workspace && splits(cache))) return ATTN_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
     if ((long long)cache->B * Hq > (1ll << 30) || (long long)Sq * (Hq / cache->Hkv) > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15u ||
@@ -246,7 +259,7 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     if ((rc = row_strides(q_strides, cache->B, Hq, Sq, cache->D, p.q_stride, &qb)) != ATTN_OK) return rc;
     const size_t rows = (size_t)cache->B * Hq * Sq, ob = rows * cache->D * 2, lb = rows * 4;
     const size_t nl = q_lens ? (size_t)cache->B * 4 : 0, wb = (size_t)workspace_bytes;
-    struct { const void* p; size_t n; } written[3] = {{out, ob}, {lse, lse ? lb : 0}, {workspace, wb}};
+    struct { const void* p; size_t n; } written[3] = {{out, ob}, {lse, lse ? lb : 0}, {workspace, workspace ? wb : 0}};
     for (int i = 0; i < 3; ++i) {
         if (written[i].n == 0) continue;
         if (meets_cache(cache, written[i].p, written[i].n, true) || host::ranges_overlap(written[i].p, written[i].n, q, qb) ||
@@ -261,7 +274,15 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     if ((rc = host::current_device(&sms, &status, &device)) != ATTN_OK) return rc;
     if ((rc = setup_cache_kernels(device)) != ATTN_OK) return rc;
     const int group = Hq / cache->Hkv, R = rows_per_unit(group, Sq);
-    if (workspace_bytes < workspace_bytes_of(R, sms)) return ATTN_ERR_INVALID_ARG;
+    const Workspace ws = workspace_of(cache, R, sms);
+    if (workspace_bytes < ws.bytes) return ATTN_ERR_INVALID_ARG;
+    if (ws.bytes > 0) {
+        char* at = static_cast<char*>(workspace);
+        p.part_o = reinterpret_cast<float*>(at);
+        p.part_ml = reinterpret_cast<float2*>(at + ws.ml);
+        p.tickets = reinterpret_cast<unsigned long long*>(at + ws.tickets);
+        p.ticket = next_ticket();
+    }
     alignas(64) CUtensorMap tk, tv;
     const long long outer = (long long)cache->num_blocks * cache->Hkv;
     if (host::encode_byte_box(&tk, device, cache->k, cache->D, cache->block_size, outer, cache->block_size) != ATTN_OK ||
@@ -289,11 +310,13 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     p.plan.q_tiles = (Sq + p.plan.qper - 1) / p.plan.qper;
     if ((long long)cache->B * p.plan.q_tiles > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     p.plan.heads = cache->Hkv * p.hgroups;
+    p.plan.whole = splits(cache) ? 0 : 1;
+    const long long tiles = tiles_of(cache);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (R) {
-        case 8: return launch_fwd<8>(tk, tv, p, sms, workspace, st);
-        case 16: return launch_fwd<16>(tk, tv, p, sms, workspace, st);
-        case 32: return launch_fwd<32>(tk, tv, p, sms, workspace, st);
-        default: return launch_fwd<64>(tk, tv, p, sms, workspace, st);
+        case 8: return launch_fwd<8>(tk, tv, p, sms, tiles, st);
+        case 16: return launch_fwd<16>(tk, tv, p, sms, tiles, st);
+        case 32: return launch_fwd<32>(tk, tv, p, sms, tiles, st);
+        default: return launch_fwd<64>(tk, tv, p, sms, tiles, st);
     }
 }

@@ -72,7 +72,9 @@ ATTN_HD unsigned long long cache_offset(int block, int head, int slot, int Hkv, 
 // that share a key/value head; it takes the key tiles (128 keys) 0 .. tiles-1.
 // All units' tiles stand in one row, by sequence, query tile, head, key tile,
 // and CTA c of G takes tiles [c T / G, (c + 1) T / G) of it, so CTAs get equal
-// work whatever the lengths; units that cross a border are joined afterwards.
+// work whatever the lengths; the pieces of a unit that crosses a border are
+// joined by the CTA that finishes last.  Where every unit is short (`whole`),
+// CTAs take whole units instead, a unit counting as one tile.
 // Lengths are device data, so this runs on the device.  The host makes sure
 // that T fits in 31 bits.
 constexpr int kCacheTile = 128;  // keys per tile
@@ -83,6 +85,7 @@ struct CachePlan {
     int qper;     // queries per query tile
     int q_tiles;  // query tiles of Sq queries
     int heads;    // head groups per sequence and query tile
+    int whole;    // 1: units are not split
 };
 
 ATTN_HD CacheSpan plan_span(const CachePlan& p, int b, bool* bad) {
@@ -101,6 +104,9 @@ ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
     return n <= kCacheTile ? 1 : (n + kCacheTile - 1) / kCacheTile;
 }
 
+// What a unit of `tiles` key tiles counts in the row of all tiles.
+ATTN_HD int plan_cost(const CachePlan& p, int tiles) { return p.whole ? 1 : tiles; }
+
 // Tiles of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
 ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
     if (first >= last) return 0;
@@ -112,7 +118,7 @@ ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
             qt = 0;
             s = plan_span(p, ++b, bad);
         }
-        if (qt < plan_q_tiles(p, s)) sum += plan_tiles(p, s, qt) * p.heads;
+        if (qt < plan_q_tiles(p, s)) sum += plan_cost(p, plan_tiles(p, s, qt)) * p.heads;
         ++qt;
     }
     return sum;
@@ -135,7 +141,7 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
             s = plan_span(p, x.b, &bad);
         }
         if (x.qt < plan_q_tiles(p, s)) {
-            const int tiles = plan_tiles(p, s, x.qt);
+            const int tiles = plan_cost(p, plan_tiles(p, s, x.qt));
             if (offset < tiles * p.heads) {
                 x.h = offset / tiles;
                 x.t = offset - x.h * tiles;
@@ -157,10 +163,9 @@ ATTN_HD int plan_begin(int total, int cta, int ctas) {
     const int q = total / ctas, r = total - q * ctas;
     return q * cta + (r * cta) / ctas;
 }
-// The last CTA with a piece of a unit that begins in `cta` and ends before tile `unit_end`.
-ATTN_HD int plan_last(int total, int cta, int ctas, int unit_end) {
-    while (plan_begin(total, cta + 1, ctas) < unit_end) ++cta;
-    return cta;
+// The CTA of plan_ctas() many that takes a tile: the largest with plan_begin() <= tile.
+ATTN_HD int plan_cta(int total, int tile, int ctas) {
+    return (int)((((long long)tile + 1) * ctas - 1) / total);
 }
 
 // A CTA's share of one unit: key tiles t .. t + n - 1 of its `tiles`.
@@ -191,10 +196,10 @@ ATTN_HD bool cursor_next(const CachePlan& p, CacheCursor& c, CacheUnit& u) {
     u.h = c.at.h;
     u.t = c.at.t;
     u.tiles = c.tiles;
-    u.n = c.tiles - c.at.t < c.left ? c.tiles - c.at.t : c.left;
+    u.n = p.whole || c.tiles - c.at.t < c.left ? c.tiles - c.at.t : c.left;
     u.s = c.s;
     u.keys = plan_keys(p, c.s, c.at.qt);
-    c.left -= u.n;
+    c.left -= plan_cost(p, u.n);
     c.at.t = 0;
     if (++c.at.h == p.heads) {
         c.at.h = 0;

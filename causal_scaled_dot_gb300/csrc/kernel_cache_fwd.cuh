@@ -30,8 +30,8 @@
 // the R rows: four interleave better, since a vote makes the warps of one wait
 // for its slowest.
 // CTAs take equal runs of key tiles of all units (cache_index.h); a unit that
-// crosses into the next CTA leaves partial (O, M, l), which a second kernel
-// joins, already resident when the first one ends.
+// crosses into the next CTA leaves partial (O, M, l), and whichever CTA is the
+// last to leave its piece joins them, in the order of the pieces.
 //
 // What bounds it: one token over a long cache moves 2 bytes per (key, d) pair
 // and is bound by HBM; with R = 64 the exponentials (16 a cycle and SM) and the
@@ -65,6 +65,10 @@ struct CacheFwdParams {
     float scale_log2;       // scale * log2(e)
     float* part_o;          // [G][2][R][128] partial sums of w code
     float2* part_ml;        // [G][2][R] their M - 6 and sum of w / vs
+    // [G]: pieces left of the unit that begins in a CTA, below a number (the upper 48 bits) that marks this
+    // launch: whatever stood there before counts as none.  0 again after each join.
+    unsigned long long* tickets;
+    unsigned long long ticket;
     unsigned long long wait_limit_ns;
 };
 
@@ -96,7 +100,8 @@ struct CacheLayout {
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kNanSeen = kAbort + 4;  // [2]
-    static constexpr uint32_t kDynamicSmem = kNanSeen + 8 + 1024;
+    static constexpr uint32_t kShared = kNanSeen + 8;  // 2 x CacheShared
+    static constexpr uint32_t kDynamicSmem = kShared + 2 * 64 + 1024;
     static_assert(kInfo % 16 == 0 && kRows % 16 == 0 && kUnit % 16 == 0 && kTab % 16 == 0 && kScan % 8 == 0 && kBars % 8 == 0,
                   "alignment");
     static_assert(kCtas * (kDynamicSmem + 1024) <= 228 * 1024, "shared memory budget");
@@ -128,7 +133,13 @@ struct CacheWork {
     int rows;        // rows in use
     int pad[6];
 };
-static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48, "shared memory layout");
+// A unit that this CTA shares with others, for the join: slot 0 begun elsewhere, 1 begun here.
+struct CacheShared {
+    CacheUnit u;
+    int first, pieces;  // the CTA where it begins, and the CTAs that share it (0: no such unit)
+    int last;           // 1: this CTA was the last to leave its piece
+};
+static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48 && sizeof(CacheShared) <= 64, "shared memory layout");
 
 template <int R>
 __device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
@@ -139,8 +150,9 @@ __device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
 // of the block calls it, `scan` is shared memory (20 int, then an int4).
 // Returns the CTAs that share the tiles.
 template <int kThreads>
-__device__ int cache_locate(const CachePlan& p, int* scan, int cta, int ctas, unsigned int* status, int* begin, int* end,
-                            int* total, CachePlace* place, bool at_end) {
+__device__ int cache_locate(const CachePlan& p, int* scan, unsigned int* status, int* begin, int* end, int* total,
+                            CachePlace* place) {
+    const int cta = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pairs = p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
     const int first = min(tid * per, pairs), last = min(first + per, pairs);
@@ -163,10 +175,10 @@ __device__ int cache_locate(const CachePlan& p, int* scan, int cta, int ctas, un
         all += x;
     }
     *total = all;
-    ctas = plan_ctas(all, ctas);
+    const int ctas = plan_ctas(all, gridDim.x);
     *begin = plan_begin(all, cta, ctas);
     *end = plan_begin(all, cta + 1, ctas);
-    const int want = at_end ? *end : *begin;
+    const int want = *begin;
     if (want >= before && want < before + mine)
         *reinterpret_cast<CachePlace*>(scan + 20) = plan_find(p, first, want - before);
     __syncthreads();
@@ -382,8 +394,8 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
 
 // ---------------------------------------------------------------- warps 2-3: query rows
 template <int R>
-__device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint32_t base, uint8_t* smem,
-                                 volatile int* abort_flag) {
+__device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int pos, int total, int ctas, uint32_t base,
+                                 uint8_t* smem, volatile int* abort_flag) {
     using L = CacheLayout<R>;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
     // A lane takes 8 elements of a row: D / 8 lanes a row, 2 or 4 rows a step; warp w takes every other step.
@@ -463,6 +475,13 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, uint3
                 work->keys_all = p.plan.causal ? max(u.s.first + q0 + 1, 0) : u.s.len;
                 work->slot = u.n == u.tiles ? -1 : u.t > 0 ? 0 : 1;
                 work->rows = min(p.plan.qper, u.s.count - q0) * p.hper;
+                if (u.n < u.tiles) {
+                    CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot;
+                    shared->u = u;
+                    shared->first = plan_cta(total, pos - u.t, ctas);
+                    shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
+                }
+                pos += u.n;
             }
         } else if (w == 0 && lane == 0) {
             work->n = 0;
@@ -809,6 +828,66 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
     }
 }
 
+// Counts a piece of a unit as left; true for the last of them.
+__device__ __noinline__ bool cache_last_piece(unsigned long long* at, unsigned long long ticket, int pieces) {
+    unsigned long long had = ticket + pieces - 1, now;  // a guess that is right for the last
+    for (;;) {  // as many tries as there are pieces and two at most: a failure is another piece's success
+        now = (had ^ ticket) >> 16 ? ticket + 1 : had + 1;
+        const unsigned long long seen = atomicCAS(at, had, now);
+        if (seen == had) break;
+        had = seen;
+    }
+    if ((int)(now & 0xffff) != pieces) return false;
+    atomicExch(at, 0ull);
+    return true;
+}
+
+// Joins a row's pieces, a warp per row: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
+// They are slot 1 of the first CTA and slot 0 of the following ones.
+template <int R>
+__device__ void cache_join_row(const CacheFwdParams& p, const CacheShared& shared, int r, long long at) {
+    constexpr int kBatch = 8;  // pieces under way at once
+    const int lane = threadIdx.x & 31, n = shared.pieces;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += kBatch) {
+        float2 ml[kBatch];
+        float4 v[kBatch];
+        float top = m;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            ml[x] = make_float2(-INFINITY, 0.f);
+            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + x < n) {
+                const long long from = ((long long)(shared.first + x0 + x) * 2 + (x0 + x == 0 ? 1 : 0)) * R + r;
+                ml[x] = __ldcg(p.part_ml + from);
+                if (lane * 4 < p.c.D) v[x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * 128) + lane);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+        const float ref = top == -INFINITY ? 0.f : top, keep = ptx::ex2(m - ref);
+        l *= keep;
+        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+        m = top;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const float f = ptx::ex2(ml[x].x - ref);
+            l += f * ml[x].y;
+            o.x += f * v[x].x;
+            o.y += f * v[x].y;
+            o.z += f * v[x].z;
+            o.w += f * v[x].w;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : ptx::rcp(l);
+    if (lane * 4 < p.c.D)
+        *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
+            make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
+}
+
 template <int R>
 __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCtas)
     attn_cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -822,7 +901,6 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // uniform, also to the compiler
 
-    ptx::launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             ptx::mbar_init(cache_bar<R>(base, L::kKFull + s), 1);
@@ -840,6 +918,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         }
         ptx::mbar_init(cache_bar<R>(base, L::kDrain), 1);
         *abort_flag = 0;
+        for (int x = 0; x < 2; ++x) reinterpret_cast<CacheShared*>(smem + L::kShared)[x].pieces = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
@@ -851,8 +930,8 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     ptx::tc_fence_before();
     int begin, end, total;
     CachePlace place;
-    cache_locate<L::kThreads>(p.plan, reinterpret_cast<int*>(smem + L::kScan), blockIdx.x, gridDim.x, p.c.status,
-                              &begin, &end, &total, &place, false);  // barriers of the block within
+    const int ctas = cache_locate<L::kThreads>(p.plan, reinterpret_cast<int*>(smem + L::kScan), p.c.status, &begin, &end,
+                                               &total, &place);  // barriers of the block within
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
@@ -863,7 +942,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     } else if (warp == 1) {
         cache_mma_role<R>(p, base, smem, tmem, abort_flag);
     } else if (warp < 4) {
-        cache_query_role<R>(p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+        cache_query_role<R>(p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
     } else {
         cache_softmax_role<R>(p, base, smem, tmem, abort_flag);
     }
@@ -874,59 +953,23 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-}
-
-// Joins a unit's partial results: CTA x joins the unit that begins in CTA x of
-// the first kernel and ends in a later one (there is at most one), rows
-// blockIdx.y * 8 .. + 7, a warp each: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
-template <int R>
-__global__ void __launch_bounds__(256) attn_cache_join_kernel(const CacheFwdParams p, int ctas) {
-    __shared__ __align__(16) int scan[20 + 4];
-    int begin, end, total;
-    CachePlace at;
-    ctas = cache_locate<256>(p.plan, scan, blockIdx.x, ctas, p.c.status, &begin, &end, &total, &at, true);
-    CacheUnit u;
-    bool mine = false;
-    if (begin < end && at.b < p.plan.B && at.t > 0 && end - at.t >= begin) {
-        CachePlace start = at;
-        start.t = 0;
-        CacheCursor cur = cursor_at(p.plan, start, 0x7fffffff);
-        mine = cursor_next(p.plan, cur, u);
+    // Every piece of this CTA is left.  Of each unit that it shares, whoever counts last joins the pieces.
+    CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared);
+    if (shared[0].pieces == 0 && shared[1].pieces == 0) return;
+    if (threadIdx.x < 2) {
+        CacheShared& x = shared[threadIdx.x];
+        __threadfence();
+        x.last = x.pieces > 0 && *abort_flag == 0 && cache_last_piece(p.tickets + x.first, p.ticket, x.pieces);
+        __threadfence();
     }
-    ptx::wait_prerequisites();
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    int i, hq;
-    if (!mine || !cache_row(p, u, r, &i, &hq)) return;
-    // Pieces: slot 1 of this CTA, slot 0 of the following ones up to the unit's end.
-    const int n = plan_last(total, blockIdx.x, ctas, end - at.t + u.tiles) - blockIdx.x + 1;
-    auto piece = [&](int x) { return ((long long)(blockIdx.x + x) * 2 + (x == 0 ? 1 : 0)) * R + r; };
-    float m = -INFINITY;
-    for (int x = lane; x < n; x += 32) m = fmaxf(m, p.part_ml[piece(x)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-        const float2 ml = p.part_ml[piece(x)];
-        const float f = ptx::ex2(ml.x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + piece(x) * 128 + lane * 4);
-        l += f * ml.y;
-        o.x += f * v.x;
-        o.y += f * v.y;
-        o.z += f * v.z;
-        o.w += f * v.w;
+    __syncthreads();
+    for (int i = warp; i < 2 * R; i += L::kThreads / 32) {
+        const CacheShared& x = shared[i / R];
+        const int row = i % R;
+        int qi, hq;
+        if (x.pieces > 0 && x.last && cache_row(p, x.u, row, &qi, &hq))
+            cache_join_row<R>(p, x, row, ((long long)x.u.b * p.Hq + hq) * p.Sq + qi);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long row = ((long long)u.b * p.Hq + hq) * p.Sq + i;
-    if (lane * 4 < p.c.D) {
-        uint2 w;
-        w.x = ptx::pack_bf16x2(o.x * inv, o.y * inv);
-        w.y = ptx::pack_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(p.out + row * p.c.D + lane * 4) = w;
-    }
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
 }
 
 }  // namespace attn

@@ -174,10 +174,5 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// Programmatic dependent launch: lets the next kernel of the stream, when it was
-// launched for that, start now; and waits until the previous kernel's work is done and visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 }  // namespace ptx
 }  // namespace attn

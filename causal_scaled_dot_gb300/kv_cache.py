@@ -11,6 +11,7 @@ in the CUDA library.  There are no gradients through a cache.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -19,6 +20,10 @@ import torch
 from . import native
 
 _DIMS3 = ctypes.c_longlong * 3
+# The current stream's handle by device index.  A step calls write and attention once per layer, and
+# building a Stream object takes longer than the rest of a call's checks.
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _strides(name, x):
@@ -78,6 +83,7 @@ class KVCache:
             raise ValueError("a cache needs at least one block, head and sequence")
         self._tensors = named
         self._device = k.device
+        self._index = k.device.index
         self._sizes = (B, Hkv, D)
         self._capacity = max_blocks * block_size
         self._c = native.AttnCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -108,7 +114,7 @@ class KVCache:
 
     def _rows(self, name, x, heads, S=None, strided=True):
         """Checks a bf16 tensor [B, heads, S, D] on the cache's device; returns S and its strides."""
-        if not x.is_cuda or x.dtype != torch.bfloat16 or x.device != self._device:
+        if x.dtype != torch.bfloat16 or x.device != self._device:
             raise ValueError(f"{name} must be a bf16 tensor on {self._device}")
         B, Hkv, D = self._sizes
         shape = x.shape
@@ -124,32 +130,34 @@ class KVCache:
     def _counts(self, name, t):
         if t is None:
             return None
-        if not t.is_cuda or t.device != self._device or t.dtype != torch.int32 or tuple(t.shape) != (self._sizes[0],) \
+        if t.device != self._device or t.dtype != torch.int32 or tuple(t.shape) != (self._sizes[0],) \
                 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor [{self._sizes[0]}] on {self._device}")
         return t.data_ptr()
 
-    def _call(self, where, fn, stream, check_status):
-        """fn(stream handle) with the cache's device current; memory that fn allocates belongs to that stream."""
-        device = self._device
-        if stream is None and torch.cuda.current_device() == device.index:
-            handle = torch.cuda.current_stream(device).cuda_stream
-            result, rc = fn(handle)
-        else:
-            with torch.cuda.device(device):
-                if stream is None:
-                    stream = torch.cuda.current_stream(device)
-                elif isinstance(stream, int):
-                    stream = torch.cuda.ExternalStream(stream, device=device)
-                handle = stream.cuda_stream
-                with torch.cuda.stream(stream):
-                    result, rc = fn(handle)
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The cache's device current, and `stream` (a torch.cuda.Stream, a handle, or None for the
+        device's current stream) current on it, so that memory allocated within belongs to that
+        stream; yields its handle."""
+        with torch.cuda.device(self._device):
+            if stream is None:
+                stream = torch.cuda.current_stream(self._device)
+            elif isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self._device)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+    def _here(self, stream) -> bool:
+        """Whether a call can run as things are: on the current device's current stream."""
+        return stream is None and torch.cuda.current_device() == self._index
+
+    def _done(self, where, rc, handle, check_status) -> None:
         if rc != native.ATTN_OK:
             raise native.AttnError(rc, where)
         if check_status:
-            with torch.cuda.device(device):
+            with torch.cuda.device(self._device):
                 native.attn_sync_status(handle)
-        return result
 
     def write(self, k, v, new_lens=None, stream=None, check_status: bool = False) -> None:
         """Quantise the step's new tokens k, v (bf16 [B, Hkv, S, D], any strides of
@@ -159,9 +167,13 @@ class KVCache:
         S, ks = self._rows("k", k, self._sizes[1])
         _, vs = self._rows("v", v, self._sizes[1], S)
         n = self._counts("new_lens", new_lens)
-        kp, vp = k.data_ptr(), v.data_ptr()
-        self._call("attn_cache_write",
-                   lambda st: (None, self._lib.attn_cache_write(self._ref, kp, ks, vp, vs, n, S, st)), stream, check_status)
+        if self._here(stream):
+            st = _stream_handle(self._index)
+            rc = self._lib.attn_cache_write(self._ref, k.data_ptr(), ks, v.data_ptr(), vs, n, S, st)
+        else:
+            with self._on(stream) as st:
+                rc = self._lib.attn_cache_write(self._ref, k.data_ptr(), ks, v.data_ptr(), vs, n, S, st)
+        self._done("attn_cache_write", rc, st, check_status)
 
     def read(self, S: int, first: int = 0, k_out=None, v_out=None, stream=None, check_status: bool = False):
         """Positions first .. first+S-1 of every sequence as bf16 (k, v), each
@@ -175,12 +187,14 @@ class KVCache:
             if t is not None:
                 self._rows(name, t, Hkv, S, strided=False)
 
-        def fn(st):
-            k = torch.zeros((B, Hkv, S, D), dtype=torch.bfloat16, device=self._device) if k_out is None else k_out
-            v = torch.zeros((B, Hkv, S, D), dtype=torch.bfloat16, device=self._device) if v_out is None else v_out
-            return (k, v), self._lib.attn_cache_read(self._ref, k.data_ptr(), v.data_ptr(), first, S, st)
-
-        return self._call("attn_cache_read", fn, stream, check_status)
+        with contextlib.nullcontext(_stream_handle(self._index)) if self._here(stream) else self._on(stream) as st:
+            if k_out is None:
+                k_out = torch.zeros((B, Hkv, S, D), dtype=torch.bfloat16, device=self._device)
+            if v_out is None:
+                v_out = torch.zeros((B, Hkv, S, D), dtype=torch.bfloat16, device=self._device)
+            rc = self._lib.attn_cache_read(self._ref, k_out.data_ptr(), v_out.data_ptr(), first, S, st)
+        self._done("attn_cache_read", rc, st, check_status)
+        return k_out, v_out
 
     def attention(self, q, causal: bool = True, scale: float | None = None, q_lens=None, out=None, lse=None,
                   return_lse: bool = True, stream=None, check_status: bool = False):
@@ -196,26 +210,35 @@ class KVCache:
             raise ValueError(f"q has {Hq} heads: a multiple of the cache's {Hkv} is needed")
         if out is not None:
             self._rows("out", out, Hq, Sq, strided=False)
-        if lse is not None and (not lse.is_cuda or lse.device != self._device or lse.dtype != torch.float32
+        if lse is not None and (lse.device != self._device or lse.dtype != torch.float32
                                 or tuple(lse.shape) != (B, Hq, Sq) or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor [{B}, {Hq}, {Sq}] on {self._device}")
         n = self._counts("q_lens", q_lens)
         if scale is None:
             scale = 1.0 / math.sqrt(D)
 
-        def fn(st):
-            need = self._workspace_bytes.get((Hq, Sq))
-            if need is None:
-                need = self._workspace_bytes[Hq, Sq] = native.attn_cache_workspace(Hq, Hkv, Sq, D)
-            o = torch.empty((B, Hq, Sq, D), dtype=torch.bfloat16, device=self._device) if out is None else out
-            if lse is None and return_lse:
-                s = torch.empty((B, Hq, Sq), dtype=torch.float32, device=self._device)
-            else:
-                s = lse
-            w = torch.empty(need, dtype=torch.uint8, device=self._device)
-            rc = self._lib.attn_cache_fwd(self._ref, q.data_ptr(), qs, o.data_ptr(), None if s is None else s.data_ptr(),
-                                          n, Hq, Sq, scale, 1 if causal else 0, w.data_ptr(), need, st)
-            return (o, s), rc
+        if self._here(stream):
+            st = _stream_handle(self._index)
+            out, lse, rc = self._attend(q, qs, out, lse, n, Hq, Sq, scale, causal, return_lse, st)
+        else:
+            with self._on(stream) as st:
+                out, lse, rc = self._attend(q, qs, out, lse, n, Hq, Sq, scale, causal, return_lse, st)
+        self._done("attn_cache_fwd", rc, st, check_status)
+        return (out, lse) if return_lse else out
 
-        o, s = self._call("attn_cache_fwd", fn, stream, check_status)
-        return (o, s) if return_lse else o
+    def _attend(self, q, qs, out, lse, n, Hq, Sq, scale, causal, return_lse, st):
+        need = self._workspace_bytes.get((Hq, Sq))
+        if need is None:
+            c = ctypes.c_ulonglong(0)
+            rc = self._lib.attn_cache_workspace(self._ref, Hq, Sq, ctypes.byref(c))
+            if rc != native.ATTN_OK:
+                return None, None, rc
+            need = self._workspace_bytes[Hq, Sq] = c.value
+        if out is None:
+            out = torch.empty((self._sizes[0], Hq, Sq, self._sizes[2]), dtype=torch.bfloat16, device=self._device)
+        if lse is None and return_lse:
+            lse = torch.empty((self._sizes[0], Hq, Sq), dtype=torch.float32, device=self._device)
+        w = torch.empty(need, dtype=torch.uint8, device=self._device) if need else None
+        rc = self._lib.attn_cache_fwd(self._ref, q.data_ptr(), qs, out.data_ptr(), None if lse is None else lse.data_ptr(), n,
+                                      Hq, Sq, scale, 1 if causal else 0, None if w is None else w.data_ptr(), need, st)
+        return out, lse, rc

@@ -96,7 +96,7 @@ def load() -> ctypes.CDLL:
         lib.attn_cache_read.restype = ci
         lib.attn_cache_fwd.argtypes = [cache_p, vp, ll3_p, vp, vp, vp, ci, ci, cf, ci, vp, u64, vp]
         lib.attn_cache_fwd.restype = ci
-        lib.attn_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(u64)]
+        lib.attn_cache_workspace.argtypes = [cache_p, ci, ci, ctypes.POINTER(u64)]
         lib.attn_cache_workspace.restype = ci
         _lib = lib
         return lib
@@ -409,16 +409,6 @@ def attn_fwd_fp8(q, k, v, q_descale: float, k_descale: float, v_descale: float, 
     if check and rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_fp8")
     return rc
-
-
-def attn_cache_workspace(Hq: int, Hkv: int, Sq: int, D: int) -> int:
-    """The C entry point ``attn_cache_workspace``: bytes that ``attn_cache_fwd`` needs
-    on the current device for these sizes."""
-    n = ctypes.c_ulonglong(0)
-    rc = load().attn_cache_workspace(int(Hq), int(Hkv), int(Sq), int(D), ctypes.byref(n))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_cache_workspace")
-    return n.value
 
 
 def attn_sync_status(stream=None, check: bool = True) -> int:

@@ -437,9 +437,10 @@ int attn_cache_read(const attn_cache_t *cache, void *k, void *v, int first, int 
  *   causal    non-zero: the query at position p (see attn_cache_t) sees keys
  *             0 .. p; zero: all keys 0 .. seq_lens[b]-1.
  *   workspace  device memory, 16-byte aligned, of at least the bytes that
- *             attn_cache_workspace gives; contents before and after are
- *             unspecified.  Calls that may run at the same time (other streams,
- *             graphs replayed side by side) need a workspace each.
+ *             attn_cache_workspace gives (NULL when it gives 0); contents before
+ *             and after are unspecified, but a workspace is not to be written
+ *             by others while it serves.  Calls that may run at the same time
+ *             (other streams, graphs replayed side by side) need one each.
  * A query that sees no key (an idle slot, or a position < 0) gets O = 0 and
  * LSE = -inf.  Keys that no query row may see (past seq_lens[b], after the
  * position) do not affect it whatever their codes.  Scores accumulate in fp32
@@ -456,11 +457,11 @@ int attn_cache_fwd(const attn_cache_t *cache, const void *q, const long long *q_
 
 /*
  * attn_cache_workspace -- *bytes receives the workspace that attn_cache_fwd
- * needs on the current device for these sizes; it does not depend on the batch
- * or on the sequence lengths.  Errors: ATTN_ERR_INVALID_ARG for a size < 1, Hq
- * not a multiple of Hkv or a NULL bytes; ATTN_ERR_UNSUPPORTED as attn_fwd.
+ * needs on the current device for a cache of these sizes (its lengths do not
+ * matter) and Hq and Sq; 0 for caches of up to 512 tokens a sequence.  Errors as
+ * attn_cache_fwd.
  */
-int attn_cache_workspace(int Hq, int Hkv, int Sq, int D, unsigned long long *bytes);
+int attn_cache_workspace(const attn_cache_t *cache, int Hq, int Sq, unsigned long long *bytes);
 
 /*
  * attn_sync_status -- synchronise `stream` and report device-side failures of

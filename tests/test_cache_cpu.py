@@ -87,7 +87,7 @@ def test_read_refusals(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(q=None), ATTN_ERR_INVALID_ARG), (dict(out=None), ATTN_ERR_INVALID_ARG), (dict(ws=None), ATTN_ERR_INVALID_ARG),
+    (dict(q=None), ATTN_ERR_INVALID_ARG), (dict(out=None), ATTN_ERR_INVALID_ARG), (dict(ws=None, wb=0), ATTN_ERR_INVALID_ARG),
     (dict(Hq=3), ATTN_ERR_INVALID_ARG), (dict(Hq=0), ATTN_ERR_INVALID_ARG), (dict(Sq=0), ATTN_ERR_INVALID_ARG),
     (dict(scale=0.0), ATTN_ERR_INVALID_ARG), (dict(scale=float("nan")), ATTN_ERR_INVALID_ARG),
     (dict(scale=-1.0), ATTN_ERR_INVALID_ARG), (dict(q=7 * T + 8), ATTN_ERR_MISALIGNED),
@@ -102,12 +102,14 @@ def test_attention_refusals(kw, code):
 
 
 def test_workspace_refusals():
-    n = ctypes.c_ulonglong(0)
+    n = ctypes.c_ulonglong(7)
     f = native.load().attn_cache_workspace
-    assert f(8, 2, 1, 128, None) == ATTN_ERR_INVALID_ARG
-    for bad in ((0, 1, 1, 128), (8, 3, 1, 128), (8, 2, 0, 128)):
-        assert f(*bad, ctypes.byref(n)) == ATTN_ERR_INVALID_ARG
-    assert f(8, 2, 1, 80, ctypes.byref(n)) == ATTN_ERR_UNSUPPORTED
+    assert f(cache(), 8, 1, None) == ATTN_ERR_INVALID_ARG
+    assert f(None, 8, 1, ctypes.byref(n)) == ATTN_ERR_INVALID_ARG
+    for bad in ((0, 1), (9, 1), (8, 0)):
+        assert f(cache(), *bad, ctypes.byref(n)) == ATTN_ERR_INVALID_ARG
+    assert f(cache(D=80), 8, 1, ctypes.byref(n)) == ATTN_ERR_UNSUPPORTED
+    assert f(cache(max_blocks=8), 8, 1, ctypes.byref(n)) == 0 and n.value == 0  # 512 tokens: no unit is split
 
 
 def test_status_string_of_a_bad_cache():
@@ -269,8 +271,12 @@ using namespace attn;
 int main() {
     for (int total : {1, 303, 304, 70000, 0x7ffffffe, 0x7fffffff})
         for (int ctas : {1, 152, 304, 32767})
-            for (int c = 0; c <= ctas; ++c)
-                CHECK(plan_begin(total, c, ctas) == (int)((long long)total * c / ctas));
+            for (int c = 0; c <= ctas; ++c) {
+                const int t = plan_begin(total, c, ctas);
+                CHECK(t == (int)((long long)total * c / ctas));
+                if (ctas <= total && c < ctas) CHECK(plan_cta(total, t, ctas) == c);
+                if (ctas <= total && c > 0) CHECK(plan_cta(total, t - 1, ctas) == c - 1);
+            }
     std::srand(7);
     for (int round = 0; round < 400; ++round) {
         CachePlan p{};
@@ -281,6 +287,7 @@ int main() {
         p.qper = 1 + std::rand() % 16;
         p.q_tiles = (p.Sq + p.qper - 1) / p.qper;
         p.heads = 1 + std::rand() % 5;
+        p.whole = std::rand() % 4 == 0;
         std::vector<int> lens(p.B), counts(p.B);
         for (int b = 0; b < p.B; ++b) {
             lens[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (p.capacity + 1);
@@ -304,7 +311,7 @@ int main() {
                 const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
                 for (int h = 0; h < p.heads; ++h) {
                     want.push_back({b, qt, h, tiles, keys});
-                    total += tiles;
+                    total += p.whole ? 1 : tiles;
                 }
             }
         }
@@ -319,7 +326,7 @@ int main() {
         CHECK(all == total);
         const int given = 1 + std::rand() % 70, ctas = plan_ctas(total, given);
         size_t unit = 0;
-        int tile = 0, pieces = 0, expect_last = -1;
+        int tile = 0, pieces = 0, expect_first = -1, expect_last = -1;
         for (int c = 0; c < given; ++c) {
             const int begin = plan_begin(total, c, ctas), end = plan_begin(total, c + 1, ctas);
             CHECK((begin == end) == (c >= ctas));  // no CTA without a tile among those that share them
@@ -329,6 +336,7 @@ int main() {
             while (begin >= before + sum[t]) before += sum[t++];
             CacheCursor cur = cursor_at(p, plan_find(p, t * per, begin - before), end - begin);
             CacheUnit u;
+            int pos = begin;  // of the share in the row of all tiles
             while (cursor_next(p, cur, u)) {
                 CHECK(unit < want.size());
                 const U& w = want[unit];
@@ -336,15 +344,20 @@ int main() {
                 CHECK(u.t + u.n <= u.tiles);
                 tile += u.n;
                 ++pieces;
+                if (pieces == 1 && tile < u.tiles) {
+                    CHECK(!p.whole);
+                    expect_first = c;
+                    expect_last = plan_cta(total, pos - u.t + u.tiles - 1, ctas);
+                }
+                if (pieces > 1) CHECK(plan_cta(total, pos - u.t, ctas) == expect_first);  // every piece finds the first
                 if (tile == u.tiles) {
-                    CHECK(pieces == 1 || expect_last == c);  // the piece that the join takes last
+                    CHECK(pieces == 1 || (expect_last == c && pieces == expect_last - expect_first + 1));
                     tile = pieces = 0;
                     ++unit;
-                } else if (pieces == 1) {
-                    CHECK(end - tile >= begin);  // it begins in this CTA
-                    expect_last = plan_last(total, c, ctas, end - tile + u.tiles);
                 }
+                pos += p.whole ? 1 : u.n;
             }
+            CHECK(pos == end);
         }
         CHECK(unit == want.size() && tile == 0);
     }

@@ -392,3 +392,33 @@ def test_results_do_not_depend_on_stream_or_repetition():
         got = cache.attention(q, stream=stream, check_status=True)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(cache.attention(q, return_lse=False), want[0])
+
+
+def test_workspace_contents_do_not_matter():
+    """One workspace for calls of different shapes, full of whatever was there: zeros, ones, random
+    bytes, the last call's partial results."""
+    import ctypes
+    from causal_scaled_dot_gb300 import native
+    cache, table = make(2, 2, 64, 64, 5000, seed=18)
+    fill(cache, table, [5000, 800], seed=161)
+    lib, n = native.load(), ctypes.c_ulonglong(0)
+    st = torch.cuda.current_stream().cuda_stream
+    sizes = [(2, 1), (4, 7), (16, 4), (2, 90)]
+    need = 0
+    for Hq, Sq in sizes:
+        assert lib.attn_cache_workspace(ctypes.byref(cache._c), Hq, Sq, ctypes.byref(n)) == 0
+        need = max(need, n.value)
+    work = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for round_, content in enumerate((0, 255, None, "random", "random", None)):
+        for Hq, Sq in sizes:
+            q = rows((2, Hq, Sq, 64), 162 + round_).cuda()
+            if content == "random":
+                work.random_(0, 256)
+            elif content is not None:
+                work.fill_(content)
+            want = cache.attention(q)
+            o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+            assert lib.attn_cache_fwd(ctypes.byref(cache._c), q.data_ptr(), None, o.data_ptr(), lse.data_ptr(), None, Hq, Sq,
+                                      0.125, 1, work.data_ptr(), need, st) == 0
+            native.attn_sync_status()
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
