@@ -154,11 +154,12 @@ int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, i
 
 int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH; }
 
-template <int kThreads>
-int launch_write(const CacheWriteParams& p, cudaStream_t st) {
-    const long long per = 256 / kThreads, grid = (p.num_units + per - 1) / per;
-    if (grid > (1ll << 31) - 1) return ATTN_ERR_UNSUPPORTED;
-    attn_cache_write_kernel<kThreads><<<(unsigned)grid, 256, 0, st>>>(p);
+// Launches a write or read kernel with the threads per unit that hold the
+// largest unit's elements at 64 a thread.
+template <typename P, typename K>
+int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
+    const int per = 256 / threads;
+    kernel<<<(p.num_units + per - 1) / per, 256, 0, st>>>(p);
     return launched();
 }
 
@@ -195,13 +196,15 @@ extern "C" int attn_cache_write(const attn_cache_t* cache, const void* k, const 
     // S tokens from any slot touch at most this many blocks (and no more than there are).
     const long long touched = ((long long)S + bs - 2) / bs + 1;
     p.blocks_per_seq = (int)(touched < cache->max_blocks ? touched : cache->max_blocks);
-    p.num_units = (long long)cache->B * cache->Hkv * 2 * p.blocks_per_seq;
-    const int elements = (S < bs ? S : bs) * cache->D;  // of the largest unit
+    const long long units = (long long)cache->B * cache->Hkv * 2 * p.blocks_per_seq;
+    if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
+    p.num_units = (int)units;
+    const int elements = (S < bs ? S : bs) * cache->D;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (elements <= 64 * 32) return launch_write<32>(p, st);
-    if (elements <= 64 * 64) return launch_write<64>(p, st);
-    if (elements <= 64 * 128) return launch_write<128>(p, st);
-    return launch_write<256>(p, st);
+    if (elements <= 64 * 32) return launch_rw(attn_cache_write_kernel<32>, 32, p, st);
+    if (elements <= 64 * 64) return launch_rw(attn_cache_write_kernel<64>, 64, p, st);
+    if (elements <= 64 * 128) return launch_rw(attn_cache_write_kernel<128>, 128, p, st);
+    return launch_rw(attn_cache_write_kernel<256>, 256, p, st);
 }
 
 extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int first, int S, void* stream) {
@@ -223,11 +226,20 @@ extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int 
     p.v = static_cast<__nv_bfloat16*>(v);
     p.first = first;
     p.S = S;
-    p.num_vec = (long long)(n / 16);
-    const long long want = (p.num_vec + 255) / 256, most = (long long)sms * 8;
-    const dim3 grid((unsigned)(want < most ? want : most), k && v ? 2 : 1);
-    attn_cache_read_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched();
+    // Blocks from first's on, no further than the cache's capacity.
+    const int bs = cache->block_size, from = first / bs;
+    const long long to = ((long long)first + S + bs - 1) / bs, blocks = (to < cache->max_blocks ? to : cache->max_blocks) - from;
+    if (blocks < 1) return ATTN_OK;  // past every sequence's end
+    const long long units = (long long)cache->B * cache->Hkv * (k && v ? 2 : 1) * blocks;
+    if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
+    p.blocks_per_seq = (int)blocks;
+    p.num_units = (int)units;
+    const int elements = (S < bs ? S : bs) * cache->D;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (elements <= 64 * 32) return launch_rw(attn_cache_read_kernel<32>, 32, p, st);
+    if (elements <= 64 * 64) return launch_rw(attn_cache_read_kernel<64>, 64, p, st);
+    if (elements <= 64 * 128) return launch_rw(attn_cache_read_kernel<128>, 128, p, st);
+    return launch_rw(attn_cache_read_kernel<256>, 256, p, st);
 }
 
 extern "C" int attn_cache_workspace(const attn_cache_t* cache, int Hq, int Sq, unsigned long long* bytes) {

@@ -9,8 +9,11 @@
 // unit's threads, and the codes leave from the registers.  Bound by the bytes:
 // 2 in and 1 out per element.
 //
-// Read: one 16-byte load of codes and two 16-byte stores of bf16 per step, flat
-// over the requested rows; bound by the bytes (1 in, 2 out per element).
+// Read: the same units the other way; bound by the bytes (1 in, 2 out per element).
+//
+// Both are latency-bound per unit (length, then table and data, then the rest),
+// so what counts is that a unit's loads leave together and that many units are
+// resident: 64 elements a thread, three or four blocks of 256 threads an SM.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,7 +34,7 @@ struct CacheWriteParams {
     const int* new_lens;                 // or null: S each
     int S;
     int blocks_per_seq;                  // blocks that S tokens can touch
-    long long num_units;                 // B * Hkv * 2 * blocks_per_seq
+    int num_units;                       // B * Hkv * 2 * blocks_per_seq
 };
 
 // The smallest power of two s >= 2^-126 with amax <= 448 s, for finite amax >= 0:
@@ -54,47 +57,45 @@ __device__ __forceinline__ float2 e4m3_unpair(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A unit's place: sequence, head, K or V, and which of the blocks that the call touches.
+struct CacheRwUnit {
+    int b, h, is_v, blk;
+};
+__device__ __forceinline__ CacheRwUnit cache_rw_unit(int unit, int blocks, int Hkv, int kinds) {
+    CacheRwUnit u;
+    const int x = unit / blocks;
+    u.blk = unit - x * blocks;
+    const int y = kinds == 2 ? x >> 1 : x;
+    u.is_v = kinds == 2 ? x & 1 : 0;
+    u.b = y / Hkv;
+    u.h = y - u.b * Hkv;
+    return u;
+}
+
 // kThreads threads per unit, 256 / kThreads units per CTA; 8 vectors of 8
 // elements per thread cover block_size * D <= 64 * kThreads elements.
 template <int kThreads>
-__global__ void __launch_bounds__(256) attn_cache_write_kernel(const CacheWriteParams p) {
+__global__ void __launch_bounds__(256, 3) attn_cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
     constexpr int kVec = 8;
     __shared__ float warp_max[8];
     const CacheView& c = p.c;
     const int t = threadIdx.x % kThreads;
-    const long long unit = (long long)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+    const int unit = blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
     bool active = unit < p.num_units, bad = false;
-    int b = 0, h = 0, is_v = 0, slot0 = 0, rows = 0, row0 = 0, block = -1;
-    if (active) {
-        const int blk = (int)(unit % p.blocks_per_seq);
-        const long long x = unit / p.blocks_per_seq;
-        is_v = (int)(x & 1);
-        h = (int)((x >> 1) % c.Hkv);
-        b = (int)((x >> 1) / c.Hkv);
-        const CacheSpan s = cache_span(c.seq_lens[b], p.new_lens ? p.new_lens[b] : p.S,
-                                       c.max_blocks * c.block_size, p.S, &bad);
-        const int begin = s.first < 0 ? 0 : s.first;     // first position written
-        const int lb = (begin >> c.block_shift) + blk;   // this unit's block of the sequence
-        const int pos0 = blk == 0 ? begin : lb << c.block_shift;
-        const int end = min(s.len, (lb + 1) << c.block_shift);
-        active = pos0 < end;
-        if (active) {
-            slot0 = pos0 & (c.block_size - 1);
-            rows = end - pos0;
-            row0 = pos0 - s.first;
-            block = cache_block(c.block_table[(long long)b * c.max_blocks + lb], c.num_blocks, &bad);
-            active = block >= 0;
-        }
-    }
-    if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
-    if (kThreads == 32 && !active) return;  // whole warps: no barrier below
+    const CacheRwUnit u = cache_rw_unit(active ? unit : 0, p.blocks_per_seq, c.Hkv, 2);
+    const CacheSpan s = cache_span(c.seq_lens[u.b], p.new_lens ? p.new_lens[u.b] : p.S, c.max_blocks * c.block_size, p.S, &bad);
+    const int begin = s.first < 0 ? 0 : s.first;       // first position written
+    const int lb = (begin >> c.block_shift) + u.blk;   // this unit's block of the sequence
+    const int pos0 = u.blk == 0 ? begin : lb << c.block_shift;
+    const int end = min(s.len, (lb + 1) << c.block_shift);
+    active = active && pos0 < end;
+    const int slot0 = pos0 & (c.block_size - 1), rows = active ? end - pos0 : 0, row0 = pos0 - s.first;
+    const int entry = active ? __ldg(c.block_table + (long long)u.b * c.max_blocks + lb) : 0;
 
-    const int vec_per_row = c.D / 8, n_vec = active ? rows * vec_per_row : 0;
-    const long long* st = is_v ? p.v_stride : p.k_stride;
-    const __nv_bfloat16* src = (is_v ? p.v : p.k) + b * st[0] + h * st[1] + (long long)row0 * st[2];
-    float* scale_at = active ? (is_v ? c.v_scale : c.k_scale) + (long long)block * c.Hkv + h : nullptr;
-    const float s_old = active && slot0 > 0 ? *scale_at : 0.f;
-
+    const int row_shift = c.D == 128 ? 4 : 3, n_vec = rows << row_shift;  // D / 8 vectors a row
+    const long long stride = u.is_v ? p.v_stride[2] : p.k_stride[2];
+    const __nv_bfloat16* src = u.is_v ? p.v + u.b * p.v_stride[0] + u.h * p.v_stride[1]
+                                      : p.k + u.b * p.k_stride[0] + u.h * p.k_stride[1];
     uint4 x[kVec];
     float amax = 0.f;
 #pragma unroll
@@ -102,9 +103,14 @@ __global__ void __launch_bounds__(256) attn_cache_write_kernel(const CacheWriteP
         const int v = t + i * kThreads;
         x[i] = make_uint4(0, 0, 0, 0);
         if (v < n_vec)
-            x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (long long)(v / vec_per_row) * st[2] +
-                                                         (v % vec_per_row) * 8));
+            x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (row0 + (v >> row_shift)) * stride) + (v & ((1 << row_shift) - 1)));
     }
+    const int block = active ? cache_block(entry, c.num_blocks, &bad) : -1;
+    active = block >= 0;
+    if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
+    if (kThreads == 32 && !active) return;  // whole warps: no barrier below
+    float* scale_at = active ? (u.is_v ? c.v_scale : c.k_scale) + (long long)block * c.Hkv + u.h : nullptr;
+    const float s_old = active && slot0 > 0 ? *scale_at : 0.f;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(256) attn_cache_write_kernel(const CacheWriteP
 
     const float s_new = fmaxf(e4m3_pow2_scale(amax), s_old);
     const float inv = 1.f / s_new;  // exact for the powers of two that this kernel stores (at most 2^120)
-    unsigned char* dst = (is_v ? c.v : c.k) + cache_offset(block, h, slot0, c.Hkv, c.block_size, c.D);
+    unsigned char* dst = (u.is_v ? c.v : c.k) + cache_offset(block, u.h, slot0, c.Hkv, c.block_size, c.D);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const int v = t + i * kThreads;
@@ -146,8 +152,8 @@ __global__ void __launch_bounds__(256) attn_cache_write_kernel(const CacheWriteP
     }
     if (slot0 > 0 && s_new > s_old) {  // the block's earlier tokens move to the larger scale
         const float ratio = s_old * inv;
-        uint2* had = reinterpret_cast<uint2*>((is_v ? c.v : c.k) + cache_offset(block, h, 0, c.Hkv, c.block_size, c.D));
-        for (int v = t; v < slot0 * vec_per_row; v += kThreads) {
+        uint2* had = reinterpret_cast<uint2*>((u.is_v ? c.v : c.k) + cache_offset(block, u.h, 0, c.Hkv, c.block_size, c.D));
+        for (int v = t; v < slot0 << row_shift; v += kThreads) {
             const uint2 w = had[v];
             uint32_t code[4];
 #pragma unroll
@@ -165,45 +171,54 @@ struct CacheReadParams {
     CacheView c;
     __nv_bfloat16 *k, *v;  // [B, Hkv, S, D], either may be null
     int first, S;
-    long long num_vec;     // 16-element vectors of one output
+    int blocks_per_seq;    // blocks that S positions from `first` on touch
+    int num_units;         // B * Hkv * blocks_per_seq, twice when both are read
 };
 
-// blockIdx.y: 0 reads K, 1 reads V (or the one that is asked for).
-__global__ void __launch_bounds__(256) attn_cache_read_kernel(const CacheReadParams p) {
+// Units and threads as above; 4 vectors of 16 codes per thread.
+template <int kThreads>
+__global__ void __launch_bounds__(256, 4) attn_cache_read_kernel(const __grid_constant__ CacheReadParams p) {
+    constexpr int kVec = 4;
     const CacheView& c = p.c;
-    const bool is_v = blockIdx.y == 1 || p.k == nullptr;
-    const unsigned char* code = is_v ? c.v : c.k;
-    const float* scale = is_v ? c.v_scale : c.k_scale;
-    __nv_bfloat16* out = is_v ? p.v : p.k;
-    const int vec_per_row = c.D / 16;
+    const int t = threadIdx.x % kThreads, unit = blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+    if (unit >= p.num_units) return;
+    const CacheRwUnit u = cache_rw_unit(unit, p.blocks_per_seq, c.Hkv, p.k && p.v ? 2 : 1);
+    const bool is_v = u.is_v || !p.k;
+    const int lb = (p.first >> c.block_shift) + u.blk;
     bool bad = false;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.num_vec; i += (long long)gridDim.x * 256) {
-        const int d = (int)(i % vec_per_row) * 16;
-        const long long row = i / vec_per_row;
-        const int s = (int)(row % p.S);
-        const long long bh = row / p.S;
-        const int h = (int)(bh % c.Hkv), b = (int)(bh / c.Hkv);
-        const int len = cache_clamp(c.seq_lens[b], c.max_blocks * c.block_size, &bad);
-        const long long pos = (long long)p.first + s;
-        if (pos >= len) continue;
-        const int block = cache_block(c.block_table[(long long)b * c.max_blocks + (pos >> c.block_shift)],
-                                      c.num_blocks, &bad);
-        if (block < 0) continue;
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(
-            code + cache_offset(block, h, (int)pos & (c.block_size - 1), c.Hkv, c.block_size, c.D) + d));
-        const float f = scale[(long long)block * c.Hkv + h];
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    const int len = cache_clamp(c.seq_lens[u.b], c.max_blocks * c.block_size, &bad);
+    const int pos0 = max(p.first, lb << c.block_shift), end = min(min(len, p.first + p.S), (lb + 1) << c.block_shift);
+    if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
+    if (pos0 >= end) return;
+    const int block = cache_block(__ldg(c.block_table + (long long)u.b * c.max_blocks + lb), c.num_blocks, &bad);
+    if (block < 0) {
+        if (t == 0) atomicOr(c.status, kStatusBadCache);
+        return;
+    }
+    const uint4* code = reinterpret_cast<const uint4*>(
+        (is_v ? c.v : c.k) + cache_offset(block, u.h, pos0 & (c.block_size - 1), c.Hkv, c.block_size, c.D));
+    const float scale = (is_v ? c.v_scale : c.k_scale)[(long long)block * c.Hkv + u.h];
+    uint4* out = reinterpret_cast<uint4*>((is_v ? p.v : p.k) +
+                                          (((long long)u.b * c.Hkv + u.h) * p.S + (pos0 - p.first)) * c.D);
+    const int n_vec = (end - pos0) * c.D / 16;
+    uint4 x[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        if (t + i * kThreads < n_vec) x[i] = __ldcs(code + t + i * kThreads);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        if (t + i * kThreads >= n_vec) break;
+        const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float2 e = e4m3_unpair(in[j >> 1] >> (16 * (j & 1)) & 0xffffu);
-            o[j] = ptx::pack_bf16x2(e.x * f, e.y * f);
+            o[j] = ptx::pack_bf16x2(e.x * scale, e.y * scale);
         }
-        uint4* to = reinterpret_cast<uint4*>(out + i * 16);
+        uint4* to = out + 2 * (t + i * kThreads);
         to[0] = make_uint4(o[0], o[1], o[2], o[3]);
         to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    if (bad) atomicOr(c.status, kStatusBadCache);
 }
 
 }  // namespace attn

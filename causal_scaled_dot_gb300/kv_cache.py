@@ -24,6 +24,10 @@ _DIMS3 = ctypes.c_longlong * 3
 # building a Stream object takes longer than the rest of a call's checks.
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# Workspaces by (device, stream): calls on one stream run one after the other, so they share one.
+# Captured calls do not take part: each has its own from the graph's memory, as graphs may be
+# replayed on any stream.
+_workspaces: dict = {}
 
 
 def _strides(name, x):
@@ -202,7 +206,7 @@ class KVCache:
         ``write``) over the cache (``attn_cache_fwd``).  Sequence b's ``q_lens[b]``
         (int32 [B]; default Sq each) first rows stand for its last positions; rows past
         them are left as they were in ``out`` / ``lse`` when given, and unspecified
-        otherwise.  The workspace is allocated per call, so calls may overlap."""
+        otherwise."""
         B, Hkv, D = self._sizes
         Sq, qs = self._rows("q", q, 0)
         Hq = q.shape[1]
@@ -238,7 +242,14 @@ class KVCache:
             out = torch.empty((self._sizes[0], Hq, Sq, self._sizes[2]), dtype=torch.bfloat16, device=self._device)
         if lse is None and return_lse:
             lse = torch.empty((self._sizes[0], Hq, Sq), dtype=torch.float32, device=self._device)
-        w = torch.empty(need, dtype=torch.uint8, device=self._device) if need else None
+        w = None
+        if need:
+            if torch.cuda.is_current_stream_capturing():
+                w = torch.empty(need, dtype=torch.uint8, device=self._device)
+            else:
+                w = _workspaces.get((self._index, st))
+                if w is None or w.numel() < need:
+                    w = _workspaces[self._index, st] = torch.empty(need, dtype=torch.uint8, device=self._device)
         rc = self._lib.attn_cache_fwd(self._ref, q.data_ptr(), qs, out.data_ptr(), None if lse is None else lse.data_ptr(), n,
                                       Hq, Sq, scale, 1 if causal else 0, None if w is None else w.data_ptr(), need, st)
         return out, lse, rc
