@@ -14,6 +14,7 @@
 #include "host.h"
 #include "kernel_cache_fwd.cuh"
 #include "kernel_cache_rw.cuh"
+#include "kernel_cache_wide.cuh"
 
 namespace attn {
 namespace {
@@ -84,20 +85,22 @@ CacheView view_of(const attn_cache_t* c, unsigned int* status) {
     return v;
 }
 
-// Query rows of a unit: the smallest of 8, 16, 32 and 64 that holds all rows of
-// a key/value head, else 64.  A tile's products take the same time whatever R
-// is (A is the cache's side) until R = 64, while the softmax works on all R
-// rows, used or not.
+// Query rows of a unit: the least form that takes them all, and 128 from 33 rows on.  Up to 8192 keys,
+// 32 heads over 8: 16 x 8 tokens of 4 heads (32 rows) take 51 us with 32 rows a unit and 67 with 128; 32 x 8 of 8
+// (64 rows) 154 with 128, and 180 with 64 in the form of 32.
 int rows_per_unit(long long group, long long Sq) {
     const long long rows = group * Sq;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
-int ctas_per_sm(int R) { return R == 8 ? CacheLayout<8>::kCtas : R == 16 ? CacheLayout<16>::kCtas
-                                     : R == 32 ? CacheLayout<32>::kCtas : CacheLayout<64>::kCtas; }
+int ctas_per_sm(int R) { return R == 128 ? CacheWideLayout::kCtas : R == 8 ? CacheLayout<8>::kCtas : 1; }
+
 // Key tiles that a unit may have, by the cache's capacity; up to 4 (512 tokens)
 // units are not split: joining two pieces takes about as long as three more
 // tiles in the same CTA.
 constexpr int kWholeTiles = 4;
+// Tiles that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 33 us with 4, 45
+// with 1, 39 with 2 or 6; 1 joins more pieces, 6 leaves SMs without work.
+constexpr int kWideLeast = 4;
 long long tiles_of(const attn_cache_t* c) {
     return ((long long)c->max_blocks * c->block_size + kCacheTile - 1) / kCacheTile;
 }
@@ -137,18 +140,22 @@ int setup_cache_kernels(int dev) {
     if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
     std::lock_guard<std::mutex> lock(g_cache_mutex);
     if (g_cache_ready[dev] == 0)
-        g_cache_ready[dev] = allow_smem<8>() && allow_smem<16>() && allow_smem<32>() && allow_smem<64>() ? 1 : ATTN_ERR_DEVICE;
+        g_cache_ready[dev] = allow_smem<8>() && allow_smem<16>() && allow_smem<32>() &&
+                                     cudaFuncSetAttribute(attn_cache_fwd_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          (int)CacheWideLayout::kDynamicSmem) == cudaSuccess
+                                 ? 1
+                                 : ATTN_ERR_DEVICE;
     return g_cache_ready[dev] == 1 ? ATTN_OK : g_cache_ready[dev];
 }
 
-template <int R>
-int launch_fwd(const CUtensorMap& tk, const CUtensorMap& tv, CacheFwdParams p, int sms, long long tiles, cudaStream_t st) {
-    using L = CacheLayout<R>;
+template <typename L, typename K>
+int launch_fwd(K kernel, const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int sms, long long tiles,
+               cudaStream_t st) {
     const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads, most = (long long)sms * L::kCtas;
     if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
     const long long work = p.plan.whole ? units : units * tiles;  // of the plan, at most
     const int grid = (int)(work < most ? work : most);
-    attn_cache_fwd_kernel<R><<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);
+    kernel<<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
@@ -323,12 +330,13 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     if ((long long)cache->B * p.plan.q_tiles > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     p.plan.heads = cache->Hkv * p.hgroups;
     p.plan.whole = splits(cache) ? 0 : 1;
+    p.plan.least = R == 128 && !p.plan.whole ? kWideLeast : 1;
     const long long tiles = tiles_of(cache);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (R) {
-        case 8: return launch_fwd<8>(tk, tv, p, sms, tiles, st);
-        case 16: return launch_fwd<16>(tk, tv, p, sms, tiles, st);
-        case 32: return launch_fwd<32>(tk, tv, p, sms, tiles, st);
-        default: return launch_fwd<64>(tk, tv, p, sms, tiles, st);
+        case 8: return launch_fwd<CacheLayout<8>>(attn_cache_fwd_kernel<8>, tk, tv, p, sms, tiles, st);
+        case 16: return launch_fwd<CacheLayout<16>>(attn_cache_fwd_kernel<16>, tk, tv, p, sms, tiles, st);
+        case 32: return launch_fwd<CacheLayout<32>>(attn_cache_fwd_kernel<32>, tk, tv, p, sms, tiles, st);
+        default: return launch_fwd<CacheWideLayout>(attn_cache_fwd_wide_kernel, tk, tv, p, sms, tiles, st);
     }
 }

@@ -86,6 +86,7 @@ struct CachePlan {
     int q_tiles;  // query tiles of Sq queries
     int heads;    // head groups per sequence and query tile
     int whole;    // 1: units are not split
+    int least;    // tiles that a CTA takes at least (but for the total's remainder), 1 or more
 };
 
 ATTN_HD CacheSpan plan_span(const CachePlan& p, int b, bool* bad) {
@@ -153,9 +154,12 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
     }
 }
 
-// The CTAs that share `total` tiles: all, or one per tile, so that none
-// between the first and the last piece of a unit is without a tile.
-ATTN_HD int plan_ctas(int total, int ctas) { return total < ctas ? total : ctas; }
+// The CTAs that share `total` tiles: all, or as many as leave each `least`
+// tiles, and so none without a tile between the first and the last piece of a unit.
+ATTN_HD int plan_ctas(const CachePlan& p, int total, int ctas) {
+    const int most = (total + p.least - 1) / p.least;
+    return most < ctas ? most : ctas;
+}
 // First tile of CTA `cta` of plan_ctas() many (the total for those past them):
 // total * cta / ctas, for fewer than 2^15 CTAs.
 ATTN_HD int plan_begin(int total, int cta, int ctas) {

@@ -12,16 +12,21 @@
 // decoding step are the narrow N side of the instruction and not its M = 128:
 //     S^T [128 keys x 2R] = K [128 x D] * Qp^T,   Qp = R rows hi, R rows lo
 //     O^T [D x 2R]       += V^T [D x 128 keys] * Pp^T
-// with R = 8, 16, 32 or 64 query rows (the queries of a tile times the query
-// heads of one key/value head).  In S^T a thread owns one key, so a block's
-// scales are one factor per thread.  V's scale vs joins the weight:
-//     w_j = 2^(s_j + log2 vs_j - M + 6),   M = max_j (s_j + log2 vs_j),
+// with R = 8, 16 or 32 query rows (the queries of a tile times the query heads
+// of one key/value head); kernel_cache_wide.cuh takes more.  A product of K = 32 takes 64 cycles for any N up
+// to 128 (the 128 rows of the cache's operand have to be read), so the pieces
+// are columns of one product rather than two products into the same columns.
+// In S^T a thread owns one key, so a block's scales are one factor per thread.  V's scale vs joins the weight:
+//     w_j = 2^(s_j + log2 vs_j - M + 4),   M = max_j (s_j + log2 vs_j),
 //     O = (sum_j w_j code_j) / (sum_j w_j / vs_j),
-// so that a row's largest w is near 2^6 whatever the scales and lo's underflow
-// (2^-10) is 2^-16 of it.  M moves only when some w passes 448 (E4M3's largest):
+// so that a row's largest w is near 2^4 whatever the scales and lo's underflow
+// (2^-10) is 2^-14 of it.  M rises only when some w passes 448 (E4M3's largest):
 // then the warpgroup finds the tile's maxima and rescales O^T in tensor memory;
-// otherwise a tile needs one vote of the warpgroup and no reduction.  The sum of
-// w / vs is kept per thread (per key) and reduced at the end.
+// otherwise a tile needs one vote of the warpgroup and no reduction.  M falls
+// where a tile's weights have become too small for E4M3; a look at a tile costs
+// twice its time, so that is looked for on the tile after each rise (a unit's first
+// counts as one), 8 after that and then on every 32nd.
+// The sum of w / vs is kept per thread (per key) and reduced at the end.
 //
 // Roles: warp 0 copies pages (lane i takes page i of a tile) with
 // the tables and scales of the pages ahead already in registers; warp 1
@@ -34,9 +39,8 @@
 // last to leave its piece joins them, in the order of the pieces.
 //
 // What bounds it: one token over a long cache moves 2 bytes per (key, d) pair
-// and is bound by HBM; with R = 64 the exponentials (16 a cycle and SM) and the
-// softmax's issue slots (about 8 instructions a score) come next to the tensor
-// cores.
+// and is bound by HBM; with R = 32 the latency of a tile's steps (products, vote,
+// weights, fences) is longer than its bytes take.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -60,11 +64,11 @@ struct CacheFwdParams {
     float* lse;             // may be null
     int Hq, Sq, group;
     int hper;               // query heads of a unit
-    int hper_inv;           // ceil(2^16 / hper): r / hper = r * hper_inv >> 16 for r < 64
+    int hper_inv;           // ceil(2^16 / hper): r / hper = r * hper_inv >> 16 for r < 128
     int hgroups;            // units that share a key/value head: ceil(group / hper)
     float scale_log2;       // scale * log2(e)
     float* part_o;          // [G][2][R][128] partial sums of w code
-    float2* part_ml;        // [G][2][R] their M - 6 and sum of w / vs
+    float2* part_ml;        // [G][2][R] their M - 4 and sum of w / vs
     // [G]: pieces left of the unit that begins in a CTA, below a number (the upper 48 bits) that marks this
     // launch: whatever stood there before counts as none.  0 again after each join.
     unsigned long long* tickets;
@@ -76,19 +80,22 @@ template <int R>
 struct CacheLayout {
     static constexpr int kWgs = R >= 32 ? 4 : 2;   // softmax warpgroups
     static constexpr int kThreads = 128 + 128 * kWgs;
-    static constexpr int kN = 2 * R;               // columns of S^T and O^T: hi and lo pieces
     static constexpr int kH = R / kWgs;            // rows of one softmax warpgroup
     static constexpr int kCtas = R == 8 ? 2 : 1;   // per SM
-    static constexpr int kStages = R == 8 ? 3 : R == 16 ? 6 : R == 32 ? 5 : 4;
+    static constexpr int kStages = R == 8 ? 3 : R == 16 ? 6 : 5;
+    static constexpr int kN = 2 * R;               // rows of Qp and Pp: hi and lo pieces
+    static constexpr int kWidth = 2 * kH;          // columns of one softmax warpgroup: its rows' hi, then lo pieces
+    // Row r's hi piece in Qp, S^T and O^T; the lo piece is kH further.
+    __host__ __device__ static constexpr int hi_row(int r) { return r / kH * 2 * kH + r % kH; }
     static constexpr uint32_t kTileBytes = 128 * 128;       // 128 keys x 128 bytes
     static constexpr uint32_t kStageBytes = 2 * kTileBytes; // K, V
     static constexpr uint32_t kQ = kStages * kStageBytes;   // 2 x [2R x 128 bytes]
     static constexpr uint32_t kP = kQ + 2 * kN * 128;       // 2 x [2R x 128 keys]
-    static constexpr uint32_t kInfo = kP + 2 * kN * 128;    // per stage: 8 K scales, 8 V scales, bad pages
-    static constexpr uint32_t kInfoBytes = 80;
+    static constexpr uint32_t kInfo = kP + 2 * kN * 128;  // per stage and page: K's scale, log2 of V's, 1 / V's; bad pages
+    static constexpr uint32_t kInfoBytes = 112;
     static constexpr uint32_t kRows = kInfo + kStages * kInfoBytes;  // 2 x [R] CacheRow
     static constexpr uint32_t kUnit = kRows + 2 * R * 16;            // 2 x CacheWork
-    static constexpr uint32_t kTab = kUnit + 2 * 48;                 // [R / 2] float4 {two rows' factors, their 6 - M}
+    static constexpr uint32_t kTab = kUnit + 2 * 48;                 // [R / 2] float4 {two rows' factors, their 4 - M}
     static constexpr uint32_t kFac = kTab + R * 8;                   // [R] float: what l and O are multiplied by
     static constexpr uint32_t kRed = kFac + R * 4;                   // [R][4 warps] float
     static constexpr uint32_t kNanAt = kRed + R * 16;                // 2 x [128] first key with NaN in V's column
@@ -105,13 +112,9 @@ struct CacheLayout {
     static_assert(kInfo % 16 == 0 && kRows % 16 == 0 && kUnit % 16 == 0 && kTab % 16 == 0 && kScan % 8 == 0 && kBars % 8 == 0,
                   "alignment");
     static_assert(kCtas * (kDynamicSmem + 1024) <= 228 * 1024, "shared memory budget");
-    static constexpr uint32_t kTmemCols = 4 * kN;     // S^T twice, O^T twice
-    static_assert(kCtas * kTmemCols <= 512, "tensor memory budget");
-    static constexpr uint32_t kS = 0, kO = 2 * kN;
-    // Rows go through the softmax C at a time; row r of a warpgroup has its hi piece in
-    // column column(r) of the warpgroup's 2H columns, and its lo piece C further.
-    static constexpr int kC = kH < 16 ? kH : 16;
-    __host__ __device__ static constexpr int column(int r) { return r / kC * 2 * kC + r % kC; }
+    static constexpr uint32_t kS = 0, kO = 2 * kN;  // S^T of two tiles, O^T of two units
+    static constexpr uint32_t kTmemCols = kO + 2 * kN;
+    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kCtas * kTmemCols <= 512, "tensor memory budget");
     // Pp^T: R = 8 keeps a row per column (K-major, 128 keys = 128 bytes); else a row per key (MN-major,
     // 2R bytes), where a thread writes its key's codes 16 at a time.
     static constexpr bool kPerKey = R > 8;
@@ -141,9 +144,9 @@ struct CacheShared {
 };
 static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48 && sizeof(CacheShared) <= 64, "shared memory layout");
 
-template <int R>
+template <typename L>
 __device__ __forceinline__ uint32_t cache_bar(uint32_t base, int i) {
-    return base + CacheLayout<R>::kBars + 8u * (uint32_t)i;
+    return base + L::kBars + 8u * (uint32_t)i;
 }
 
 // Sums the plan over the block and finds this CTA's run of tiles; every thread
@@ -175,7 +178,7 @@ __device__ int cache_locate(const CachePlan& p, int* scan, unsigned int* status,
         all += x;
     }
     *total = all;
-    const int ctas = plan_ctas(all, gridDim.x);
+    const int ctas = plan_ctas(p, all, gridDim.x);
     *begin = plan_begin(all, cta, ctas);
     *end = plan_begin(all, cta + 1, ctas);
     const int want = *begin;
@@ -195,13 +198,36 @@ __device__ __forceinline__ bool cache_row(const CacheFwdParams& p, const CacheUn
     return iq < p.plan.qper && *i < u.s.count && g < p.group;
 }
 
+// log2 of a row's largest weight when its maximum M is new.  The weights of the tiles after it may be up to 448 /
+// 2^4 = 28 times that before M has to rise, which scores of unit variance hardly ever ask for (with 2^6 and 7
+// times, a step of 128 rows x 64 keys met it in one of ten).
+constexpr float kCacheRoom = 4.f;
+constexpr float kCacheTop = 448.f;  // E4M3's largest value
+// Where a tile's largest weight is below this, M falls to the tile's maximum: one key far above the rest (a first
+// token that every row attends to) would else leave the rest of a long sequence to lo's underflow, 2^-14 of it.
+constexpr float kCacheLow = 0.25f, kCacheLowLog2 = -2.f;
+// ... but not further than this below the largest M that the row has had: what is left out then is 2^-34 of that
+// key's weight, and no sum passes 2^126 (a weight of 448 over a V scale of 2^-80, 2^17 times, 20 bits up).
+constexpr float kCacheFall = 20.f;
+
+// The maximum that a row with M = had and the largest M so far `peak` takes at a tile whose maximum is `tile`;
+// *moves: it has to.
+__device__ __forceinline__ float cache_new_max(float had, float peak, float tile, bool* moves) {
+    const bool falls = tile > -INFINITY && tile < had + (kCacheLowLog2 - kCacheRoom) && had > peak - kCacheFall;
+    *moves = falls || tile > had + (8.8f - kCacheRoom);  // 2^8.8 < 448
+    return falls ? fmaxf(tile, peak - kCacheFall) : fmaxf(had, tile);
+}
+
+// log2 of the least scale of V that a weight is computed for (values below 4e-22).
+constexpr float kCacheLeastScale = -80.f;
+
 // ---------------------------------------------------------------- warp 0: pages
-template <int R>
+template <typename L>
 __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur,
                                 uint32_t base, uint8_t* smem, volatile int* abort_flag) {
-    using L = CacheLayout<R>;
     const CacheView& c = p.c;
     const int lane = threadIdx.x & 31;
+    const bool leader = ptx::elect_one();
     const int pages = kCacheTile >> c.block_shift;  // of one tile
     const uint64_t lim = p.wait_limit_ns;
     int stage = 0;
@@ -252,16 +278,20 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 next_sc = scales(g, next);
                 ahead = entry(g, window + 64);
             }
-            bool ok = ptx::mbar_wait_call(cache_bar<R>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
+            bool ok = ptx::mbar_wait_call(cache_bar<L>(base, L::kEmpty + stage), phase ^ 1u, abort_flag, p.c.status, lim);
             if (!__all_sync(0xffffffffu, ok)) goto drain;
             const int i = lane - at;
             const bool mine = i >= 0 && i < pages;
-            if (mine) {
-                // A page that is not there is read past the last block, where TMA fills zeros.
-                const int row = block < 0 ? c.num_blocks * c.Hkv : block * c.Hkv + g.hk;
-                const uint32_t dst = base + (uint32_t)stage * L::kStageBytes + (uint32_t)(i << c.block_shift) * 128u;
-                ptx::tma_load_3d(dst, tm_k, cache_bar<R>(base, L::kKFull + stage), 0, 0, row);
-                ptx::tma_load_3d(dst + L::kTileBytes, tm_v, cache_bar<R>(base, L::kVFull + stage), 0, 0, row);
+            // A page that is not there is read past the last block, where TMA fills zeros.  Each page's row goes
+            // to the whole warp, and one lane issues all copies: their operands have to be uniform.
+            const int row = block < 0 ? c.num_blocks * c.Hkv : block * c.Hkv + g.hk;
+            uint32_t dst = base + (uint32_t)stage * L::kStageBytes;
+            for (int x = 0; x < pages; ++x, dst += 128u << c.block_shift) {
+                const int r = __shfl_sync(0xffffffffu, row, at + x);
+                if (leader) {
+                    ptx::tma_load_3d(dst, tm_k, cache_bar<L>(base, L::kKFull + stage), 0, 0, r);
+                    ptx::tma_load_3d(dst + L::kTileBytes, tm_v, cache_bar<L>(base, L::kVFull + stage), 0, 0, r);
+                }
             }
             if (t == u.t) {
                 block2 = more2 ? block_of(g2, u2.t * pages + lane, e2) : -1;
@@ -271,15 +301,17 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
             const uint32_t missing = __ballot_sync(0xffffffffu, mine && block < 0 && window < g.last) >> at;
             float* info = reinterpret_cast<float*>(smem + L::kInfo + stage * L::kInfoBytes);
             if (mine) {
+                const float lvs = fmaxf(ptx::lg2(sc.y), kCacheLeastScale);
                 info[i] = sc.x;
-                info[8 + i] = sc.y;
+                info[8 + i] = lvs;
+                info[16 + i] = ptx::ex2(-lvs);
             }
-            if (lane == 0) reinterpret_cast<int*>(info)[16] = (int)missing;
+            if (leader) reinterpret_cast<int*>(info)[24] = (int)missing;
             __syncwarp();
             // The copies' bytes may come in before they are announced: the phase ends with this arrival at the earliest.
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kKFull + stage), L::kTileBytes);
-                ptx::mbar_arrive_expect_tx(cache_bar<R>(base, L::kVFull + stage), L::kTileBytes);
+            if (leader) {
+                ptx::mbar_arrive_expect_tx(cache_bar<L>(base, L::kKFull + stage), L::kTileBytes);
+                ptx::mbar_arrive_expect_tx(cache_bar<L>(base, L::kVFull + stage), L::kTileBytes);
             }
             pend |= 1u << stage;
             pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
@@ -300,8 +332,8 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
 drain:
     for (int s = 0; s < L::kStages; ++s)
         if (pend & (1u << s)) {
-            ptx::drain_wait(cache_bar<R>(base, L::kKFull + s), (pend_par >> s) & 1u, lim);
-            ptx::drain_wait(cache_bar<R>(base, L::kVFull + s), (pend_par >> s) & 1u, lim);
+            ptx::drain_wait(cache_bar<L>(base, L::kKFull + s), (pend_par >> s) & 1u, lim);
+            ptx::drain_wait(cache_bar<L>(base, L::kVFull + s), (pend_par >> s) & 1u, lim);
         }
 }
 
@@ -319,31 +351,43 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
     const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](int bar, uint32_t par) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<R>(base, bar), par, abort_flag, p.c.status, lim));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<L>(base, bar), par, abort_flag, p.c.status, lim));
         return ok;
     };
-    int stage = 0, g = 0;       // stage and number of the tile whose S^T is next
-    uint32_t phase = 0;
-    int prev_stage = -1, prev_unit = 0, prev_phase = 0;  // the tile whose O^T step is still to come
+    struct Ring {  // a stage and its phase
+        int stage;
+        uint32_t phase;
+        __device__ void next() {
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    };
+    Ring ring{0, 0u}, prev{0, 0u};  // of the tile whose S^T is next, and of the one before
+    int g = 0;                      // number of that tile
+    int prev_unit = -1;             // unit of the tile whose O^T is still to come
     bool prev_first = false, prev_last = false;
     auto issue_pv = [&]() -> bool {  // of tile g - 1
-        const int pb = (g - 1) & 1, ub = prev_unit & 1;
-        if (!wait(L::kVFull + prev_stage, prev_phase)) return false;
+        const int ub = prev_unit & 1;
         if (prev_first && !wait(L::kOFree + ub, ((prev_unit >> 1) & 1) ^ 1)) return false;
-        if (!wait(L::kPFull + pb, ((g - 1) >> 1) & 1)) return false;
+        if (!wait(L::kPFull + ((g - 1) & 1), ((g - 1) >> 1) & 1)) return false;
+        if (!wait(L::kVFull + prev.stage, prev.phase)) return false;
         ptx::tc_fence_after();
-        const uint32_t o = tmem + L::kO + (uint32_t)ub * L::kN, pp = base + L::kP + (uint32_t)pb * L::kN * 128;
-        // V: 32 keys = 32 rows of 128 bytes further per step.  Pp: 32 bytes, or 32 rows.
-        const uint64_t v = ptx::sdesc_rows<128>(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes);
+        const uint32_t o = tmem + L::kO + (uint32_t)(ub * L::kN);
+        const uint32_t pp = base + L::kP + (uint32_t)((g - 1) & 1) * (L::kN * 128);
+        const uint32_t accumulate = prev_first ? 0u : 1u;
+        // V: 32 keys = 32 rows of 128 bytes further per product.  Pp: 32 bytes, or 32 rows.
+        const uint64_t v = ptx::sdesc_rows<128>(base + (uint32_t)prev.stage * L::kStageBytes + L::kTileBytes);
         if (leader) {
             if constexpr (L::kPerKey)
-                ptx::mma_ss_f8_x4<256, 2 * L::kN>(o, v, ptx::sdesc_rows<L::kN>(pp), kIdescO, prev_first ? 0u : 1u);
+                ptx::mma_ss_f8_x4<256, 2 * L::kN>(o, v, ptx::sdesc_rows<L::kN>(pp), kIdescO, accumulate);
             else
-                ptx::mma_ss_f8_x4<256, 2>(o, v, ptx::sdesc_rows<128>(pp), kIdescO, prev_first ? 0u : 1u);
-            ptx::mma_commit(cache_bar<R>(base, L::kEmpty + prev_stage));
-            if (prev_last) ptx::mma_commit(cache_bar<R>(base, L::kOFull + ub));
+                ptx::mma_ss_f8_x4<256, 2>(o, v, ptx::sdesc_rows<128>(pp), kIdescO, accumulate);
+            ptx::mma_commit(cache_bar<L>(base, L::kEmpty + prev.stage));
+            if (prev_last) ptx::mma_commit(cache_bar<L>(base, L::kOFull + ub));
         }
-        prev_stage = -1;
+        prev_unit = -1;
         return true;
     };
     for (int unit = 0; ok; ++unit) {
@@ -351,18 +395,18 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
         if (!wait(L::kQFull + ub, (unit >> 1) & 1)) break;
         const int n = __shfl_sync(0xffffffffu, reinterpret_cast<const CacheWork*>(smem + L::kUnit)[ub].n, 0);
         if (n == 0) break;
+        const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
         for (int k = 0; k < n; ++k, ++g) {
             const int sb = g & 1;
             // While this tile's K is still on its way, the last tile's O^T goes first.
-            if (prev_stage >= 0 && !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<R>(base, L::kKFull + stage), phase)) &&
+            if (prev_unit >= 0 && !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<L>(base, L::kKFull + ring.stage), ring.phase)) &&
                 !issue_pv())
                 break;
-            // The buffer of S^T is free: every warp has written the weights of tile g - 2, whose O^T step is issued.
-            if (!wait(L::kKFull + stage, phase)) break;
+            // The buffer of S^T is free: every warp has written the weights of tile g - 2, whose O^T is issued.
+            if (!wait(L::kKFull + ring.stage, ring.phase)) break;
             ptx::tc_fence_after();
-            const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes);
-            const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
-            const uint32_t st = tmem + L::kS + (uint32_t)sb * L::kN;
+            const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)ring.stage * L::kStageBytes);
+            const uint32_t st = tmem + L::kS + (uint32_t)(sb * L::kN);
             if (leader) {
                 if (wide) {
                     ptx::mma_ss_f8_x4<2, 2>(st, a, b, kIdescS, 0u);
@@ -370,25 +414,21 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
                     ptx::mma_ss_f8(st, a, b, kIdescS, 0u);
                     ptx::mma_ss_f8(st, a + 2, b + 2, kIdescS, 1u);
                 }
-                ptx::mma_commit(cache_bar<R>(base, L::kSFull + sb));
-                if (k == n - 1) ptx::mma_commit(cache_bar<R>(base, L::kQEmpty + ub));
+                ptx::mma_commit(cache_bar<L>(base, L::kSFull + sb));
+                if (k + 1 == n) ptx::mma_commit(cache_bar<L>(base, L::kQEmpty + ub));
             }
-            if (prev_stage >= 0 && !issue_pv()) break;
-            prev_stage = stage;
-            prev_phase = (int)phase;
+            if (prev_unit >= 0 && !issue_pv()) break;
+            prev = ring;
+            ring.next();
             prev_unit = unit;
             prev_first = k == 0;
-            prev_last = k == n - 1;
-            if (++stage == L::kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            prev_last = k + 1 == n;
         }
     }
-    if (ok && prev_stage >= 0) issue_pv();
+    if (ok && prev_unit >= 0) issue_pv();
     if (leader) {
-        ptx::mma_commit(cache_bar<R>(base, L::kDrain));
-        ptx::drain_wait(cache_bar<R>(base, L::kDrain), 0u, lim);
+        ptx::mma_commit(cache_bar<L>(base, L::kDrain));
+        ptx::drain_wait(cache_bar<L>(base, L::kDrain), 0u, lim);
     }
 }
 
@@ -424,7 +464,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
         const int ub = unit & 1;
         const bool more = cursor_next(p.plan, cur, u);
         if (more) load(u, row0);
-        const bool ok = ptx::mbar_wait_call(cache_bar<R>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
+        const bool ok = ptx::mbar_wait_call(cache_bar<L>(base, L::kQEmpty + ub), ((unit >> 1) & 1) ^ 1, abort_flag, p.c.status,
                                        p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, ok)) return;
         CacheWork* work = reinterpret_cast<CacheWork*>(smem + L::kUnit) + ub;
@@ -455,14 +495,14 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
                         lo[e >> 1] |= e4m3_pair(a - hf.x, b - hf.y) << (16 * (e & 1));
                     }
                     if (r < R) {
-                        const int n = (r / L::kH) * 2 * L::kH + L::column(r % L::kH);
+                        const int n = L::hi_row(r);
                         uint8_t* q8 = smem + L::kQ + ub * L::kN * 128;
                         auto put = [&](int row, const uint32_t* c) {
                             *reinterpret_cast<uint2*>(q8 + row * 128 + (((part >> 1) ^ (row & 7)) << 4) + (part & 1) * 8) =
                                 make_uint2(c[0], c[1]);
                         };
                         put(n, hi);
-                        put(n + L::kC, lo);
+                        put(n + L::kH, lo);
                         if (part == 0) rows[r] = CacheRow{at[k] >= 0 ? scale * p.scale_log2 : 0.f, seen[k], at[k]};
                     }
                 }
@@ -488,12 +528,39 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(cache_bar<R>(base, L::kQFull + ub));
+        if (lane == 0) ptx::mbar_arrive(cache_bar<L>(base, L::kQFull + ub));
         if (!more) return;
     }
 }
 
 // ---------------------------------------------------------------- warps 4 on: softmax
+// Takes NaN codes out of a key's 128 bytes of V (at `line`, row `row` of a tile)
+// and lowers at[d] to the key for each; true if there were any.
+__device__ __noinline__ bool cache_take_nan(uint32_t line, int row, int key, int* at) {
+    bool found = false;
+#pragma unroll 1
+    for (int x = 0; x < 8; ++x) {
+        const uint4 v = ptx::ld_shared_v4(line + 16 * x);
+        uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        bool here = false;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            // 0x7f in a byte's low bits: adding 1 to them carries into its top bit
+            uint32_t hit = ((word[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            if (hit) here = true;
+            while (hit) {
+                const int b = (__ffs(hit) - 1) >> 3;
+                hit &= hit - 1;
+                word[y] &= ~(0xffu << (8 * b));
+                atomicMin(at + (x ^ (row & 7)) * 16 + y * 4 + b, key);
+            }
+        }
+        if (here) ptx::st_shared_v4(line + 16 * x, word[0], word[1], word[2], word[3]);
+        found |= here;
+    }
+    return found;
+}
+
 // Adds each of a warp's H rows over its lanes; lane i returns the sum of row
 // i / (32 / H).  Half of the rows change hands in the first step, a quarter in the next.
 template <int H>
@@ -518,14 +585,11 @@ template <int R>
 __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
                                    volatile int* abort_flag) {
     using L = CacheLayout<R>;
-    constexpr int H = L::kH, C = L::kC;
-    constexpr float kTop = 448.f;        // E4M3's largest value
-    constexpr float kRoom = 6.f;         // log2 of a row's largest weight when its maximum is new
-    constexpr float kLeastScale = -80.f; // log2 of the least scale of V that a weight is computed for
+    constexpr int H = L::kH, W = L::kWidth;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wg = (warp - 4) >> 2, wq = warp & 3;
     const int j = wq * 32 + lane;  // this thread's key of a tile (lane of S^T) and its d (lane of O^T)
-    const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * 2 * H);
+    const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(wg * W);
     const uint64_t lim = p.wait_limit_ns;
     float4* tab = reinterpret_cast<float4*>(smem + L::kTab) + wg * (H / 2);
     float* fac = reinterpret_cast<float*>(smem + L::kFac) + wg * H;
@@ -535,17 +599,16 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
     // results, so that it meets its warpgroup at every barrier and nobody is left there.
     bool alive = true;
     auto wait = [&](int which, uint32_t par) {
-        if (alive) alive = ptx::mbar_wait_call(cache_bar<R>(base, which), par, abort_flag, p.c.status, lim);
+        if (alive) alive = ptx::mbar_wait_call(cache_bar<L>(base, which), par, abort_flag, p.c.status, lim);
         __syncwarp();
     };
     auto arrive = [&](int which) {
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(cache_bar<R>(base, which));
+        if (lane == 0) ptx::mbar_arrive(cache_bar<L>(base, which));
     };
     const int page = j >> p.c.block_shift;  // of a tile
     int g = 0, stage = 0;   // number and stage of the current tile
-    uint32_t nan_phase = 0; // bit ub: phase of barrier kNan + ub
-    uint32_t phase = 0;
+    uint32_t phase = 0, nan_phase = 0;  // nan_phase, bit ub: phase of barrier kNan + ub
     float l[H];  // this thread's keys' part of the rows' sums of w / vs
     for (int unit = 0;; ++unit) {
         const int ub = unit & 1;
@@ -572,191 +635,157 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 #pragma unroll
         for (int r = 0; r < H; ++r) l[r] = 0.f;
         bool todo = true;  // some row that sees keys has no maximum yet
+        float peak = -INFINITY;       // the largest maximum that row `lane` has had
+        int look_at = 0, look_gap = 8;  // the next tile where the maxima are looked at anyhow, and how far the one after
 
         for (int k = 0; k < work.n; ++k, ++g) {
-            const int t = work.t + k, sb = g & 1;
-            // S^T is there; so are the scales beside K, which were written before it, and the O^T step of
-            // tile g - 2 is done, which came before it: its buffer of Pp is free.
+            const int sb = g & 1;
+            // S^T is there; so are the scales beside K, which were written before it, and the O^T of tile g - 2
+            // is done, which came before it: its buffer of Pp is free.
             wait(L::kSFull + sb, (g >> 1) & 1);
             ptx::tc_fence_after();
             const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
-            const float ks = info[page], lvs = fmaxf(ptx::lg2(info[8 + page]), kLeastScale), ivs = ptx::ex2(-lvs);
-            const int missing = reinterpret_cast<const int*>(info)[16];
-            const int key = t * kCacheTile + j;
-            const bool full = (t + 1) * kCacheTile <= work.keys_all && missing == 0;
-            const bool here = key < work.keys && !((missing >> page) & 1);
-            if ((t + 1) * kCacheTile > work.keys_all && wg == 0) {
+            const int missing = reinterpret_cast<const int*>(info)[24];
+            const int key = (work.t + k) * kCacheTile + j;
+            const float ks = info[page], lvs = info[8 + page], ivs = info[16 + page];
+            const bool some = (work.t + k + 1) * kCacheTile > work.keys_all;  // some row does not see some key
+            const bool full = !some && missing == 0, here = key < work.keys && !((missing >> page) & 1);
+            if (some && wg == 0) {
                 // A weight of 0 times NaN is NaN: keys that nobody sees become 0 in V, and NaN that only
                 // some rows see is taken out and noted by the first position that has it.
                 wait(L::kVFull + stage, phase);
                 const uint32_t line = base + (uint32_t)stage * L::kStageBytes + L::kTileBytes + (uint32_t)j * 128u;
                 if (alive && key >= work.keys) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) ptx::st_shared_v4(line + 16 * x, 0, 0, 0, 0);
+                    for (int y = 0; y < 8; ++y) ptx::st_shared_v4(line + 16 * y, 0, 0, 0, 0);
                 } else if (alive && key >= work.keys_all) {
-#pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 v = ptx::ld_shared_v4(line + 16 * x);
-                        uint32_t word[4] = {v.x, v.y, v.z, v.w};
-                        bool found = false;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            // 0x7f in a byte's low bits: adding 1 to them carries into its top bit
-                            uint32_t hit = ((word[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            if (hit) found = true;
-                            while (hit) {
-                                const int b = (__ffs(hit) - 1) >> 3;
-                                hit &= hit - 1;
-                                word[y] &= ~(0xffu << (8 * b));
-                                atomicMin(nan_at + (x ^ (j & 7)) * 16 + y * 4 + b, key);
-                            }
-                        }
-                        if (found) {
-                            *nan_seen = 1;
-                            ptx::st_shared_v4(line + 16 * x, word[0], word[1], word[2], word[3]);
-                        }
-                    }
+                    if (cache_take_nan(line, j, key, nan_at)) *nan_seen = 1;
                 }
             }
             if (!idle) {
-                const uint32_t s_addr = my_tmem + L::kS + (uint32_t)sb * L::kN;
-                const uint32_t p_line = base + L::kP + (uint32_t)sb * L::kN * 128u;
-                const uint64_t ks2 = ptx::f2(ks, ks), ivs2 = ptx::f2(ivs, ivs);
-                auto sees = [&](int r) { return here && key < rows[r].keys; };
+                const uint32_t s_addr = my_tmem + L::kS + (uint32_t)(sb * L::kN);
+                const uint32_t p_tile = base + L::kP + (uint32_t)sb * (L::kN * 128);
                 // The weights of this thread's key for every row, into Pp; returns the largest.  `add`: the
                 // rows whose sum takes them.
                 auto pass = [&](auto masked, uint32_t add) {
+                    constexpr bool kMasked = decltype(masked)::value;
                     float top = 0.f;
+                    uint32_t s[W];
+                    ptx::tmem_load<W>(s_addr, s);
+                    const uint64_t ks2 = ptx::f2(ks, ks), ivs2 = ptx::f2(ivs, ivs), lvs2 = ptx::f2(lvs, lvs);
+                    const uint64_t minus = ptx::f2(-1.f, -1.f);
+                    uint32_t hi[H / 2], lo[H / 2];
 #pragma unroll
-                    for (int c = 0; c < H; c += C) {
-                        uint32_t s[2 * C];
-                        ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
-                        uint32_t hi[C / 2], lo[C / 2];
-#pragma unroll
-                        for (int i = 0; i < C; i += 2) {
-                            const int r = c + i;
-                            const float4 f = tab[r / 2];
-                            const uint64_t x = ptx::mul2(ptx::add2(ptx::f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                                                   ptx::f2(__uint_as_float(s[C + i]), __uint_as_float(s[C + i + 1]))),
-                                                         ks2);
-                            const uint64_t y = ptx::fma2(x, ptx::f2(f.x, f.y), ptx::f2(f.z + lvs, f.w + lvs));
-                            float y0, y1;
-                            ptx::f2_split(y, y0, y1);
-                            if (decltype(masked)::value) {
-                                y0 = sees(r) ? y0 : -INFINITY;
-                                y1 = sees(r + 1) ? y1 : -INFINITY;
-                            }
-                            const float w0 = ptx::ex2(y0), w1 = ptx::ex2(y1);
-                            top = ptx::max3(top, w0, w1);
-                            const uint64_t w = ptx::f2(w0, w1);
-                            float l0 = l[r], l1 = l[r + 1];
-                            ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l0, l1)), l0, l1);
-                            if (!decltype(masked)::value || add == ~0u || (add >> r & 1)) l[r] = l0;
-                            if (!decltype(masked)::value || add == ~0u || (add >> (r + 1) & 1)) l[r + 1] = l1;
-                            // hi: w at 4 significant bits, to nearest (w (2^20 + 1) less its own excess over w)
-                            const uint64_t big = ptx::mul2(w, ptx::f2(1048577.f, 1048577.f));
-                            const uint64_t minus = ptx::f2(-1.f, -1.f);
-                            const uint64_t h = ptx::fma2(ptx::fma2(w, minus, big), minus, big);
-                            float h0, h1, r0, r1;
-                            ptx::f2_split(h, h0, h1);
-                            ptx::f2_split(ptx::fma2(h, minus, w), r0, r1);
-                            hi[i / 2] = e4m3_pair(h0, h1);
-                            lo[i / 2] = e4m3_pair(r0, r1);
+                    for (int r = 0; r < H; r += 2) {
+                        const float4 f = tab[r / 2];
+                        uint64_t z = ptx::f2(__uint_as_float(s[r]), __uint_as_float(s[r + 1]));
+                        z = ptx::add2(z, ptx::f2(__uint_as_float(s[H + r]), __uint_as_float(s[H + r + 1])));
+                        z = ptx::fma2(ptx::mul2(z, ks2), ptx::f2(f.x, f.y), ptx::add2(ptx::f2(f.z, f.w), lvs2));
+                        float y0, y1;
+                        ptx::f2_split(z, y0, y1);
+                        if constexpr (kMasked) {
+                            y0 = here && key < rows[r].keys ? y0 : -INFINITY;
+                            y1 = here && key < rows[r + 1].keys ? y1 : -INFINITY;
                         }
-                        if constexpr (L::kPerKey) {
-                            // 2C bytes of this key's row: C hi codes, then C lo codes
-                            constexpr uint32_t kTurn = L::kN == 128 ? 0 : L::kN == 64 ? 1 : 2;  // key bits that swizzle
-                            const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
-                            auto piece = [&](uint32_t i) { return p_line + (uint32_t)j * L::kN + ((i ^ turn) << 4); };
-                            const uint32_t i0 = (uint32_t)(wg * 2 * H + 2 * c) / 16;
-                            auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
-                            if constexpr (C == 16) {
-                                ptx::st_shared_v4(piece(i0), four(hi), four(hi + 2), four(hi + 4), four(hi + 6));
-                                ptx::st_shared_v4(piece(i0 + 1), four(lo), four(lo + 2), four(lo + 4), four(lo + 6));
-                            } else {
-                                ptx::st_shared_v4(piece(i0), four(hi), four(hi + 2), four(lo), four(lo + 2));
-                            }
-                        } else {
-                            auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's eight
-                                ptx::st_shared_u8(p_line + (uint32_t)(wg * 2 * H + n) * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4) +
-                                                      (uint32_t)(j & 15),
-                                                  code);
-                            };
+                        const float w0 = ptx::ex2(y0), w1 = ptx::ex2(y1);
+                        top = ptx::max3(top, w0, w1);
+                        const uint64_t w = ptx::f2(w0, w1);
+                        float l0, l1;
+                        ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l[r], l[r + 1])), l0, l1);
+                        if (!kMasked || add >> r & 1) l[r] = l0;
+                        if (!kMasked || add >> (r + 1) & 1) l[r + 1] = l1;
+                        // hi: w at 4 significant bits, to nearest; lo: the rest
+                        const float h0 = __uint_as_float((__float_as_uint(w0) + 0x80000u) & 0xfff00000u);
+                        const float h1 = __uint_as_float((__float_as_uint(w1) + 0x80000u) & 0xfff00000u);
+                        float r0, r1;
+                        ptx::f2_split(ptx::fma2(ptx::f2(h0, h1), minus, w), r0, r1);
+                        hi[r / 2] = e4m3_pair(h0, h1);
+                        lo[r / 2] = e4m3_pair(r0, r1);
+                    }
+                    auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
+                    if constexpr (L::kPerKey) {
+                        constexpr uint32_t kTurn = L::kN == 64 ? 1 : 2;  // key bits that swizzle
+                        const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
+                        ptx::st_shared_v4(p_tile + (uint32_t)j * L::kN + (((uint32_t)wg ^ turn) << 4), four(hi), four(hi + 2),
+                                          four(lo), four(lo + 2));
+                    } else {
+                        auto put = [&](int n, uint32_t code) {  // n: row of the warpgroup's eight
+                            ptx::st_shared_u8(p_tile + (uint32_t)(wg * 2 * H + n) * 128u + (((uint32_t)(j >> 4) ^ (uint32_t)(n & 7)) << 4) +
+                                                  (uint32_t)(j & 15),
+                                              code);
+                        };
 #pragma unroll
-                            for (int i = 0; i < C; i += 2) {
-                                put(i, hi[i / 2]);
-                                put(i + 1, hi[i / 2] >> 8);
-                                put(C + i, lo[i / 2]);
-                                put(C + i + 1, lo[i / 2] >> 8);
-                            }
+                        for (int r = 0; r < H; r += 2) {
+                            put(r, hi[r / 2]);
+                            put(r + 1, hi[r / 2] >> 8);
+                            put(H + r, lo[r / 2]);
+                            put(H + r + 1, lo[r / 2] >> 8);
                         }
                     }
                     return top;
                 };
-                // First as it stands; once more when a maximum has to move, or only so while a row has none.
+                // First as it stands; once more when a maximum has to rise.  The maxima come first while a row has
+                // none, and on a tile now and then.
                 uint32_t add = ~0u;
-                for (bool move = todo;;) {
-                    if (move) {
-                        // The rows' maxima move: of s + log2 vs over the tile, through the order of the bit patterns.
-#pragma unroll 1
-                        for (int c = 0; c < H; c += C) {
-                            uint32_t s[2 * C];
-                            ptx::tmem_load<2 * C>(s_addr + 2 * c, s);
+                bool passed = false;
+                for (bool look = todo || k == look_at;;) {
+                    if (look) {
+                        // The rows' maxima of s + log2 vs over the tile, through the order of the bit patterns.
+                        uint32_t s[W];
+                        ptx::tmem_load<W>(s_addr, s);
 #pragma unroll
-                            for (int i = 0; i < C; ++i) {
-                                float y = fmaf((__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * ks, rows[c + i].factor, lvs);
-                                if (!full) y = sees(c + i) ? y : -INFINITY;
-                                const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
-                                if (lane == c + i) red[(c + i) * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-                            }
+                        for (int r = 0; r < H; ++r) {
+                            const float z = fmaf((__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks, rows[r].factor, lvs);
+                            const float y = fmaxf(full || (here && key < rows[r].keys) ? z : -INFINITY, -INFINITY);
+                            const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+                            if (lane == r) red[r * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
                         }
                         ptx::bar_sync(bar, 128);
                         // Every warp works out the same new maxima, a row per lane.
-                        float f = 1.f;
-                        bool open = false;
+                        bool open = false, moves = false;
                         float m = -INFINITY;
                         if (lane < H) {
-                            const float had = row_max;
                             const float4 x = reinterpret_cast<const float4*>(red)[lane];
-                            m = had;
-                            if (rows[lane].at >= 0) m = fmaxf(fmaxf(fmaxf(m, x.x), fmaxf(x.y, x.z)), x.w);
-                            f = had == -INFINITY ? 0.f : ptx::ex2(had - m);
-                            open = m == -INFINITY && rows[lane].at >= 0 && rows[lane].keys > 0;
+                            const bool used = rows[lane].at >= 0;
+                            m = cache_new_max(row_max, peak, used ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : -INFINITY, &moves);
+                            open = m == -INFINITY && used && rows[lane].keys > 0;
                         }
-                        // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
-                        const uint32_t anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
-                        if (!todo) add = anew;
                         todo = __any_sync(0xffffffffu, open);
-                        row_max = m;
-                        if (wq == 0 && lane < H) {
-                            fac[lane] = f;
-                            reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kRoom - m;
-                        }
-                        ptx::bar_sync(bar, 128);
-#pragma unroll
-                        for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
-                        if (k > 0) {
-                            // the O^T step of the tile before is done: its stage is empty
-                            wait(L::kEmpty + (stage == 0 ? L::kStages : stage) - 1, stage == 0 ? phase ^ 1u : phase);
-                            ptx::tc_fence_after();
-                            const uint32_t o_addr = my_tmem + L::kO + (uint32_t)ub * L::kN;
-#pragma unroll 1
-                            for (int c = 0; c < H; c += C) {
-                                uint32_t s[2 * C];
-                                ptx::tmem_load<2 * C>(o_addr + 2 * c, s);
-#pragma unroll
-                                for (int i = 0; i < C; ++i) {
-                                    const float x = fac[c + i];
-                                    s[i] = __float_as_uint(__uint_as_float(s[i]) * x);
-                                    s[C + i] = __float_as_uint(__uint_as_float(s[C + i]) * x);
-                                }
-                                ptx::tmem_store<2 * C>(o_addr + 2 * c, s);
+                        const bool moved = __any_sync(0xffffffffu, moves), rises = __any_sync(0xffffffffu, moves && m > row_max);
+                        uint32_t anew = 0;
+                        if (moved) {
+                            // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
+                            const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
+                            anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
+                            if (passed) add = anew;
+                            row_max = m;
+                            peak = fmaxf(peak, m);
+                            if (wq == 0 && lane < H) {
+                                fac[lane] = f;
+                                reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kCacheRoom - m;
                             }
                         }
+                        ptx::bar_sync(bar, 128);  // `red` may be written again, and the new factors read
+                        if (moved) {
+#pragma unroll
+                            for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
+                            if (k > 0) {
+                                // the tile before is through the tensor core once its stage is empty
+                                wait(L::kEmpty + (stage == 0 ? L::kStages : stage) - 1, stage == 0 ? phase ^ 1u : phase);
+                                ptx::tc_fence_after();
+                                const uint32_t o_addr = my_tmem + L::kO + (uint32_t)(ub * L::kN);
+                                ptx::tmem_load<W>(o_addr, s);
+#pragma unroll
+                                for (int i = 0; i < W; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * fac[i % H]);
+                                ptx::tmem_store<W>(o_addr, s);
+                            }
+                        }
+                        look_at = k + (rises ? 1 : look_gap);
+                        if (!rises) look_gap = 32;
                     }
-                    const float top = move || !full ? pass(std::true_type(), add) : pass(std::false_type(), ~0u);
-                    if (move || !ptx::bar_any(bar, 128, top > kTop)) break;
-                    move = true;
+                    const float top = passed || !full ? pass(std::true_type(), add) : pass(std::false_type(), ~0u);
+                    if (look || !ptx::bar_any(bar, 128, top > kCacheTop)) break;
+                    passed = look = true;
                 }
                 ptx::tc_fence_before();
             }
@@ -787,7 +816,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         const long long slot = (long long)blockIdx.x * 2 + work.slot;
         if (!idle && j < H) {
             const float4 x = reinterpret_cast<const float4*>(red)[j];
-            const float sum = x.x + x.y + (x.z + x.w), m = row_max - kRoom;
+            const float sum = x.x + x.y + (x.z + x.w), m = row_max - kCacheRoom;
             float f = 1.f;
             if (work.slot < 0) {
                 f = sum == 0.f ? 0.f : ptx::rcp(sum);
@@ -803,22 +832,18 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         ptx::tc_fence_after();
         if (!idle) {
             const int first_nan = nan ? nan_at[j] : 0x7fffffff;
-#pragma unroll 1
-            for (int c = 0; c < H; c += C) {
-                uint32_t s[2 * C];
-                ptx::tmem_load<2 * C>(my_tmem + L::kO + (uint32_t)ub * L::kN + 2 * c, s);
-                if (alive && j < p.c.D) {
+            uint32_t s[W];
+            ptx::tmem_load<W>(my_tmem + L::kO + (uint32_t)(ub * L::kN), s);
+            if (alive && j < p.c.D) {
 #pragma unroll
-                    for (int i = 0; i < C; ++i) {
-                        const int r = c + i;
-                        const CacheRow row = rows[r];
-                        float o = (__uint_as_float(s[i]) + __uint_as_float(s[C + i])) * fac[r];
-                        if (first_nan < row.keys) o = NAN;
-                        if (work.slot >= 0)
-                            p.part_o[(slot * R + wg * H + r) * 128 + j] = o;
-                        else if (row.at >= 0)
-                            p.out[row.at * p.c.D + j] = __float2bfloat16(o);
-                    }
+                for (int r = 0; r < H; ++r) {
+                    const CacheRow row = rows[r];
+                    float o = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * fac[r];
+                    if (first_nan < row.keys) o = NAN;
+                    if (work.slot >= 0)
+                        p.part_o[(slot * R + wg * H + r) * 128 + j] = o;
+                    else if (row.at >= 0)
+                        p.out[row.at * p.c.D + j] = __float2bfloat16(o);
                 }
             }
         }
@@ -842,50 +867,75 @@ __device__ __noinline__ bool cache_last_piece(unsigned long long* at, unsigned l
     return true;
 }
 
-// Joins a row's pieces, a warp per row: O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
-// They are slot 1 of the first CTA and slot 0 of the following ones.
-template <int R>
-__device__ void cache_join_row(const CacheFwdParams& p, const CacheShared& shared, int r, long long at) {
-    constexpr int kBatch = 8;  // pieces under way at once
+// Joins rows r, r + 1, ... of a shared unit (`count` of them, a warp for all):
+// O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i over the pieces, which are slot 1 of the first CTA and slot 0 of the
+// following ones, R rows each.
+__device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shared, int R, int r, int count) {
+    constexpr int kBatch = 4;  // rows under way at once
     const int lane = threadIdx.x & 31, n = shared.pieces;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int x0 = 0; x0 < n; x0 += kBatch) {
-        float2 ml[kBatch];
-        float4 v[kBatch];
-        float top = m;
+    for (; count > 0; r += kBatch, count -= kBatch) {
+        float m[kBatch], l[kBatch];
+        float4 o[kBatch];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            ml[x] = make_float2(-INFINITY, 0.f);
-            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + x < n) {
-                const long long from = ((long long)(shared.first + x0 + x) * 2 + (x0 + x == 0 ? 1 : 0)) * R + r;
-                ml[x] = __ldcg(p.part_ml + from);
-                if (lane * 4 < p.c.D) v[x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * 128) + lane);
+        for (int y = 0; y < kBatch; ++y) {
+            m[y] = -INFINITY;
+            l[y] = 0.f;
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 2
+        for (int x = 0; x < n; ++x) {
+            const long long from = ((long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0)) * R + r;
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                ml[y] = make_float2(-INFINITY, 0.f);
+                v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (y < count) {
+                    ml[y] = __ldcg(p.part_ml + from + y);
+                    if (lane * 4 < p.c.D) v[y] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (from + y) * 128) + lane);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                const float top = fmaxf(m[y], ml[y].x), ref = top == -INFINITY ? 0.f : top;
+                const float keep = ptx::ex2(m[y] - ref), f = ptx::ex2(ml[y].x - ref);
+                m[y] = top;
+                l[y] = l[y] * keep + f * ml[y].y;
+                o[y].x = o[y].x * keep + f * v[y].x;
+                o[y].y = o[y].y * keep + f * v[y].y;
+                o[y].z = o[y].z * keep + f * v[y].z;
+                o[y].w = o[y].w * keep + f * v[y].w;
             }
         }
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
-        const float ref = top == -INFINITY ? 0.f : top, keep = ptx::ex2(m - ref);
-        l *= keep;
-        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-        m = top;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const float f = ptx::ex2(ml[x].x - ref);
-            l += f * ml[x].y;
-            o.x += f * v[x].x;
-            o.y += f * v[x].y;
-            o.z += f * v[x].z;
-            o.w += f * v[x].w;
+        for (int y = 0; y < kBatch; ++y) {
+            int qi, hq;
+            if (y >= count || !cache_row(p, shared.u, r + y, &qi, &hq)) continue;
+            const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
+            const float inv = l[y] == 0.f ? 0.f : ptx::rcp(l[y]);
+            if (lane * 4 < p.c.D)
+                *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
+                    make_uint2(ptx::pack_bf16x2(o[y].x * inv, o[y].y * inv), ptx::pack_bf16x2(o[y].z * inv, o[y].w * inv));
+            if (lane == 0 && p.lse != nullptr) p.lse[at] = l[y] == 0.f ? -INFINITY : (m[y] + ptx::lg2(l[y])) * kLn2;
         }
     }
-    const float inv = l == 0.f ? 0.f : ptx::rcp(l);
-    if (lane * 4 < p.c.D)
-        *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
-            make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-    if (lane == 0 && p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
+}
+
+// The end of a CTA, by all its threads, once every piece is left: of each unit that it shares, whoever counts
+// last joins the pieces.
+template <typename F>
+__device__ void cache_join(const CacheFwdParams& p, CacheShared* shared, bool aborted, F join) {
+    if (shared[0].pieces == 0 && shared[1].pieces == 0) return;
+    if (threadIdx.x < 2) {
+        CacheShared& x = shared[threadIdx.x];
+        __threadfence();
+        x.last = x.pieces > 0 && !aborted && cache_last_piece(p.tickets + x.first, p.ticket, x.pieces);
+        __threadfence();
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x)
+        if (shared[x].pieces > 0 && shared[x].last) join(shared[x]);
 }
 
 template <int R>
@@ -903,20 +953,20 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
-            ptx::mbar_init(cache_bar<R>(base, L::kKFull + s), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kVFull + s), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kEmpty + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kKFull + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kVFull + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kEmpty + s), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(cache_bar<R>(base, L::kQFull + i), 2);    // the query warps
-            ptx::mbar_init(cache_bar<R>(base, L::kQEmpty + i), 4 * L::kWgs + 1);  // the softmax warps and the last S^T product
-            ptx::mbar_init(cache_bar<R>(base, L::kSFull + i), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kPFull + i), 4 * L::kWgs);
-            ptx::mbar_init(cache_bar<R>(base, L::kOFull + i), 1);
-            ptx::mbar_init(cache_bar<R>(base, L::kOFree + i), 4 * L::kWgs);
-            ptx::mbar_init(cache_bar<R>(base, L::kNan + i), 4);      // softmax warpgroup 0
+            ptx::mbar_init(cache_bar<L>(base, L::kQFull + i), 2);    // the query warps
+            ptx::mbar_init(cache_bar<L>(base, L::kQEmpty + i), 4 * L::kWgs + 1);  // the softmax warps and the last S^T product
+            ptx::mbar_init(cache_bar<L>(base, L::kSFull + i), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kPFull + i), 4 * L::kWgs);
+            ptx::mbar_init(cache_bar<L>(base, L::kOFull + i), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kOFree + i), 4 * L::kWgs);
+            ptx::mbar_init(cache_bar<L>(base, L::kNan + i), 4);      // softmax warpgroup 0
         }
-        ptx::mbar_init(cache_bar<R>(base, L::kDrain), 1);
+        ptx::mbar_init(cache_bar<L>(base, L::kDrain), 1);
         *abort_flag = 0;
         for (int x = 0; x < 2; ++x) reinterpret_cast<CacheShared*>(smem + L::kShared)[x].pieces = 0;
         ptx::fence_barrier_init();
@@ -938,7 +988,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     if (begin == end) {
         // no tile for this CTA
     } else if (warp == 0) {
-        cache_load_role<R>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
     } else if (warp == 1) {
         cache_mma_role<R>(p, base, smem, tmem, abort_flag);
     } else if (warp < 4) {
@@ -953,23 +1003,11 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-    // Every piece of this CTA is left.  Of each unit that it shares, whoever counts last joins the pieces.
-    CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared);
-    if (shared[0].pieces == 0 && shared[1].pieces == 0) return;
-    if (threadIdx.x < 2) {
-        CacheShared& x = shared[threadIdx.x];
-        __threadfence();
-        x.last = x.pieces > 0 && *abort_flag == 0 && cache_last_piece(p.tickets + x.first, p.ticket, x.pieces);
-        __threadfence();
-    }
-    __syncthreads();
-    for (int i = warp; i < 2 * R; i += L::kThreads / 32) {
-        const CacheShared& x = shared[i / R];
-        const int row = i % R;
-        int qi, hq;
-        if (x.pieces > 0 && x.last && cache_row(p, x.u, row, &qi, &hq))
-            cache_join_row<R>(p, x, row, ((long long)x.u.b * p.Hq + hq) * p.Sq + qi);
-    }
+    cache_join(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0, [&](const CacheShared& x) {
+        constexpr int kWarps = L::kThreads / 32, kPer = (R + kWarps - 1) / kWarps;
+        const int first = warp * kPer;
+        if (first < R) cache_join_rows(p, x, R, first, min(kPer, R - first));
+    });
 }
 
 }  // namespace attn

@@ -1,0 +1,518 @@
+// kernel_cache_wide.cuh -- attention over the 8-bit cache for many query rows:
+// the rows are the tensor core's M.
+//
+// With more than a few rows a tile's exponentials come before its bytes, and the
+// row-per-column form of kernel_cache_fwd.cuh, where 128 threads vote on a
+// maximum for every few scores, is bound by the latency of its steps.  Here a
+// thread owns a query row of a tile of 128 and sees all its scores:
+//     S [128 rows x 128 keys]  = Qhi K^T + Qlo K^T     (both pieces into the same columns)
+//     O [128 rows x D]        += Phi V  + Plo V        (P as an operand in tensor memory)
+// so the running maximum, the sum and the rescaling of O are the thread's own,
+// without a barrier between warps.  Everything else -- the pieces of q and of the
+// weights, V's scale within the weight, the plan and the join -- is as there.
+//
+// A CTA is one warpgroup of softmax, a warp that copies pages and a warp that
+// issues products; two CTAs share an SM.  A step is 64 keys, half a tile: the
+// products of one half run while the other half's weights are worked out.
+// Tensor memory of a CTA: S of two halves [0, 64), [64, 128), O [128, 256); the
+// weights' codes, four a column, replace the scores they came from (hi in a
+// half's columns 0-15, lo in 16-31).
+//
+// What bounds it, per 128 rows x 64 keys: two softmax warps a scheduler, each about
+// 600 issue slots of weights (1250 cycles side by side) and 700 cycles of waits,
+// vote, fences and tensor memory around them; the products take 640 of those 1900.
+// 2 x 1024 tokens at the end of 8192, 32 heads over 8, D = 128: 276 us, 934
+// TFLOP/s counted once per product (the two pieces make it twice that).
+#pragma once
+
+#include <type_traits>
+
+#include "kernel_cache_fwd.cuh"
+
+namespace attn {
+
+struct CacheWideLayout {
+    static constexpr int kR = 128;                 // query rows of a unit
+    static constexpr int kThreads = 192;           // warps 0-3 softmax, 4 pages, 5 products
+    static constexpr int kCtas = 2;                // per SM
+    static constexpr int kStages = 2;
+    static constexpr uint32_t kTileBytes = 128 * 128;
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;
+    static constexpr uint32_t kQ = kStages * kStageBytes;             // hi, lo: 128 rows x 128 bytes each
+    static constexpr uint32_t kInfo = kQ + 2 * kTileBytes;
+    static constexpr uint32_t kInfoBytes = 112;
+    static constexpr uint32_t kNanAt = kInfo + kStages * kInfoBytes;  // 2 x [128] first key with NaN in V's column
+    static constexpr uint32_t kScan = kNanAt + 1024;                  // 20 int + 4 int
+    static constexpr uint32_t kShared = kScan + 96;                   // 2 x CacheShared
+    static constexpr uint32_t kBars = kShared + 128;
+    static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kSFull = kQFull + 1,
+                         kPFull = kSFull + 2, kPvDone = kPFull + 2, kOFull = kPvDone + 1, kDrain = kOFull + 1, kNumBars = kDrain + 1;
+    static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kNanSeen = kAbort + 4;  // [2]
+    static constexpr uint32_t kDynamicSmem = kNanSeen + 8 + 1024;
+    static_assert(kInfo % 16 == 0 && kScan % 16 == 0 && kShared % 8 == 0 && kBars % 8 == 0, "alignment");
+    static_assert(kCtas * (kDynamicSmem + 1024) <= 228 * 1024, "shared memory budget");
+    static constexpr uint32_t kTmemCols = 256, kS = 0, kO = 128;
+};
+
+// The halves of a unit's key tile t that have a key some row sees (one at least).
+__device__ __forceinline__ int cache_halves(const CacheUnit& u, int t) { return t * kCacheTile + 64 < u.keys ? 2 : 1; }
+
+__device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, uint32_t base, uint32_t tmem,
+                                    volatile int* abort_flag) {
+    using L = CacheWideLayout;
+    constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, 64, false);
+    constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, 128, true);
+    const uint64_t lim = p.wait_limit_ns;
+    const bool wide = p.c.D == 128, leader = ptx::elect_one();
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t par) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<L>(base, bar), par, abort_flag, p.c.status, lim));
+        return ok;
+    };
+    const uint64_t q_hi = ptx::sdesc_rows<128>(base + L::kQ), q_lo = ptx::sdesc_rows<128>(base + L::kQ + L::kTileBytes);
+    int stage = 0;            // of the half whose S is next
+    uint32_t phase = 0;
+    uint32_t step = 0;        // number of that half
+    // The half before, whose O is still to come: its stage, half, and what it ends.
+    int prev_stage = -1, prev_half = 0;
+    uint32_t prev_phase = 0;
+    bool prev_first = false, prev_ends_tile = false, prev_ends_unit = false;
+    auto issue_pv = [&]() -> bool {
+        const uint32_t sb = (step - 1) & 1;
+        if (prev_half == 0 && !wait(L::kVFull + prev_stage, prev_phase)) return false;
+        if (!wait(L::kPFull + (int)sb, ((step - 1) >> 1) & 1)) return false;
+        ptx::tc_fence_after();
+        if (leader) {
+            // 64 keys = 64 rows of 128 bytes; a product takes 32.
+            const uint64_t vd = ptx::sdesc_rows<128>(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes +
+                                                     (uint32_t)prev_half * 8192u);
+            const uint32_t w = tmem + L::kS + sb * 64;
+            ptx::mma_ts_f8(tmem + L::kO, w, vd, kIdescO, prev_first ? 0u : 1u);
+            ptx::mma_ts_f8(tmem + L::kO, w + 8, vd + 256, kIdescO, 1u);
+            ptx::mma_ts_f8(tmem + L::kO, w + 16, vd, kIdescO, 1u);
+            ptx::mma_ts_f8(tmem + L::kO, w + 24, vd + 256, kIdescO, 1u);
+            ptx::mma_commit(cache_bar<L>(base, L::kPvDone));
+            if (prev_ends_tile) ptx::mma_commit(cache_bar<L>(base, L::kEmpty + prev_stage));
+            if (prev_ends_unit) ptx::mma_commit(cache_bar<L>(base, L::kOFull));
+        }
+        prev_stage = -1;
+        return true;
+    };
+    CacheUnit u;
+    for (int unit = 0; ok && cursor_next(p.plan, cur, u); ++unit) {
+        const int n = __shfl_sync(0xffffffffu, u.n, 0);
+        if (!wait(L::kQFull, unit & 1)) break;
+        for (int k = 0; ok && k < n; ++k) {
+            const int halves = __shfl_sync(0xffffffffu, cache_halves(u, u.t + k), 0);
+            for (int h = 0; h < halves; ++h, ++step) {
+                // While the tile's K is still on its way, the last half's O goes first.
+                if (prev_stage >= 0 && h == 0 &&
+                    !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<L>(base, L::kKFull + stage), phase)) && !issue_pv())
+                    break;
+                if (h == 0 && !wait(L::kKFull + stage, phase)) break;
+                ptx::tc_fence_after();
+                // In order behind the O of two halves ago, which reads its weights out of these columns.
+                if (leader) {
+                    const uint64_t kd = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes + (uint32_t)h * 8192u);
+                    const uint32_t st = tmem + L::kS + (step & 1) * 64;
+                    if (wide) {
+                        ptx::mma_ss_f8_x4<2, 2>(st, q_hi, kd, kIdescS, 0u);
+                        ptx::mma_ss_f8_x4<2, 2>(st, q_lo, kd, kIdescS, 1u);
+                    } else {  // D = 64: the other half of the rows is zero in K
+                        ptx::mma_ss_f8(st, q_hi, kd, kIdescS, 0u);
+                        ptx::mma_ss_f8(st, q_hi + 2, kd + 2, kIdescS, 1u);
+                        ptx::mma_ss_f8(st, q_lo, kd, kIdescS, 1u);
+                        ptx::mma_ss_f8(st, q_lo + 2, kd + 2, kIdescS, 1u);
+                    }
+                    ptx::mma_commit(cache_bar<L>(base, L::kSFull + (int)(step & 1)));
+                }
+                if (prev_stage >= 0 && !issue_pv()) break;
+                prev_stage = stage;
+                prev_phase = phase;
+                prev_half = h;
+                prev_first = k == 0 && h == 0;
+                prev_ends_tile = h == halves - 1;
+                prev_ends_unit = prev_ends_tile && k == n - 1;
+            }
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // The next unit's q comes after this one's O.
+        if (ok && prev_stage >= 0) issue_pv();
+    }
+    if (leader) {
+        ptx::mma_commit(cache_bar<L>(base, L::kDrain));
+        ptx::drain_wait(cache_bar<L>(base, L::kDrain), 0u, lim);
+    }
+}
+
+__device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur, int pos, int total, int ctas,
+                                        uint32_t base, uint8_t* smem, uint32_t tmem, volatile int* abort_flag) {
+    using L = CacheWideLayout;
+    const int r = threadIdx.x, lane = r & 31;  // this thread's row of a unit, and its lane of S and O
+    const uint32_t my_tmem = tmem + ((uint32_t)(r & ~31) << 16);
+    const int D = p.c.D, shift = p.c.block_shift;
+    // A wait that ran out leaves this false: the lane goes on without waiting and without writing results.  No
+    // warp waits for another here but through the bounded barriers.
+    bool alive = true;
+    auto wait = [&](int which, uint32_t par) {
+        if (alive) alive = ptx::mbar_wait_call(cache_bar<L>(base, which), par, abort_flag, p.c.status, p.wait_limit_ns);
+        __syncwarp();
+    };
+    auto arrive = [&](int which) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(cache_bar<L>(base, which));
+    };
+    int stage = 0;
+    uint32_t phase = 0, step = 0;
+    CacheUnit u;
+    for (int unit = 0; cursor_next(p.plan, cur, u); ++unit) {
+        int* nan_at = reinterpret_cast<int*>(smem + L::kNanAt) + (unit & 1) * 128;
+        volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kNanSeen) + (unit & 1);
+        // ---- q in two pieces, a row per thread: all its loads leave together
+        int qi, hq;
+        const bool used = cache_row(p, u, r, &qi, &hq);
+        const long long at = used ? ((long long)u.b * p.Hq + hq) * p.Sq + qi : -1;
+        const int keys = !used ? 0 : p.plan.causal ? max(u.s.first + qi + 1, 0) : u.s.len;
+        const int keys_all = p.plan.causal ? max(u.s.first + u.qt * p.plan.qper + 1, 0) : u.s.len;
+        float factor;  // of the row's scores
+        {
+            uint4 x[16];
+            const __nv_bfloat16* from = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + qi * p.q_stride[2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = used && i < D / 8 ? reinterpret_cast<const uint4*>(from)[i] : make_uint4(0, 0, 0, 0);
+            // the largest magnitude, by bit pattern; not finite: the whole row is NaN
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+            m = max(m & 0xffffu, m >> 16);
+            const float scale = e4m3_pow2_scale(__uint_as_float(m << 16));
+            const float inv = m >= 0x7f80u ? NAN : __uint_as_float((254u << 23) - __float_as_uint(scale));
+            factor = scale * p.scale_log2;
+            const uint32_t line = base + L::kQ + (uint32_t)r * 128u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
+                                       x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float a0 = __uint_as_float(v[e] << 16) * inv, a1 = __uint_as_float(v[e] & 0xffff0000u) * inv;
+                    const float a2 = __uint_as_float(v[e + 1] << 16) * inv, a3 = __uint_as_float(v[e + 1] & 0xffff0000u) * inv;
+                    const uint32_t h0 = e4m3_pair(a0, a1), h1 = e4m3_pair(a2, a3);
+                    const float2 f0 = e4m3_unpair(h0), f1 = e4m3_unpair(h1);
+                    hi[e / 2] = h0 | h1 << 16;
+                    lo[e / 2] = e4m3_pair(a0 - f0.x, a1 - f0.y) | (uint32_t)e4m3_pair(a2 - f1.x, a3 - f1.y) << 16;
+                }
+                const uint32_t to = line + (uint32_t)((i ^ (r & 7)) << 4);
+                ptx::st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+                ptx::st_shared_v4(to + L::kTileBytes, lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        if (!used) factor = 0.f;
+        nan_at[r] = 0x7fffffff;
+        if (r == 0) {
+            *nan_seen = 0;
+            if (u.n < u.tiles) {
+                CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared) + (u.t > 0 ? 0 : 1);
+                shared->u = u;
+                shared->first = plan_cta(total, pos - u.t, ctas);
+                shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
+            }
+        }
+        pos += plan_cost(p.plan, u.n);
+        ptx::fence_proxy_async_smem();
+        arrive(L::kQFull);
+
+        float row_max = -INFINITY, peak = -INFINITY, l = 0.f;  // of s + log2 vs, its largest so far, and the sum of w / vs
+        bool rose = false;  // some row's maximum did, at the half before
+        for (int k = 0; k < u.n; ++k) {
+            const int halves = cache_halves(u, u.t + k);
+            const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
+            for (int h = 0; h < halves; ++h, ++step) {
+                const int key0 = (u.t + k) * kCacheTile + h * 64;
+                const uint32_t s_addr = my_tmem + L::kS + (step & 1) * 64;
+                // S is there, the scales beside K too, and the O of two halves ago is done, which came before it.
+                wait(L::kSFull + (int)(step & 1), (step >> 1) & 1);
+                ptx::tc_fence_after();
+                const int missing = reinterpret_cast<const int*>(info)[24];
+                const bool full = key0 + 64 <= keys_all && missing == 0;
+                if (h == 0 && key0 + kCacheTile > keys_all) {  // as in kernel_cache_fwd.cuh, a key of V per thread
+                    wait(L::kVFull + stage, phase);
+                    const uint32_t line = base + (uint32_t)stage * L::kStageBytes + L::kTileBytes + (uint32_t)r * 128u;
+                    if (alive && key0 + r >= u.keys) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) ptx::st_shared_v4(line + 16 * y, 0, 0, 0, 0);
+                    } else if (alive && key0 + r >= keys_all) {
+                        if (cache_take_nan(line, r, key0 + r, nan_at)) *nan_seen = 1;
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                // y = s + log2 vs + base of 16 keys, which share a block: s is the score times K's scale and the row's factor.
+                const int seen = keys - key0;  // keys of the half that this row sees
+                auto scores = [&](auto masked, int i, const uint32_t* s, float at0, float* y) {
+                    const int page = (h * 64 + i * 16) >> shift;
+                    const float f = info[page] * factor, c = info[8 + page] + at0;
+                    const uint64_t f2 = ptx::f2(f, f), c2 = ptx::f2(c, c);
+                    const int last = missing >> page & 1 ? 0 : seen - i * 16;
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        ptx::f2_split(ptx::fma2(ptx::f2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, c2), y[x], y[x + 1]);
+                        if (decltype(masked)::value) {
+                            y[x] = x < last ? y[x] : -INFINITY;
+                            y[x + 1] = x + 1 < last ? y[x + 1] : -INFINITY;
+                        }
+                    }
+                };
+                uint32_t code[32];  // four codes each: hi, then lo
+                float sum;
+                // The weights against the row's maximum as it stands; returns the largest.
+                auto pass = [&](auto masked) {
+                    const float at0 = row_max == -INFINITY ? -INFINITY : kCacheRoom - row_max;
+                    float top = 0.f;
+                    sum = 0.f;
+                    uint32_t both[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i % 2 == 0) ptx::tmem_load<32>(s_addr + 16 * i, both);
+                        const uint32_t* s = both + i % 2 * 16;
+                        float y[16];
+                        scores(masked, i, s, at0, y);
+                        const float ivs = info[16 + ((h * 64 + i * 16) >> shift)];
+                        uint64_t part = ptx::f2(0.f, 0.f);
+#pragma unroll
+                        for (int x = 0; x < 16; x += 4) {
+                            float w[4], g[4], rest[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(y[x + e]);
+                            top = ptx::max3(top, w[0], w[1]);
+                            top = ptx::max3(top, w[2], w[3]);
+                            const uint64_t w01 = ptx::f2(w[0], w[1]), w23 = ptx::f2(w[2], w[3]), minus = ptx::f2(-1.f, -1.f);
+                            part = ptx::add2(part, ptx::add2(w01, w23));
+                            // hi: w at 4 significant bits, to nearest; lo: the rest
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) g[e] = __uint_as_float((__float_as_uint(w[e]) + 0x80000u) & 0xfff00000u);
+                            ptx::f2_split(ptx::fma2(ptx::f2(g[0], g[1]), minus, w01), rest[0], rest[1]);
+                            ptx::f2_split(ptx::fma2(ptx::f2(g[2], g[3]), minus, w23), rest[2], rest[3]);
+                            code[i * 4 + x / 4] = ptx::pack_e4m3x4(g[0], g[1], g[2], g[3]);
+                            code[16 + i * 4 + x / 4] = ptx::pack_e4m3x4(rest[0], rest[1], rest[2], rest[3]);
+                        }
+                        float a, b;
+                        ptx::f2_split(part, a, b);
+                        sum = fmaf(a + b, ivs, sum);
+                    }
+                    return top;
+                };
+                // First as it stands; once more when some row's maximum has to rise or fall, or only so while one has none.
+                bool rises = false;
+                for (bool move = __any_sync(0xffffffffu, row_max == -INFINITY && seen > 0);;) {
+                    if (move) {
+                        // Every row of the warp takes the maximum that it should have.
+                        float m = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t s[16];
+                            ptx::tmem_load<16>(s_addr + 16 * i, s);
+                            float y[16];
+                            scores(std::true_type(), i, s, 0.f, y);
+#pragma unroll
+                            for (int x = 0; x < 16; x += 2) m = ptx::max3(m, y[x], y[x + 1]);
+                        }
+                        bool moves;
+                        const float had = row_max;
+                        m = cache_new_max(row_max, peak, used ? m : -INFINITY, &moves);
+                        const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
+                        row_max = m;
+                        peak = fmaxf(peak, m);
+                        rises = __any_sync(0xffffffffu, moves && m > had);
+                        l *= f;
+                        if (k > 0 || h > 0) {
+                            // The half before has its weights against the old maximum: its product has to be in O.
+                            wait(L::kPvDone, (step - 1) & 1);
+                            ptx::tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 32) {
+                                uint32_t s[32];
+                                ptx::tmem_load<32>(my_tmem + L::kO + c, s);
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * f);
+                                ptx::tmem_store<32>(my_tmem + L::kO + c, s);
+                            }
+                        }
+                    }
+                    const float top = full ? pass(std::false_type()) : pass(std::true_type());
+                    // A fall is looked for after a rise and at every eighth tile, and everywhere once it is urgent (at every
+                    // step: 8% more time at scores of deviation 2.5, whose maxima vary that much).
+                    const bool low = top < (rose || (h == 0 && (k & 7) == 1) ? kCacheLow : kCacheLow / 16.f) && top > 0.f &&
+                                     row_max > peak - kCacheFall;
+                    if (move || !__any_sync(0xffffffffu, top > kCacheTop || low)) break;
+                    move = true;
+                }
+                rose = rises;
+                l += sum;
+                ptx::tmem_st32(s_addr, code);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                arrive(L::kPFull + (int)(step & 1));
+            }
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+
+        // ---- the row leaves
+        wait(L::kOFull, unit & 1);
+        ptx::tc_fence_after();
+        const bool whole = u.n == u.tiles, nan = *nan_seen != 0;
+        const long long slot = (long long)blockIdx.x * 2 + (u.t > 0 ? 0 : 1);
+        const float f = !whole ? 1.f : l == 0.f ? 0.f : ptx::rcp(l);
+        if (alive && whole && at >= 0 && p.lse != nullptr)
+            p.lse[at] = l == 0.f ? -INFINITY : (row_max - kCacheRoom + ptx::lg2(l)) * kLn2;
+        if (alive && !whole && used) p.part_ml[slot * L::kR + r] = make_float2(row_max - kCacheRoom, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t s[32];
+            ptx::tmem_load<32>(my_tmem + L::kO + c, s);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * f);
+            if (nan) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (nan_at[c + x] < keys) s[x] = 0x7fffffffu;
+            }
+            if (alive && used) {
+                if (!whole) {  // four columns of all rows side by side: [32][128] float4
+                    uint4* to = reinterpret_cast<uint4*>(p.part_o) + (slot * 32 + c / 4) * L::kR + r;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) to[x * L::kR] = make_uint4(s[4 * x], s[4 * x + 1], s[4 * x + 2], s[4 * x + 3]);
+                } else {
+                    uint4* to = reinterpret_cast<uint4*>(p.out + at * D + c);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = ptx::pack_bf16x2(__uint_as_float(s[8 * x + 2 * e]), __uint_as_float(s[8 * x + 2 * e + 1]));
+                        to[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+        ptx::tc_fence_before();
+    }
+}
+
+// Joins a shared unit, a row per thread of warps 0-3; 32 columns of two pieces are under way at once.
+__device__ void cache_wide_join(const CacheFwdParams& p, const CacheShared& shared) {
+    using L = CacheWideLayout;
+    const int r = threadIdx.x, n = shared.pieces;
+    int qi, hq;
+    if (r >= L::kR || !cache_row(p, shared.u, r, &qi, &hq)) return;
+    const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
+    // The pieces: slot 1 of the first CTA, slot 0 of the following ones.
+    auto slot = [&](int x) { return (long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0); };
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+        const float2 ml = __ldcg(p.part_ml + slot(x) * L::kR + r);
+        const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+        l = l * ptx::ex2(m - ref) + ptx::ex2(ml.x - ref) * ml.y;
+        m = top;
+    }
+    const float inv = l == 0.f ? 0.f : ptx::rcp(l), ref = m == -INFINITY ? 0.f : m;
+    if (p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
+    for (int c = 0; c < p.c.D / 4; c += 8) {
+        float4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int x = 0; x < n; ++x) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (slot(x) * 32 + c + i) * L::kR + r);
+            const float f = ptx::ex2(__ldcg(p.part_ml + slot(x) * L::kR + r).x - ref);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = make_float4(o[i].x + f * v[i].x, o[i].y + f * v[i].y, o[i].z + f * v[i].z, o[i].w + f * v[i].w);
+        }
+        uint4* to = reinterpret_cast<uint4*>(p.out + at * p.c.D + c * 4);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+            to[i / 2] = make_uint4(ptx::pack_bf16x2(o[i].x * inv, o[i].y * inv), ptx::pack_bf16x2(o[i].z * inv, o[i].w * inv),
+                                   ptx::pack_bf16x2(o[i + 1].x * inv, o[i + 1].y * inv),
+                                   ptx::pack_bf16x2(o[i + 1].z * inv, o[i + 1].w * inv));
+    }
+}
+
+__global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kCtas)
+    attn_cache_fwd_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                               const __grid_constant__ CacheFwdParams p) {
+    using L = CacheWideLayout;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+
+    if (threadIdx.x == 160) {
+        for (int s = 0; s < L::kStages; ++s) {
+            ptx::mbar_init(cache_bar<L>(base, L::kKFull + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kVFull + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kEmpty + s), 1);
+        }
+        ptx::mbar_init(cache_bar<L>(base, L::kQFull), 4);  // the softmax warps
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(cache_bar<L>(base, L::kSFull + i), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kPFull + i), 4);
+        }
+        ptx::mbar_init(cache_bar<L>(base, L::kPvDone), 1);
+        ptx::mbar_init(cache_bar<L>(base, L::kOFull), 1);
+        ptx::mbar_init(cache_bar<L>(base, L::kDrain), 1);
+        *abort_flag = 0;
+        for (int x = 0; x < 2; ++x) reinterpret_cast<CacheShared*>(smem + L::kShared)[x].pieces = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp == 4) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), L::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    int begin, end, total;
+    CachePlace place;
+    const int ctas = cache_locate<L::kThreads>(p.plan, reinterpret_cast<int*>(smem + L::kScan), p.c.status, &begin, &end,
+                                               &total, &place);  // barriers of the block within
+    ptx::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+    if (begin == end) {
+        // no tile for this CTA
+    } else if (warp == 4) {
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+    } else if (warp == 5) {
+        cache_wide_mma_role(p, cursor_at(p.plan, place, end - begin), base, tmem, abort_flag);
+    } else {
+        cache_wide_softmax_role(p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, tmem, abort_flag);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, L::kTmemCols);
+    }
+    cache_join(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0,
+               [&](const CacheShared& x) { cache_wide_join(p, x); });
+}
+
+}  // namespace attn

@@ -60,6 +60,15 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same with A read from tensor memory (four codes a column, 8 columns).
+__device__ __forceinline__ void mma_ts_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Four steps over 128 keys, the operands' descriptors advancing by kA and kB
 // (in 16-byte units) each.
 template <int kA, int kB>
@@ -150,6 +159,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)x) : "memory");

@@ -445,8 +445,10 @@ int attn_cache_read(const attn_cache_t *cache, void *k, void *v, int first, int 
  * LSE = -inf.  Keys that no query row may see (past seq_lens[b], after the
  * position) do not affect it whatever their codes.  Scores accumulate in fp32
  * from q rounded to 2^-18 of its row's largest element; the probabilities that
- * multiply V keep 8 bits or 2^-16 of the row's largest weight, whichever is
- * coarser; sums and LSE are fp32.
+ * multiply V keep 8 bits or 2^-14 of the row's largest weight, whichever is
+ * coarser (that largest one counts where it stands and the keys close by: one
+ * key far above all others does not cost the others their bits further on);
+ * sums and LSE are fp32.  V's scales below 2^-80 count as 2^-80.
  * Results are deterministic.  Asynchronous on `stream`; allocates nothing.
  * out and lse may overlap neither each other nor any input.  Other errors as
  * attn_fwd (scale finite and > 0).

@@ -77,8 +77,9 @@ def attention(q, k, v, scale, first, causal):
     The tolerance counts, against this exact result: q rounded to 2^-18 of its row's largest
     element (a score moves by at most scale * 2^-18 max|q| sum|k|, and 2^-20 of the sum of its
     products' magnitudes for the fp32 accumulation and exp2), the weights rounded to 2^-8 of
-    themselves plus 2^-16 of the largest one (weights as they multiply V's codes, so weighted
-    by V's scale: the bound takes the largest |v| in that key's row), and O's rounding to bf16, 2^-8 |O|."""
+    themselves plus 2^-14 of the largest one (weights as they multiply V's codes, so weighted
+    by V's scale: the bound takes the largest |v| in that key's row; half a step of the smallest
+    codes is 2^-10, and a row's largest weight counts 2^4 at least), and O's rounding to bf16, 2^-8 |O|."""
     Hq, n, D = q.shape
     Hkv, length = k.shape[:2]
     group = Hq // Hkv
@@ -103,8 +104,8 @@ def attention(q, k, v, scale, first, causal):
             ds = float(ds.max()) + 2.0 ** -20
             mag = np.abs(V)
             heavy = (w * mag.max(1)).max()
-            # sum over keys of 2^-16 of the largest weight-times-V-scale, in units of each key's codes
-            floor = 2.0 ** -16 * heavy * (mag / np.maximum(mag.max(1, keepdims=True), 1e-300)).sum(0) * 2
+            # sum over keys of 2^-14 of the largest weight-times-V-scale, in units of each key's codes
+            floor = 2.0 ** -14 * heavy * (mag / np.maximum(mag.max(1, keepdims=True), 1e-300)).sum(0) * 2
             tol[h, i] = (2.0 ** -8 + 2 * ds) * (w @ mag) + floor + 2.0 ** -8 * np.abs(o[h, i]) + 1e-30
             tol_lse[h, i] = ds + 2.0 ** -20 * (abs(lse[h, i]) + abs(m))
     return o, lse, tol, tol_lse

@@ -288,6 +288,7 @@ int main() {
         p.q_tiles = (p.Sq + p.qper - 1) / p.qper;
         p.heads = 1 + std::rand() % 5;
         p.whole = std::rand() % 4 == 0;
+        p.least = 1 + std::rand() % 6;
         std::vector<int> lens(p.B), counts(p.B);
         for (int b = 0; b < p.B; ++b) {
             lens[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (p.capacity + 1);
@@ -324,7 +325,7 @@ int main() {
             all += sum[t] = plan_chunk(p, a, z, &bad);
         }
         CHECK(all == total);
-        const int given = 1 + std::rand() % 70, ctas = plan_ctas(total, given);
+        const int given = 1 + std::rand() % 70, ctas = plan_ctas(p, total, given);
         size_t unit = 0;
         int tile = 0, pieces = 0, expect_first = -1, expect_last = -1;
         for (int c = 0; c < given; ++c) {

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from causal_scaled_dot_gb300.kv_cache import KVCache
 from tests.cache_util import PlainCache, attention, make, rows, to_f64
 
 pytestmark = pytest.mark.gpu
@@ -205,6 +206,19 @@ def test_attention_long_cache_is_joined(lens, Hq, Hkv, D, block, Sq):
     check_attention(cache, plain, table, lens, Hq, Sq)
 
 
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(33, 1, 1), (64, 2, 1), (128, 1, 1), (129, 1, 1), (300, 1, 1), (8, 1, 5), (6, 2, 43),
+                                       (200, 1, 2), (2, 2, 129)])
+@pytest.mark.parametrize("D,block", [(128, 64), (64, 16)])
+def test_attention_many_rows(D, block, Hq, Hkv, Sq):
+    """Around the sizes where a key/value head's rows (query heads x queries) fill units of 32 and 128,
+    over caches with and without joined pieces."""
+    for lens in ([0, 450, Sq + 63, 64], [2100, Sq, 1]):
+        cache, table = make(len(lens), Hkv, D, block, max(lens), seed=12)
+        plain = fill(cache, table, lens, seed=71)
+        check_attention(cache, plain, table, lens, Hq, Sq)
+        check_attention(cache, plain, table, lens, Hq, Sq, q_lens=[max(Sq - 1 - b, 0) for b in range(len(lens))], causal=False)
+
+
 def test_attention_large_batch_of_short_sequences():
     lens = [(37 * b) % 200 for b in range(300)]
     cache, table = make(300, 2, 64, 16, 200, seed=11)
@@ -228,6 +242,38 @@ def test_attention_sharp_scores_and_scales_far_apart():
     for sigma in (0.01, 1.0, 20.0):
         check_attention(cache, plain, table, [t], 4, 1, sigma=sigma)
         check_attention(cache, plain, table, [t], 4, 30, sigma=sigma)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Sq", [(2, 2, 64, 1), (32, 2, 128, 1), (8, 1, 128, 4), (16, 2, 64, 8), (8, 1, 128, 40)])
+@pytest.mark.parametrize("at", [0, 1500])
+def test_attention_one_key_far_above_the_rest(Hq, Hkv, D, Sq, at):
+    """A key that every row attends to, e^14 times the others, with values of zero: O is what the rest
+    of a long sequence adds up to.  The others' scores differ by 1 at most and their values are
+    positive, so O's relative error is at most a weight's: 2^-10 (half a step of the smallest codes) of
+    0.25 / e where the row's maximum just does not fall, 2^-6.5, and the bf16 of O and the weights, 2^-8
+    each; the 127 keys in that key's own tile may be lost."""
+    length, block, B = 4000, 64, 40  # 40 sequences over the same blocks: a CTA's share of one is long
+    rng = np.random.default_rng(7)
+    one, table = make(1, Hkv, D, block, length, 3)
+    set_lens(one, [length])
+    plain = PlainCache(one.k.shape[0], Hkv, block, D)
+    k = torch.tensor(rng.uniform(-0.5, 0.5, (1, Hkv, length, D)) * (np.arange(D) == 1), dtype=torch.bfloat16)
+    v = torch.tensor(rng.uniform(1, 2, (1, Hkv, length, D)), dtype=torch.bfloat16)
+    k[:, :, at, 0] = 14.0
+    v[:, :, at] = 0
+    one.write(k.cuda(), v.cuda())
+    plain.write(to_f64(k), to_f64(v), table, [length], [length])
+    cache = KVCache(one.k, one.v, one.k_scale, one.v_scale, one.block_table.repeat(B, 1), one.seq_lens.repeat(B))
+    q = torch.zeros(B, Hq, Sq, D, dtype=torch.bfloat16)
+    q[..., :2] = 1.0
+    o = to_f64(cache.attention(q.cuda(), scale=1.0)[0])
+    ks, vs = plain.values("k", table[0], length), plain.values("v", table[0], length)
+    for i in range(Sq):
+        n = length - Sq + i + 1
+        for h in range(Hq):
+            p = np.exp(ks[h * Hkv // Hq][:n, :2].sum(1))
+            ref = (p / p.sum()) @ vs[h * Hkv // Hq][:n]
+            assert (np.abs(o[:, h, i] - ref) <= (2 ** -6.5 + 2 ** -7 + 127 / n) * ref).all()
 
 
 def test_attention_ignores_what_no_row_may_see():
