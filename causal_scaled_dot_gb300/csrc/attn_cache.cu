@@ -101,6 +101,10 @@ constexpr int kWholeTiles = 4;
 // Tiles that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 33 us with 4, 45
 // with 1, 39 with 2 or 6; 1 joins more pieces, 6 leaves SMs without work.
 constexpr int kWideLeast = 4;
+// CTAs that a unit keeps busy at most when there are no more units: one CTA joins the pieces.  One sequence of 131072
+// keys, 8 / 16 / 32 / 128 rows over one key/value head: 28 / 31 / 41 / 97 us with 64, 26 / 34 / 47 / 145 with 128, and
+// 39 / 38 / 48 / 95 with 32.
+constexpr int kMostPieces = 64;
 long long tiles_of(const attn_cache_t* c) {
     return ((long long)c->max_blocks * c->block_size + kCacheTile - 1) / kCacheTile;
 }
@@ -153,7 +157,7 @@ int launch_fwd(K kernel, const CUtensorMap& tk, const CUtensorMap& tv, const Cac
                cudaStream_t st) {
     const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads, most = (long long)sms * L::kCtas;
     if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
-    const long long work = p.plan.whole ? units : units * tiles;  // of the plan, at most
+    const long long work = p.plan.whole ? units : units * (tiles < kMostPieces ? tiles : kMostPieces);  // CTAs of use
     const int grid = (int)(work < most ? work : most);
     kernel<<<grid, L::kThreads, L::kDynamicSmem, st>>>(tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;

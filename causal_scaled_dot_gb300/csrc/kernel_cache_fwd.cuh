@@ -70,7 +70,8 @@ struct CacheFwdParams {
     float* part_o;          // [G][2][R][128] partial sums of w code
     float2* part_ml;        // [G][2][R] their M - 4 and sum of w / vs
     // [G]: pieces left of the unit that begins in a CTA, below a number (the upper 48 bits) that marks this
-    // launch: whatever stood there before counts as none.  0 again after each join.
+    // launch: whatever stood there before counts as none.  0 again after each join, since a captured launch
+    // comes again with its number.
     unsigned long long* tickets;
     unsigned long long ticket;
     unsigned long long wait_limit_ns;
@@ -198,6 +199,20 @@ __device__ __forceinline__ bool cache_row(const CacheFwdParams& p, const CacheUn
     return iq < p.plan.qper && *i < u.s.count && g < p.group;
 }
 
+// Notes a unit that CTAs share, whose first tile here is tile `pos` of all.
+__device__ __forceinline__ void cache_share(CacheShared* shared, const CacheUnit& u, int pos, int total, int ctas) {
+    shared->u = u;
+    shared->first = plan_cta(total, pos - u.t, ctas);
+    shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
+}
+// Each CTA that shares a unit does this before it counts its piece: a counter that does not carry this launch's
+// number becomes 0 pieces of this launch.  An exchange that fails met another CTA's, which did the same.
+__device__ __noinline__ void cache_open_ticket(const CacheFwdParams& p, int first) {
+    unsigned long long* at = p.tickets + first;
+    const unsigned long long had = __ldcg(at);
+    if ((had ^ p.ticket) >> 16) atomicCAS(at, had, p.ticket);
+}
+
 // log2 of a row's largest weight when its maximum M is new.  The weights of the tiles after it may be up to 448 /
 // 2^4 = 28 times that before M has to rise, which scores of unit variance hardly ever ask for (with 2^6 and 7
 // times, a step of 128 rows x 64 keys met it in one of ten).
@@ -223,8 +238,8 @@ constexpr float kCacheLeastScale = -80.f;
 
 // ---------------------------------------------------------------- warp 0: pages
 template <typename L>
-__device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur,
-                                uint32_t base, uint8_t* smem, volatile int* abort_flag) {
+__device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur, int pos,
+                                int total, int ctas, uint32_t base, uint8_t* smem, volatile int* abort_flag) {
     const CacheView& c = p.c;
     const int lane = threadIdx.x & 31;
     const bool leader = ptx::elect_one();
@@ -296,6 +311,8 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
             if (t == u.t) {
                 block2 = more2 ? block_of(g2, u2.t * pages + lane, e2) : -1;
                 sc2 = scales(g2, block2);
+                if (leader && u.n < u.tiles) cache_open_ticket(p, plan_cta(total, pos - u.t, ctas));
+                __syncwarp();
             }
             // pages that some row should see but that the table places outside the cache
             const uint32_t missing = __ballot_sync(0xffffffffu, mine && block < 0 && window < g.last) >> at;
@@ -321,6 +338,7 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 phase ^= 1u;
             }
         }
+        pos += u.n;
         more = more2;
         u = u2;
         g = g2;
@@ -515,13 +533,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
                 work->keys_all = p.plan.causal ? max(u.s.first + q0 + 1, 0) : u.s.len;
                 work->slot = u.n == u.tiles ? -1 : u.t > 0 ? 0 : 1;
                 work->rows = min(p.plan.qper, u.s.count - q0) * p.hper;
-                if (u.n < u.tiles) {
-                    CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot;
-                    shared->u = u;
-                    shared->first = plan_cta(total, pos - u.t, ctas);
-                    shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
-                }
-                pos += u.n;
+                if (u.n < u.tiles) cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot, u, pos, total, ctas);
             }
         } else if (w == 0 && lane == 0) {
             work->n = 0;
@@ -530,6 +542,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(cache_bar<L>(base, L::kQFull + ub));
         if (!more) return;
+        pos += u.n;
     }
 }
 
@@ -854,71 +867,88 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 }
 
 // Counts a piece of a unit as left; true for the last of them.
-__device__ __noinline__ bool cache_last_piece(unsigned long long* at, unsigned long long ticket, int pieces) {
-    unsigned long long had = ticket + pieces - 1, now;  // a guess that is right for the last
-    for (;;) {  // as many tries as there are pieces and two at most: a failure is another piece's success
-        now = (had ^ ticket) >> 16 ? ticket + 1 : had + 1;
-        const unsigned long long seen = atomicCAS(at, had, now);
-        if (seen == had) break;
-        had = seen;
-    }
-    if ((int)(now & 0xffff) != pieces) return false;
+__device__ __noinline__ bool cache_last_piece(unsigned long long* at, int pieces) {
+    if ((int)(atomicAdd(at, 1ull) & 0xffff) + 1 != pieces) return false;
     atomicExch(at, 0ull);
     return true;
 }
 
-// Joins rows r, r + 1, ... of a shared unit (`count` of them, a warp for all):
+// Joins rows r .. r + kRows - 1 of a shared unit, a warp for all:
 // O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i over the pieces, which are slot 1 of the first CTA and slot 0 of the
-// following ones, R rows each.
-__device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shared, int R, int r, int count) {
-    constexpr int kBatch = 4;  // rows under way at once
+// following ones, R rows each.  A lane takes every 32nd piece's (M, l), and 4 columns of every piece's O, of which
+// 8 are under way at once.
+template <int kRows>
+__device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shared, int R, int r) {
     const int lane = threadIdx.x & 31, n = shared.pieces;
-    for (; count > 0; r += kBatch, count -= kBatch) {
-        float m[kBatch], l[kBatch];
-        float4 o[kBatch];
+    const bool mine = lane * 4 < p.c.D;
+    auto slot = [&](int x) { return ((long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0)) * R + r; };
+    auto piece = [&](int x, int y) { return x < n ? __ldcg(p.part_ml + slot(x) + y) : make_float2(-INFINITY, 0.f); };
+    float m[kRows], l[kRows];  // of the lane's pieces, then of all
 #pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-            m[y] = -INFINITY;
-            l[y] = 0.f;
-            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int y = 0; y < kRows; ++y) {
+        m[y] = -INFINITY;
+        l[y] = 0.f;
+    }
+    float2 near[kRows];  // of piece `lane`
+    constexpr int kAhead = 8 / kRows;
+    float4 v[kAhead][kRows];
+    auto load = [&](int x0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int y = 0; y < kRows; ++y)
+                v[i][y] = mine && x0 + i < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(x0 + i) + y) * 128) + lane)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) near[y] = piece(lane, y);
+    load(0);
+    for (int x0 = 0; x0 < n; x0 += 32) {
+#pragma unroll
+        for (int y = 0; y < kRows; ++y) {
+            const float2 ml = x0 == 0 ? near[y] : piece(x0 + lane, y);
+            const float top = fmaxf(m[y], ml.x), ref = top == -INFINITY ? 0.f : top;
+            l[y] = l[y] * ptx::ex2(m[y] - ref) + ptx::ex2(ml.x - ref) * ml.y;
+            m[y] = top;
         }
-#pragma unroll 2
-        for (int x = 0; x < n; ++x) {
-            const long long from = ((long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0)) * R + r;
-            float2 ml[kBatch];
-            float4 v[kBatch];
+    }
+    float ref[kRows];
+    float4 o[kRows];
 #pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                ml[y] = make_float2(-INFINITY, 0.f);
-                v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (y < count) {
-                    ml[y] = __ldcg(p.part_ml + from + y);
-                    if (lane * 4 < p.c.D) v[y] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (from + y) * 128) + lane);
+    for (int y = 0; y < kRows; ++y) {
+        float top = m[y];
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        ref[y] = top == -INFINITY ? 0.f : top;
+        l[y] *= ptx::ex2(m[y] - ref[y]);
+        m[y] = top;
+        for (int x = 16; x > 0; x >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], x);
+        o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int x0 = 0; x0 < n; x0 += 32) {
+        float f[kRows];  // of the lane's piece
+#pragma unroll
+        for (int y = 0; y < kRows; ++y) f[y] = ptx::ex2((x0 == 0 ? near[y] : piece(x0 + lane, y)).x - ref[y]);
+        for (int x = x0; x < min(n, x0 + 32); x += kAhead) {
+            if (x > 0) load(x);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int y = 0; y < kRows; ++y) {
+                    const float g = __shfl_sync(0xffffffffu, f[y], (x + i) & 31);
+                    o[y] = make_float4(o[y].x + g * v[i][y].x, o[y].y + g * v[i][y].y, o[y].z + g * v[i][y].z, o[y].w + g * v[i][y].w);
                 }
-            }
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const float top = fmaxf(m[y], ml[y].x), ref = top == -INFINITY ? 0.f : top;
-                const float keep = ptx::ex2(m[y] - ref), f = ptx::ex2(ml[y].x - ref);
-                m[y] = top;
-                l[y] = l[y] * keep + f * ml[y].y;
-                o[y].x = o[y].x * keep + f * v[y].x;
-                o[y].y = o[y].y * keep + f * v[y].y;
-                o[y].z = o[y].z * keep + f * v[y].z;
-                o[y].w = o[y].w * keep + f * v[y].w;
-            }
         }
+    }
 #pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-            int qi, hq;
-            if (y >= count || !cache_row(p, shared.u, r + y, &qi, &hq)) continue;
-            const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
-            const float inv = l[y] == 0.f ? 0.f : ptx::rcp(l[y]);
-            if (lane * 4 < p.c.D)
-                *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
-                    make_uint2(ptx::pack_bf16x2(o[y].x * inv, o[y].y * inv), ptx::pack_bf16x2(o[y].z * inv, o[y].w * inv));
-            if (lane == 0 && p.lse != nullptr) p.lse[at] = l[y] == 0.f ? -INFINITY : (m[y] + ptx::lg2(l[y])) * kLn2;
-        }
+    for (int y = 0; y < kRows; ++y) {
+        int qi, hq;
+        if (!cache_row(p, shared.u, r + y, &qi, &hq)) continue;
+        const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
+        const float inv = l[y] == 0.f ? 0.f : ptx::rcp(l[y]);
+        if (mine)
+            *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
+                make_uint2(ptx::pack_bf16x2(o[y].x * inv, o[y].y * inv), ptx::pack_bf16x2(o[y].z * inv, o[y].w * inv));
+        if (lane == 0 && p.lse != nullptr) p.lse[at] = l[y] == 0.f ? -INFINITY : (m[y] + ptx::lg2(l[y])) * kLn2;
     }
 }
 
@@ -930,7 +960,7 @@ __device__ void cache_join(const CacheFwdParams& p, CacheShared* shared, bool ab
     if (threadIdx.x < 2) {
         CacheShared& x = shared[threadIdx.x];
         __threadfence();
-        x.last = x.pieces > 0 && !aborted && cache_last_piece(p.tickets + x.first, p.ticket, x.pieces);
+        x.last = x.pieces > 0 && !aborted && cache_last_piece(p.tickets + x.first, x.pieces);
         __threadfence();
     }
     __syncthreads();
@@ -988,7 +1018,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     if (begin == end) {
         // no tile for this CTA
     } else if (warp == 0) {
-        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
     } else if (warp == 1) {
         cache_mma_role<R>(p, base, smem, tmem, abort_flag);
     } else if (warp < 4) {
@@ -1004,9 +1034,9 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
     cache_join(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0, [&](const CacheShared& x) {
-        constexpr int kWarps = L::kThreads / 32, kPer = (R + kWarps - 1) / kWarps;
-        const int first = warp * kPer;
-        if (first < R) cache_join_rows(p, x, R, first, min(kPer, R - first));
+        constexpr int kWarps = L::kThreads / 32, kRows = (R + kWarps - 1) / kWarps;
+        static_assert(R % kRows == 0, "rows of a warp");
+        if (warp * kRows < R) cache_join_rows<kRows>(p, x, R, warp * kRows);
     });
 }
 

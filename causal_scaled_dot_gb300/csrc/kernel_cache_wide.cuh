@@ -219,16 +219,12 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
         nan_at[r] = 0x7fffffff;
         if (r == 0) {
             *nan_seen = 0;
-            if (u.n < u.tiles) {
-                CacheShared* shared = reinterpret_cast<CacheShared*>(smem + L::kShared) + (u.t > 0 ? 0 : 1);
-                shared->u = u;
-                shared->first = plan_cta(total, pos - u.t, ctas);
-                shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
-            }
+            if (u.n < u.tiles)
+                cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + (u.t > 0 ? 0 : 1), u, pos, total, ctas);
         }
-        pos += plan_cost(p.plan, u.n);
         ptx::fence_proxy_async_smem();
         arrive(L::kQFull);
+        pos += plan_cost(p.plan, u.n);
 
         float row_max = -INFINITY, peak = -INFINITY, l = 0.f;  // of s + log2 vs, its largest so far, and the sum of w / vs
         bool rose = false;  // some row's maximum did, at the half before
@@ -498,7 +494,7 @@ __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kC
     if (begin == end) {
         // no tile for this CTA
     } else if (warp == 4) {
-        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), base, smem, abort_flag);
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
     } else if (warp == 5) {
         cache_wide_mma_role(p, cursor_at(p.plan, place, end - begin), base, tmem, abort_flag);
     } else {
