@@ -107,9 +107,11 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
         for (int k = 0; ok && k < n; ++k) {
             const int halves = __shfl_sync(0xffffffffu, cache_halves(u, u.t + k), 0);
             for (int h = 0; h < halves; ++h, ++step) {
-                // While the tile's K is still on its way, the last half's O goes first.
+                // The last half's O goes first when its weights are there before the tile's K.
                 if (prev_stage >= 0 && h == 0 &&
-                    !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<L>(base, L::kKFull + stage), phase)) && !issue_pv())
+                    cache_comes_first<1>(cache_bar<L>(base, L::kPFull + (int)((step - 1) & 1)), ((step - 1) >> 1) & 1,
+                                      cache_bar<L>(base, L::kKFull + stage), phase) &&
+                    !issue_pv())
                     break;
                 if (h == 0 && !wait(L::kKFull + stage, phase)) break;
                 ptx::tc_fence_after();
