@@ -21,8 +21,10 @@
 // What bounds it, per 128 rows x 64 keys: two softmax warps a scheduler, each about
 // 600 issue slots of weights (1250 cycles side by side) and 700 cycles of waits,
 // vote, fences and tensor memory around them; the products take 640 of those 1900.
-// 2 x 1024 tokens at the end of 8192, 32 heads over 8, D = 128: 276 us, 934
-// TFLOP/s counted once per product (the two pieces make it twice that).
+// Two threads a row (half of a step's keys each) double what is around the weights:
+// 318 us where this takes 276, and a step of 128 keys leaves no tensor memory for
+// a second buffer of S.  2 x 1024 tokens at the end of 8192, 32 heads over 8, D =
+// 128: 276 us, 935 TFLOP/s counted once per product (the two pieces make it twice).
 #pragma once
 
 #include <type_traits>
@@ -45,7 +47,7 @@ struct CacheWideLayout {
     static constexpr uint32_t kScan = kNanAt + 1024;                  // 20 int + 4 int
     static constexpr uint32_t kShared = kScan + 96;                   // 2 x CacheShared
     static constexpr uint32_t kBars = kShared + 128;
-    static constexpr int kKFull = 0, kVFull = kStages, kEmpty = 2 * kStages, kQFull = 3 * kStages, kSFull = kQFull + 1,
+    static constexpr int kKFull = 0, kVFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kSFull = kQFull + 1,
                          kPFull = kSFull + 2, kPvDone = kPFull + 2, kOFull = kPvDone + 1, kDrain = kOFull + 1, kNumBars = kDrain + 1;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
@@ -77,11 +79,9 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
     uint32_t step = 0;        // number of that half
     // The half before, whose O is still to come: its stage, half, and what it ends.
     int prev_stage = -1, prev_half = 0;
-    uint32_t prev_phase = 0;
     bool prev_first = false, prev_ends_tile = false, prev_ends_unit = false;
     auto issue_pv = [&]() -> bool {
         const uint32_t sb = (step - 1) & 1;
-        if (prev_half == 0 && !wait(L::kVFull + prev_stage, prev_phase)) return false;
         if (!wait(L::kPFull + (int)sb, ((step - 1) >> 1) & 1)) return false;
         ptx::tc_fence_after();
         if (leader) {
@@ -107,13 +107,11 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
         for (int k = 0; ok && k < n; ++k) {
             const int halves = __shfl_sync(0xffffffffu, cache_halves(u, u.t + k), 0);
             for (int h = 0; h < halves; ++h, ++step) {
-                // The last half's O goes first when its weights are there before the tile's K.
-                if (prev_stage >= 0 && h == 0 &&
-                    cache_comes_first<1>(cache_bar<L>(base, L::kPFull + (int)((step - 1) & 1)), ((step - 1) >> 1) & 1,
-                                      cache_bar<L>(base, L::kKFull + stage), phase) &&
-                    !issue_pv())
-                    break;
-                if (h == 0 && !wait(L::kKFull + stage, phase)) break;
+                // Where the tile's pages are still on their way, the last half's O goes first.
+                if (h == 0 && !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<L>(base, L::kKFull + stage), phase))) {
+                    if (prev_stage >= 0 && !issue_pv()) break;
+                    if (!wait(L::kKFull + stage, phase)) break;
+                }
                 ptx::tc_fence_after();
                 // In order behind the O of two halves ago, which reads its weights out of these columns.
                 if (leader) {
@@ -132,7 +130,6 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
                 }
                 if (prev_stage >= 0 && !issue_pv()) break;
                 prev_stage = stage;
-                prev_phase = phase;
                 prev_half = h;
                 prev_first = k == 0 && h == 0;
                 prev_ends_tile = h == halves - 1;
@@ -463,8 +460,7 @@ __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kC
 
     if (threadIdx.x == 160) {
         for (int s = 0; s < L::kStages; ++s) {
-            ptx::mbar_init(cache_bar<L>(base, L::kKFull + s), 1);
-            ptx::mbar_init(cache_bar<L>(base, L::kVFull + s), 1);
+            ptx::mbar_init(cache_bar<L>(base, L::kKFull + s), 2);  // K and V
             ptx::mbar_init(cache_bar<L>(base, L::kEmpty + s), 1);
         }
         ptx::mbar_init(cache_bar<L>(base, L::kQFull), 4);  // the softmax warps
