@@ -468,3 +468,73 @@ def test_workspace_contents_do_not_matter():
                                       0.125, 1, work.data_ptr(), need, st) == 0
             native.attn_sync_status()
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_offsets_past_32_bits():
+    """Blocks on both sides of 2^32 bytes of codes, and the cache's last one."""
+    Hkv, block, D = 8, 128, 128
+    total = 2 ** 32 // (Hkv * block * D) + 5
+    code = lambda: torch.empty((total, Hkv, block, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # noqa: E731
+    scale = lambda: torch.empty((total, Hkv), device="cuda")  # noqa: E731
+    table = [[total - 1, 0, total - 5], [1, total - 3, total - 2]]
+    cache = KVCache(code(), code(), scale(), scale(), ints(table), ints([0, 0]))
+    small = [[0, 1, 2], [3, 4, 5]]  # the plain cache's own numbers for the same blocks
+    lens, plain = [300, 384], PlainCache(6, Hkv, block, D)
+    k, v = rows((2, Hkv, 384, D), 5), rows((2, Hkv, 384, D), 6)
+    set_lens(cache, lens)
+    cache.write(k.cuda(), v.cuda(), new_lens=ints(lens), check_status=True)
+    plain.write(to_f64(k), to_f64(v), small, lens, lens)
+    got_k, got_v = cache.read(384)
+    for b, t in enumerate(lens):
+        assert np.array_equal(to_f64(got_k)[b, :, :t], to_f64(torch.from_numpy(plain.values("k", small[b], t)).bfloat16()))
+        assert np.array_equal(to_f64(got_v)[b, :, :t], to_f64(torch.from_numpy(plain.values("v", small[b], t)).bfloat16()))
+    for Sq in (1, 20):
+        check_attention(cache, plain, small, lens, 16, Sq)
+
+
+@pytest.mark.parametrize("Hq,Sq", [(2, 1), (6, 3), (2, 70)])
+def test_attention_takes_any_positive_scale(Hq, Sq):
+    """Scales that no write makes: not powers of two, far apart between blocks and heads."""
+    lens = [700, 33]
+    cache, table = make(2, 2, 128, 32, 700, seed=13)
+    plain = fill(cache, table, lens, seed=81)
+    g = torch.Generator().manual_seed(3)
+    for name, spread in (("k_scale", 0.3), ("v_scale", 6.0)):
+        by = torch.exp(torch.randn(cache.k_scale.shape, generator=g) * spread).float()
+        getattr(cache, name).mul_(by.cuda())
+        setattr(plain, name, np.where(np.isfinite(to_f64(getattr(cache, name))), to_f64(getattr(cache, name)), 1.0))
+    check_attention(cache, plain, table, lens, Hq, Sq)
+
+
+@pytest.mark.parametrize("Hq,Sq", [(2, 1), (2, 40)])
+@pytest.mark.parametrize("zero", ["some", "all"])
+def test_attention_over_blocks_of_zeros(Hq, Sq, zero):
+    """Blocks whose values are all zero have the smallest scale; their keys count all the same."""
+    lens = [600, 90]
+    cache, table = make(2, 2, 64, 16, 600, seed=14)
+    plain = PlainCache(cache.k.shape[0], 2, 16, 64)
+    k, v = rows((2, 2, 600, 64), 91), rows((2, 2, 600, 64), 92)
+    v[:, :, 64:330] = 0
+    if zero == "all":
+        v.zero_()
+    set_lens(cache, lens)
+    cache.write(k.cuda(), v.cuda(), new_lens=ints(lens))
+    plain.write(to_f64(k), to_f64(v), table, lens, lens)
+    check_attention(cache, plain, table, lens, Hq, Sq)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two caches, each on its own stream with its own workspace, run side by side as they run alone."""
+    made, want = [], []
+    for i, (lens, Hq, Sq) in enumerate((([9000, 200], 8, 1), ([5000, 4000], 4, 64))):
+        cache, table = make(2, 2, 128, 64, max(lens), seed=15 + i)
+        fill(cache, table, lens, seed=95 + i)
+        q = rows((2, Hq, Sq, 128), 96 + i).cuda()
+        made.append((cache, q, torch.cuda.Stream()))
+        want.append(cache.attention(q))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [cache.attention(q, stream=stream) for cache, q, stream in made]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
