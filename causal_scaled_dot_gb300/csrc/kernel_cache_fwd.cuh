@@ -355,12 +355,10 @@ drain:
         }
 }
 
-// Whether barrier a's phase ends before barrier b's, looked at in turn (b if both have).  After kLooks: true, for the
-// caller to wait for a.  64 looks spare one token of 32 heads over 4096 keys 0.5 us of 13.5; where rows are many, and
-// K mostly there, one look is right more often (32 rows: 2% less time).
-template <int kLooks>
+// Whether barrier a's phase ends before barrier b's, looked at in turn; false: b's has ended.  After 64 looks: true, for
+// the caller to wait for a.  (With one look, 128 short sequences of 16 heads take 52.6 us instead of 49.3.)
 __device__ __forceinline__ bool cache_comes_first(uint32_t a, uint32_t a_phase, uint32_t b, uint32_t b_phase) {
-    for (int i = 0; i < kLooks; ++i) {
+    for (int i = 0; i < 64; ++i) {
         if (__any_sync(0xffffffffu, ptx::mbar_test_wait(b, b_phase))) return false;
         if (__any_sync(0xffffffffu, ptx::mbar_test_wait(a, a_phase))) return true;
     }
@@ -428,14 +426,16 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
         const uint64_t b = ptx::sdesc_rows<128>(base + L::kQ + (uint32_t)ub * L::kN * 128);
         for (int k = 0; k < n; ++k, ++g) {
             const int sb = g & 1;
-            // The last tile's O^T goes first when its weights are there before this tile's K.
-            if (prev_unit >= 0 &&
-                cache_comes_first<R == 32 ? 1 : 64>(cache_bar<L>(base, L::kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1,
-                                  cache_bar<L>(base, L::kKFull + ring.stage), ring.phase) &&
-                !issue_pv())
-                break;
+            // The last tile's O^T goes first when its weights are there before this tile's K.  (A look at a barrier takes
+            // 200 cycles here, so K is not waited for when it has been seen.)
+            bool k_there = false;
+            if (prev_unit >= 0) {
+                k_there = !cache_comes_first(cache_bar<L>(base, L::kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1,
+                                             cache_bar<L>(base, L::kKFull + ring.stage), ring.phase);
+                if (!k_there && !issue_pv()) break;
+            }
             // The buffer of S^T is free: every warp has written the weights of tile g - 2, whose O^T is issued.
-            if (!wait(L::kKFull + ring.stage, ring.phase)) break;
+            if (!k_there && !wait(L::kKFull + ring.stage, ring.phase)) break;
             ptx::tc_fence_after();
             const uint64_t a = ptx::sdesc_rows<128>(base + (uint32_t)ring.stage * L::kStageBytes);
             const uint32_t st = tmem + L::kS + (uint32_t)(sb * L::kN);

@@ -24,6 +24,8 @@ _DIMS3 = ctypes.c_longlong * 3
 # building a Stream object takes longer than the rest of a call's checks.
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_BF16 = torch.bfloat16
 # Workspaces by (device, stream): calls on one stream run one after the other, so they share one.
 # Captured calls do not take part: each has its own from the graph's memory, as graphs may be
 # replayed on any stream.
@@ -31,9 +33,7 @@ _workspaces: dict = {}
 
 
 def _strides(name, x):
-    """{batch, head, token} strides of [B, H, S, D] for the C call: None when contiguous."""
-    if x.is_contiguous():
-        return None
+    """{batch, head, token} strides of [B, H, S, D] for the C call (NULL stands for contiguous)."""
     if x.shape[3] > 1 and x.stride(3) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # The stride of a dimension of one element is never used, and may be any number.
@@ -118,18 +118,20 @@ class KVCache:
 
     def _rows(self, name, x, heads, S=None, strided=True):
         """Checks a bf16 tensor [B, heads, S, D] on the cache's device; returns S and its strides."""
-        if x.dtype != torch.bfloat16 or x.device != self._device:
+        if x.dtype is not _BF16 or x.device != self._device:
             raise ValueError(f"{name} must be a bf16 tensor on {self._device}")
         B, Hkv, D = self._sizes
         shape = x.shape
         if len(shape) != 4 or shape[0] != B or shape[3] != D or shape[2] < 1 or (heads and shape[1] != heads) or (
                 S is not None and shape[2] != S):
             raise ValueError(f"{name} must be [{B}, {heads or 'Hq'}, {S or 'S'}, {D}], got {list(shape)}")
-        if not strided and not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if strided and x.requires_grad and torch.is_grad_enabled():
+        contiguous = x.is_contiguous()
+        if not strided:
+            if not contiguous:
+                raise ValueError(f"{name} must be contiguous")
+        elif x.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
-        return shape[2], _strides(name, x) if strided else None
+        return shape[2], None if contiguous else _strides(name, x)
 
     def _counts(self, name, t):
         if t is None:
@@ -154,7 +156,7 @@ class KVCache:
 
     def _here(self, stream) -> bool:
         """Whether a call can run as things are: on the current device's current stream."""
-        return stream is None and torch.cuda.current_device() == self._index
+        return stream is None and _current_device() == self._index
 
     def _done(self, where, rc, handle, check_status) -> None:
         if rc != native.ATTN_OK:
