@@ -79,6 +79,7 @@ struct CacheFwdParams {
 
 template <int R>
 struct CacheLayout {
+    static constexpr bool kWide = false;
     static constexpr int kWgs = R >= 32 ? 4 : 2;   // softmax warpgroups
     static constexpr int kThreads = 128 + 128 * kWgs;
     static constexpr int kH = R / kWgs;            // rows of one softmax warpgroup
@@ -158,6 +159,8 @@ __device__ int cache_locate(const CachePlan& p, int* scan, unsigned int* status,
                             CachePlace* place) {
     const int cta = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::launch_next();
+    ptx::wait_previous();
     const int pairs = p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
     const int first = min(tid * per, pairs), last = min(first + per, pairs);
     bool bad = false;

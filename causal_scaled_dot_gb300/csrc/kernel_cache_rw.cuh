@@ -81,6 +81,8 @@ template <int kThreads>
 __global__ void __launch_bounds__(256, 4) attn_cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
     constexpr int kVec = 8;
     __shared__ uint32_t warp_max[8];
+    ptx::launch_next();
+    ptx::wait_previous();
     const CacheView& c = p.c;
     const int t = threadIdx.x % kThreads;
     const int unit = blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
@@ -196,6 +198,8 @@ struct CacheReadParams {
 template <int kThreads>
 __global__ void __launch_bounds__(256, 4) attn_cache_read_kernel(const __grid_constant__ CacheReadParams p) {
     constexpr int kVec = 8;
+    ptx::launch_next();
+    ptx::wait_previous();
     const CacheView& c = p.c;
     const int t = threadIdx.x % kThreads, unit = blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
     if (unit >= p.num_units) return;

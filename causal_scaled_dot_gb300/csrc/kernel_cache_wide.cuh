@@ -35,6 +35,7 @@ namespace attn {
 
 struct CacheWideLayout {
     static constexpr int kR = 128;                 // query rows of a unit
+    static constexpr bool kWide = true;
     static constexpr int kThreads = 192;           // warps 0-3 softmax, 4 pages, 5 products
     static constexpr int kCtas = 2;                // per SM
     static constexpr int kStages = 2;
