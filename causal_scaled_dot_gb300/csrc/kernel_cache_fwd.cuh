@@ -159,6 +159,8 @@ __device__ int cache_locate(const CachePlan& p, int* scan, unsigned int* status,
                             CachePlace* place) {
     const int cta = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // A later launch's block on this SM waits for this one and may hold tensor memory meanwhile.  It takes none that this
+    // one needs: shared memory admits two R = 8 blocks (64 columns each) or one beside a wide one (256), and no other pair.
     ptx::launch_next();
     ptx::wait_previous();
     const int pairs = p.B * p.q_tiles, per = (pairs + kThreads - 1) / kThreads;
