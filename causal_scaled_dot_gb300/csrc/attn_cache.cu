@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -101,10 +102,11 @@ constexpr int kWholeTiles = 4;
 // Tiles that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 33 us with 4, 45
 // with 1, 39 with 2 or 6; 1 joins more pieces, 6 leaves SMs without work.
 constexpr int kWideLeast = 4;
-// CTAs that a unit keeps busy at most when there are no more units: one CTA joins the pieces.  One sequence of 131072
-// keys, 8 / 16 / 32 / 128 rows over one key/value head: 28 / 31 / 41 / 97 us with 64, 26 / 34 / 47 / 145 with 128, and
-// 39 / 38 / 48 / 95 with 32.
-constexpr int kMostPieces = 64;
+// CTAs that a unit keeps busy at most when there are few, and those that few units keep busy at least.  131072 keys, one
+// unit of 8 / 16 / 32 / 128 rows: 22 / 24 / 30 / 54 us with 128 CTAs, 27 / 28 / 36 / 59 with 64; two units of 128 rows:
+// 58 with 128, 64 with 256; four of 4 rows over up to 41891 keys: 19 with 256, 26 with 304, which leave no room for the
+// next call's start.
+constexpr int kMostPieces = 64, kFewBlocks = 128;
 long long tiles_of(const attn_cache_t* c) {
     return ((long long)c->max_blocks * c->block_size + kCacheTile - 1) / kCacheTile;
 }
@@ -114,13 +116,13 @@ struct Workspace {  // offsets of its parts, and its size
     unsigned long long ml, tickets, bytes;
 };
 Workspace workspace_of(const attn_cache_t* c, int R, int sms) {
-    // two partial units per CTA: R rows of 128 sums, and (M, l); a ticket per CTA
+    // two partial units per CTA: R rows of 128 sums, and (M, l); two tickets per CTA
     const unsigned long long ctas = (unsigned long long)sms * ctas_per_sm(R);
     Workspace w{};
     if (!splits(c)) return w;
     w.ml = ctas * 2 * R * 128 * 4;
     w.tickets = w.ml + ctas * 2 * R * 8;
-    w.bytes = w.tickets + ctas * 8;
+    w.bytes = w.tickets + ctas * 16;
     return w;
 }
 
@@ -179,9 +181,10 @@ int launch_fwd(K kernel, const CUtensorMap& tk, const CUtensorMap& tv, const Cac
                cudaStream_t st) {
     const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads, most = (long long)sms * L::kCtas;
     if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
-    const long long work = p.plan.whole ? units : units * (tiles < kMostPieces ? tiles : kMostPieces);  // CTAs of use
-    const int grid = (int)(work < most ? work : most);
-    return launch(kernel, grid, L::kThreads, L::kDynamicSmem, !L::kWide, st, tk, tv, p);
+    const long long work = p.plan.whole ? units : units * tiles;  // CTAs that would get something
+    const long long use = p.plan.whole || units * kMostPieces > kFewBlocks ? units * kMostPieces : kFewBlocks;
+    const long long grid = std::min(std::min(work, use), most);
+    return launch(kernel, (int)grid, L::kThreads, L::kDynamicSmem, !L::kWide, st, tk, tv, p);
 }
 
 // Launches a write or read kernel with the threads per unit that hold the

@@ -169,6 +169,7 @@ ATTN_HD int plan_begin(int total, int cta, int ctas) {
 }
 // The CTA of plan_ctas() many that takes a tile: the largest with plan_begin() <= tile.
 ATTN_HD int plan_cta(int total, int tile, int ctas) {
+    if (total < 1 << 22 && ctas < 1 << 10) return (int)((((unsigned)tile + 1) * (unsigned)ctas - 1) / (unsigned)total);
     return (int)((((long long)tile + 1) * ctas - 1) / total);
 }
 

@@ -69,8 +69,8 @@ struct CacheFwdParams {
     float scale_log2;       // scale * log2(e)
     float* part_o;          // [G][2][R][128] partial sums of w code
     float2* part_ml;        // [G][2][R] their M - 4 and sum of w / vs
-    // [G]: pieces left of the unit that begins in a CTA, below a number (the upper 48 bits) that marks this
-    // launch: whatever stood there before counts as none.  0 again after each join, since a captured launch
+    // [2][G]: pieces left of a group, and groups of the unit that begins in a CTA, below a number (the upper 48
+    // bits) that marks this launch: whatever stood there before counts as none.  0 again after each join, since a captured launch
     // comes again with its number.
     unsigned long long* tickets;
     unsigned long long ticket;
@@ -84,6 +84,7 @@ struct CacheLayout {
     static constexpr int kThreads = 128 + 128 * kWgs;
     static constexpr int kH = R / kWgs;            // rows of one softmax warpgroup
     static constexpr int kCtas = R == 8 ? 2 : 1;   // per SM
+    static constexpr int kJoin = 24;               // pieces that one CTA joins
     static constexpr int kStages = R == 8 ? 3 : R == 16 ? 6 : 5;
     static constexpr int kN = 2 * R;               // rows of Qp and Pp: hi and lo pieces
     static constexpr int kWidth = 2 * kH;          // columns of one softmax warpgroup: its rows' hi, then lo pieces
@@ -142,7 +143,7 @@ struct CacheWork {
 struct CacheShared {
     CacheUnit u;
     int first, pieces;  // the CTA where it begins, and the CTAs that share it (0: no such unit)
-    int last;           // 1: this CTA was the last to leave its piece
+    int last;           // 1: this CTA was the last of its group to leave its piece, then of all groups
 };
 static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48 && sizeof(CacheShared) <= 64, "shared memory layout");
 
@@ -210,12 +211,33 @@ __device__ __forceinline__ void cache_share(CacheShared* shared, const CacheUnit
     shared->first = plan_cta(total, pos - u.t, ctas);
     shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
 }
+// Pieces that one CTA joins: up to `most` all of them, else the square root, so that groups of pieces are joined side by
+// side and then the groups: 128 rows of one key/value head over 131072 keys, 128 pieces, take 54 us instead of 145, and
+// 8 rows 22 instead of 26; for fewer pieces the second round costs more than it saves (10 pieces of 1 row: 16.1 us
+// against 13.7).
+__device__ __forceinline__ int cache_group(int pieces, int most) {
+    if (pieces <= most) return pieces;
+    int n = 2;
+    while (n * n < pieces) ++n;
+    return n;
+}
+// Counter of the group that a unit's piece is in, and of the unit's groups.  A group of one piece needs none, so no two
+// units meet at one.
+__device__ __forceinline__ unsigned long long* cache_ticket(const CacheFwdParams& p, int first, int piece, int group) {
+    return p.tickets + first + (piece < group ? 0 : piece / group * group);
+}
+__device__ __forceinline__ unsigned long long* cache_unit_ticket(const CacheFwdParams& p, int first) {
+    return p.tickets + gridDim.x + first;
+}
 // Each CTA that shares a unit does this before it counts its piece: a counter that does not carry this launch's
 // number becomes 0 pieces of this launch.  An exchange that fails met another CTA's, which did the same.
-__device__ __noinline__ void cache_open_ticket(const CacheFwdParams& p, int first) {
-    unsigned long long* at = p.tickets + first;
-    const unsigned long long had = __ldcg(at);
-    if ((had ^ p.ticket) >> 16) atomicCAS(at, had, p.ticket);
+__device__ __noinline__ void cache_open_tickets(const CacheFwdParams& p, int begin, int tiles, int total, int ctas, int most) {
+    const int first = plan_cta(total, begin, ctas), pieces = plan_cta(total, begin + tiles - 1, ctas) - first + 1;
+    const int group = cache_group(pieces, most);
+    unsigned long long *a = cache_ticket(p, first, blockIdx.x - first, group), *b = cache_unit_ticket(p, first);
+    const unsigned long long had_a = __ldcg(a), had_b = __ldcg(b);
+    if ((had_a ^ p.ticket) >> 16) atomicCAS(a, had_a, p.ticket);
+    if (group < pieces && (had_b ^ p.ticket) >> 16) atomicCAS(b, had_b, p.ticket);
 }
 
 // log2 of a row's largest weight when its maximum M is new.  The weights of the tiles after it may be up to 448 /
@@ -316,7 +338,7 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
             if (t == u.t) {
                 block2 = more2 ? block_of(g2, u2.t * pages + lane, e2) : -1;
                 sc2 = scales(g2, block2);
-                if (leader && u.n < u.tiles) cache_open_ticket(p, plan_cta(total, pos - u.t, ctas));
+                if (leader && u.n < u.tiles) cache_open_tickets(p, pos - u.t, u.tiles, total, ctas, L::kJoin);
                 __syncwarp();
             }
             // pages that some row should see but that the table places outside the cache
@@ -892,15 +914,25 @@ __device__ __noinline__ bool cache_last_piece(unsigned long long* at, int pieces
     return true;
 }
 
+// Pieces x0, x0 + step, ... (`n` of them) of a shared unit.  Each is slot 1 of the CTA where the unit begins or slot 0 of
+// a following one.  `final`: the joined rows go to out and lse, else to the place of piece x0.
+struct CacheJoin {
+    const CacheShared& shared;
+    int x0, n, step;
+    bool final;
+    __device__ long long slot(int x) const {
+        const int piece = x0 + x * step;
+        return (long long)(shared.first + piece) * 2 + (piece == 0 ? 1 : 0);
+    }
+};
 // Joins rows r .. r + kRows - 1 of a shared unit, a warp for all:
-// O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i over the pieces, which are slot 1 of the first CTA and slot 0 of the
-// following ones, R rows each.  A lane takes every 32nd piece's (M, l), and 4 columns of every piece's O, of which
+// O = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i over the pieces, R rows each.  A lane takes every 32nd piece's (M, l), and 4 columns of every piece's O, of which
 // 8 are under way at once.
 template <int kRows>
-__device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shared, int R, int r) {
-    const int lane = threadIdx.x & 31, n = shared.pieces;
+__device__ void cache_join_rows(const CacheFwdParams& p, const CacheJoin& join, int R, int r) {
+    const int lane = threadIdx.x & 31, n = join.n;
     const bool mine = lane * 4 < p.c.D;
-    auto slot = [&](int x) { return ((long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0)) * R + r; };
+    auto slot = [&](int x) { return join.slot(x) * R + r; };
     auto piece = [&](int x, int y) { return x < n ? __ldcg(p.part_ml + slot(x) + y) : make_float2(-INFINITY, 0.f); };
     float m[kRows], l[kRows];  // of the lane's pieces, then of all
 #pragma unroll
@@ -960,9 +992,15 @@ __device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shar
     }
 #pragma unroll
     for (int y = 0; y < kRows; ++y) {
+        if (!join.final) {  // where this warp alone has read
+            if (mine) *(reinterpret_cast<float4*>(p.part_o + (slot(0) + y) * 128) + lane) = o[y];
+            __syncwarp();
+            if (lane == 0) p.part_ml[slot(0) + y] = make_float2(m[y], l[y]);
+            continue;
+        }
         int qi, hq;
-        if (!cache_row(p, shared.u, r + y, &qi, &hq)) continue;
-        const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
+        if (!cache_row(p, join.shared.u, r + y, &qi, &hq)) continue;
+        const long long at = ((long long)join.shared.u.b * p.Hq + hq) * p.Sq + qi;
         const float inv = l[y] == 0.f ? 0.f : ptx::rcp(l[y]);
         if (mine)
             *reinterpret_cast<uint2*>(p.out + at * p.c.D + lane * 4) =
@@ -971,20 +1009,43 @@ __device__ void cache_join_rows(const CacheFwdParams& p, const CacheShared& shar
     }
 }
 
-// The end of a CTA, by all its threads, once every piece is left: of each unit that it shares, whoever counts
-// last joins the pieces.
-template <typename F>
+// The end of a CTA, by all its threads, once every piece is left: of each unit that it shares, whoever counts last in
+// its group joins the group's pieces, and whoever is the last of those joins the groups.
+template <typename L, typename F>
 __device__ void cache_join(const CacheFwdParams& p, CacheShared* shared, bool aborted, F join) {
     if (shared[0].pieces == 0 && shared[1].pieces == 0) return;
     if (threadIdx.x < 2) {
         CacheShared& x = shared[threadIdx.x];
         __threadfence();
-        x.last = x.pieces > 0 && !aborted && cache_last_piece(p.tickets + x.first, x.pieces);
+        x.last = 0;
+        if (x.pieces > 0 && !aborted) {
+            const int piece = blockIdx.x - x.first, group = cache_group(x.pieces, L::kJoin);
+            const int n = piece < group ? group : min(group, x.pieces - piece / group * group);
+            x.last = n == 1 || cache_last_piece(cache_ticket(p, x.first, piece, group), n);
+        }
         __threadfence();
     }
     __syncthreads();
-    for (int x = 0; x < 2; ++x)
-        if (shared[x].pieces > 0 && shared[x].last) join(shared[x]);
+    for (int i = 0; i < 2; ++i) {
+        CacheShared& x = shared[i];
+        if (x.pieces == 0 || !x.last) continue;
+        const int group = cache_group(x.pieces, L::kJoin);
+        if (group == x.pieces) {
+            join(CacheJoin{x, 0, group, 1, true});
+            continue;
+        }
+        const int groups = (x.pieces + group - 1) / group, begin = (blockIdx.x - x.first) / group * group;
+        const int n = min(group, x.pieces - begin);
+        if (n > 1) join(CacheJoin{x, begin, n, 1, false});
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            x.last = cache_last_piece(cache_unit_ticket(p, x.first), groups);
+            __threadfence();
+        }
+        __syncthreads();
+        if (x.last) join(CacheJoin{x, 0, groups, group, true});
+    }
 }
 
 template <int R>
@@ -1053,7 +1114,7 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-    cache_join(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0, [&](const CacheShared& x) {
+    cache_join<L>(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0, [&](const CacheJoin& x) {
         constexpr int kWarps = L::kThreads / 32, kRows = (R + kWarps - 1) / kWarps;
         static_assert(R % kRows == 0, "rows of a warp");
         if (warp * kRows < R) cache_join_rows<kRows>(p, x, R, warp * kRows);

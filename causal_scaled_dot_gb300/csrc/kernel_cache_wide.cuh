@@ -38,6 +38,7 @@ struct CacheWideLayout {
     static constexpr bool kWide = true;
     static constexpr int kThreads = 192;           // warps 0-3 softmax, 4 pages, 5 products
     static constexpr int kCtas = 2;                // per SM
+    static constexpr int kJoin = 8;                // pieces that one CTA joins
     static constexpr int kStages = 2;
     static constexpr uint32_t kTileBytes = 128 * 128;
     static constexpr uint32_t kStageBytes = 2 * kTileBytes;
@@ -406,14 +407,14 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
 }
 
 // Joins a shared unit, a row per thread of warps 0-3; 32 columns of two pieces are under way at once.
-__device__ void cache_wide_join(const CacheFwdParams& p, const CacheShared& shared) {
+__device__ void cache_wide_join(const CacheFwdParams& p, const CacheJoin& join) {
     using L = CacheWideLayout;
-    const int r = threadIdx.x, n = shared.pieces;
+    const int r = threadIdx.x, n = join.n;
+    const CacheUnit& u = join.shared.u;
     int qi, hq;
-    if (r >= L::kR || !cache_row(p, shared.u, r, &qi, &hq)) return;
-    const long long at = ((long long)shared.u.b * p.Hq + hq) * p.Sq + qi;
-    // The pieces: slot 1 of the first CTA, slot 0 of the following ones.
-    auto slot = [&](int x) { return (long long)(shared.first + x) * 2 + (x == 0 ? 1 : 0); };
+    if (r >= L::kR || !cache_row(p, u, r, &qi, &hq)) return;
+    const long long at = ((long long)u.b * p.Hq + hq) * p.Sq + qi;
+    auto slot = [&](int x) { return join.slot(x); };
     float m = -INFINITY, l = 0.f;
 #pragma unroll 4
     for (int x = 0; x < n; ++x) {
@@ -423,7 +424,7 @@ __device__ void cache_wide_join(const CacheFwdParams& p, const CacheShared& shar
         m = top;
     }
     const float inv = l == 0.f ? 0.f : ptx::rcp(l), ref = m == -INFINITY ? 0.f : m;
-    if (p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
+    if (join.final && p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
     for (int c = 0; c < p.c.D / 4; c += 8) {
         float4 o[8];
 #pragma unroll
@@ -438,6 +439,11 @@ __device__ void cache_wide_join(const CacheFwdParams& p, const CacheShared& shar
             for (int i = 0; i < 8; ++i)
                 o[i] = make_float4(o[i].x + f * v[i].x, o[i].y + f * v[i].y, o[i].z + f * v[i].z, o[i].w + f * v[i].w);
         }
+        if (!join.final) {  // where this thread alone has read
+#pragma unroll
+            for (int i = 0; i < 8; ++i) reinterpret_cast<float4*>(p.part_o)[(slot(0) * 32 + c + i) * L::kR + r] = o[i];
+            continue;
+        }
         uint4* to = reinterpret_cast<uint4*>(p.out + at * p.c.D + c * 4);
 #pragma unroll
         for (int i = 0; i < 8; i += 2)
@@ -445,6 +451,7 @@ __device__ void cache_wide_join(const CacheFwdParams& p, const CacheShared& shar
                                    ptx::pack_bf16x2(o[i + 1].x * inv, o[i + 1].y * inv),
                                    ptx::pack_bf16x2(o[i + 1].z * inv, o[i + 1].w * inv));
     }
+    if (!join.final) p.part_ml[slot(0) * L::kR + r] = make_float2(m, l);
 }
 
 __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kCtas)
@@ -506,8 +513,8 @@ __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kC
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-    cache_join(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0,
-               [&](const CacheShared& x) { cache_wide_join(p, x); });
+    cache_join<L>(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0,
+               [&](const CacheJoin& x) { cache_wide_join(p, x); });
 }
 
 }  // namespace attn

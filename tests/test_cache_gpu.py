@@ -199,7 +199,8 @@ def test_attention_several_tokens(D, block, Hq, Hkv, Sq, causal):
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,D,block,Sq", [([20011], 8, 1, 128, 64, 1), ([9000, 5], 4, 2, 64, 16, 2),
-                                                    ([2500], 64, 1, 128, 128, 2)])
+                                                    ([2500], 64, 1, 128, 128, 2), ([9000, 700], 40, 1, 128, 64, 1),
+                                                    ([12345], 9, 1, 64, 32, 1), ([20011, 3000], 50, 2, 64, 64, 4)])
 def test_attention_long_cache_is_joined(lens, Hq, Hkv, D, block, Sq):
     cache, table = make(len(lens), Hkv, D, block, max(lens), seed=10)
     plain = fill(cache, table, lens, seed=51)
