@@ -99,8 +99,12 @@ int ctas_per_sm(int R) { return R == 128 ? CacheWideLayout::kCtas : R == 8 ? Cac
 // units are not split: joining two pieces takes about as long as three more
 // tiles in the same CTA.
 constexpr int kWholeTiles = 4;
-// Tiles that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 33 us with 4, 45
-// with 1, 39 with 2 or 6; 1 joins more pieces, 6 leaves SMs without work.
+// What changing to a unit costs a CTA, in key tiles: q, the first maximum, the row's leaving.  Counted as nothing (0),
+// CTAs with many short units end last: 33 sequences of up to 2060 tokens and one empty slot, 16 heads of 64, take 60 us,
+// and 37 with 3; 16 x 5 drafted tokens 51 and 47; 4 x 64 tokens over 2000 keys 34 and 27.  With 2 and 4, 0 to 3 % more.
+constexpr int kStart = 3;
+// Places that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 27 us with 4,
+// 30 with 1, 33 with 6; 1 joins more pieces, 6 leaves SMs without work.
 constexpr int kWideLeast = 4;
 // CTAs that a unit keeps busy at most when there are few, and those that few units keep busy at least.  131072 keys, one
 // unit of 8 / 16 / 32 / 128 rows: 22 / 24 / 30 / 54 us with 128 CTAs, 27 / 28 / 36 / 59 with 64; two units of 128 rows:
@@ -180,7 +184,7 @@ template <typename L, typename K>
 int launch_fwd(K kernel, const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int sms, long long tiles,
                cudaStream_t st) {
     const long long units = (long long)p.plan.B * p.plan.q_tiles * p.plan.heads, most = (long long)sms * L::kCtas;
-    if (units > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
+    if (units > 0x7fffffffll / (tiles + p.plan.start)) return ATTN_ERR_UNSUPPORTED;
     const long long work = p.plan.whole ? units : units * tiles;  // CTAs that would get something
     const long long use = p.plan.whole || units * kMostPieces > kFewBlocks ? units * kMostPieces : kFewBlocks;
     const long long grid = std::min(std::min(work, use), most);
@@ -356,6 +360,7 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     p.plan.heads = cache->Hkv * p.hgroups;
     p.plan.whole = splits(cache) ? 0 : 1;
     p.plan.least = R == 128 && !p.plan.whole ? kWideLeast : 1;
+    p.plan.start = p.plan.whole ? 0 : kStart;
     const long long tiles = tiles_of(cache);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (R) {

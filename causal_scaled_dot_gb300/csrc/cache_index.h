@@ -71,10 +71,11 @@ ATTN_HD unsigned long long cache_offset(int block, int head, int slot, int Hkv, 
 // A unit is one sequence, one tile of query rows and one group of query heads
 // that share a key/value head; it takes the key tiles (128 keys) 0 .. tiles-1.
 // All units' tiles stand in one row, by sequence, query tile, head, key tile,
-// and CTA c of G takes tiles [c T / G, (c + 1) T / G) of it, so CTAs get equal
-// work whatever the lengths; the pieces of a unit that crosses a border are
+// with `start` empty places before each unit's (what changing to it costs, in
+// tiles), and CTA c of G takes places [c T / G, (c + 1) T / G) of it, so CTAs get
+// equal work whatever the lengths; the pieces of a unit that crosses a border are
 // joined by the CTA that finishes last.  Where every unit is short (`whole`),
-// CTAs take whole units instead, a unit counting as one tile.
+// CTAs take whole units instead, a unit counting as one place.
 // Lengths are device data, so this runs on the device.  The host makes sure
 // that T fits in 31 bits.
 constexpr int kCacheTile = 128;  // keys per tile
@@ -86,7 +87,8 @@ struct CachePlan {
     int q_tiles;  // query tiles of Sq queries
     int heads;    // head groups per sequence and query tile
     int whole;    // 1: units are not split
-    int least;    // tiles that a CTA takes at least (but for the total's remainder), 1 or more
+    int least;    // places that a CTA takes at least (but for the total's remainder), 1 or more
+    int start;    // places before a unit's tiles
 };
 
 ATTN_HD CacheSpan plan_span(const CachePlan& p, int b, bool* bad) {
@@ -105,10 +107,10 @@ ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
     return n <= kCacheTile ? 1 : (n + kCacheTile - 1) / kCacheTile;
 }
 
-// What a unit of `tiles` key tiles counts in the row of all tiles.
-ATTN_HD int plan_cost(const CachePlan& p, int tiles) { return p.whole ? 1 : tiles; }
+// Places of a unit of `tiles` key tiles.
+ATTN_HD int plan_cost(const CachePlan& p, int tiles) { return p.whole ? 1 : p.start + tiles; }
 
-// Tiles of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
+// Places of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
 ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
     if (first >= last) return 0;
     int sum = 0;
@@ -126,10 +128,9 @@ ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
 }
 
 struct CachePlace {
-    int b, qt, h, t;
+    int b, qt, h, s;  // the s-th of a unit's places
 };
-// The place of the tile `offset` tiles after the start of pair `first`
-// (offset < the tiles of the pairs from there on).
+// The place `offset` places after the start of pair `first` (offset < the places of the pairs from there on).
 ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
     bool bad = false;
     const int b = p.q_tiles == 1 ? first : first / p.q_tiles;
@@ -145,7 +146,7 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
             const int tiles = plan_cost(p, plan_tiles(p, s, x.qt));
             if (offset < tiles * p.heads) {
                 x.h = offset / tiles;
-                x.t = offset - x.h * tiles;
+                x.s = offset - x.h * tiles;
                 return x;
             }
             offset -= tiles * p.heads;
@@ -154,40 +155,41 @@ ATTN_HD CachePlace plan_find(const CachePlan& p, int first, int offset) {
     }
 }
 
-// The CTAs that share `total` tiles: all, or as many as leave each `least`
-// tiles, and so none without a tile between the first and the last piece of a unit.
+// The CTAs that share `total` places: all, or as many as leave each `least`, and so none without a tile between the
+// first and the last piece of a unit.
 ATTN_HD int plan_ctas(const CachePlan& p, int total, int ctas) {
     const int most = (total + p.least - 1) / p.least;
     return most < ctas ? most : ctas;
 }
-// First tile of CTA `cta` of plan_ctas() many (the total for those past them):
+// First place of CTA `cta` of plan_ctas() many (the total for those past them):
 // total * cta / ctas, for fewer than 2^15 CTAs.
 ATTN_HD int plan_begin(int total, int cta, int ctas) {
     if (cta >= ctas) return total;
     const int q = total / ctas, r = total - q * ctas;
     return q * cta + (r * cta) / ctas;
 }
-// The CTA of plan_ctas() many that takes a tile: the largest with plan_begin() <= tile.
-ATTN_HD int plan_cta(int total, int tile, int ctas) {
-    if (total < 1 << 22 && ctas < 1 << 10) return (int)((((unsigned)tile + 1) * (unsigned)ctas - 1) / (unsigned)total);
-    return (int)((((long long)tile + 1) * ctas - 1) / total);
+// The CTA of plan_ctas() many that takes a place: the largest with plan_begin() <= place.
+ATTN_HD int plan_cta(int total, int place, int ctas) {
+    if (total < 1 << 22 && ctas < 1 << 10) return (int)((((unsigned)place + 1) * (unsigned)ctas - 1) / (unsigned)total);
+    return (int)((((long long)place + 1) * ctas - 1) / total);
 }
 
 // A CTA's share of one unit: key tiles t .. t + n - 1 of its `tiles`.
 struct CacheUnit {
     int b, qt, h, t, n, tiles, keys;
+    int at;  // place of its tile 0 in the row of all
     CacheSpan s;
 };
-// Walks the units of a run of `left` tiles from a place on.
+// Walks the units of a run of `left` places, the first of which is place `pos` of the row.
 struct CacheCursor {
     CachePlace at;
-    int left;
+    int pos, left;
     CacheSpan s;
     int tiles;
 };
-ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, int left) {
+ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, int pos, int left) {
     bool bad = false;
-    CacheCursor c{at, at.b < p.B ? left : 0, {}, 0};
+    CacheCursor c{at, pos, at.b < p.B ? left : 0, {}, 0};
     if (c.left > 0) {
         c.s = plan_span(p, at.b, &bad);
         c.tiles = plan_tiles(p, c.s, at.qt);
@@ -199,13 +201,21 @@ ATTN_HD bool cursor_next(const CachePlan& p, CacheCursor& c, CacheUnit& u) {
     u.b = c.at.b;
     u.qt = c.at.qt;
     u.h = c.at.h;
-    u.t = c.at.t;
     u.tiles = c.tiles;
-    u.n = p.whole || c.tiles - c.at.t < c.left ? c.tiles - c.at.t : c.left;
+    const int rest = plan_cost(p, c.tiles) - c.at.s, places = rest < c.left ? rest : c.left;
+    const int start = p.whole ? 0 : p.start, end = p.whole ? c.tiles : c.at.s + places - start;
+    u.t = c.at.s > start ? c.at.s - start : 0;
+    u.n = end - u.t;
+    u.at = c.pos - c.at.s + start;
     u.s = c.s;
     u.keys = plan_keys(p, c.s, c.at.qt);
-    c.left -= plan_cost(p, u.n);
-    c.at.t = 0;
+    c.left -= places;
+    c.pos += places;
+    c.at.s = 0;
+    if (u.n <= 0) {  // the run ends before the unit's tiles
+        c.left = 0;
+        return false;
+    }
     if (++c.at.h == p.heads) {
         c.at.h = 0;
         bool bad = false;

@@ -205,11 +205,11 @@ __device__ __forceinline__ bool cache_row(const CacheFwdParams& p, const CacheUn
     return iq < p.plan.qper && *i < u.s.count && g < p.group;
 }
 
-// Notes a unit that CTAs share, whose first tile here is tile `pos` of all.
-__device__ __forceinline__ void cache_share(CacheShared* shared, const CacheUnit& u, int pos, int total, int ctas) {
+// Notes a unit that CTAs share.
+__device__ __forceinline__ void cache_share(CacheShared* shared, const CacheUnit& u, int total, int ctas) {
     shared->u = u;
-    shared->first = plan_cta(total, pos - u.t, ctas);
-    shared->pieces = plan_cta(total, pos - u.t + u.tiles - 1, ctas) - shared->first + 1;
+    shared->first = plan_cta(total, u.at, ctas);
+    shared->pieces = plan_cta(total, u.at + u.tiles - 1, ctas) - shared->first + 1;
 }
 // Pieces that one CTA joins: up to `most` all of them, else the square root, so that groups of pieces are joined side by
 // side and then the groups: 128 rows of one key/value head over 131072 keys, 128 pieces, take 54 us instead of 145, and
@@ -265,7 +265,7 @@ constexpr float kCacheLeastScale = -80.f;
 
 // ---------------------------------------------------------------- warp 0: pages
 template <typename L>
-__device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur, int pos,
+__device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CacheFwdParams& p, CacheCursor cur,
                                 int total, int ctas, uint32_t base, uint8_t* smem, volatile int* abort_flag) {
     const CacheView& c = p.c;
     const int lane = threadIdx.x & 31;
@@ -296,7 +296,8 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
     CacheUnit u, u2;
     bool more = cursor_next(p.plan, cur, u);
     Pages g = pages_of(u);
-    int e = entry(g, u.t * pages + lane), block = block_of(g, u.t * pages + lane, e);
+    const int e = more ? entry(g, u.t * pages + lane) : -1;
+    int block = more ? block_of(g, u.t * pages + lane, e) : -1;
     float2 sc = scales(g, block);
     while (more) {
         const bool more2 = cursor_next(p.plan, cur, u2);
@@ -338,7 +339,7 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
             if (t == u.t) {
                 block2 = more2 ? block_of(g2, u2.t * pages + lane, e2) : -1;
                 sc2 = scales(g2, block2);
-                if (leader && u.n < u.tiles) cache_open_tickets(p, pos - u.t, u.tiles, total, ctas, L::kJoin);
+                if (leader && u.n < u.tiles) cache_open_tickets(p, u.at, u.tiles, total, ctas, L::kJoin);
                 __syncwarp();
             }
             // pages that some row should see but that the table places outside the cache
@@ -365,7 +366,6 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
                 phase ^= 1u;
             }
         }
-        pos += u.n;
         more = more2;
         u = u2;
         g = g2;
@@ -493,7 +493,7 @@ __device__ void cache_mma_role(const CacheFwdParams& p, uint32_t base, uint8_t* 
 
 // ---------------------------------------------------------------- warps 2-3: query rows
 template <int R>
-__device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int pos, int total, int ctas, uint32_t base,
+__device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int total, int ctas, uint32_t base,
                                  uint8_t* smem, volatile int* abort_flag) {
     using L = CacheLayout<R>;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
@@ -574,7 +574,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
                 work->keys_all = p.plan.causal ? max(u.s.first + q0 + 1, 0) : u.s.len;
                 work->slot = u.n == u.tiles ? -1 : u.t > 0 ? 0 : 1;
                 work->rows = min(p.plan.qper, u.s.count - q0) * p.hper;
-                if (u.n < u.tiles) cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot, u, pos, total, ctas);
+                if (u.n < u.tiles) cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot, u, total, ctas);
             }
         } else if (w == 0 && lane == 0) {
             work->n = 0;
@@ -583,7 +583,6 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int p
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(cache_bar<L>(base, L::kQFull + ub));
         if (!more) return;
-        pos += u.n;
     }
 }
 
@@ -1099,11 +1098,11 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
     if (begin == end) {
         // no tile for this CTA
     } else if (warp == 0) {
-        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, begin, end - begin), total, ctas, base, smem, abort_flag);
     } else if (warp == 1) {
         cache_mma_role<R>(p, base, smem, tmem, abort_flag);
     } else if (warp < 4) {
-        cache_query_role<R>(p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
+        cache_query_role<R>(p, cursor_at(p.plan, place, begin, end - begin), total, ctas, base, smem, abort_flag);
     } else {
         cache_softmax_role<R>(p, base, smem, tmem, abort_flag);
     }

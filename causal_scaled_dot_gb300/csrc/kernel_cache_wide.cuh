@@ -151,7 +151,7 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
     }
 }
 
-__device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur, int pos, int total, int ctas,
+__device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur, int total, int ctas,
                                         uint32_t base, uint8_t* smem, uint32_t tmem, volatile int* abort_flag) {
     using L = CacheWideLayout;
     const int r = threadIdx.x, lane = r & 31;  // this thread's row of a unit, and its lane of S and O
@@ -221,11 +221,10 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
         if (r == 0) {
             *nan_seen = 0;
             if (u.n < u.tiles)
-                cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + (u.t > 0 ? 0 : 1), u, pos, total, ctas);
+                cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + (u.t > 0 ? 0 : 1), u, total, ctas);
         }
         ptx::fence_proxy_async_smem();
         arrive(L::kQFull);
-        pos += plan_cost(p.plan, u.n);
 
         float row_max = -INFINITY, peak = -INFINITY, l = 0.f;  // of s + log2 vs, its largest so far, and the sum of w / vs
         bool rose = false;  // some row's maximum did, at the half before
@@ -500,11 +499,11 @@ __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kC
     if (begin == end) {
         // no tile for this CTA
     } else if (warp == 4) {
-        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, abort_flag);
+        cache_load_role<L>(&tm_k, &tm_v, p, cursor_at(p.plan, place, begin, end - begin), total, ctas, base, smem, abort_flag);
     } else if (warp == 5) {
-        cache_wide_mma_role(p, cursor_at(p.plan, place, end - begin), base, tmem, abort_flag);
+        cache_wide_mma_role(p, cursor_at(p.plan, place, begin, end - begin), base, tmem, abort_flag);
     } else {
-        cache_wide_softmax_role(p, cursor_at(p.plan, place, end - begin), begin, total, ctas, base, smem, tmem, abort_flag);
+        cache_wide_softmax_role(p, cursor_at(p.plan, place, begin, end - begin), total, ctas, base, smem, tmem, abort_flag);
     }
 
     ptx::tc_fence_before();

@@ -289,6 +289,7 @@ int main() {
         p.heads = 1 + std::rand() % 5;
         p.whole = std::rand() % 4 == 0;
         p.least = 1 + std::rand() % 6;
+        p.start = p.whole ? 0 : std::rand() % 4;
         std::vector<int> lens(p.B), counts(p.B);
         for (int b = 0; b < p.B; ++b) {
             lens[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (p.capacity + 1);
@@ -299,7 +300,7 @@ int main() {
         p.seq_lens = lens.data();
         p.q_lens = std::rand() % 3 ? counts.data() : nullptr;
         // the units, written down one by one
-        struct U { int b, qt, h, tiles, keys; };
+        struct U { int b, qt, h, tiles, keys, at; };
         std::vector<U> want;
         int total = 0;
         for (int b = 0; b < p.B; ++b) {
@@ -311,8 +312,8 @@ int main() {
                 if (keys < 0) keys = 0;
                 const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
                 for (int h = 0; h < p.heads; ++h) {
-                    want.push_back({b, qt, h, tiles, keys});
-                    total += p.whole ? 1 : tiles;
+                    want.push_back({b, qt, h, tiles, keys, total + p.start});
+                    total += p.whole ? 1 : p.start + tiles;
                 }
             }
         }
@@ -330,35 +331,37 @@ int main() {
         int tile = 0, pieces = 0, expect_first = -1, expect_last = -1;
         for (int c = 0; c < given; ++c) {
             const int begin = plan_begin(total, c, ctas), end = plan_begin(total, c + 1, ctas);
-            CHECK((begin == end) == (c >= ctas));  // no CTA without a tile among those that share them
+            CHECK((begin == end) == (c >= ctas));  // no CTA without a place among those that share them
             if (begin == end) continue;
             int before = 0;
             int t = 0;
             while (begin >= before + sum[t]) before += sum[t++];
-            CacheCursor cur = cursor_at(p, plan_find(p, t * per, begin - before), end - begin);
+            CacheCursor cur = cursor_at(p, plan_find(p, t * per, begin - before), begin, end - begin);
             CacheUnit u;
-            int pos = begin;  // of the share in the row of all tiles
+            int seen = begin;  // places up to the last tile taken
             while (cursor_next(p, cur, u)) {
                 CHECK(unit < want.size());
                 const U& w = want[unit];
                 CHECK(u.b == w.b && u.qt == w.qt && u.h == w.h && u.tiles == w.tiles && u.keys == w.keys && u.t == tile && u.n > 0);
+                CHECK(u.at == w.at);
+                if (!p.whole) CHECK(u.at + u.t >= seen && u.at + u.t + u.n <= end && (u.t == 0 || u.at + u.t == begin));
+                seen = p.whole ? u.at + 1 : u.at + u.t + u.n;
                 CHECK(u.t + u.n <= u.tiles);
                 tile += u.n;
                 ++pieces;
                 if (pieces == 1 && tile < u.tiles) {
                     CHECK(!p.whole);
                     expect_first = c;
-                    expect_last = plan_cta(total, pos - u.t + u.tiles - 1, ctas);
+                    expect_last = plan_cta(total, u.at + u.tiles - 1, ctas);
                 }
-                if (pieces > 1) CHECK(plan_cta(total, pos - u.t, ctas) == expect_first);  // every piece finds the first
+                if (pieces > 1) CHECK(plan_cta(total, u.at, ctas) == expect_first);  // every piece finds the first
                 if (tile == u.tiles) {
                     CHECK(pieces == 1 || (expect_last == c && pieces == expect_last - expect_first + 1));
                     tile = pieces = 0;
                     ++unit;
                 }
-                pos += p.whole ? 1 : u.n;
             }
-            CHECK(pos == end);
+            CHECK(end - seen <= p.start);
         }
         CHECK(unit == want.size() && tile == 0);
     }
