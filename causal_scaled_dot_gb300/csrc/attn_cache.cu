@@ -358,9 +358,10 @@ extern "C" int attn_cache_fwd(const attn_cache_t* cache, const void* q, const lo
     p.plan.q_tiles = (Sq + p.plan.qper - 1) / p.plan.qper;
     if ((long long)cache->B * p.plan.q_tiles > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     p.plan.heads = cache->Hkv * p.hgroups;
-    p.plan.whole = splits(cache) ? 0 : 1;
+    const long long units = (long long)cache->B * p.plan.q_tiles * p.plan.heads;
+    p.plan.whole = splits(cache) ? 0 : units <= (long long)sms * ctas_per_sm(R) ? 1 : 2;
     p.plan.least = R == 128 && !p.plan.whole ? kWideLeast : 1;
-    p.plan.start = p.plan.whole ? 0 : kStart;
+    p.plan.start = p.plan.whole == 1 ? 0 : kStart;
     const long long tiles = tiles_of(cache);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (R) {

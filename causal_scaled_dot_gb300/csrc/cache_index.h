@@ -75,7 +75,8 @@ ATTN_HD unsigned long long cache_offset(int block, int head, int slot, int Hkv, 
 // tiles), and CTA c of G takes places [c T / G, (c + 1) T / G) of it, so CTAs get
 // equal work whatever the lengths; the pieces of a unit that crosses a border are
 // joined by the CTA that finishes last.  Where every unit is short (`whole`),
-// CTAs take whole units instead, a unit counting as one place.
+// CTAs take whole units instead: one place each (1), for no more units than CTAs,
+// or by the CTA where its first place falls (2).
 // Lengths are device data, so this runs on the device.  The host makes sure
 // that T fits in 31 bits.
 constexpr int kCacheTile = 128;  // keys per tile
@@ -86,7 +87,7 @@ struct CachePlan {
     int qper;     // queries per query tile
     int q_tiles;  // query tiles of Sq queries
     int heads;    // head groups per sequence and query tile
-    int whole;    // 1: units are not split
+    int whole;    // 1, 2: units are not split
     int least;    // places that a CTA takes at least (but for the total's remainder), 1 or more
     int start;    // places before a unit's tiles
 };
@@ -108,7 +109,7 @@ ATTN_HD int plan_tiles(const CachePlan& p, const CacheSpan& s, int qt) {
 }
 
 // Places of a unit of `tiles` key tiles.
-ATTN_HD int plan_cost(const CachePlan& p, int tiles) { return p.whole ? 1 : p.start + tiles; }
+ATTN_HD int plan_cost(const CachePlan& p, int tiles) { return p.whole == 1 ? 1 : p.start + tiles; }
 
 // Places of the (sequence, query tile) pairs first .. last - 1, pair = b * q_tiles + qt.
 ATTN_HD int plan_chunk(const CachePlan& p, int first, int last, bool* bad) {
@@ -187,12 +188,33 @@ struct CacheCursor {
     CacheSpan s;
     int tiles;
 };
+// To the next unit, `places` further.
+ATTN_HD void cursor_step(const CachePlan& p, CacheCursor& c, int places) {
+    c.left -= places;
+    c.pos += places;
+    c.at.s = 0;
+    if (++c.at.h < p.heads) return;
+    c.at.h = 0;
+    bool bad = false;
+    if (++c.at.qt >= plan_q_tiles(p, c.s)) {
+        c.at.qt = 0;
+        do {
+            if (++c.at.b >= p.B) {
+                c.left = 0;
+                return;
+            }
+            c.s = plan_span(p, c.at.b, &bad);
+        } while (c.s.count == 0);
+    }
+    c.tiles = plan_tiles(p, c.s, c.at.qt);
+}
 ATTN_HD CacheCursor cursor_at(const CachePlan& p, const CachePlace& at, int pos, int left) {
     bool bad = false;
     CacheCursor c{at, pos, at.b < p.B ? left : 0, {}, 0};
     if (c.left > 0) {
         c.s = plan_span(p, at.b, &bad);
         c.tiles = plan_tiles(p, c.s, at.qt);
+        if (p.whole && at.s > 0) cursor_step(p, c, plan_cost(p, c.tiles) - at.s);  // the CTA before has it
     }
     return c;
 }
@@ -202,35 +224,18 @@ ATTN_HD bool cursor_next(const CachePlan& p, CacheCursor& c, CacheUnit& u) {
     u.qt = c.at.qt;
     u.h = c.at.h;
     u.tiles = c.tiles;
-    const int rest = plan_cost(p, c.tiles) - c.at.s, places = rest < c.left ? rest : c.left;
-    const int start = p.whole ? 0 : p.start, end = p.whole ? c.tiles : c.at.s + places - start;
+    const int rest = plan_cost(p, c.tiles) - c.at.s, places = p.whole || rest < c.left ? rest : c.left;
+    const int start = p.whole == 1 ? 0 : p.start;
     u.t = c.at.s > start ? c.at.s - start : 0;
-    u.n = end - u.t;
+    u.n = (p.whole ? c.tiles : c.at.s + places - start) - u.t;
     u.at = c.pos - c.at.s + start;
     u.s = c.s;
     u.keys = plan_keys(p, c.s, c.at.qt);
-    c.left -= places;
-    c.pos += places;
-    c.at.s = 0;
     if (u.n <= 0) {  // the run ends before the unit's tiles
         c.left = 0;
         return false;
     }
-    if (++c.at.h == p.heads) {
-        c.at.h = 0;
-        bool bad = false;
-        if (++c.at.qt >= plan_q_tiles(p, c.s)) {
-            c.at.qt = 0;
-            do {
-                if (++c.at.b >= p.B) {
-                    c.left = 0;
-                    return true;
-                }
-                c.s = plan_span(p, c.at.b, &bad);
-            } while (c.s.count == 0);
-        }
-        c.tiles = plan_tiles(p, c.s, c.at.qt);
-    }
+    cursor_step(p, c, places);
     return true;
 }
 

@@ -287,9 +287,9 @@ int main() {
         p.qper = 1 + std::rand() % 16;
         p.q_tiles = (p.Sq + p.qper - 1) / p.qper;
         p.heads = 1 + std::rand() % 5;
-        p.whole = std::rand() % 4 == 0;
+        p.whole = std::rand() % 2 ? 0 : std::rand() % 3;
         p.least = 1 + std::rand() % 6;
-        p.start = p.whole ? 0 : std::rand() % 4;
+        p.start = p.whole == 1 ? 0 : std::rand() % 4;
         std::vector<int> lens(p.B), counts(p.B);
         for (int b = 0; b < p.B; ++b) {
             lens[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (p.capacity + 1);
@@ -313,7 +313,7 @@ int main() {
                 const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
                 for (int h = 0; h < p.heads; ++h) {
                     want.push_back({b, qt, h, tiles, keys, total + p.start});
-                    total += p.whole ? 1 : p.start + tiles;
+                    total += p.whole == 1 ? 1 : p.start + tiles;
                 }
             }
         }
@@ -345,7 +345,8 @@ int main() {
                 CHECK(u.b == w.b && u.qt == w.qt && u.h == w.h && u.tiles == w.tiles && u.keys == w.keys && u.t == tile && u.n > 0);
                 CHECK(u.at == w.at);
                 if (!p.whole) CHECK(u.at + u.t >= seen && u.at + u.t + u.n <= end && (u.t == 0 || u.at + u.t == begin));
-                seen = p.whole ? u.at + 1 : u.at + u.t + u.n;
+                if (p.whole) CHECK(u.at - p.start >= begin && u.at - p.start < end);
+                seen = p.whole == 1 ? u.at + 1 : u.at + u.t + u.n;
                 CHECK(u.t + u.n <= u.tiles);
                 tile += u.n;
                 ++pieces;
@@ -361,7 +362,7 @@ int main() {
                     ++unit;
                 }
             }
-            CHECK(end - seen <= p.start);
+            if (!p.whole) CHECK(end - seen <= p.start);
         }
         CHECK(unit == want.size() && tile == 0);
     }
