@@ -95,10 +95,11 @@ int rows_per_unit(long long group, long long Sq) {
 }
 int ctas_per_sm(int R) { return R == 128 ? CacheWideLayout::kCtas : R == 8 ? CacheLayout<8>::kCtas : 1; }
 
-// Key tiles that a unit may have, by the cache's capacity; up to 4 (512 tokens)
-// units are not split: joining two pieces takes about as long as three more
-// tiles in the same CTA.
-constexpr int kWholeTiles = 4;
+// Key tiles that a unit may have, by the cache's capacity, where units are not split: up to 8 (1024 tokens) joining the
+// pieces takes longer than the tiles in one CTA do.  4 x 200 tokens over up to 1000 keys 27 us, and 33 with 4; 15 x 80
+// heads over 967 keys 16.5 and 20.5; one token of 8 heads over 1000 keys 11.7 and 11.0.  With 11, 2 x 32 heads over 1400
+// keys 14.0 instead of 12.5.
+constexpr int kWholeTiles = 8;
 // What changing to a unit costs a CTA, in key tiles: q, the first maximum, the row's leaving.  Counted as nothing (0),
 // CTAs with many short units end last: 33 sequences of up to 2060 tokens and one empty slot, 16 heads of 64, take 60 us,
 // and 37 with 3; 16 x 5 drafted tokens 51 and 47; 4 x 64 tokens over 2000 keys 34 and 27.  With 2 and 4, 0 to 3 % more.

@@ -24,7 +24,7 @@
 // Two threads a row (half of a step's keys each) double what is around the weights:
 // 318 us where this takes 276, and a step of 128 keys leaves no tensor memory for
 // a second buffer of S.  2 x 1024 tokens at the end of 8192, 32 heads over 8, D =
-// 128: 276 us, 935 TFLOP/s counted once per product (the two pieces make it twice).
+// 128: 280 us, 920 TFLOP/s counted once per product (the two pieces make it twice).
 #pragma once
 
 #include <type_traits>

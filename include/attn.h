@@ -460,7 +460,7 @@ int attn_cache_fwd(const attn_cache_t *cache, const void *q, const long long *q_
 /*
  * attn_cache_workspace -- *bytes receives the workspace that attn_cache_fwd
  * needs on the current device for a cache of these sizes (its lengths do not
- * matter) and Hq and Sq; 0 for caches of up to 512 tokens a sequence.  Errors as
+ * matter) and Hq and Sq; 0 for caches of up to 1024 tokens a sequence.  Errors as
  * attn_cache_fwd.
  */
 int attn_cache_workspace(const attn_cache_t *cache, int Hq, int Sq, unsigned long long *bytes);

@@ -19,7 +19,7 @@ T = 1 << 40  # fake, never-dereferenced addresses, 2^40 bytes apart
 
 def cache(**kw):
     a = dict(k=T, v=2 * T, k_scale=3 * T, v_scale=4 * T, block_table=5 * T, seq_lens=6 * T, num_blocks=100, block_size=64,
-             max_blocks=10, B=2, Hkv=2, D=128)
+             max_blocks=20, B=2, Hkv=2, D=128)  # 1280 tokens: the attention needs a workspace
     a.update(kw)
     return native.AttnCache(*(a[n] for n, _ in native.AttnCache._fields_))
 
@@ -109,7 +109,8 @@ def test_workspace_refusals():
     for bad in ((0, 1), (9, 1), (8, 0)):
         assert f(cache(), *bad, ctypes.byref(n)) == ATTN_ERR_INVALID_ARG
     assert f(cache(D=80), 8, 1, ctypes.byref(n)) == ATTN_ERR_UNSUPPORTED
-    assert f(cache(max_blocks=8), 8, 1, ctypes.byref(n)) == 0 and n.value == 0  # 512 tokens: no unit is split
+    for blocks in (8, 16):  # up to 1024 tokens: no unit is split
+        assert f(cache(max_blocks=blocks), 8, 1, ctypes.byref(n)) == 0 and n.value == 0
 
 
 def test_status_string_of_a_bad_cache():

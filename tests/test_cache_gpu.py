@@ -227,6 +227,16 @@ def test_attention_large_batch_of_short_sequences():
     check_attention(cache, plain, table, lens, 4, 1)
 
 
+@pytest.mark.parametrize("Hq,Sq", [(4, 1), (4, 20)])
+def test_attention_one_long_sequence_among_empty_and_short_ones(Hq, Sq):
+    """Units are split here, and most are smaller than what a CTA is given."""
+    lens = [0 if b % 3 else (29 * b) % 260 for b in range(150)]
+    lens[77] = 2900
+    cache, table = make(150, 2, 64, 64, 2900, seed=11)
+    plain = fill(cache, table, lens, seed=62)
+    check_attention(cache, plain, table, lens, Hq, Sq)
+
+
 def test_attention_sharp_scores_and_scales_far_apart():
     """Large queries (one key takes nearly all the weight, the running maximum moves often) over
     blocks whose scales differ by 2^40, for K and V alike."""
