@@ -86,9 +86,9 @@ CacheView view_of(const attn_cache_t* c, unsigned int* status) {
     return v;
 }
 
-// Query rows of a unit: the least form that takes them all, and 128 from 33 rows on.  Up to 8192 keys,
-// 32 heads over 8: 16 x 8 tokens of 4 heads (32 rows) take 51 us with 32 rows a unit and 67 with 128; 32 x 8 of 8
-// (64 rows) 154 with 128, and 180 with 64 in the form of 32.
+// Query rows of a unit: the least form that takes them all, and 128 from 33 rows on.  Up to 8192 keys, 8 key/value heads:
+// 16 x 5 tokens of 4 query heads each (20 rows) took 51 us with 32 rows a unit and 67 with 128; 32 x 8 of 8 (64 rows) 154
+// with 128, and 180 with 64 in the form of 32.
 int rows_per_unit(long long group, long long Sq) {
     const long long rows = group * Sq;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;

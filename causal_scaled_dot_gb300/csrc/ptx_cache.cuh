@@ -28,15 +28,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// N consecutive columns (8, 16, 32 or 64) of the warp's 32 lanes, and the wait
+// N consecutive columns (8, 16 or 32) of the warp's 32 lanes, and the wait
 // for them: no use of the registers is scheduled before it.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t* r) {
     if constexpr (N == 8) tmem_ld8(taddr, r);
     if constexpr (N == 16) tmem_ld16(taddr, r);
-    if constexpr (N >= 32)
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, r + i);
+    if constexpr (N == 32) tmem_ld32(taddr, r);
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
@@ -45,9 +43,7 @@ template <int N>
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* r) {
     if constexpr (N == 8) tmem_st8(taddr, r);
     if constexpr (N == 16) tmem_st16(taddr, r);
-    if constexpr (N >= 32)
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tmem_st32(taddr + i, r + i);
+    if constexpr (N == 32) tmem_st32(taddr, r);
     tmem_st_wait();
 }
 
@@ -165,15 +161,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)x) : "memory");
-}
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
