@@ -529,12 +529,17 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int t
         CacheWork* work = reinterpret_cast<CacheWork*>(smem + L::kUnit) + ub;
         if (more) {
             CacheRow* rows = reinterpret_cast<CacheRow*>(smem + L::kRows) + ub * R;
+            const int used = min(p.plan.qper, u.s.count - u.qt * p.plan.qper) * p.hper;  // no row from here on is in use
 #pragma unroll 1
             for (int r0 = row0; r0 - row0 < R; r0 += kBatch * 2 * per) {
                 if (r0 != row0) load(u, r0);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
                     const int r = r0 + k * 2 * per;
+                    if (r - lane / lanes >= used) {  // the step's rows; what stands in Qp for them only meets factors of 0
+                        if (r < R && part == 0) rows[r] = CacheRow{0.f, 0, -1};
+                        continue;
+                    }
                     const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                     // the largest magnitude, by bit pattern; not finite: the whole row is NaN
                     uint32_t m = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
@@ -573,7 +578,7 @@ __device__ void cache_query_role(const CacheFwdParams& p, CacheCursor cur, int t
                 work->keys = u.keys;
                 work->keys_all = p.plan.causal ? max(u.s.first + q0 + 1, 0) : u.s.len;
                 work->slot = u.n == u.tiles ? -1 : u.t > 0 ? 0 : 1;
-                work->rows = min(p.plan.qper, u.s.count - q0) * p.hper;
+                work->rows = used;
                 if (u.n < u.tiles) cache_share(reinterpret_cast<CacheShared*>(smem + L::kShared) + work->slot, u, total, ctas);
             }
         } else if (w == 0 && lane == 0) {

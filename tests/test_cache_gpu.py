@@ -549,3 +549,49 @@ def test_calls_on_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_among_copies_and_on_a_side_stream():
+    """A graph of copies, clears and cache calls in turn, with a read on a side stream, gives what the calls give one by one."""
+    B, Hq, Hkv, D, n = 3, 8, 2, 128, 4
+    cache, _ = make(B, Hkv, D, 32, 2000, seed=21)
+    fill(cache, cache.block_table.tolist(), [1500, 700, 40], seed=201)
+    src = [rows((B, h, n, D), 210 + i).cuda() for i, h in enumerate((Hkv, Hkv, Hq))]
+    k, v, q = (torch.empty_like(x) for x in src)
+    out = torch.empty_like(q)
+    kept, lse = torch.empty_like(q), torch.empty((B, Hq, n), device="cuda")
+    back = [torch.zeros((B, Hkv, 300, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    start = cache.seq_lens.clone()
+
+    def step(side):
+        cache.seq_lens.copy_(start)
+        cache.seq_lens.add_(n)
+        for to, x in zip((k, v, q), src):
+            to.copy_(x)
+        out.zero_()
+        cache.write(k, v)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for x in back:
+                x.zero_()
+            cache.read(300, 450, *back)
+        cache.attention(q, out=out, lse=lse)
+        kept.copy_(out)
+        here.wait_stream(side)
+
+    side = torch.cuda.Stream()
+    step(side)
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (kept, lse, *back)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(side)
+    for i in range(6):
+        for x in (kept, lse, *back):
+            x.fill_(3)
+        src[2].add_(0)  # a kernel right before the replay
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((kept, lse, *back), want):
+            assert torch.equal(a, b), i
