@@ -284,11 +284,13 @@ __device__ void cache_load_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v
         return Pages{c.block_table + (long long)u.b * c.max_blocks, (u.keys + c.block_size - 1) >> c.block_shift,
                      p.hgroups == 1 ? u.h : u.h / p.hgroups};
     };
-    auto entry = [&](const Pages& g, int page) { return page < g.last ? __ldg(g.table + page) : -1; };
+    // Ordinary loads: a write that this launch overlapped (launch()) may have changed scales since it started, which the
+    // non-coherent path would not have to see.
+    auto entry = [&](const Pages& g, int page) { return page < g.last ? g.table[page] : -1; };
     auto block_of = [&](const Pages& g, int page, int e) { return page < g.last ? cache_block(e, c.num_blocks, &bad) : -1; };
     auto scales = [&](const Pages& g, int block) {
         const long long at = (long long)block * c.Hkv + g.hk;
-        return block < 0 ? make_float2(0.f, 0.f) : make_float2(__ldg(c.k_scale + at), __ldg(c.v_scale + at));
+        return block < 0 ? make_float2(0.f, 0.f) : make_float2(c.k_scale[at], c.v_scale[at]);
     };
     // This lane's page of a window of 32: its block (-1: none) and scales.  What comes after it is under way
     // meanwhile: of a long unit the next window's blocks and scales and the table entries of the one after

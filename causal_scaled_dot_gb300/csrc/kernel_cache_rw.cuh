@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256, 4) attn_cache_write_kernel(const __grid_c
     const int end = min(s.len, (lb + 1) << c.block_shift);
     active = active && pos0 < end;
     const int slot0 = pos0 & (c.block_size - 1), rows = active ? end - pos0 : 0, row0 = pos0 - s.first;
-    const int entry = active ? __ldg(c.block_table + (long long)u.b * c.max_blocks + lb) : 0;
+    const int entry = active ? c.block_table[(long long)u.b * c.max_blocks + lb] : 0;
 
     const int row_shift = c.D == 128 ? 4 : 3, n_vec = rows << row_shift;  // D / 8 vectors a row
     const long long stride = u.is_v ? p.v_stride[2] : p.k_stride[2];
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256, 4) attn_cache_read_kernel(const __grid_co
     const int lb = (p.first >> c.block_shift) + u.blk;
     bool bad = false;
     // beside the length, which decides whether it is used (lb < max_blocks: the call's positions are within the table)
-    const int entry = __ldg(c.block_table + (long long)u.b * c.max_blocks + lb);
+    const int entry = c.block_table[(long long)u.b * c.max_blocks + lb];
     const int len = cache_clamp(c.seq_lens[u.b], c.max_blocks * c.block_size, &bad);
     const int pos0 = max(p.first, lb << c.block_shift), end = min(min(len, p.first + p.S), (lb + 1) << c.block_shift);
     if (bad && t == 0) atomicOr(c.status, kStatusBadCache);

@@ -1,0 +1,52 @@
+"""Calls on the 8-bit cache one after the other, on several streams and in captured graphs: each gives
+what it gives alone."""
+import threading
+
+import pytest
+import torch
+
+from causal_scaled_dot_gb300.kv_cache import KVCache
+from tests.cache_util import make, rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,block,Sq", [(8, 2, 128, 16, 1), (16, 16, 64, 64, 1), (4, 1, 128, 32, 5), (32, 4, 64, 128, 9)])
+def test_attention_between_writes_that_raise_the_scales(Hq, Hkv, D, block, Sq):
+    """Attention, write, attention, read ... without a wait in between: every call sees the scales, codes and
+    table of the write before it.  The expected results are the same calls with a wait after each."""
+    B, n, steps = 5, 1100, 24
+    cache, table = make(B, Hkv, D, block, n, seed=31)
+    lens = [n, n - 7, 300, block + 3, 9]
+    fill_k, fill_v = rows((B, Hkv, n, D), 1), rows((B, Hkv, n, D), 2, 0.5)
+    # the last tokens once more, each time larger, so that their block's scale grows and its other codes move
+    grow = [2.0 ** (s % 12) for s in range(steps)]
+    k = [(rows((B, Hkv, 3, D), 10 + s).float() * grow[s]).bfloat16().cuda() for s in range(steps)]
+    q = rows((B, Hq, Sq, D), 5).cuda()
+
+    def run(wait):
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cache.write(fill_k.cuda(), fill_v.cuda(), new_lens=cache.seq_lens.clone())
+        got = []
+        for s in range(steps):
+            got.append(cache.attention(q))
+            wait()
+            cache.write(k[s], k[s])
+            wait()
+            got.append(cache.attention(q))
+            wait()
+            got.append(cache.read(20, first=max(0, lens[3] - 20)))
+            wait()
+        torch.cuda.synchronize()
+        return got
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(4):
+        for i, (a, b) in enumerate(zip(run(lambda: None), want)):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), i
