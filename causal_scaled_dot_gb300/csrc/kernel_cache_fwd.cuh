@@ -725,9 +725,11 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
             if (!idle) {
                 const uint32_t s_addr = my_tmem + L::kS + (uint32_t)(sb * L::kN);
                 const uint32_t p_tile = base + L::kP + (uint32_t)sb * (L::kN * 128);
-                // The weights of this thread's key for every row, into Pp; returns the largest.  `add`: the
-                // rows whose sum takes them.
-                auto pass = [&](auto masked, uint32_t add) {
+                // The weights of this thread's key for every row, into Pp, and `sum`, the rows' sums with them; returns the
+                // largest.  The sums count once the weights do: one that is too large, over V's least scale, may be past
+                // what a float holds.
+                float sum[H];
+                auto pass = [&](auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
                     float top = 0.f;
                     uint32_t s[W];
@@ -750,10 +752,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         const float w0 = ptx::ex2(y0), w1 = ptx::ex2(y1);
                         top = ptx::max3(top, w0, w1);
                         const uint64_t w = ptx::f2(w0, w1);
-                        float l0, l1;
-                        ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l[r], l[r + 1])), l0, l1);
-                        if (!kMasked || add >> r & 1) l[r] = l0;
-                        if (!kMasked || add >> (r + 1) & 1) l[r + 1] = l1;
+                        ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l[r], l[r + 1])), sum[r], sum[r + 1]);
                         // hi: w at 4 significant bits, to nearest; lo: the rest
                         const float h0 = __uint_as_float((__float_as_uint(w0) + 0x80000u) & 0xfff00000u);
                         const float h1 = __uint_as_float((__float_as_uint(w1) + 0x80000u) & 0xfff00000u);
@@ -786,8 +785,6 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                 };
                 // First as it stands; once more when a maximum has to rise.  The maxima come first while a row has
                 // none, and on a tile now and then.
-                uint32_t add = ~0u;
-                bool passed = false;
                 for (bool look = todo || k == look_at;;) {
                     if (look) {
                         // The rows' maxima of s + log2 vs over the tile, through the order of the bit patterns.
@@ -812,12 +809,8 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         }
                         todo = __any_sync(0xffffffffu, open);
                         const bool moved = __any_sync(0xffffffffu, moves), rises = __any_sync(0xffffffffu, moves && m > row_max);
-                        uint32_t anew = 0;
                         if (moved) {
-                            // A row whose sum is as good as nothing beside its new maximum starts anew (it may have overflowed).
                             const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
-                            anew = __ballot_sync(0xffffffffu, f < 0x1p-100f);
-                            if (passed) add = anew;
                             row_max = m;
                             peak = fmaxf(peak, m);
                             if (wq == 0 && lane < H) {
@@ -828,7 +821,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         ptx::bar_sync(bar, 128);  // `red` may be written again, and the new factors read
                         if (moved) {
 #pragma unroll
-                            for (int r = 0; r < H; ++r) l[r] = anew >> r & 1 ? 0.f : l[r] * fac[r];
+                            for (int r = 0; r < H; ++r) l[r] *= fac[r];
                             if (k > 0) {
                                 // the tile before is through the tensor core once its stage is empty
                                 wait(L::kEmpty + (stage == 0 ? L::kStages : stage) - 1, stage == 0 ? phase ^ 1u : phase);
@@ -843,10 +836,12 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         look_at = k + (rises ? 1 : look_gap);
                         if (!rises) look_gap = 32;
                     }
-                    const float top = passed || !full ? pass(std::true_type(), add) : pass(std::false_type(), ~0u);
+                    const float top = full ? pass(std::false_type()) : pass(std::true_type());
                     if (look || !ptx::bar_any(bar, 128, top > kCacheTop)) break;
-                    passed = look = true;
+                    look = true;
                 }
+#pragma unroll
+                for (int r = 0; r < H; ++r) l[r] = sum[r];
                 ptx::tc_fence_before();
             }
             ptx::fence_proxy_async_smem();

@@ -1,0 +1,85 @@
+"""The 8-bit cache's attention where many small weights add up, where scores or V's scales are far
+apart, and where a row is not finite: against float64 on the same codes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from causal_scaled_dot_gb300.kv_cache import KVCache
+from tests.cache_util import PlainCache, make, to_f64
+
+pytestmark = pytest.mark.gpu
+
+LN2 = math.log(2.0)
+# Query heads and queries over one key/value head: 1, 4, 8 | 16 | 20, 32 rows of the forms for few
+# rows, and 40, 128 of the form for many.
+SHAPES = [(1, 1), (4, 1), (8, 1), (16, 1), (4, 5), (32, 1), (8, 5), (128, 1)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def one_channel(scores, values, D, block=64, sequences=1):
+    """A cache of one key/value head whose key j has `scores[j]` in channel 0 and `values[j]` in every
+    channel of V, for `sequences` sequences over the same blocks, and its values in float64.  Many
+    sequences make a thread block's share of one of them long."""
+    n = len(scores)
+    one, table = make(1, 1, D, block, n, seed=3)
+    k, v = np.zeros((1, 1, n, D)), np.zeros((1, 1, n, D))
+    k[0, 0, :, 0] = scores
+    v[0, 0] = np.asarray(values)[:, None]
+    k, v = (torch.tensor(x, dtype=torch.bfloat16) for x in (k, v))
+    one.seq_lens.fill_(n)
+    one.write(k.cuda(), v.cuda(), check_status=True)
+    plain = PlainCache(one.k.shape[0], 1, block, D)
+    plain.write(to_f64(k), to_f64(v), table, [n], [n])
+    cache = KVCache(one.k, one.v, one.k_scale, one.v_scale, one.block_table.repeat(sequences, 1), one.seq_lens.repeat(sequences))
+    return cache, plain.values("k", table[0], n)[0, :, 0], plain.values("v", table[0], n)[0, :, 0]
+
+
+def ask(cache, Hq, Sq):
+    """O and LSE for queries that take a key's channel 0 as its score in powers of two."""
+    B, _, D = cache._sizes
+    q = torch.zeros(B, Hq, Sq, D, dtype=torch.bfloat16)
+    q[..., 0] = 1
+    o, lse = cache.attention(q.cuda(), scale=LN2, causal=False, check_status=True)
+    return to_f64(o), to_f64(lse)
+
+
+def want(scores, values):
+    top = scores.max()
+    w = np.exp2(scores - top)
+    return w @ values / w.sum(), (top + math.log2(w.sum())) * LN2
+
+
+@pytest.mark.parametrize("Hq,Sq", SHAPES)
+@pytest.mark.parametrize("jump", [30, 44, 56, 80, 96, 120])
+@pytest.mark.parametrize("tile", [0, 4, 20])
+def test_a_jump_of_the_scores_over_values_of_zero(Hq, Sq, jump, tile):
+    """V of zeros has the smallest scale, whose inverse a key's weight is multiplied by for the sum: a key
+    far above the ones before it leaves O = 0 and LSE its score."""
+    n = 30 * 128
+    scores = np.zeros(n)
+    scores[tile * 128 + 17] = jump
+    cache, s, v = one_channel(scores, np.zeros(n), 64, sequences=320)
+    o, lse = ask(cache, Hq, Sq)
+    assert (o == 0).all()
+    assert np.abs(lse - want(s, v)[1]).max() <= 2.0 ** -16 * jump
+
+
+@pytest.mark.parametrize("Hq,Sq", SHAPES)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 24, 2.0 ** 28])
+def test_values_of_zero_before_large_ones(Hq, Sq, size):
+    """Keys whose V is zero keep their share of the sum beside keys whose V is large."""
+    n = 20 * 128
+    values = np.zeros(n)
+    values[12 * 128:] = size
+    cache, s, v = one_channel(np.zeros(n), values, 64, sequences=320)
+    o, lse = ask(cache, Hq, Sq)
+    ref, ref_lse = want(s, v)
+    assert np.abs(o / ref - 1).max() <= 2.0 ** -8 + 2.0 ** -9
+    assert np.abs(lse - ref_lse).max() <= 2.0 ** -16 * abs(ref_lse)
