@@ -742,7 +742,9 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         const float4 f = tab[r / 2];
                         uint64_t z = ptx::f2(__uint_as_float(s[r]), __uint_as_float(s[r + 1]));
                         z = ptx::add2(z, ptx::f2(__uint_as_float(s[H + r]), __uint_as_float(s[H + r + 1])));
-                        z = ptx::fma2(ptx::mul2(z, ks2), ptx::f2(f.x, f.y), ptx::add2(ptx::f2(f.z, f.w), lvs2));
+                        // K's scale and the row's factor first: with K near its type's limit and a small q, the sum of
+                        // products times K's scale alone is past a float's.
+                        z = ptx::fma2(z, ptx::mul2(ptx::f2(f.x, f.y), ks2), ptx::add2(ptx::f2(f.z, f.w), lvs2));
                         float y0, y1;
                         ptx::f2_split(z, y0, y1);
                         if constexpr (kMasked) {
@@ -792,7 +794,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         ptx::tmem_load<W>(s_addr, s);
 #pragma unroll
                         for (int r = 0; r < H; ++r) {
-                            const float z = fmaf((__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * ks, rows[r].factor, lvs);
+                            const float z = fmaf(__uint_as_float(s[r]) + __uint_as_float(s[H + r]), rows[r].factor * ks, lvs);
                             const float y = fmaxf(full || (here && key < rows[r].keys) ? z : -INFINITY, -INFINITY);
                             const int b = __float_as_int(y), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
                             if (lane == r) red[r * 4 + wq] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from causal_scaled_dot_gb300.kv_cache import KVCache
-from tests.cache_util import PlainCache, make, to_f64
+from tests.cache_util import PlainCache, attention, make, rows, to_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,21 @@ def test_values_of_zero_before_large_ones(Hq, Sq, size):
     ref, ref_lse = want(s, v)
     assert np.abs(o / ref - 1).max() <= 2.0 ** -8 + 2.0 ** -9
     assert np.abs(lse - ref_lse).max() <= 2.0 ** -16 * abs(ref_lse)
+
+
+@pytest.mark.parametrize("Hq,Sq", [(2, 1), (6, 3), (4, 16), (2, 70)])
+def test_large_keys_and_a_small_scale(Hq, Sq):
+    """Scores are moderate though K alone is near the type's largest value."""
+    B, Hkv, D, block, t = 1, 2, 128, 32, 700
+    cache, table = make(B, Hkv, D, block, t, seed=12)
+    k, v = (rows((B, Hkv, t, D), 71).double() * 2.0 ** 114).bfloat16(), rows((B, Hkv, t, D), 72)
+    q = (rows((B, Hq, Sq, D), 73).double() * 2.0 ** -100).bfloat16()
+    plain = PlainCache(cache.k.shape[0], Hkv, block, D)
+    cache.seq_lens.fill_(t)
+    cache.write(k.cuda(), v.cuda(), check_status=True)
+    plain.write(to_f64(k), to_f64(v), table, [t], [t])
+    scale = 2.0 ** -14 / math.sqrt(D)
+    o, lse = cache.attention(q.cuda(), scale=scale, check_status=True)
+    ref, ref_l, tol, tol_l = attention(to_f64(q)[0], plain.values("k", table[0], t), plain.values("v", table[0], t), scale, t - Sq,
+                                       True)
+    assert (np.abs(to_f64(o)[0] - ref) <= tol).all() and (np.abs(to_f64(lse)[0] - ref_l) <= tol_l).all()
