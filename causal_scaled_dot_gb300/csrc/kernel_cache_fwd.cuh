@@ -6,7 +6,8 @@
 // E4M3's 4 significant bits, q and the softmax weights, enters as two E4M3
 // pieces, x = hi + lo with hi the nearest code and lo the nearest code to the
 // rest: 8 significant bits, which is all of a bf16 q (down to 2^-18 of its row's
-// largest element, where lo underflows) and bf16's precision for the weights.
+// largest element, where lo underflows) and bf16's precision for the weights,
+// whose lo stands 2^4 times larger, in columns of its own.
 //
 // Both products are computed transposed, so that the few query rows of a
 // decoding step are the narrow N side of the instruction and not its M = 128:
@@ -20,12 +21,12 @@
 //     w_j = 2^(s_j + log2 vs_j - M + 4),   M = max_j (s_j + log2 vs_j),
 //     O = (sum_j w_j code_j) / (sum_j w_j / vs_j),
 // so that a row's largest w is near 2^4 whatever the scales and lo's underflow
-// (2^-10) is 2^-14 of it.  M rises only when some w passes 448 (E4M3's largest):
-// then the warpgroup finds the tile's maxima and rescales O^T in tensor memory;
-// otherwise a tile needs one vote of the warpgroup and no reduction.  M falls
-// where a tile's weights have become too small for E4M3; a look at a tile costs
-// twice its time, so that is looked for on the tile after each rise (a unit's first
-// counts as one), 8 after that and then on every 32nd.
+// (2^-14) is 2^-18 of it.  M rises only when some w passes 448 (E4M3's largest), and
+// falls where no weight of a tile reaches 1, since what the others then lose to the
+// underflow may be all that a long sequence consists of: the weights lost in a tile are
+// less than 2^-7 of its largest one.  Then the warpgroup finds the tile's maxima and
+// rescales O^T in tensor memory, which costs twice a tile's time; otherwise a tile needs
+// one vote of the warpgroup, with the rows that reached 1 beside it, and no reduction.
 // The sum of w / vs is kept per thread (per key) and reduced at the end.
 //
 // Roles: warp 0 copies pages (lane i takes page i of a tile) with
@@ -110,7 +111,8 @@ struct CacheLayout {
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kNanSeen = kAbort + 4;  // [2]
-    static constexpr uint32_t kShared = kNanSeen + 8;  // 2 x CacheShared
+    static constexpr uint32_t kReach = (kNanSeen + 8 + 15) & ~15u;   // 2 x [kWgs][4 warps]: rows with a weight of 1
+    static constexpr uint32_t kShared = kReach + 2 * kWgs * 16;      // 2 x CacheShared
     static constexpr uint32_t kDynamicSmem = kShared + 2 * 64 + 1024;
     static_assert(kInfo % 16 == 0 && kRows % 16 == 0 && kUnit % 16 == 0 && kTab % 16 == 0 && kScan % 8 == 0 && kBars % 8 == 0,
                   "alignment");
@@ -245,17 +247,19 @@ __device__ __noinline__ void cache_open_tickets(const CacheFwdParams& p, int beg
 // times, a step of 128 rows x 64 keys met it in one of ten).
 constexpr float kCacheRoom = 4.f;
 constexpr float kCacheTop = 448.f;  // E4M3's largest value
-// Where a tile's largest weight is below this, M falls to the tile's maximum: one key far above the rest (a first
-// token that every row attends to) would else leave the rest of a long sequence to lo's underflow, 2^-14 of it.
-constexpr float kCacheLow = 0.25f, kCacheLowLog2 = -2.f;
-// ... but not further than this below the largest M that the row has had: what is left out then is 2^-34 of that
+// Where no weight of a tile reaches 2^low, M falls to the tile's maximum: one key far above the rest (a first
+// token that every row attends to) would else leave the rest of a long sequence to lo's underflow.  Here low = 0, and
+// a weight of 1 is code 0x38; with 0.25 instead, four times as much may be lost in a tile.
+constexpr float kCacheLow = 0.f;
+constexpr uint32_t kCacheReach = 0x38;
+// ... but not further than this below the largest M that the row has had: what is left out then is 2^-38 of that
 // key's weight, and no sum passes 2^126 (a weight of 448 over a V scale of 2^-80, 2^17 times, 20 bits up).
 constexpr float kCacheFall = 20.f;
 
 // The maximum that a row with M = had and the largest M so far `peak` takes at a tile whose maximum is `tile`;
 // *moves: it has to.
-__device__ __forceinline__ float cache_new_max(float had, float peak, float tile, bool* moves) {
-    const bool falls = tile > -INFINITY && tile < had + (kCacheLowLog2 - kCacheRoom) && had > peak - kCacheFall;
+__device__ __forceinline__ float cache_new_max(float had, float peak, float tile, float low, bool* moves) {
+    const bool falls = tile > -INFINITY && tile < had + (low - kCacheRoom) && had > peak - kCacheFall;
     *moves = falls || tile > had + (8.8f - kCacheRoom);  // 2^8.8 < 448
     return falls ? fmaxf(tile, peak - kCacheFall) : fmaxf(had, tile);
 }
@@ -696,7 +700,8 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         for (int r = 0; r < H; ++r) l[r] = 0.f;
         bool todo = true;  // some row that sees keys has no maximum yet
         float peak = -INFINITY;       // the largest maximum that row `lane` has had
-        int look_at = 0, look_gap = 8;  // the next tile where the maxima are looked at anyhow, and how far the one after
+        // Rows whose maximum may fall, row r as bit 8 (r mod 4) + r / 4, where its code in Pp has its byte.
+        uint32_t can_fall = 0;
 
         for (int k = 0; k < work.n; ++k, ++g) {
             const int sb = g & 1;
@@ -729,6 +734,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                 // largest.  The sums count once the weights do: one that is too large, over V's least scale, may be past
                 // what a float holds.
                 float sum[H];
+                uint32_t reach = 0;  // rows whose weight reached 1 here (where no key is masked), as in can_fall
                 auto pass = [&](auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
                     float top = 0.f;
@@ -755,15 +761,19 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         top = ptx::max3(top, w0, w1);
                         const uint64_t w = ptx::f2(w0, w1);
                         ptx::f2_split(ptx::fma2(w, ivs2, ptx::f2(l[r], l[r + 1])), sum[r], sum[r + 1]);
-                        // hi: w at 4 significant bits, to nearest; lo: the rest
-                        const float h0 = __uint_as_float((__float_as_uint(w0) + 0x80000u) & 0xfff00000u);
-                        const float h1 = __uint_as_float((__float_as_uint(w1) + 0x80000u) & 0xfff00000u);
+                        // hi: the nearest code; lo: the nearest code to 2^4 times what hi leaves
+                        hi[r / 2] = e4m3_pair(w0, w1);
+                        const float2 h = e4m3_unpair(hi[r / 2]);
                         float r0, r1;
-                        ptx::f2_split(ptx::fma2(ptx::f2(h0, h1), minus, w), r0, r1);
-                        hi[r / 2] = e4m3_pair(h0, h1);
+                        ptx::f2_split(ptx::fma2(ptx::f2(h.x, h.y), ptx::f2(-16.f, -16.f), ptx::mul2(w, ptx::f2(16.f, 16.f))), r0, r1);
                         lo[r / 2] = e4m3_pair(r0, r1);
                     }
                     auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
+                    if constexpr (!kMasked) {
+                        constexpr uint32_t kCarry = (0x80u - kCacheReach) * 0x01010101u;  // into a byte's top bit from 1 on
+                        reach = (four(hi) + kCarry) >> 7 & 0x01010101u;
+                        if constexpr (H == 8) reach |= (four(hi + 2) + kCarry) >> 6 & 0x02020202u;
+                    }
                     if constexpr (L::kPerKey) {
                         constexpr uint32_t kTurn = L::kN == 64 ? 1 : 2;  // key bits that swizzle
                         const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
@@ -785,9 +795,9 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                     }
                     return top;
                 };
-                // First as it stands; once more when a maximum has to rise.  The maxima come first while a row has
-                // none, and on a tile now and then.
-                for (bool look = todo || k == look_at;;) {
+                // First as it stands; once more when a maximum has to rise or fall.  The maxima come first while a row
+                // has none.
+                for (bool look = todo;;) {
                     if (look) {
                         // The rows' maxima of s + log2 vs over the tile, through the order of the bit patterns.
                         uint32_t s[W];
@@ -806,15 +816,17 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         if (lane < H) {
                             const float4 x = reinterpret_cast<const float4*>(red)[lane];
                             const bool used = rows[lane].at >= 0;
-                            m = cache_new_max(row_max, peak, used ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : -INFINITY, &moves);
+                            m = cache_new_max(row_max, peak, used ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : -INFINITY, kCacheLow, &moves);
                             open = m == -INFINITY && used && rows[lane].keys > 0;
                         }
                         todo = __any_sync(0xffffffffu, open);
-                        const bool moved = __any_sync(0xffffffffu, moves), rises = __any_sync(0xffffffffu, moves && m > row_max);
+                        const bool moved = __any_sync(0xffffffffu, moves);
                         if (moved) {
                             const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
                             row_max = m;
                             peak = fmaxf(peak, m);
+                            const uint32_t can = __ballot_sync(0xffffffffu, m > -INFINITY && m > peak - kCacheFall);
+                            can_fall = ((can & 15u) * 0x00204081u & 0x01010101u) | ((can >> 4 & 15u) * 0x00204081u & 0x01010101u) << 1;
                             if (wq == 0 && lane < H) {
                                 fac[lane] = f;
                                 reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kCacheRoom - m;
@@ -835,12 +847,17 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                                 ptx::tmem_store<W>(o_addr, s);
                             }
                         }
-                        look_at = k + (rises ? 1 : look_gap);
-                        if (!rises) look_gap = 32;
                     }
                     const float top = full ? pass(std::false_type()) : pass(std::true_type());
-                    if (look || !ptx::bar_any(bar, 128, top > kCacheTop)) break;
-                    look = true;
+                    if (look) break;
+                    // All four warps decide by what each has written, two tiles' words in turn: alike after an abort too.
+                    uint32_t* reached = reinterpret_cast<uint32_t*>(smem + L::kReach) + (sb * L::kWgs + wg) * 4;
+                    reach = __reduce_or_sync(0xffffffffu, full ? reach : ~0u);
+                    if (lane == 0) reached[wq] = reach;
+                    look = ptx::bar_any(bar, 128, top > kCacheTop);
+                    const uint4 x = *reinterpret_cast<const uint4*>(reached);
+                    look = look || (can_fall & ~(x.x | x.y | x.z | x.w)) != 0;
+                    if (!look) break;
                 }
 #pragma unroll
                 for (int r = 0; r < H; ++r) l[r] = sum[r];
@@ -895,7 +912,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
 #pragma unroll
                 for (int r = 0; r < H; ++r) {
                     const CacheRow row = rows[r];
-                    float o = (__uint_as_float(s[r]) + __uint_as_float(s[H + r])) * fac[r];
+                    float o = fmaf(__uint_as_float(s[H + r]), 0.0625f, __uint_as_float(s[r])) * fac[r];
                     if (first_nan < row.keys) o = NAN;
                     if (work.slot >= 0)
                         p.part_o[(slot * R + wg * H + r) * 128 + j] = o;

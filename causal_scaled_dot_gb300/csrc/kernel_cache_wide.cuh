@@ -60,6 +60,9 @@ struct CacheWideLayout {
     static constexpr uint32_t kTmemCols = 256, kS = 0, kO = 128;
 };
 
+// Where a half's largest weight of a row is below this, the row's maximum falls to it.
+constexpr float kCacheWideLow = 0.25f, kCacheWideLowLog2 = -2.f;
+
 // The halves of a unit's key tile t that have a key some row sees (one at least).
 __device__ __forceinline__ int cache_halves(const CacheUnit& u, int t) { return t * kCacheTile + 64 < u.keys ? 2 : 1; }
 
@@ -322,7 +325,7 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                         }
                         bool moves;
                         const float had = row_max;
-                        m = cache_new_max(row_max, peak, used ? m : -INFINITY, &moves);
+                        m = cache_new_max(row_max, peak, used ? m : -INFINITY, kCacheWideLowLog2, &moves);
                         const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
                         row_max = m;
                         peak = fmaxf(peak, m);
@@ -345,7 +348,7 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                     const float top = full ? pass(std::false_type()) : pass(std::true_type());
                     // A fall is looked for after a rise and at every eighth tile, and everywhere once it is urgent (at every
                     // step: 8% more time at scores of deviation 2.5, whose maxima vary that much).
-                    const bool low = top < (rose || (h == 0 && (k & 7) == 1) ? kCacheLow : kCacheLow / 16.f) && top > 0.f &&
+                    const bool low = top < (rose || (h == 0 && (k & 7) == 1) ? kCacheWideLow : kCacheWideLow / 16.f) && top > 0.f &&
                                      row_max > peak - kCacheFall;
                     if (move || !__any_sync(0xffffffffu, top > kCacheTop || low)) break;
                     move = true;

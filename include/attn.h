@@ -444,10 +444,12 @@ int attn_cache_read(const attn_cache_t *cache, void *k, void *v, int first, int 
  * A query that sees no key (an idle slot, or a position < 0) gets O = 0 and
  * LSE = -inf.  Keys that no query row may see (past seq_lens[b], after the
  * position) do not affect it whatever their codes.  Scores accumulate in fp32
- * from q rounded to 2^-18 of its row's largest element; the probabilities that
- * multiply V keep 8 bits or 2^-14 of the row's largest weight, whichever is
- * coarser (that largest one counts where it stands and the keys close by: one
- * key far above all others does not cost the others their bits further on);
+ * from q rounded to 2^-18 of its row's largest element.  The weights that
+ * multiply V's codes (probability times V's scale) keep 8 bits or 2^-18 of the
+ * row's largest, whichever is coarser, and what is lost of them in 128 keys next
+ * to each other adds up to less than 2^-7 of the largest there, so that one key
+ * far above all others does not cost the others theirs.  With more than 32 query
+ * rows of a key/value head (query heads times Sq) that is 2^-14, and 2^-2.
  * sums and LSE are fp32.  V's scales below 2^-80 count as 2^-80.
  * Results are deterministic.  Asynchronous on `stream`; allocates nothing.
  * out and lse may overlap neither each other nor any input.  Other errors as

@@ -56,6 +56,51 @@ def want(scores, values):
     return w @ values / w.sum(), (top + math.log2(w.sum())) * LN2
 
 
+def lost(scores):
+    """What weights that are too small add up to, at the most, as a share of the sum: 2^-7 of the largest
+    weight among each 128 keys."""
+    w = np.exp2(scores - scores.max())
+    return 2.0 ** -7 * w.reshape(-1, 128).max(1).sum() / w.sum()
+
+
+@pytest.mark.parametrize("Hq,Sq", [s for s in SHAPES if s[0] * s[1] <= 32])
+@pytest.mark.parametrize("near,every", [(10, None), (10, 128), (5, 64), (9, 64), (3, 64)])
+@pytest.mark.parametrize("low", [0.0, -1.0, -3.0])
+def test_small_weights_add_up(Hq, Sq, near, every, low):
+    """One key 2^15 above the rest, some 2^-10 .. 2^-5 of it, and thousands that matter only together: with
+    V = 1 the answer is 1, and with V = 1 for those thousands alone it is their share."""
+    n = 42 * 128
+    scores = np.full(n, low)
+    scores[0] = 15
+    if every is None:
+        scores[[128 + 5, 9 * 128 + 7]] = near
+    else:
+        scores[3::every] = near
+        scores[0] = 15
+    for values in (np.ones(n), np.where(scores == low, 1.0, 0.0)):
+        cache, s, v = one_channel(scores, values, 64, sequences=320)
+        o, lse = ask(cache, Hq, Sq)
+        ref, ref_lse = want(s, v)
+        # the weights' rounding (2^-8 of each), O's (2^-9, as bf16), and what is lost
+        assert np.abs(o - ref).max() <= (2.0 ** -8 + 2.0 ** -9) * ref + lost(s), (ref, o.min(), o.max())
+        assert np.abs(lse - ref_lse).max() <= 2.0 ** -16 * abs(ref_lse)
+
+
+@pytest.mark.parametrize("Hq,Sq", [s for s in SHAPES if s[0] * s[1] <= 32])
+def test_normal_tails_add_up(Hq, Sq):
+    """Scores of deviation 2 nats under one key 10 nats above: O of V = 1 stays 1."""
+    rng = np.random.default_rng(5)
+    n = 8192
+    for _ in range(3):
+        scores = rng.standard_normal(n) * 2 / LN2
+        scores[0] = 10 / LN2
+        cache, s, v = one_channel(scores, np.ones(n), 128, sequences=160)
+        o, lse = ask(cache, Hq, Sq)
+        ref, ref_lse = want(s, v)
+        assert np.abs(o - 1).max() <= 2.0 ** -8 + 2.0 ** -9 + lost(s)
+        assert np.abs(lse - ref_lse).max() <= 2.0 ** -16 * abs(ref_lse)
+
+
 @pytest.mark.parametrize("Hq,Sq", SHAPES)
 @pytest.mark.parametrize("jump", [30, 44, 56, 80, 96, 120])
 @pytest.mark.parametrize("tile", [0, 4, 20])
