@@ -242,25 +242,28 @@ __device__ __noinline__ void cache_open_tickets(const CacheFwdParams& p, int beg
     if (group < pieces && (had_b ^ p.ticket) >> 16) atomicCAS(b, had_b, p.ticket);
 }
 
-// log2 of a row's largest weight when its maximum M is new.  The weights of the tiles after it may be up to 448 /
-// 2^4 = 28 times that before M has to rise, which scores of unit variance hardly ever ask for (with 2^6 and 7
-// times, a step of 128 rows x 64 keys met it in one of ten).
-constexpr float kCacheRoom = 4.f;
-constexpr float kCacheTop = 448.f;  // E4M3's largest value
-// Where no weight of a tile reaches 2^low, M falls to the tile's maximum: one key far above the rest (a first
-// token that every row attends to) would else leave the rest of a long sequence to lo's underflow.  Here low = 0, and
-// a weight of 1 is code 0x38; with 0.25 instead, four times as much may be lost in a tile.
-constexpr float kCacheLow = 0.f;
-constexpr uint32_t kCacheReach = 0x38;
-// ... but not further than this below the largest M that the row has had: what is left out then is 2^-38 of that
+// Where a row's weights stand, as log2: its largest one when its maximum M is new, the one that some weight of a tile has to
+// reach for M to stay, and the one that none may pass.
+struct CacheRange {
+    float room, low, top;
+};
+// Room: the weights of the tiles after may be up to 448 / 2^4 = 28 times the largest before M has to rise, which scores of
+// unit variance hardly ever ask for (with 2^6 and 7 times, a step of 128 rows x 64 keys met it in one of ten).
+// Low: where no weight of a tile reaches 1, M falls to the tile's maximum.  One key far above the rest (a first token that
+// every row attends to) would else leave the rest of a long sequence to lo's underflow.  With 2^-2 instead of 1 four
+// times as much may be lost in a tile.
+constexpr CacheRange kCacheRange{4.f, 0.f, 8.8f};  // 2^8.8 < 448
+constexpr float kCacheTop = 448.f;                 // E4M3's largest value
+constexpr uint32_t kCacheReach = 0x38;             // the code of 1
+// M does not fall further than this below the largest M that the row has had: what is left out then is 2^-38 of that
 // key's weight, and no sum passes 2^126 (a weight of 448 over a V scale of 2^-80, 2^17 times, 20 bits up).
 constexpr float kCacheFall = 20.f;
 
 // The maximum that a row with M = had and the largest M so far `peak` takes at a tile whose maximum is `tile`;
 // *moves: it has to.
-__device__ __forceinline__ float cache_new_max(float had, float peak, float tile, float low, bool* moves) {
-    const bool falls = tile > -INFINITY && tile < had + (low - kCacheRoom) && had > peak - kCacheFall;
-    *moves = falls || tile > had + (8.8f - kCacheRoom);  // 2^8.8 < 448
+__device__ __forceinline__ float cache_new_max(CacheRange range, float had, float peak, float tile, bool* moves) {
+    const bool falls = tile > -INFINITY && tile < had + (range.low - range.room) && had > peak - kCacheFall;
+    *moves = falls || tile > had + (range.top - range.room);
     return falls ? fmaxf(tile, peak - kCacheFall) : fmaxf(had, tile);
 }
 
@@ -816,7 +819,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         if (lane < H) {
                             const float4 x = reinterpret_cast<const float4*>(red)[lane];
                             const bool used = rows[lane].at >= 0;
-                            m = cache_new_max(row_max, peak, used ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : -INFINITY, kCacheLow, &moves);
+                            m = cache_new_max(kCacheRange, row_max, peak, used ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : -INFINITY, &moves);
                             open = m == -INFINITY && used && rows[lane].keys > 0;
                         }
                         todo = __any_sync(0xffffffffu, open);
@@ -829,7 +832,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                             can_fall = ((can & 15u) * 0x00204081u & 0x01010101u) | ((can >> 4 & 15u) * 0x00204081u & 0x01010101u) << 1;
                             if (wq == 0 && lane < H) {
                                 fac[lane] = f;
-                                reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kCacheRoom - m;
+                                reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kCacheRange.room - m;
                             }
                         }
                         ptx::bar_sync(bar, 128);  // `red` may be written again, and the new factors read
@@ -890,7 +893,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
         const long long slot = (long long)blockIdx.x * 2 + work.slot;
         if (!idle && j < H) {
             const float4 x = reinterpret_cast<const float4*>(red)[j];
-            const float sum = x.x + x.y + (x.z + x.w), m = row_max - kCacheRoom;
+            const float sum = x.x + x.y + (x.z + x.w), m = row_max - kCacheRange.room;
             float f = 1.f;
             if (work.slot < 0) {
                 f = sum == 0.f ? 0.f : ptx::rcp(sum);

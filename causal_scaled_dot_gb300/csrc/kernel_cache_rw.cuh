@@ -54,9 +54,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ float2 e4m3_unpair(uint32_t two) {
+// Two codes (bits 0-15) as two f16, exact.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+__device__ __forceinline__ float2 e4m3_unpair(uint32_t two) {
+    const uint32_t h = e4m3_to_f16x2(two);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 

@@ -5,26 +5,27 @@
 // row-per-column form of kernel_cache_fwd.cuh, where 128 threads vote on a
 // maximum for every few scores, is bound by the latency of its steps.  Here a
 // thread owns a query row of a tile of 128 and sees all its scores:
-//     S [128 rows x 128 keys]  = Qhi K^T + Qlo K^T     (both pieces into the same columns)
-//     O [128 rows x D]        += Phi V  + Plo V        (P as an operand in tensor memory)
+//     S [128 rows x 128 keys]  = Qhi K^T + Qlo K^T     (E4M3, both pieces into the same columns)
+//     O [128 rows x D]        += P V                   (f16, P as an operand in tensor memory)
 // so the running maximum, the sum and the rescaling of O are the thread's own,
-// without a barrier between warps.  Everything else -- the pieces of q and of the
-// weights, V's scale within the weight, the plan and the join -- is as there.
+// without a barrier between warps.  V's scale within the weight, the plan and the join are as there.
+//
+// The weights are f16: two E4M3 pieces into the same columns would stand on one grid of
+// 2^-9, and weights below it would be lost, which thousands of keys together are not;
+// f16 reaches to 2^-24 under a largest weight of 2^6 .. 2^15, with 11 bits.  V's codes
+// are widened for it, exactly, a half at a time: its rows of K are free once its S is
+// there, so the first 64 columns of V go there and the others back to where V came from.
 //
 // A CTA is one warpgroup of softmax, a warp that copies pages and a warp that
 // issues products; two CTAs share an SM.  A step is 64 keys, half a tile: the
 // products of one half run while the other half's weights are worked out.
 // Tensor memory of a CTA: S of two halves [0, 64), [64, 128), O [128, 256); the
-// weights' codes, four a column, replace the scores they came from (hi in a
-// half's columns 0-15, lo in 16-31).
+// weights, two a column, replace the scores they came from (a half's first 32 columns).
 //
-// What bounds it, per 128 rows x 64 keys: two softmax warps a scheduler, each about
-// 600 issue slots of weights (1250 cycles side by side) and 700 cycles of waits,
-// vote, fences and tensor memory around them; the products take 640 of those 1900.
-// Two threads a row (half of a step's keys each) double what is around the weights:
-// 318 us where this takes 276, and a step of 128 keys leaves no tensor memory for
-// a second buffer of S.  2 x 1024 tokens at the end of 8192, 32 heads over 8, D =
-// 128: 280 us, 920 TFLOP/s counted once per product (the two pieces make it twice).
+// 2 x 1024 tokens at the end of 8192, 32 heads over 8, D = 128: 285 us, 904 TFLOP/s.  Two threads a row (half
+// of a step's keys each) double what is around the weights, and a step of 128 keys leaves no tensor memory for a second
+// buffer of S.  The wait for the O of two halves ago before each S costs 1.6 % of that: products of different kinds are
+// not counted on to end in the order they were issued.
 #pragma once
 
 #include <type_traits>
@@ -60,8 +61,11 @@ struct CacheWideLayout {
     static constexpr uint32_t kTmemCols = 256, kS = 0, kO = 128;
 };
 
-// Where a half's largest weight of a row is below this, the row's maximum falls to it.
-constexpr float kCacheWideLow = 0.25f, kCacheWideLowLog2 = -2.f;
+// log2 of a row's largest weight when its maximum is new, below which a half's largest lets the maximum fall, and that no
+// weight may pass (f16's largest is almost 2^16).  With 2^-8 the weights lost in a half, less than 2^-25 each, are less
+// than 2^-11 of its largest.
+constexpr CacheRange kCacheWideRange{6.f, -8.f, 15.f};
+constexpr float kCacheWideLow = 0x1p-8f, kCacheWideTop = 0x1p15f;
 
 // The halves of a unit's key tile t that have a key some row sees (one at least).
 __device__ __forceinline__ int cache_halves(const CacheUnit& u, int t) { return t * kCacheTile + 64 < u.keys ? 2 : 1; }
@@ -70,9 +74,9 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
                                     volatile int* abort_flag) {
     using L = CacheWideLayout;
     constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, 64, false);
-    constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, 128, true);
     const uint64_t lim = p.wait_limit_ns;
     const bool wide = p.c.D == 128, leader = ptx::elect_one();
+    const uint32_t idesc_o = wide ? ptx::idesc_f16_f32(128, 128, true) : ptx::idesc_f16_f32(128, 64, true);
     bool ok = true;
     auto wait = [&](int bar, uint32_t par) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_call(cache_bar<L>(base, bar), par, abort_flag, p.c.status, lim));
@@ -90,14 +94,10 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
         if (!wait(L::kPFull + (int)sb, ((step - 1) >> 1) & 1)) return false;
         ptx::tc_fence_after();
         if (leader) {
-            // 64 keys = 64 rows of 128 bytes; a product takes 32.
-            const uint64_t vd = ptx::sdesc_rows<128>(base + (uint32_t)prev_stage * L::kStageBytes + L::kTileBytes +
-                                                     (uint32_t)prev_half * 8192u);
-            const uint32_t w = tmem + L::kS + sb * 64;
-            ptx::mma_ts_f8(tmem + L::kO, w, vd, kIdescO, prev_first ? 0u : 1u);
-            ptx::mma_ts_f8(tmem + L::kO, w + 8, vd + 256, kIdescO, 1u);
-            ptx::mma_ts_f8(tmem + L::kO, w + 16, vd, kIdescO, 1u);
-            ptx::mma_ts_f8(tmem + L::kO, w + 24, vd + 256, kIdescO, 1u);
+            // 64 keys = 64 rows of 128 bytes in each block of 64 columns.
+            const uint64_t vd = ptx::sdesc_sw128(base + (uint32_t)prev_stage * L::kStageBytes + (uint32_t)prev_half * 8192u,
+                                                 L::kTileBytes, 1024);
+            ptx::mma_ts_k64(tmem + L::kO, tmem + L::kS + sb * 64, vd, idesc_o, prev_first ? 0u : 1u);
             ptx::mma_commit(cache_bar<L>(base, L::kPvDone));
             if (prev_ends_tile) ptx::mma_commit(cache_bar<L>(base, L::kEmpty + prev_stage));
             if (prev_ends_unit) ptx::mma_commit(cache_bar<L>(base, L::kOFull));
@@ -112,13 +112,15 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
         for (int k = 0; ok && k < n; ++k) {
             const int halves = __shfl_sync(0xffffffffu, cache_halves(u, u.t + k), 0);
             for (int h = 0; h < halves; ++h, ++step) {
+                // The O of two halves ago, the last one issued here, has read its weights out of the columns of this S.
+                // (At a unit's start all of the unit before is done, or its O would not have left.)
+                if ((k > 0 || h > 0) && !wait(L::kPvDone, step & 1)) break;
                 // Where the tile's pages are still on their way, the last half's O goes first.
                 if (h == 0 && !__any_sync(0xffffffffu, ptx::mbar_test_wait(cache_bar<L>(base, L::kKFull + stage), phase))) {
                     if (prev_stage >= 0 && !issue_pv()) break;
                     if (!wait(L::kKFull + stage, phase)) break;
                 }
                 ptx::tc_fence_after();
-                // In order behind the O of two halves ago, which reads its weights out of these columns.
                 if (leader) {
                     const uint64_t kd = ptx::sdesc_rows<128>(base + (uint32_t)stage * L::kStageBytes + (uint32_t)h * 8192u);
                     const uint32_t st = tmem + L::kS + (step & 1) * 64;
@@ -154,6 +156,50 @@ __device__ void cache_wide_mma_role(const CacheFwdParams& p, CacheCursor cur, ui
     }
 }
 
+// Widens V's codes of a half's 64 keys, rows `row0` on of a tile, to f16, MN-major in rows of 64 columns: columns 0-63 to
+// the key's row of K's place (the products that read it are done) and 64-127 to its own.  Two lanes of a warp share a key.
+// A weight of 0 times NaN is NaN: a key that nobody sees becomes 0, and NaN that only some rows see is taken out and
+// noted by the first position that has it.
+__device__ __forceinline__ void cache_widen_half(uint32_t at_stage, int row0, int key0, int D, int keys, int keys_all, int* nan_at,
+                                                 volatile int* nan_seen) {
+    using L = CacheWideLayout;
+    const int lane = threadIdx.x & 31, part = lane >> 4, i = (threadIdx.x >> 5) * 16 + (lane & 15), row = row0 + i, key = key0 + i;
+    const uint32_t k_row = at_stage + (uint32_t)row * 128u, v_row = k_row + L::kTileBytes;
+    const bool gone = key >= keys;
+    if (key0 + 64 > keys_all) {
+        if (part == 0 && !gone && key >= keys_all && cache_take_nan(v_row, row, key, nan_at)) *nan_seen = 1;
+        __syncwarp();
+    }
+    uint4 x[4];
+    auto load = [&](int first, int n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c >= n) break;
+            x[c] = ptx::ld_shared_v4(v_row + (uint32_t)(((first + c) ^ (row & 7)) << 4));
+            if (gone) x[c] = make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto store = [&](uint32_t to, int first, int n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c >= n) break;
+            const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                ptx::st_shared_v4(to + (uint32_t)((((first + c) * 2 + y) ^ (row & 7)) << 4), e4m3_to_f16x2(w[2 * y]),
+                                  e4m3_to_f16x2(w[2 * y] >> 16), e4m3_to_f16x2(w[2 * y + 1]), e4m3_to_f16x2(w[2 * y + 1] >> 16));
+        }
+    };
+    if (D == 128) {
+        load(4 * part, 4);
+        __syncwarp();  // both halves of a key's codes are read before its row is written
+        store(part ? v_row : k_row, 0, 4);
+    } else {
+        load(2 * part, 2);
+        store(k_row, 2 * part, 2);
+    }
+}
+
 __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur, int total, int ctas,
                                         uint32_t base, uint8_t* smem, uint32_t tmem, volatile int* abort_flag) {
     using L = CacheWideLayout;
@@ -184,6 +230,7 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
         const int keys = !used ? 0 : p.plan.causal ? max(u.s.first + qi + 1, 0) : u.s.len;
         const int keys_all = p.plan.causal ? max(u.s.first + u.qt * p.plan.qper + 1, 0) : u.s.len;
         float factor;  // of the row's scores
+        bool finite;
         {
             uint4 x[16];
             const __nv_bfloat16* from = p.q + u.b * p.q_stride[0] + hq * p.q_stride[1] + qi * p.q_stride[2];
@@ -197,7 +244,8 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                                          __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
             m = max(m & 0xffffu, m >> 16);
             const float scale = e4m3_pow2_scale(__uint_as_float(m << 16));
-            const float inv = m >= 0x7f80u ? NAN : __uint_as_float((254u << 23) - __float_as_uint(scale));
+            finite = m < 0x7f80u;
+            const float inv = finite ? __uint_as_float((254u << 23) - __float_as_uint(scale)) : NAN;
             factor = scale * p.scale_log2;
             const uint32_t line = base + L::kQ + (uint32_t)r * 128u;
 #pragma unroll
@@ -229,8 +277,8 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
         ptx::fence_proxy_async_smem();
         arrive(L::kQFull);
 
-        float row_max = -INFINITY, peak = -INFINITY, l = 0.f;  // of s + log2 vs, its largest so far, and the sum of w / vs
-        bool rose = false;  // some row's maximum did, at the half before
+        // of s + log2 vs, its largest so far, and the sum of w / vs; a row of NaN needs none, and is not to ask for one
+        float row_max = used && !finite ? 0.f : -INFINITY, peak = row_max, l = 0.f;
         for (int k = 0; k < u.n; ++k) {
             const int halves = cache_halves(u, u.t + k);
             const float* info = reinterpret_cast<const float*>(smem + L::kInfo + stage * L::kInfoBytes);
@@ -242,17 +290,6 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                 ptx::tc_fence_after();
                 const int missing = reinterpret_cast<const int*>(info)[24];
                 const bool full = key0 + 64 <= keys_all && missing == 0;
-                if (h == 0 && key0 + kCacheTile > keys_all) {  // as in kernel_cache_fwd.cuh, a key of V per thread
-                    wait(L::kVFull + stage, phase);
-                    const uint32_t line = base + (uint32_t)stage * L::kStageBytes + L::kTileBytes + (uint32_t)r * 128u;
-                    if (alive && key0 + r >= u.keys) {
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) ptx::st_shared_v4(line + 16 * y, 0, 0, 0, 0);
-                    } else if (alive && key0 + r >= keys_all) {
-                        if (cache_take_nan(line, r, key0 + r, nan_at)) *nan_seen = 1;
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
                 // y = s + log2 vs + base of 16 keys, which share a block: s is the score times K's scale and the row's factor.
                 const int seen = keys - key0;  // keys of the half that this row sees
                 auto scores = [&](auto masked, int i, const uint32_t* s, float at0, float* y) {
@@ -269,11 +306,11 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                         }
                     }
                 };
-                uint32_t code[32];  // four codes each: hi, then lo
+                uint32_t code[32];  // two weights each
                 float sum;
                 // The weights against the row's maximum as it stands; returns the largest.
                 auto pass = [&](auto masked) {
-                    const float at0 = row_max == -INFINITY ? -INFINITY : kCacheRoom - row_max;
+                    const float at0 = row_max == -INFINITY ? -INFINITY : kCacheWideRange.room - row_max;
                     float top = 0.f;
                     sum = 0.f;
                     uint32_t both[32];
@@ -287,20 +324,14 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                         uint64_t part = ptx::f2(0.f, 0.f);
 #pragma unroll
                         for (int x = 0; x < 16; x += 4) {
-                            float w[4], g[4], rest[4];
+                            float w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(y[x + e]);
                             top = ptx::max3(top, w[0], w[1]);
                             top = ptx::max3(top, w[2], w[3]);
-                            const uint64_t w01 = ptx::f2(w[0], w[1]), w23 = ptx::f2(w[2], w[3]), minus = ptx::f2(-1.f, -1.f);
-                            part = ptx::add2(part, ptx::add2(w01, w23));
-                            // hi: w at 4 significant bits, to nearest; lo: the rest
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) g[e] = __uint_as_float((__float_as_uint(w[e]) + 0x80000u) & 0xfff00000u);
-                            ptx::f2_split(ptx::fma2(ptx::f2(g[0], g[1]), minus, w01), rest[0], rest[1]);
-                            ptx::f2_split(ptx::fma2(ptx::f2(g[2], g[3]), minus, w23), rest[2], rest[3]);
-                            code[i * 4 + x / 4] = ptx::pack_e4m3x4(g[0], g[1], g[2], g[3]);
-                            code[16 + i * 4 + x / 4] = ptx::pack_e4m3x4(rest[0], rest[1], rest[2], rest[3]);
+                            part = ptx::add2(part, ptx::add2(ptx::f2(w[0], w[1]), ptx::f2(w[2], w[3])));
+                            code[i * 8 + x / 2] = ptx::pack_f16x2(w[0], w[1]);
+                            code[i * 8 + x / 2 + 1] = ptx::pack_f16x2(w[2], w[3]);
                         }
                         float a, b;
                         ptx::f2_split(part, a, b);
@@ -309,7 +340,6 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                     return top;
                 };
                 // First as it stands; once more when some row's maximum has to rise or fall, or only so while one has none.
-                bool rises = false;
                 for (bool move = __any_sync(0xffffffffu, row_max == -INFINITY && seen > 0);;) {
                     if (move) {
                         // Every row of the warp takes the maximum that it should have.
@@ -324,19 +354,17 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                             for (int x = 0; x < 16; x += 2) m = ptx::max3(m, y[x], y[x + 1]);
                         }
                         bool moves;
-                        const float had = row_max;
-                        m = cache_new_max(row_max, peak, used ? m : -INFINITY, kCacheWideLowLog2, &moves);
+                        m = cache_new_max(kCacheWideRange, row_max, peak, used ? m : -INFINITY, &moves);
                         const float f = row_max == -INFINITY ? 0.f : ptx::ex2(row_max - m);
                         row_max = m;
                         peak = fmaxf(peak, m);
-                        rises = __any_sync(0xffffffffu, moves && m > had);
                         l *= f;
                         if (k > 0 || h > 0) {
                             // The half before has its weights against the old maximum: its product has to be in O.
                             wait(L::kPvDone, (step - 1) & 1);
                             ptx::tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < 128; c += 32) {
+                            for (int c = 0; c < D; c += 32) {
                                 uint32_t s[32];
                                 ptx::tmem_load<32>(my_tmem + L::kO + c, s);
 #pragma unroll
@@ -346,17 +374,17 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                         }
                     }
                     const float top = full ? pass(std::false_type()) : pass(std::true_type());
-                    // A fall is looked for after a rise and at every eighth tile, and everywhere once it is urgent (at every
-                    // step: 8% more time at scores of deviation 2.5, whose maxima vary that much).
-                    const bool low = top < (rose || (h == 0 && (k & 7) == 1) ? kCacheWideLow : kCacheWideLow / 16.f) && top > 0.f &&
-                                     row_max > peak - kCacheFall;
-                    if (move || !__any_sync(0xffffffffu, top > kCacheTop || low)) break;
+                    const bool low = top < kCacheWideLow && top > 0.f && row_max > peak - kCacheFall;
+                    if (move || !__any_sync(0xffffffffu, top > kCacheWideTop || low)) break;
                     move = true;
                 }
-                rose = rises;
                 l += sum;
                 ptx::tmem_st32(s_addr, code);
                 ptx::tmem_st_wait();
+                if (h == 0) wait(L::kVFull + stage, phase);
+                if (__all_sync(0xffffffffu, alive))
+                    cache_widen_half(base + (uint32_t)stage * L::kStageBytes, h * 64, key0, D, u.keys, keys_all, nan_at, nan_seen);
+                ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
                 arrive(L::kPFull + (int)(step & 1));
             }
@@ -373,8 +401,8 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
         const long long slot = (long long)blockIdx.x * 2 + (u.t > 0 ? 0 : 1);
         const float f = !whole ? 1.f : l == 0.f ? 0.f : ptx::rcp(l);
         if (alive && whole && at >= 0 && p.lse != nullptr)
-            p.lse[at] = l == 0.f ? -INFINITY : (row_max - kCacheRoom + ptx::lg2(l)) * kLn2;
-        if (alive && !whole && used) p.part_ml[slot * L::kR + r] = make_float2(row_max - kCacheRoom, l);
+            p.lse[at] = l == 0.f ? -INFINITY : (row_max - kCacheWideRange.room + ptx::lg2(l)) * kLn2;
+        if (alive && !whole && used) p.part_ml[slot * L::kR + r] = make_float2(row_max - kCacheWideRange.room, l);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t s[32];

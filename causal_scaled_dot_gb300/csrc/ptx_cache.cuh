@@ -56,15 +56,6 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same with A read from tensor memory (four codes a column, 8 columns).
-__device__ __forceinline__ void mma_ts_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // Four steps over 128 keys, the operands' descriptors advancing by kA and kB
 // (in 16-byte units) each.
 template <int kA, int kB>
@@ -86,6 +77,16 @@ __device__ __forceinline__ void mma_ss_f8_x4(uint32_t d, uint64_t a, uint64_t b,
 // MN-major, bit 16: B is.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
     return idesc_e4m3_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
+}
+// Instruction descriptor for kind::f16, f16 A (K-major) and B, fp32 D; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Two floats -> packed f16x2 (round to nearest even); `lo` in bits 0-15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 // Shared-memory descriptor of an operand with rows of 128, 64 or 32 bytes in the
 // swizzle of that width (16-byte piece i of row k sits at i ^ (k mod 8), i ^

@@ -446,11 +446,13 @@ int attn_cache_read(const attn_cache_t *cache, void *k, void *v, int first, int 
  * position) do not affect it whatever their codes.  Scores accumulate in fp32
  * from q rounded to 2^-18 of its row's largest element.  The weights that
  * multiply V's codes (probability times V's scale) keep 8 bits or 2^-18 of the
- * row's largest, whichever is coarser, and what is lost of them in 128 keys next
- * to each other adds up to less than 2^-7 of the largest there, so that one key
- * far above all others does not cost the others theirs.  With more than 32 query
- * rows of a key/value head (query heads times Sq) that is 2^-14, and 2^-2.
- * sums and LSE are fp32.  V's scales below 2^-80 count as 2^-80.
+ * row's largest, whichever is coarser; 11 bits or 2^-31 with more than 32 query
+ * rows of a key/value head (query heads times Sq).  What is lost of them in 128
+ * keys next to each other adds up to less than 2^-7 of the largest there, or is
+ * less than 2^-38 of the row's largest each: one key far above all others does
+ * not cost the others theirs.  Sums and LSE are fp32.  V's scales below 2^-80
+ * count as 2^-80, and keys whose V scale is 2^100 and more below another's in
+ * the same row may be missing from its sum.
  * Results are deterministic.  Asynchronous on `stream`; allocates nothing.
  * out and lse may overlap neither each other nor any input.  Other errors as
  * attn_fwd (scale finite and > 0).
