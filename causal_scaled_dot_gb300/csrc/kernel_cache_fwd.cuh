@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "cache_index.h"
+#include "cache_tickets.h"
 #include "common.cuh"
 #include "kernel_cache_rw.cuh"
 #include "ptx.cuh"
@@ -70,10 +71,7 @@ struct CacheFwdParams {
     float scale_log2;       // scale * log2(e)
     float* part_o;          // [G][2][R][128] partial sums of w code
     float2* part_ml;        // [G][2][R] their M - 4 and sum of w / vs
-    // [2][G]: pieces left of a group, and groups of the unit that begins in a CTA, below a number (the upper 48
-    // bits) that marks this launch: whatever stood there before counts as none.  0 again after each join, since a captured launch
-    // comes again with its number.
-    unsigned long long* tickets;
+    unsigned long long* tickets;  // [2][G], cache_tickets.h, and this launch's number
     unsigned long long ticket;
     unsigned long long wait_limit_ns;
 };
@@ -145,7 +143,7 @@ struct CacheWork {
 struct CacheShared {
     CacheUnit u;
     int first, pieces;  // the CTA where it begins, and the CTAs that share it (0: no such unit)
-    int last;           // 1: this CTA was the last of its group to leave its piece, then of all groups
+    int last;           // CacheLast: whether this CTA was the last of its group to leave its piece, then of all groups
 };
 static_assert(sizeof(CacheRow) == 16 && sizeof(CacheWork) == 48 && sizeof(CacheShared) <= 64, "shared memory layout");
 
@@ -195,6 +193,12 @@ __device__ int cache_locate(const CachePlan& p, int* scan, unsigned int* status,
         *reinterpret_cast<CachePlace*>(scan + 20) = plan_find(p, first, want - before);
     __syncthreads();
     *place = want < all ? *reinterpret_cast<const CachePlace*>(scan + 20) : CachePlace{p.B, 0, 0, 0};
+    if (tid == 0) {  // for cache_shared_again
+        scan[0] = *begin;
+        scan[1] = *end;
+        scan[2] = all;
+        scan[3] = ctas;
+    }
     return ctas;
 }
 
@@ -213,33 +217,18 @@ __device__ __forceinline__ void cache_share(CacheShared* shared, const CacheUnit
     shared->first = plan_cta(total, u.at, ctas);
     shared->pieces = plan_cta(total, u.at + u.tiles - 1, ctas) - shared->first + 1;
 }
-// Pieces that one CTA joins: up to `most` all of them, else the square root, so that groups of pieces are joined side by
-// side and then the groups: 128 rows of one key/value head over 131072 keys, 128 pieces, take 54 us instead of 145, and
-// 8 rows 22 instead of 26; for fewer pieces the second round costs more than it saves (10 pieces of 1 row: 16.1 us
-// against 13.7).
-__device__ __forceinline__ int cache_group(int pieces, int most) {
-    if (pieces <= most) return pieces;
-    int n = 2;
-    while (n * n < pieces) ++n;
-    return n;
-}
-// Counter of the group that a unit's piece is in, and of the unit's groups.  A group of one piece needs none, so no two
-// units meet at one.
-__device__ __forceinline__ unsigned long long* cache_ticket(const CacheFwdParams& p, int first, int piece, int group) {
-    return p.tickets + first + (piece < group ? 0 : piece / group * group);
-}
-__device__ __forceinline__ unsigned long long* cache_unit_ticket(const CacheFwdParams& p, int first) {
-    return p.tickets + gridDim.x + first;
-}
-// Each CTA that shares a unit does this before it counts its piece: a counter that does not carry this launch's
-// number becomes 0 pieces of this launch.  An exchange that fails met another CTA's, which did the same.
+struct CacheTicketMemory {
+    static __device__ __forceinline__ unsigned long long load(unsigned long long* at) { return __ldcg(at); }
+    static __device__ __forceinline__ void compare_exchange(unsigned long long* at, unsigned long long had, unsigned long long to) {
+        atomicCAS(at, had, to);
+    }
+    static __device__ __forceinline__ unsigned long long add(unsigned long long* at, unsigned long long n) { return atomicAdd(at, n); }
+    static __device__ __forceinline__ void set(unsigned long long* at, unsigned long long bits) { atomicOr(at, bits); }
+    static __device__ __forceinline__ void clear(unsigned long long* at) { atomicExch(at, 0ull); }
+};
 __device__ __noinline__ void cache_open_tickets(const CacheFwdParams& p, int begin, int tiles, int total, int ctas, int most) {
     const int first = plan_cta(total, begin, ctas), pieces = plan_cta(total, begin + tiles - 1, ctas) - first + 1;
-    const int group = cache_group(pieces, most);
-    unsigned long long *a = cache_ticket(p, first, blockIdx.x - first, group), *b = cache_unit_ticket(p, first);
-    const unsigned long long had_a = __ldcg(a), had_b = __ldcg(b);
-    if ((had_a ^ p.ticket) >> 16) atomicCAS(a, had_a, p.ticket);
-    if (group < pieces && (had_b ^ p.ticket) >> 16) atomicCAS(b, had_b, p.ticket);
+    tickets_open<CacheTicketMemory>(p.tickets, gridDim.x, p.ticket, first, pieces, blockIdx.x - first, most);
 }
 
 // Where a row's weights stand, as log2: its largest one when its maximum M is new, the one that some weight of a tile has to
@@ -930,13 +919,6 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
     }
 }
 
-// Counts a piece of a unit as left; true for the last of them.
-__device__ __noinline__ bool cache_last_piece(unsigned long long* at, int pieces) {
-    if ((int)(atomicAdd(at, 1ull) & 0xffff) + 1 != pieces) return false;
-    atomicExch(at, 0ull);
-    return true;
-}
-
 // Pieces x0, x0 + step, ... (`n` of them) of a shared unit.  Each is slot 1 of the CTA where the unit begins or slot 0 of
 // a following one.  `final`: the joined rows go to out and lse, else to the place of piece x0.
 struct CacheJoin {
@@ -1032,42 +1014,59 @@ __device__ void cache_join_rows(const CacheFwdParams& p, const CacheJoin& join, 
     }
 }
 
+// After a wait has run out: the units that this CTA shares, looked up again and opened, since the roles may have ended
+// before they came to them.  `scan` is as cache_locate left it.
+template <typename L>
+__device__ __noinline__ void cache_shared_again(const CacheFwdParams& p, const int* scan, CacheShared* shared) {
+    const int begin = scan[0], end = scan[1], total = scan[2], ctas = scan[3];
+    shared[0].pieces = shared[1].pieces = 0;
+    if (begin == end) return;
+    CacheCursor cur = cursor_at(p.plan, *reinterpret_cast<const CachePlace*>(scan + 20), begin, end - begin);
+    CacheUnit u;
+    while (cursor_next(p.plan, cur, u))
+        if (u.n < u.tiles) {
+            cache_share(shared + (u.t > 0 ? 0 : 1), u, total, ctas);
+            cache_open_tickets(p, u.at, u.tiles, total, ctas, L::kJoin);
+        }
+}
+
 // The end of a CTA, by all its threads, once every piece is left: of each unit that it shares, whoever counts last in
 // its group joins the group's pieces, and whoever is the last of those joins the groups.
 template <typename L, typename F>
-__device__ void cache_join(const CacheFwdParams& p, CacheShared* shared, bool aborted, F join) {
+__device__ void cache_join(const CacheFwdParams& p, const int* scan, CacheShared* shared, bool aborted, F join) {
+    if (aborted) {
+        if (threadIdx.x == 0) cache_shared_again<L>(p, scan, shared);
+        __syncthreads();
+    }
     if (shared[0].pieces == 0 && shared[1].pieces == 0) return;
     if (threadIdx.x < 2) {
         CacheShared& x = shared[threadIdx.x];
         __threadfence();
-        x.last = 0;
-        if (x.pieces > 0 && !aborted) {
-            const int piece = blockIdx.x - x.first, group = cache_group(x.pieces, L::kJoin);
-            const int n = piece < group ? group : min(group, x.pieces - piece / group * group);
-            x.last = n == 1 || cache_last_piece(cache_ticket(p, x.first, piece, group), n);
-        }
+        x.last = kMoreToCome;
+        if (x.pieces > 0)
+            x.last = tickets_leave<CacheTicketMemory>(p.tickets, x.first, x.pieces, blockIdx.x - x.first, L::kJoin, aborted);
         __threadfence();
     }
     __syncthreads();
     for (int i = 0; i < 2; ++i) {
         CacheShared& x = shared[i];
-        if (x.pieces == 0 || !x.last) continue;
+        if (x.pieces == 0 || x.last == kMoreToCome) continue;
         const int group = cache_group(x.pieces, L::kJoin);
+        const bool whole = x.last == kWasLast;  // every piece of the group was left
         if (group == x.pieces) {
-            join(CacheJoin{x, 0, group, 1, true});
+            if (whole) join(CacheJoin{x, 0, group, 1, true});
             continue;
         }
-        const int groups = (x.pieces + group - 1) / group, begin = (blockIdx.x - x.first) / group * group;
-        const int n = min(group, x.pieces - begin);
-        if (n > 1) join(CacheJoin{x, begin, n, 1, false});
+        const CacheGroup g = cache_group_of(x.pieces, group, blockIdx.x - x.first);
+        if (g.n > 1 && whole) join(CacheJoin{x, g.begin, g.n, 1, false});
         __syncthreads();
         if (threadIdx.x == 0) {
             __threadfence();
-            x.last = cache_last_piece(cache_unit_ticket(p, x.first), groups);
+            x.last = tickets_joined<CacheTicketMemory>(p.tickets, gridDim.x, x.first, x.pieces, L::kJoin, !whole);
             __threadfence();
         }
         __syncthreads();
-        if (x.last) join(CacheJoin{x, 0, groups, group, true});
+        if (x.last == kWasLast) join(CacheJoin{x, 0, (x.pieces + group - 1) / group, group, true});
     }
 }
 
@@ -1137,7 +1136,8 @@ __global__ void __launch_bounds__(CacheLayout<R>::kThreads, CacheLayout<R>::kCta
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-    cache_join<L>(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0, [&](const CacheJoin& x) {
+    cache_join<L>(p, reinterpret_cast<const int*>(smem + L::kScan), reinterpret_cast<CacheShared*>(smem + L::kShared),
+                  *abort_flag != 0, [&](const CacheJoin& x) {
         constexpr int kWarps = L::kThreads / 32, kRows = (R + kWarps - 1) / kWarps;
         static_assert(R % kRows == 0, "rows of a warp");
         if (warp * kRows < R) cache_join_rows<kRows>(p, x, R, warp * kRows);

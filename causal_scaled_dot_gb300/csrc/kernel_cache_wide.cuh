@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(CacheWideLayout::kThreads, CacheWideLayout::kC
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, L::kTmemCols);
     }
-    cache_join<L>(p, reinterpret_cast<CacheShared*>(smem + L::kShared), *abort_flag != 0,
-               [&](const CacheJoin& x) { cache_wide_join(p, x); });
+    cache_join<L>(p, reinterpret_cast<const int*>(smem + L::kScan), reinterpret_cast<CacheShared*>(smem + L::kShared),
+                  *abort_flag != 0, [&](const CacheJoin& x) { cache_wide_join(p, x); });
 }
 
 }  // namespace attn
