@@ -23,7 +23,9 @@ int encode_bf16_tiles(CUtensorMap* map, int device, const void* ptr, int D, int 
 int encode_bf16_box(CUtensorMap* map, int device, const void* ptr, int D, int S, long long outer,
                     int box_rows);
 // The view [outer, S, D] of one-byte elements with a box of 128 bytes x
-// `box_rows` rows; bytes of the box past column D read as zero.
+// `box_rows` rows; bytes of the box past column D read as zero.  Served from a
+// table of its own, so a model's many caches and the other tensors do not
+// displace each other's maps.
 int encode_byte_box(CUtensorMap* map, int device, const void* ptr, int D, int S, long long outer,
                     int box_rows);
 

@@ -1,4 +1,5 @@
-// tmap_cache.h -- a small least-recently-used cache of encoded TMA tensor maps.
+// tmap_cache.h -- caches of encoded TMA tensor maps: a small one that is searched from end to end, and
+// a larger one whose keys are hashed to sets.  Both replace the least recently used entry, of all or of the set.
 //
 // A tiled tensor map is a pure function of what the encoder is given: the base
 // address, the element type, the extents, the strides and the box.  The key
@@ -75,6 +76,31 @@ class TmapCache {
     unsigned long long used_[N] = {};  // 0: empty slot; otherwise the last use's clock
     unsigned long long clock_ = 0;
     unsigned long long hits_ = 0, misses_ = 0;
+};
+
+// `Sets` sets (a power of two) of `Ways` entries each: for callers with many buffers, such as a model's
+// layers, each with tensors of its own, where a search of everything would cost more than a map's encoding.
+template <int Sets, int Ways>
+class TmapTable {
+    static_assert(Sets > 0 && (Sets & (Sets - 1)) == 0, "a power of two");
+
+  public:
+    bool lookup(const TmapKey& key, CUtensorMap* map) { return sets_[set_of(key)].lookup(key, map); }
+    void insert(const TmapKey& key, const CUtensorMap& map) { sets_[set_of(key)].insert(key, map); }
+
+  private:
+    // Every field counts, the address by its multiples of 16 (a multiplication's upper bits depend on all bits below).
+    static int set_of(const TmapKey& k) {
+        unsigned long long h = (unsigned long long)(uintptr_t)k.ptr >> 4;
+        const unsigned long long rest[4] = {(unsigned long long)(unsigned)k.device * 8 + (unsigned)k.elem_bytes,
+                                            (unsigned long long)(unsigned)k.D * 512 + (unsigned)k.box_rows, (unsigned long long)(unsigned)k.S,
+                                            (unsigned long long)k.outer};
+        for (unsigned long long x : rest) h = (h ^ x) * 0x9E3779B97F4A7C15ull;
+        h ^= h >> 32;
+        h *= 0x9E3779B97F4A7C15ull;
+        return (int)(h >> 40) & (Sets - 1);
+    }
+    TmapCache<Ways> sets_[Sets];
 };
 
 }  // namespace attn
