@@ -212,13 +212,12 @@ __global__ void __launch_bounds__(256, 4) attn_cache_read_kernel(const __grid_co
     const bool is_v = u.is_v || !p.k;
     const int lb = (p.first >> c.block_shift) + u.blk;
     bool bad = false;
-    // beside the length, which decides whether it is used (lb < max_blocks: the call's positions are within the table)
-    const int entry = c.block_table[(long long)u.b * c.max_blocks + lb];
     const int len = cache_clamp(c.seq_lens[u.b], c.max_blocks * c.block_size, &bad);
     const int pos0 = max(p.first, lb << c.block_shift), end = min(min(len, p.first + p.S), (lb + 1) << c.block_shift);
     if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
     if (pos0 >= end) return;
-    const int block = cache_block(entry, c.num_blocks, &bad);
+    // only now: entries past a sequence's last token are not read
+    const int block = cache_block(c.block_table[(long long)u.b * c.max_blocks + lb], c.num_blocks, &bad);
     if (block < 0) {
         if (t == 0) atomicOr(c.status, kStatusBadCache);
         return;
