@@ -150,7 +150,9 @@ class KVCache:
             if stream is None:
                 stream = torch.cuda.current_stream(self._device)
             elif isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self._device)
+                # 0 and 1 stand for the default stream, which an ExternalStream of 0 is not.
+                stream = torch.cuda.default_stream(self._device) if stream in (0, 1) else torch.cuda.ExternalStream(
+                    stream, device=self._device)
             with torch.cuda.stream(stream):
                 yield stream.cuda_stream
 

@@ -1,7 +1,5 @@
 """Calls on the 8-bit cache one after the other, on several streams and in captured graphs: each gives
 what it gives alone."""
-import threading
-
 import pytest
 import torch
 
@@ -50,3 +48,26 @@ def test_attention_between_writes_that_raise_the_scales(Hq, Hkv, D, block, Sq):
     for _ in range(4):
         for i, (a, b) in enumerate(zip(run(lambda: None), want)):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), i
+
+
+def test_handles_of_the_default_stream():
+    """0 and 1 are the default stream's handles: calls on it run behind what it holds already."""
+    cache, _ = make(2, 2, 64, 32, 2000, seed=33)
+    k, q = rows((2, 2, 2000, 64), 1).cuda(), rows((2, 4, 1, 64), 2).cuda()
+    cache.seq_lens.fill_(2000)
+    cache.write(k, k)
+    want = cache.attention(q)
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    for handle in (0, 1):
+        with cache._on(handle) as st:
+            assert st == default.cuda_stream and torch.cuda.current_stream() == default
+        late = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(20_000_000)  # some milliseconds
+            late.copy_(q)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = cache.attention(late, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
