@@ -146,6 +146,8 @@ class KVCache:
         """The cache's device current, and `stream` (a torch.cuda.Stream, a handle, or None for the
         device's current stream) current on it, so that memory allocated within belongs to that
         stream; yields its handle."""
+        if not isinstance(stream, (int, type(None))) and stream.device != self._device:
+            raise ValueError(f"stream is on {stream.device} but the cache is on {self._device}")
         with torch.cuda.device(self._device):
             if stream is None:
                 stream = torch.cuda.current_stream(self._device)
