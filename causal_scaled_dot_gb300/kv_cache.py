@@ -26,6 +26,8 @@ _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _BF16 = torch.bfloat16
+# Every thread's own default stream has this handle: streams that it does not tell apart.
+_PER_THREAD = 2
 # Workspaces by (device, stream): calls on one stream run one after the other, so they share one.
 # Captured calls do not take part: each has its own from the graph's memory, as graphs may be
 # replayed on any stream.
@@ -52,7 +54,8 @@ class KVCache:
     All on one CUDA device.  ``block_table`` and ``seq_lens`` may be shared between
     layers and are updated in place by their owner; the tensors themselves stay the
     same for the cache's lifetime.  Calls run with the tensors' device current, on
-    ``stream`` (default: that device's current stream), and do not synchronise unless
+    ``stream`` (a torch.cuda.Stream of that device or a handle, not the per-thread
+    default stream's; default: that device's current stream), and do not synchronise unless
     ``check_status`` asks for it: it then raises AttnError if a device-side wait ran
     out or a block number or length lay outside the cache (one status word per
     device, shared by every stream on it)."""
@@ -146,6 +149,9 @@ class KVCache:
         """The cache's device current, and `stream` (a torch.cuda.Stream, a handle, or None for the
         device's current stream) current on it, so that memory allocated within belongs to that
         stream; yields its handle."""
+        if stream == _PER_THREAD or getattr(stream, "cuda_stream", None) == _PER_THREAD:
+            raise ValueError("the per-thread default stream is another one in each thread, which memory that belongs to "
+                             "a stream does not tell apart: pass a stream of its own")
         if not isinstance(stream, (int, type(None))) and stream.device != self._device:
             raise ValueError(f"stream is on {stream.device} but the cache is on {self._device}")
         with torch.cuda.device(self._device):
@@ -250,6 +256,9 @@ class KVCache:
             lse = torch.empty((self._sizes[0], Hq, Sq), dtype=torch.float32, device=self._device)
         w = None
         if need:
+            if st == _PER_THREAD:
+                raise ValueError("attention over a cache of this length needs a workspace, which belongs to a stream, and "
+                                 "the per-thread default stream is another one in each thread")
             if torch.cuda.is_current_stream_capturing():
                 w = torch.empty(need, dtype=torch.uint8, device=self._device)
             else:
