@@ -49,6 +49,17 @@ bool meets_cache(const attn_cache_t* c, const void* a, size_t na, bool index) {
                       host::ranges_overlap(a, na, c->seq_lens, (size_t)c->B * 4)));
 }
 
+// Whether codes or scales, which a write changes, meet each other, the table or the lengths.
+bool meets_itself(const attn_cache_t* c) {
+    const size_t n = cache_bytes(c), ns = (size_t)c->num_blocks * c->Hkv * 4;
+    const struct { const void* p; size_t n; } part[6] = {{c->k, n}, {c->v, n}, {c->k_scale, ns}, {c->v_scale, ns},
+                                                         {c->block_table, (size_t)c->B * c->max_blocks * 4}, {c->seq_lens, (size_t)c->B * 4}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (host::ranges_overlap(part[i].p, part[i].n, part[j].p, part[j].n)) return true;
+    return false;
+}
+
 // {batch, head, token} strides of rows [B, H, S, D] into `out`; *bytes
 // receives the bytes from the first element to past the last.
 int row_strides(const long long* strides, long long B, long long H, long long S, int D, long long out[3], size_t* bytes) {
@@ -218,7 +229,7 @@ extern "C" int attn_cache_write(const attn_cache_t* cache, const void* k, const 
     size_t kb = 0, vb = 0;
     if ((rc = row_strides(k_strides, cache->B, cache->Hkv, S, cache->D, p.k_stride, &kb)) != ATTN_OK) return rc;
     if ((rc = row_strides(v_strides, cache->B, cache->Hkv, S, cache->D, p.v_stride, &vb)) != ATTN_OK) return rc;
-    if (meets_cache(cache, k, kb, false) || meets_cache(cache, v, vb, false) ||
+    if (meets_itself(cache) || meets_cache(cache, k, kb, false) || meets_cache(cache, v, vb, false) ||
         (new_lens && meets_cache(cache, new_lens, (size_t)cache->B * 4, false)))
         return ATTN_ERR_INVALID_ARG;
     int sms = 0, device = -1;

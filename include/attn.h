@@ -404,7 +404,8 @@ typedef struct {
  * is written.  A block that is written must belong to one sequence (one table
  * entry) of the call; blocks that are only read may be shared.
  * One kernel on `stream`, asynchronous; allocates nothing.  k and v may not
- * overlap the cache.  Errors as attn_fwd.
+ * overlap the cache, nor the cache's codes and scales each other, its table or
+ * its lengths.  Errors as attn_fwd.
  */
 int attn_cache_write(const attn_cache_t *cache, const void *k, const long long *k_strides,
                      const void *v, const long long *v_strides, const int *new_lens, int S,
