@@ -3,7 +3,6 @@ what it gives alone."""
 import pytest
 import torch
 
-from causal_scaled_dot_gb300.kv_cache import KVCache
 from tests.cache_util import make, rows
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +70,33 @@ def test_handles_of_the_default_stream():
             got = cache.attention(late, stream=handle)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_captured_calls_replayed_at_once():
+    """Graphs of attention calls of different shapes, split over all blocks and joined, replayed on streams of their
+    own without a wait in between: each has its own workspace."""
+    made = []
+    for i, (lens, Hq, Hkv, Sq) in enumerate((([20000, 300], 8, 2, 1), ([9000, 8000], 4, 2, 9), ([16000, 5], 32, 2, 1),
+                                             ([5000, 4000], 16, 2, 16))):
+        cache, _ = make(2, Hkv, 128, 64, max(lens), seed=41 + i)
+        k = rows((2, Hkv, max(lens), 128), 50 + i).cuda()
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cache.write(k, k, new_lens=cache.seq_lens.clone())
+        q = rows((2, Hq, Sq, 128), 60 + i).cuda()
+        want = cache.attention(q, check_status=True)
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            got = cache.attention(q)
+        made.append((graph, stream, got, want, cache, q, k))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _, _, got, *_ in made:
+            got[0].fill_(3), got[1].fill_(3)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, stream, *_ in made:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for i, (_, _, got, want, *_) in enumerate(made):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i

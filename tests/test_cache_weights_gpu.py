@@ -146,3 +146,23 @@ def test_large_keys_and_a_small_scale(Hq, Sq):
     ref, ref_l, tol, tol_l = attention(to_f64(q)[0], plain.values("k", table[0], t), plain.values("v", table[0], t), scale, t - Sq,
                                        True)
     assert (np.abs(to_f64(o)[0] - ref) <= tol).all() and (np.abs(to_f64(lse)[0] - ref_l) <= tol_l).all()
+
+
+@pytest.mark.parametrize("Hq,Sq", [(8, 9), (4, 40), (130, 1), (2, 200)])
+def test_non_finite_queries_stay_in_their_row_of_many(Hq, Sq):
+    cache, table = make(1, 1, 128, 64, 1900, seed=14)
+    n = 1900
+    k, v = rows((1, 1, n, 128), 91), rows((1, 1, n, 128), 92)
+    cache.seq_lens.fill_(n)
+    cache.write(k.cuda(), v.cuda())
+    q = rows((1, Hq, Sq, 128), 93)
+    clean, clean_lse = cache.attention(q.cuda())
+    bad = torch.zeros(Hq, Sq, dtype=torch.bool)
+    for h, i, d, x in ((0, 0, 7, float("nan")), (Hq - 1, Sq - 1, 3, float("inf")), (1, Sq // 2, 127, float("-inf"))):
+        q[0, h, i, d] = x
+        bad[h, i] = True
+    o, lse = cache.attention(q.cuda(), check_status=True)
+    assert o[0, bad].isnan().all() and lse[0, bad].isnan().all()
+    # a row's maximum may move with its neighbours', so its weights may be rounded at another place
+    assert (o[0, ~bad].float() - clean[0, ~bad].float()).abs().max() <= 2.0 ** -7 * v.abs().max()
+    assert (lse[0, ~bad] - clean_lse[0, ~bad]).abs().max() <= 2.0 ** -16 * clean_lse[0, ~bad].abs().max()
