@@ -22,7 +22,7 @@
 // Tensor memory of a CTA: S of two halves [0, 64), [64, 128), O [128, 256); the
 // weights, two a column, replace the scores they came from (a half's first 32 columns).
 //
-// 2 x 1024 tokens at the end of 8192, 32 heads over 8, D = 128: 285 us, 904 TFLOP/s.  Two threads a row (half
+// 2 x 1024 tokens at the end of 8192, 32 heads over 8, D = 128: 269 us, 956 TFLOP/s.  Two threads a row (half
 // of a step's keys each) double what is around the weights, and a step of 128 keys leaves no tensor memory for a second
 // buffer of S.  The wait for the O of two halves ago before each S costs 1.6 % of that: products of different kinds are
 // not counted on to end in the order they were issued.
@@ -61,10 +61,11 @@ struct CacheWideLayout {
     static constexpr uint32_t kTmemCols = 256, kS = 0, kO = 128;
 };
 
-// log2 of a row's largest weight when its maximum is new, below which a half's largest lets the maximum fall, and that no
-// weight may pass (f16's largest is almost 2^16).  With 2^-8 the weights lost in a half, less than 2^-25 each, are less
-// than 2^-11 of its largest.
-constexpr CacheRange kCacheWideRange{6.f, -8.f, 15.f};
+// No weight may pass 2^15 (f16's largest is almost 2^16), and where a half's largest is below 2^-8, a row's maximum
+// falls to it: the weights lost in a half, less than 2^-25 each, are less than 2^-11 of its largest.  Rows of the same warp
+// that are below 2^-2 then fall too: left to fall one by one, 32 rows under a key that is 12 nats above the rest look for
+// their maxima that much more often (2 x 512 tokens over 4096: 108 us, and 95 together).
+constexpr CacheRange kCacheWideRange{6.f, -2.f, 15.f};
 constexpr float kCacheWideLow = 0x1p-8f, kCacheWideTop = 0x1p15f;
 
 // The halves of a unit's key tile t that have a key some row sees (one at least).
@@ -380,11 +381,11 @@ __device__ void cache_wide_softmax_role(const CacheFwdParams& p, CacheCursor cur
                 }
                 l += sum;
                 ptx::tmem_st32(s_addr, code);
-                ptx::tmem_st_wait();
                 if (h == 0) wait(L::kVFull + stage, phase);
                 if (__all_sync(0xffffffffu, alive))
                     cache_widen_half(base + (uint32_t)stage * L::kStageBytes, h * 64, key0, D, u.keys, keys_all, nan_at, nan_seen);
                 ptx::fence_proxy_async_smem();
+                ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 arrive(L::kPFull + (int)(step & 1));
             }
