@@ -637,6 +637,11 @@ __device__ __forceinline__ float cache_sum_rows(float* l) {
     return x;
 }
 
+// Eight rows' bits, row r's from bit r to bit 8 (r mod 4) + r / 4.
+__device__ __forceinline__ uint32_t cache_row_bits(uint32_t x) {
+    return ((x & 15u) * 0x00204081u & 0x01010101u) | ((x >> 4 & 15u) * 0x00204081u & 0x01010101u) << 1;
+}
+
 template <int R>
 __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8_t* smem, uint32_t tmem,
                                    volatile int* abort_flag) {
@@ -726,7 +731,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                 // largest.  The sums count once the weights do: one that is too large, over V's least scale, may be past
                 // what a float holds.
                 float sum[H];
-                uint32_t reach = 0;  // rows whose weight reached 1 here (where no key is masked), as in can_fall
+                uint32_t reach = 0;  // rows whose weight reached 1 here, as in can_fall
                 auto pass = [&](auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
                     float top = 0.f;
@@ -761,11 +766,9 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                         lo[r / 2] = e4m3_pair(r0, r1);
                     }
                     auto four = [](const uint32_t* v) { return __byte_perm(v[0], v[1], 0x5410); };
-                    if constexpr (!kMasked) {
-                        constexpr uint32_t kCarry = (0x80u - kCacheReach) * 0x01010101u;  // into a byte's top bit from 1 on
-                        reach = (four(hi) + kCarry) >> 7 & 0x01010101u;
-                        if constexpr (H == 8) reach |= (four(hi + 2) + kCarry) >> 6 & 0x02020202u;
-                    }
+                    constexpr uint32_t kCarry = (0x80u - kCacheReach) * 0x01010101u;  // into a byte's top bit from 1 on
+                    reach = (four(hi) + kCarry) >> 7 & 0x01010101u;
+                    if constexpr (H == 8) reach |= (four(hi + 2) + kCarry) >> 6 & 0x02020202u;
                     if constexpr (L::kPerKey) {
                         constexpr uint32_t kTurn = L::kN == 64 ? 1 : 2;  // key bits that swizzle
                         const uint32_t turn = ((uint32_t)j >> kTurn) & (L::kN / 16 - 1);
@@ -818,7 +821,7 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                             row_max = m;
                             peak = fmaxf(peak, m);
                             const uint32_t can = __ballot_sync(0xffffffffu, m > -INFINITY && m > peak - kCacheFall);
-                            can_fall = ((can & 15u) * 0x00204081u & 0x01010101u) | ((can >> 4 & 15u) * 0x00204081u & 0x01010101u) << 1;
+                            can_fall = cache_row_bits(can);
                             if (wq == 0 && lane < H) {
                                 fac[lane] = f;
                                 reinterpret_cast<float*>(tab + lane / 2)[2 + (lane & 1)] = m == -INFINITY ? -INFINITY : kCacheRange.room - m;
@@ -842,14 +845,17 @@ __device__ void cache_softmax_role(const CacheFwdParams& p, uint32_t base, uint8
                     }
                     const float top = full ? pass(std::false_type()) : pass(std::true_type());
                     if (look) break;
-                    // All four warps decide by what each has written, two tiles' words in turn: alike after an abort too.
+                    // All four warps decide by what each has written, two tiles' words in turn, and by the unit: alike after an
+                    // abort too.  Nobody falls where a page is missing.
                     uint32_t* reached = reinterpret_cast<uint32_t*>(smem + L::kReach) + (sb * L::kWgs + wg) * 4;
-                    reach = __reduce_or_sync(0xffffffffu, full ? reach : ~0u);
+                    reach = __reduce_or_sync(0xffffffffu, missing == 0 ? reach : ~0u);
                     if (lane == 0) reached[wq] = reach;
                     look = ptx::bar_any(bar, 128, top > kCacheTop);
                     const uint4 x = *reinterpret_cast<const uint4*>(reached);
-                    look = look || (can_fall & ~(x.x | x.y | x.z | x.w)) != 0;
-                    if (!look) break;
+                    uint32_t low = can_fall & ~(x.x | x.y | x.z | x.w);
+                    if (some) low &= cache_row_bits(__ballot_sync(0xffffffffu, lane < H && rows[lane].keys > key - j));
+                    if (!look && low == 0) break;
+                    look = true;
                 }
 #pragma unroll
                 for (int r = 0; r < H; ++r) l[r] = sum[r];

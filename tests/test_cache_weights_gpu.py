@@ -87,6 +87,20 @@ def test_small_weights_add_up(Hq, Sq, near, every, low):
 
 
 @pytest.mark.parametrize("Hq,Sq", SHAPES)
+@pytest.mark.parametrize("n", [200, 257, 384, 130])
+def test_keys_of_the_last_tile_keep_their_weights(Hq, Sq, n):
+    """A first key 2^22 above the rest, with V = 1 from the second tile of 128 on alone: what is left of that tile is
+    a tile whose weights are measured against its own largest, also where it is the last and cut short."""
+    scores, values = np.zeros(n), np.ones(n)
+    scores[0], values[:128] = 22, 0
+    for sequences in (1, 320):
+        cache, s, v = one_channel(scores, values, 64, sequences=sequences)
+        o, _ = ask(cache, Hq, Sq)
+        ref = want(s, v)[0]
+        assert np.abs(o / ref - 1).max() <= 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("Hq,Sq", SHAPES)
 def test_normal_tails_add_up(Hq, Sq):
     """Scores of deviation 2 nats under one key 10 nats above: O of V = 1 stays 1."""
     rng = np.random.default_rng(5)
