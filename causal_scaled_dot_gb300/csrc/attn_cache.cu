@@ -98,8 +98,8 @@ CacheView view_of(const attn_cache_t* c, unsigned int* status) {
 }
 
 // Query rows of a unit: the least form that takes them all, and 128 from 33 rows on.  Up to 8192 keys, 8 key/value heads:
-// 16 x 5 tokens of 4 query heads each (20 rows) took 51 us with 32 rows a unit and 67 with 128; 32 x 8 of 8 (64 rows) 154
-// with 128, and 180 with 64 in the form of 32.
+// 16 x 5 tokens of 4 query heads each (20 rows) take 48 us with 32 rows a unit and 63 with 128; 32 x 8 of 8 (64 rows) 109
+// with 128, and 153 as two units of 32.
 int rows_per_unit(long long group, long long Sq) {
     const long long rows = group * Sq;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
@@ -107,21 +107,20 @@ int rows_per_unit(long long group, long long Sq) {
 int ctas_per_sm(int R) { return R == 128 ? CacheWideLayout::kCtas : R == 8 ? CacheLayout<8>::kCtas : 1; }
 
 // Key tiles that a unit may have, by the cache's capacity, where units are not split: up to 8 (1024 tokens) joining the
-// pieces takes longer than the tiles in one CTA do.  4 x 200 tokens over up to 1000 keys 27 us, and 33 with 4; 15 x 80
-// heads over 967 keys 16.5 and 20.5; one token of 8 heads over 1000 keys 11.7 and 11.0.  With 11, 2 x 32 heads over 1400
-// keys 14.0 instead of 12.5.
+// pieces takes longer than the tiles in one CTA do.  4 x 200 tokens of 32 heads over 8 and up to 1000 keys 28 us, and 40
+// with 4; 15 x 80 heads of their own over 967 keys 54 and 58; one token of 8 heads over 1000 keys 11.3 and 10.5.  With 11,
+// 2 x 32 heads over 1400 keys 14.9 instead of 13.5.
 constexpr int kWholeTiles = 8;
 // What changing to a unit costs a CTA, in key tiles: q, the first maximum, the row's leaving.  Counted as nothing (0),
-// CTAs with many short units end last: 33 sequences of up to 2060 tokens and one empty slot, 16 heads of 64, take 60 us,
-// and 37 with 3; 16 x 5 drafted tokens 51 and 47; 4 x 64 tokens over 2000 keys 34 and 27.  With 2 and 4, 0 to 3 % more.
+// CTAs with many short units end last: 32 sequences of up to 2060 tokens and one empty slot, 16 heads of 64, take 46 us,
+// and 33 with 3; 16 x 5 drafted tokens 51 and 48; 4 x 64 tokens over up to 2000 keys 34 and 31.
 constexpr int kStart = 3;
-// Places that a CTA of the wide kernel takes at least.  4 x 64 tokens over up to 2000 keys, 32 heads over 8: 27 us with 4,
-// 30 with 1, 33 with 6; 1 joins more pieces, 6 leaves SMs without work.
+// Places that a CTA of the wide kernel takes at least: 1 joins more pieces, 6 leaves SMs without work.  4 x 64 tokens over
+// up to 2000 keys, 32 heads over 8: 31.0 us with 4, 30.8 with 1, 31.5 with 6.
 constexpr int kWideLeast = 4;
 // CTAs that a unit keeps busy at most when there are few, and those that few units keep busy at least.  131072 keys, one
-// unit of 8 / 16 / 32 / 128 rows: 22 / 24 / 30 / 54 us with 128 CTAs, 27 / 28 / 36 / 59 with 64; two units of 128 rows:
-// 58 with 128, 64 with 256; four of 4 rows over up to 41891 keys: 19 with 256, 26 with 304, which leave no room for the
-// next call's start.
+// unit of 8 / 16 / 32 / 128 rows: 23 / 25 / 31 / 55 us with 128 CTAs, 28 / 28 / 35 / 60 with 64; two units of 128 rows:
+// 60 with 128, 67 with 256.
 constexpr int kMostPieces = 64, kFewBlocks = 128;
 long long tiles_of(const attn_cache_t* c) {
     return ((long long)c->max_blocks * c->block_size + kCacheTile - 1) / kCacheTile;

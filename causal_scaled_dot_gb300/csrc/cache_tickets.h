@@ -17,9 +17,9 @@ namespace attn {
 constexpr unsigned long long kTicketFailed = 0x8000;  // beside a count below it
 
 // Pieces that one CTA joins: up to `most` all of them, else the square root, so that groups of pieces are joined side by
-// side and then the groups: 128 rows of one key/value head over 131072 keys, 128 pieces, take 54 us instead of 145, and
-// 8 rows 22 instead of 26; for fewer pieces the second round costs more than it saves (10 pieces of 1 row: 16.1 us
-// against 13.7).
+// side and then the groups: 128 rows of one key/value head over 131072 keys, 128 pieces, take 55 us instead of 143, and
+// 8 rows 23 instead of 27; for fewer pieces the second round costs more than it saves (30 sequences of 12800 keys in
+// about 10 pieces each: 30 us instead of 26).
 ATTN_HD int cache_group(int pieces, int most) {
     if (pieces <= most) return pieces;
     int n = 2;
