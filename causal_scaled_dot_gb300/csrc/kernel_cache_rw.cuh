@@ -65,6 +65,30 @@ __device__ __forceinline__ float2 e4m3_unpair(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// x / s so that rounding it to a code rounds x / s itself: the quotient's first 24 bits, the last of them set when
+// more follow, which a halfway value cannot have.
+__device__ __forceinline__ float e4m3_divided(float x, float s) {
+    if (!(fabsf(x) < INFINITY)) return NAN;
+    const float q = __fdiv_rz(x, s);
+    return __fmaf_rn(-q, s, x) == 0.f ? q : __uint_as_float(__float_as_uint(q) | 1u);
+}
+
+// The codes of a unit's vectors t, t + threads ... under a scale that is not a power of two, from x once more.  Out of line:
+// a prompt's write takes 11.0 us with it, 11.2 with it inlined, and 10.85 without.
+__device__ __noinline__ void cache_write_divided(const __nv_bfloat16* src, long long stride, unsigned char* dst, int t, int threads,
+                                                 int n_vec, int row_shift, float s) {
+#pragma unroll 1
+    for (int v = t; v < n_vec; v += threads) {
+        const uint4 y = *(reinterpret_cast<const uint4*>(src + (v >> row_shift) * stride) + (v & ((1 << row_shift) - 1)));
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        uint32_t code[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            code[j] = e4m3_pair(e4m3_divided(__uint_as_float(w[j] << 16), s), e4m3_divided(__uint_as_float(w[j] & 0xffff0000u), s));
+        *reinterpret_cast<uint2*>(dst + (long long)v * 8) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+    }
+}
+
 // A unit's place: sequence, head, K or V, and which of the blocks that the call touches.
 struct CacheRwUnit {
     int b, h, is_v, blk;
@@ -152,7 +176,7 @@ __global__ void __launch_bounds__(256, 4) attn_cache_write_kernel(const __grid_c
     if (!active) return;
 
     const float s_new = fmaxf(e4m3_pow2_scale(__uint_as_float(amax << 16)), s_old);
-    const float inv = 1.f / s_new;  // exact for the powers of two that this kernel stores (at most 2^120)
+    const float inv = 1.f / s_new;  // exact for the powers of two that this kernel stores (at most 2^120); else below
     const uint64_t inv2 = ptx::f2(inv, inv);
     unsigned char* dst = (u.is_v ? c.v : c.k) + cache_offset(block, u.h, slot0, c.Hkv, c.block_size, c.D);
 #pragma unroll
@@ -173,6 +197,8 @@ __global__ void __launch_bounds__(256, 4) attn_cache_write_kernel(const __grid_c
         }
         *reinterpret_cast<uint2*>(dst + (long long)v * 8) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
     }
+    if (slot0 > 0 && (__float_as_uint(s_new) & 0x7fffffu) != 0)  // a caller's scale, which the block had
+        cache_write_divided(src + row0 * stride, stride, dst, t, kThreads, n_vec, row_shift, s_new);
     if (slot0 > 0 && s_new > s_old) {  // the block's earlier tokens move to the larger scale
         const float ratio = s_old * inv;
         uint2* had = reinterpret_cast<uint2*>((u.is_v ? c.v : c.k) + cache_offset(block, u.h, 0, c.Hkv, c.block_size, c.D));

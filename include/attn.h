@@ -392,7 +392,8 @@ typedef struct {
  * 2^-126) with max|x| <= 448 s over its tokens, and code = x / s rounded to
  * nearest even: the division is exact, so codes do not depend on how the
  * tokens were split over calls beyond what moving a block to a larger scale
- * costs.  A block that held tokens before this call keeps its scale unless a
+ * costs.  A block that held tokens before this call keeps its scale, be it a
+ * power of two or a caller's, unless a
  * new token needs a larger one; its earlier codes are then multiplied by
  * (old scale / new scale) and rounded again, which is exact but for values
  * that fall below 2^-6 (E4M3's smallest normal).  Earlier tokens must have been
