@@ -58,7 +58,9 @@ class KVCache:
     default stream's; default: that device's current stream), and do not synchronise unless
     ``check_status`` asks for it: it then raises AttnError if a device-side wait ran
     out or a block number or length lay outside the cache (one status word per
-    device, shared by every stream on it)."""
+    device, shared by every stream on it).  Attention over more than 1024 tokens a
+    sequence keeps a workspace of up to 40 MB for each device and stream, for the
+    process's lifetime; captured calls take theirs from their graph's memory."""
 
     def __init__(self, k, v, k_scale, v_scale, block_table, seq_lens):
         named = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, block_table=block_table, seq_lens=seq_lens)
