@@ -15,7 +15,7 @@
 // so what counts is that a unit's loads leave together and that many units are
 // resident: 64 elements a thread, four blocks of 256 threads an SM (the write: 12.0
 // us with three, 12.8 with five, which spill).  16.8 M elements of D = 128 in blocks
-// of 64, cold: write 10.8 us, read 9.7 (4.7 and 5.2 TB/s, launch included).
+// of 64, cold: write 11.0 us, read 9.8 (4.6 and 5.1 TB/s, launch included).
 #pragma once
 
 #include <cuda_bf16.h>
