@@ -13,9 +13,13 @@
 #include "cache_index.h"
 #include "common.cuh"
 #include "host.h"
+#include "kernel_cache_append.cuh"
 #include "kernel_cache_fwd.cuh"
 #include "kernel_cache_rw.cuh"
 #include "kernel_cache_wide.cuh"
+#include "launch.h"
+#include "rope_check.h"
+#include "rows.h"
 
 namespace attn {
 namespace {
@@ -169,28 +173,6 @@ int setup_cache_kernels(int dev) {
     return g_cache_ready[dev] == 1 ? ATTN_OK : g_cache_ready[dev];
 }
 
-// A launch.  `early`: its blocks may start while the kernel before it in the stream still runs (they wait for that
-// kernel's end before they touch memory), so that the start of a call, barriers, tensor memory and instructions, overlaps
-// the end of the call before: 2.4 -> 2.1 us for a short read, 13.4 -> 13.0 for one token of 32 heads.  Not the wide
-// kernel, which leaves SMs without blocks when there is little work: its blocks then gather on the SMs that end first (4 x
-// 64 tokens over 2000 keys: 33 -> 36 us).
-template <typename K, typename... Args>
-int launch(K kernel, int grid, int threads, size_t smem, bool early, cudaStream_t st, const Args&... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(grid);
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = smem;
-    config.stream = st;
-    config.attrs = &attr;
-    config.numAttrs = early ? 1 : 0;
-    if (cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess) return ATTN_OK;
-    cudaGetLastError();  // reported here, not by a later call
-    return ATTN_ERR_LAUNCH;
-}
-
 template <typename L, typename K>
 int launch_fwd(K kernel, const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int sms, long long tiles,
                cudaStream_t st) {
@@ -208,6 +190,24 @@ template <typename P, typename K>
 int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
     const int per = 256 / threads;
     return launch(kernel, (p.num_units + per - 1) / per, 256, 0, true, st, p);
+}
+
+// q's heads a thread at most, and the units that their number comes down for (rope_plan).
+constexpr int kAppendPer = 8;
+constexpr long long kAppendUnits = 608;
+template <int D, bool kInter>
+int launch_append(int elements, CacheAppendParams& p, long long q_units, cudaStream_t st) {
+    const int threads = elements <= 64 * 32 ? 32 : elements <= 64 * 64 ? 64 : elements <= 64 * 128 ? 128 : 256;
+    const int per = 256 / threads;
+    p.write_blocks = (p.num_units + per - 1) / per;
+    if (p.write_blocks + q_units > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    const int grid = p.write_blocks + (int)q_units;
+    switch (threads) {
+        case 32: return launch(attn_cache_append_kernel<D, kInter, 32>, grid, 256, 0, true, st, p);
+        case 64: return launch(attn_cache_append_kernel<D, kInter, 64>, grid, 256, 0, true, st, p);
+        case 128: return launch(attn_cache_append_kernel<D, kInter, 128>, grid, 256, 0, true, st, p);
+        default: return launch(attn_cache_append_kernel<D, kInter, 256>, grid, 256, 0, true, st, p);
+    }
 }
 
 }  // namespace
@@ -252,6 +252,72 @@ extern "C" int attn_cache_write(const attn_cache_t* cache, const void* k, const 
     if (elements <= 64 * 64) return launch_rw(attn_cache_write_kernel<64>, 64, p, st);
     if (elements <= 64 * 128) return launch_rw(attn_cache_write_kernel<128>, 128, p, st);
     return launch_rw(attn_cache_write_kernel<256>, 256, p, st);
+}
+
+extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* rope, const attn_heads_t* in, void* q_out,
+                                 const int* new_lens, int Hq, int S, void* stream) {
+    int rc = check_cache(cache);
+    if (rc != ATTN_OK) return rc;
+    const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
+    if ((rc = host::check_rope(rope, D)) != ATTN_OK) return rc;
+    if (!in || !in->k || !in->v || S < 1 || !in->q != !q_out || (in->q && Hq < 1)) return ATTN_ERR_INVALID_ARG;
+    if (S > (1 << 29) || (in->q && Hq > (1 << 20)) || (long long)B * S > (1ll << 31) - 64) return ATTN_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(in->q) | reinterpret_cast<uintptr_t>(in->k) | reinterpret_cast<uintptr_t>(in->v) |
+         reinterpret_cast<uintptr_t>(q_out)) & 15u || reinterpret_cast<uintptr_t>(new_lens) & 3u)
+        return ATTN_ERR_MISALIGNED;
+    CacheAppendParams p{};
+    const void* from[3] = {in->q, in->k, in->v};
+    const long long* strides[3] = {in->q_strides, in->k_strides, in->v_strides};
+    size_t bytes[3] = {0, 0, 0};
+    const size_t nl = new_lens ? (size_t)B * 4 : 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!from[i]) continue;
+        const int H = i == 0 ? Hq : Hkv;
+        const long long* x = strides[i];
+        const long long used[3] = {B > 1 ? x[0] : 0, H > 1 ? x[1] : 0, S > 1 ? x[2] : 0};
+        if ((rc = row_strides(used, B, H, S, D, p.in.stride[i], &bytes[i])) != ATTN_OK) return rc;
+        p.in.p[i] = static_cast<__nv_bfloat16*>(const_cast<void*>(from[i]));
+        if (meets_cache(cache, from[i], bytes[i], false)) return ATTN_ERR_INVALID_ARG;
+    }
+    const size_t n = (size_t)cache_bytes(cache), ns = (size_t)cache->num_blocks * Hkv * 4;
+    if (meets_itself(cache) || (nl && meets_cache(cache, new_lens, nl, false)) || host::rope_meets(rope, cache->k, n, B, S, D) ||
+        host::rope_meets(rope, cache->v, n, B, S, D) || host::rope_meets(rope, cache->k_scale, ns, B, S, D) ||
+        host::rope_meets(rope, cache->v_scale, ns, B, S, D))
+        return ATTN_ERR_INVALID_ARG;
+    long long q_units = 0;
+    if (q_out) {
+        const size_t qb = (size_t)B * Hq * S * D * 2;
+        if (meets_cache(cache, q_out, qb, true) || (nl && host::ranges_overlap(q_out, qb, new_lens, nl)) ||
+            host::rope_meets(rope, q_out, qb, B, S, D))
+            return ATTN_ERR_INVALID_ARG;
+        for (int i = 0; i < 3; ++i)
+            if (host::ranges_overlap(q_out, qb, from[i], bytes[i])) return ATTN_ERR_INVALID_ARG;
+        p.out.p[0] = static_cast<__nv_bfloat16*>(q_out);
+        p.out.stride[0][0] = (long long)Hq * S * D;
+        p.out.stride[0][1] = (long long)S * D;
+        p.out.stride[0][2] = D;
+        p.plan = rope_plan((long long)B * S, Hq, 0, 0, D, kAppendPer, kAppendUnits);
+        q_units = rope_tiles(p.plan) * rope_chunks(p.plan);
+    }
+    int sms = 0, device = -1;
+    unsigned int* status = nullptr;
+    if ((rc = host::current_device(&sms, &status, &device)) != ATTN_OK) return rc;
+    p.c = view_of(cache, status);
+    host::fill_rope(rope, &p.r);
+    p.new_lens = new_lens;
+    p.S = S;
+    const int bs = cache->block_size;
+    // as in attn_cache_write
+    const long long touched = ((long long)S + bs - 2) / bs + 1;
+    p.blocks_per_seq = (int)(touched < cache->max_blocks ? touched : cache->max_blocks);
+    const long long units = (long long)B * Hkv * 2 * p.blocks_per_seq;
+    if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
+    p.num_units = (int)units;
+    const int elements = (S < bs ? S : bs) * D;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (D == 64)
+        return rope->interleaved ? launch_append<64, true>(elements, p, q_units, st) : launch_append<64, false>(elements, p, q_units, st);
+    return rope->interleaved ? launch_append<128, true>(elements, p, q_units, st) : launch_append<128, false>(elements, p, q_units, st);
 }
 
 extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int first, int S, void* stream) {

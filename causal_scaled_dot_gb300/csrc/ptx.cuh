@@ -494,6 +494,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float x0, float x1, float x2, fl
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
+// Launched with the attribute that lets its blocks start while the kernel before still runs: `launch_next` lets the kernel after
+// do so too, `wait_previous` ends when everything before has ended and is visible.  Nothing global is read or written
+// before that, and nothing that a kernel before may have written is read through the non-coherent path (__ldg), which
+// asks for data that stays the same from the launch on.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Two floats -> packed bf16x2 (round to nearest even); `lo` in bits 0-15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t r;

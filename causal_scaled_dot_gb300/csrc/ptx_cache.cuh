@@ -126,13 +126,6 @@ __device__ __forceinline__ bool mbar_wait_call(uint32_t bar, uint32_t parity, vo
     return mbar_test_wait(bar, parity) || mbar_wait_rest(bar, parity, abort_flag, status, limit_ns);
 }
 
-// Launched with the attribute that lets its blocks start while the kernel before still runs: `launch_next` lets the kernel after
-// do so too, `wait_previous` ends when everything before has ended and is visible.  Nothing global is read or written
-// before that, and nothing that a kernel before may have written is read through the non-coherent path (__ldg), which
-// asks for data that stays the same from the launch on.
-__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

@@ -1,0 +1,84 @@
+// rope_index.h -- how the rotation's work is laid out (attn_rope and attn_rope_bwd in include/attn.h): which elements
+// of a head a lane holds, and which rows a block takes.  Plain C++ without CUDA calls: host tests compile it by itself.
+#pragma once
+
+#ifdef __CUDACC__
+#define ROPE_HD __host__ __device__ __forceinline__
+#else
+#define ROPE_HD inline
+#endif
+
+namespace attn {
+
+// A row (one head of one token) is held by D / 16 lanes, two vectors of 8 elements each, so that both elements of every
+// pair are in one lane.
+constexpr int kRopeThreads = 256;
+
+// The vectors of lane `l` and whether they are rotated.  Half layout: rotated lanes hold vector l and the one rot / 2
+// elements further, element j of the one paired with element j of the other (pair 8 l + j); the rest of the head goes to
+// the other lanes in order.  Interleaved: vectors l and l + D / 16, four pairs each (pairs 4 * vector + 0 .. 3).
+struct RopeLane {
+    int a, b;        // vectors, in units of 8 elements
+    int turn_a, turn_b;
+};
+ROPE_HD RopeLane rope_lane(int l, int D, int rot, int interleaved) {
+    RopeLane x;
+    if (interleaved) {
+        x.a = l;
+        x.b = l + D / 16;
+        x.turn_a = x.a * 8 < rot;
+        x.turn_b = x.b * 8 < rot;
+    } else {
+        const int n = rot / 16;
+        x.turn_a = x.turn_b = l < n;
+        x.a = l < n ? l : 2 * l;
+        x.b = l < n ? l + n : 2 * l + 1;
+    }
+    return x;
+}
+
+// A block's rows: `tokens` (a power of two) by kRopeThreads / (D / 16) / tokens heads side by side, and up to `per` such
+// groups of heads one after the other, all of one kind (q, k or v).  The units of a tile of tokens stand side by side.
+struct RopePlan {
+    long long total;     // tokens, B * S
+    int tokens, groups;  // tokens and heads side by side
+    int per;             // heads of a thread, at most
+    int heads[3];        // of q, k and v; 0: absent
+    int chunks[3];       // units of each kind in a tile of tokens
+};
+ROPE_HD int rope_chunks(const RopePlan& p) { return p.chunks[0] + p.chunks[1] + p.chunks[2]; }
+ROPE_HD long long rope_tiles(const RopePlan& p) { return (p.total + p.tokens - 1) / p.tokens; }
+
+struct RopeUnit {
+    long long tile;
+    int kind, chunk;
+};
+ROPE_HD RopeUnit rope_unit(const RopePlan& p, unsigned int unit) {
+    const unsigned int all = (unsigned int)rope_chunks(p);
+    RopeUnit u;
+    u.tile = unit / all;
+    u.chunk = (int)(unit - (unsigned int)u.tile * all);
+    u.kind = 0;
+    while (u.chunk >= p.chunks[u.kind]) u.chunk -= p.chunks[u.kind++];
+    return u;
+}
+
+// The plan for `total` tokens and these heads: `most` tokens side by side where there are so many, and as many heads a
+// thread as still give `units` units, `per` at most.
+ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int per, long long units) {
+    RopePlan p;
+    const int rows = kRopeThreads / (D / 16);
+    p.total = total;
+    p.tokens = 1;
+    while (p.tokens < rows && p.tokens < total) p.tokens *= 2;
+    p.groups = rows / p.tokens;
+    p.heads[0] = Hq;
+    p.heads[1] = Hk;
+    p.heads[2] = Hv;
+    for (p.per = per;; p.per = (p.per + 1) / 2) {
+        for (int i = 0; i < 3; ++i) p.chunks[i] = (p.heads[i] + p.groups * p.per - 1) / (p.groups * p.per);
+        if (p.per == 1 || rope_tiles(p) * rope_chunks(p) >= units) return p;
+    }
+}
+
+}  // namespace attn

@@ -1,10 +1,15 @@
 """A paged key/value cache in 8 bits over libattn's cache entry points
-(``attn_cache_write``, ``attn_cache_read``, ``attn_cache_fwd`` in include/attn.h).
+(``attn_cache_write``, ``attn_cache_append``, ``attn_cache_read``, ``attn_cache_fwd`` in include/attn.h).
 
     cache = KVCache.empty(batch, kv_heads, head_dim, max_tokens, device="cuda")
     cache.seq_lens.add_(n)             # the step's n new tokens count from here on
     cache.write(k, v)                  # k, v [B, Hkv, n, D] bf16, quantised into the cache
     out, lse = cache.attention(q)      # q [B, Hq, n, D] bf16 over everything held
+
+or, with rotary positions (and norms of the heads) on the way into the cache, from the
+heads as projected:
+
+    q = cache.append(k, v, rotary, q=q)          # rotary: a rotary.Rotary
 
 Argument marshalling only: the tensors are the caller's (or ``empty``'s), the work runs
 in the CUDA library.  There are no gradients through a cache.
@@ -18,6 +23,7 @@ import math
 import torch
 
 from . import native
+from .rotary import _heads_of
 
 _DIMS3 = ctypes.c_longlong * 3
 # The current stream's handle by device index.  A step calls write and attention once per layer, and
@@ -192,6 +198,47 @@ class KVCache:
             with self._on(stream) as st:
                 rc = self._lib.attn_cache_write(self._ref, k.data_ptr(), ks, v.data_ptr(), vs, n, S, st)
         self._done("attn_cache_write", rc, st, check_status)
+
+    def append(self, k, v, rotary, q=None, new_lens=None, positions=None, first: int = 0, q_norm=None, k_norm=None,
+               eps: float = 1e-6, q_out=None, stream=None, check_status: bool = False):
+        """``write`` of the step's heads as projected: K normed (``k_norm``, [D] bf16 or fp32, if given) and
+        rotated by ``rotary`` (a rotary.Rotary) before it is quantised, V as it is, in one launch with the
+        step's queries q (bf16 [B, Hq, S, D], strides as k's), which come back normed and rotated,
+        contiguous, for ``attention`` (``attn_cache_append``).  A token stands at its place in the cache
+        plus ``first``, or at ``positions[b, i]`` (int32 or int64 [B, S] or [S] on the device).  Rows of q
+        past ``new_lens[b]`` are left as they were in ``q_out`` when given, and unspecified otherwise."""
+        B, Hkv, D = self._sizes
+        S, _ = self._rows("k", k, Hkv)
+        self._rows("v", v, Hkv, S)
+        Hq = 0
+        if q is not None:
+            self._rows("q", q, 0, S)
+            Hq = q.shape[1]
+            if q_out is not None:
+                self._rows("q_out", q_out, Hq, S, strided=False)
+        elif q_out is not None or q_norm is not None:
+            raise ValueError("q_out and q_norm go with q")
+        if torch.is_grad_enabled():
+            for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+                if w is not None and w.requires_grad:
+                    raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
+        n = self._counts("new_lens", new_lens)
+        c = rotary._plan(self._device, B, S, D, positions, first, q_norm, k_norm, eps)
+        heads = _heads_of(q, k, v)
+        if self._here(stream):
+            st = _stream_handle(self._index)
+            q_out, rc = self._append(c, heads, q, q_out, n, Hq, S, st)
+        else:
+            with self._on(stream) as st:
+                q_out, rc = self._append(c, heads, q, q_out, n, Hq, S, st)
+        self._done("attn_cache_append", rc, st, check_status)
+        return q_out
+
+    def _append(self, c, heads, q, q_out, n, Hq, S, st):
+        if q is not None and q_out is None:
+            q_out = torch.empty((self._sizes[0], Hq, S, self._sizes[2]), dtype=torch.bfloat16, device=self._device)
+        rc = self._lib.attn_cache_append(self._ref, c, heads, None if q_out is None else q_out.data_ptr(), n, Hq, S, st)
+        return q_out, rc
 
     def read(self, S: int, first: int = 0, k_out=None, v_out=None, stream=None, check_status: bool = False):
         """Positions first .. first+S-1 of every sequence as bf16 (k, v), each

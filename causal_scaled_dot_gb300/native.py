@@ -98,6 +98,15 @@ def load() -> ctypes.CDLL:
         lib.attn_cache_fwd.restype = ci
         lib.attn_cache_workspace.argtypes = [cache_p, ci, ci, ctypes.POINTER(u64)]
         lib.attn_cache_workspace.restype = ci
+        rope_p, heads_p = ctypes.POINTER(AttnRope), ctypes.POINTER(AttnHeads)
+        lib.attn_rope.argtypes = [rope_p, heads_p, heads_p, ci, ci, ci, ci, ci, vp]
+        lib.attn_rope.restype = ci
+        lib.attn_rope_bwd.argtypes = [rope_p, heads_p, heads_p, heads_p, vp, vp, ci, ci, ci, ci, ci, vp, u64, vp]
+        lib.attn_rope_bwd.restype = ci
+        lib.attn_rope_workspace.argtypes = [rope_p, ci, ci, ci, ci, ci, ctypes.POINTER(u64)]
+        lib.attn_rope_workspace.restype = ci
+        lib.attn_cache_append.argtypes = [cache_p, rope_p, heads_p, vp, vp, ci, ci, vp]
+        lib.attn_cache_append.restype = ci
         _lib = lib
         return lib
 
@@ -126,7 +135,23 @@ class AttnCache(ctypes.Structure):
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
 
 
+class AttnRope(ctypes.Structure):
+    """The C struct attn_rope_t (include/attn.h), field for field; ``rotary.Rotary`` fills one."""
+    _fields_ = [("turns", ctypes.c_ulonglong * 64), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("factor", ctypes.c_float), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_format", ctypes.c_int), ("positions_64", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("position_stride", ctypes.c_longlong), ("first", ctypes.c_longlong)]
+
+
+class AttnHeads(ctypes.Structure):
+    """The C struct attn_heads_t (include/attn.h), field for field."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_strides", ctypes.c_longlong * 3), ("k_strides", ctypes.c_longlong * 3),
+                ("v_strides", ctypes.c_longlong * 3)]
+
+
 ATTN_INPUT_BF16, ATTN_INPUT_E4M3 = 0, 1
+ATTN_WEIGHT_BF16, ATTN_WEIGHT_F32 = 0, 1
 
 
 def options(e4m3_descales=None, block_mask=None, keep_bits=None, dropout_p: float = 0.0, seed: int = 0,

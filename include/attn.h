@@ -7,8 +7,10 @@
  * the weights attn_fwd_dropout; their combinations attn_fwd_ex), the matching
  * gradients (attn_bwd, attn_bwd_block_masked, attn_bwd_elem_masked,
  * attn_bwd_dropout, attn_bwd_ex), the output
- * projection of the attention output (attn_out_proj), an 8-bit key/value cache
- * (attn_cache_write, attn_cache_read, and attention over it,
+ * projection of the attention output (attn_out_proj), what stands before it all
+ * (attn_rope, attn_rope_bwd with attn_rope_workspace: norms of the heads of q and
+ * k, rotary positions and the layout), an 8-bit key/value cache
+ * (attn_cache_write, attn_cache_append, attn_cache_read, and attention over it,
  * attn_cache_fwd with attn_cache_workspace), status helpers
  * (attn_sync_status, attn_selftest_wait_timeout, attn_status_string,
  * attn_version), and the forward's work order for inspection
@@ -342,6 +344,102 @@ int attn_bwd_ex(const void *q, const void *k, const void *v, const void *out, co
 int attn_out_proj(const void *out, const void *w, const float *bias, void *y, int B, int H, int S,
                   int D, int E, void *stream);
 
+/* Formats of the norms' weights of attn_rope_t. */
+enum { ATTN_WEIGHT_BF16 = 0, ATTN_WEIGHT_F32 = 1 };
+
+/*
+ * attn_rope_t -- rotary positions, with or without norms of the heads of q and
+ * k, as attn_rope, attn_rope_bwd and attn_cache_append take them.  A row x is
+ * one head of one token, D elements at position p.
+ *   Norm (where the weight w is given): u_d = x_d w_d / sqrt(mean(x^2) + eps),
+ *   over the whole head; else u = x.
+ *   Rotation: pair i < rotary_dim / 2 of elements (a, b) turns by p f_i radians
+ *       y_a = factor (u_a cos - u_b sin),   y_b = factor (u_b cos + u_a sin);
+ *   the pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) when `interleaved`;
+ *   elements from rotary_dim on stay as u.
+ * Everything in fp32, rounded once at the end.
+ *
+ *   turns        f_i / (2 pi) as a fraction of 2^64, to nearest (whole turns per
+ *                position drop out): the angle is then exact to |p| 2^-65 turns.
+ *                Entries from rotary_dim / 2 on are not read.
+ *   rotary_dim   0 .. D, a multiple of 16, or of 8 when interleaved (else
+ *                ATTN_ERR_UNSUPPORTED); 0: no rotation.
+ *   factor       finite; 1 but for scalings that ask for another.
+ *   q_weight, k_weight   device memory, [D], 16-byte aligned, bf16 or fp32 as
+ *                weight_format says; NULL: no norm.  Ignored for v.
+ *   eps          finite, at least 2^-100 (where a weight is given).
+ *   positions    device memory, int32, or int64 when positions_64 is non-zero:
+ *                row s of sequence b stands at positions[b * position_stride + s]
+ *                (position_stride in elements, 0: one row for all sequences).
+ *                Any value.  NULL: at first + s.
+ */
+typedef struct {
+    unsigned long long turns[64];
+    int rotary_dim, interleaved;
+    float factor, eps;
+    const void *q_weight, *k_weight;
+    int weight_format;
+    int positions_64;
+    const void *positions;
+    long long position_stride, first;
+} attn_rope_t;
+
+/*
+ * attn_heads_t -- rows of q, k and v, bf16 [B, H, S, D] with D contiguous, as
+ * they lie: 16-byte aligned, {batch, head, token} strides in elements, each >= 0
+ * and a multiple of 8 (those of a dimension of 1 are not read), so views of a
+ * projection's output [B, S, (Hq + 2 Hkv) D] will do.  NULL: absent.
+ */
+typedef struct {
+    void *q, *k, *v;
+    long long q_strides[3], k_strides[3], v_strides[3];
+} attn_heads_t;
+
+/*
+ * attn_rope -- norm and rotate the heads of q and k, and bring them and v into
+ * another layout (attn_fwd and attn_cache_fwd take contiguous [B, H, S, D]), in
+ * one pass.
+ *   in, out   the same of q, k and v in both, at least one; v is copied as it
+ *             is.  Rows of `out` may share elements with nothing that the call
+ *             reads or writes, except that a tensor may be written where it is
+ *             read (same address, same strides).
+ *   B * S < 2^31 - 64;  D  64 or 128.
+ * One kernel on `stream`, asynchronous; allocates nothing.  Errors as attn_fwd.
+ */
+int attn_rope(const attn_rope_t *rope, const attn_heads_t *in, const attn_heads_t *out, int B, int Hq,
+              int Hkv, int S, int D, void *stream);
+
+/*
+ * attn_rope_bwd -- the gradients of attn_rope's outputs on their way back:
+ *     g = the upstream gradient turned back (times factor),
+ *     no norm: dx = g;   norm, r = 1 / sqrt(mean(x^2) + eps):
+ *     dw_d = sum over all rows of g_d x_d r,
+ *     dx_d = r (g_d w_d - x_d r mean(g w x r)).
+ *   rope     as passed to attn_rope.
+ *   grad     upstream gradients of q, k and v; expanded ones (strides of 0) will do.
+ *   in       attn_rope's input q and k, read where they have a norm (else, and
+ *            for v, not looked at; NULL when neither has).
+ *   out      dq, dk, dv, in any layout, written; they keep apart from all else as
+ *            in attn_rope (each may be written where its `grad` or `in` was read).
+ *   dq_weight, dk_weight   [D] in the weights' format, 16-byte aligned, written;
+ *            NULL: not wanted.  A tensor of `out` may be absent when only its
+ *            weight's gradient is wanted; `grad` holds exactly what is used.
+ *   workspace  device memory, 16-byte aligned, of at least the bytes that
+ *            attn_rope_workspace gives (used only for the weights' gradients; NULL
+ *            without them); calls that may run at the same time need one each.
+ * Sums are fp32 in a fixed order: results are deterministic.  One kernel on
+ * `stream`, and a second one for the weights' gradients; asynchronous,
+ * allocates nothing.  Errors as attn_rope.
+ */
+int attn_rope_bwd(const attn_rope_t *rope, const attn_heads_t *grad, const attn_heads_t *in,
+                  const attn_heads_t *out, void *dq_weight, void *dk_weight, int B, int Hq, int Hkv, int S,
+                  int D, void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/* attn_rope_workspace -- *bytes receives the workspace that attn_rope_bwd needs
+ * for these sizes and both weights' gradients; 0 without weights. */
+int attn_rope_workspace(const attn_rope_t *rope, int B, int Hq, int Hkv, int S, int D,
+                        unsigned long long *bytes);
+
 /*
  * attn_cache_t -- a paged key/value cache in 8 bits, as attn_cache_write,
  * attn_cache_read and attn_cache_fwd take it.  A block (page) holds
@@ -411,6 +509,26 @@ typedef struct {
 int attn_cache_write(const attn_cache_t *cache, const void *k, const long long *k_strides,
                      const void *v, const long long *v_strides, const int *new_lens, int S,
                      void *stream);
+
+/*
+ * attn_cache_append -- attn_cache_write of a step's heads as the projection
+ * gives them: K normed and rotated on the way, V as it is, and q normed and
+ * rotated for the attn_cache_fwd that follows, in one kernel.
+ *   rope      as in attn_rope.  Without positions a token stands at its place in
+ *             the cache plus `first`; with them positions[b * position_stride + i]
+ *             is that of row i of sequence b.
+ *   in        k and v [B, Hkv, S, D], and q [B, Hq, S, D] or NULL, any layout.
+ *   q_out     bf16 [B, Hq, S, D] contiguous, 16-byte aligned (NULL without q); rows
+ *             from new_lens[b] on are left as they were.
+ *   new_lens, S   as in attn_cache_write.  Hq  >= 1 (ignored without q).
+ * What is written to the cache is what attn_cache_write makes of the rotated
+ * fp32 values (they are not rounded to bf16 in between).  A query row whose
+ * token has a position < 0 in the cache, and so is dropped, is rotated all the
+ * same.  q_out may overlap nothing else; otherwise as attn_cache_write.  One
+ * kernel on `stream`, asynchronous; allocates nothing.
+ */
+int attn_cache_append(const attn_cache_t *cache, const attn_rope_t *rope, const attn_heads_t *in, void *q_out,
+                      const int *new_lens, int Hq, int S, void *stream);
 
 /*
  * attn_cache_read -- positions first .. first+S-1 of every sequence back as bf16:
