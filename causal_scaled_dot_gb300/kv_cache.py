@@ -107,6 +107,7 @@ class KVCache:
         self._ref = ctypes.byref(self._c)
         self._lib = native.load()
         self._workspace_bytes = {}
+        self._steps = {}
 
     @classmethod
     def empty(cls, batch: int, kv_heads: int, head_dim: int, max_tokens: int, block_size: int = 64, device="cuda"):
@@ -208,35 +209,54 @@ class KVCache:
         plus ``first``, or at ``positions[b, i]`` (int32 or int64 [B, S] or [S] on the device).  Rows of q
         past ``new_lens[b]`` are left as they were in ``q_out`` when given, and unspecified otherwise."""
         B, Hkv, D = self._sizes
-        S, _ = self._rows("k", k, Hkv)
-        self._rows("v", v, Hkv, S)
-        Hq = 0
-        if q is not None:
-            self._rows("q", q, 0, S)
-            Hq = q.shape[1]
-            if q_out is not None:
-                self._rows("q_out", q_out, Hq, S, strided=False)
-        elif q_out is not None or q_norm is not None:
+        key = k.shape, k.stride(), v.shape, v.stride(), None if q is None else (q.shape, q.stride())
+        x = self._steps.get(key)
+        if x is None:
+            x = self._step(key, q, k, v)
+        S, Hq = x[0], x[1]
+        for name, t in (("k", k), ("v", v), ("q", q)):
+            if t is not None and (t.dtype is not _BF16 or t.device != self._device):
+                raise ValueError(f"{name} must be a bf16 tensor on {self._device}")
+        if q is None and (q_out is not None or q_norm is not None):
             raise ValueError("q_out and q_norm go with q")
+        if q_out is not None:
+            self._rows("q_out", q_out, Hq, S, strided=False)
         if torch.is_grad_enabled():
-            for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-                if w is not None and w.requires_grad:
+            for name, t in (("k", k), ("v", v), ("q", q), ("q_norm", q_norm), ("k_norm", k_norm)):
+                if t is not None and t.requires_grad:
                     raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
-        n = self._counts("new_lens", new_lens)
+        n = None if new_lens is None else self._counts("new_lens", new_lens)
         c = rotary._plan(self._device, B, S, D, positions, first, q_norm, k_norm, eps)
-        heads = _heads_of(q, k, v)
+        heads = native.AttnHeads.from_buffer_copy(x[2])
+        heads.k, heads.v = k.data_ptr(), v.data_ptr()
+        if q is not None:
+            heads.q = q.data_ptr()
         if self._here(stream):
             st = _stream_handle(self._index)
             q_out, rc = self._append(c, heads, q, q_out, n, Hq, S, st)
         else:
             with self._on(stream) as st:
                 q_out, rc = self._append(c, heads, q, q_out, n, Hq, S, st)
-        self._done("attn_cache_append", rc, st, check_status)
+        if rc or check_status:
+            self._done("attn_cache_append", rc, st, check_status)
         return q_out
+
+    def _step(self, key, q, k, v):
+        """(S, Hq, attn_heads_t without addresses) of an append's heads, checked and kept by their sizes and strides."""
+        S, _ = self._rows("k", k, self._sizes[1])
+        self._rows("v", v, self._sizes[1], S)
+        if q is not None:
+            self._rows("q", q, 0, S)
+        heads = _heads_of(q, k, v)
+        heads.q = heads.k = heads.v = None
+        if len(self._steps) >= 256:
+            self._steps.clear()
+        x = self._steps[key] = S, 0 if q is None else q.shape[1], heads
+        return x
 
     def _append(self, c, heads, q, q_out, n, Hq, S, st):
         if q is not None and q_out is None:
-            q_out = torch.empty((self._sizes[0], Hq, S, self._sizes[2]), dtype=torch.bfloat16, device=self._device)
+            q_out = q.new_empty((self._sizes[0], Hq, S, self._sizes[2]))
         rc = self._lib.attn_cache_append(self._ref, c, heads, None if q_out is None else q_out.data_ptr(), n, Hq, S, st)
         return q_out, rc
 

@@ -13,21 +13,18 @@ Argument marshalling only: the work runs in the CUDA library.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import weakref
-from fractions import Fraction
 
 import torch
 
 from . import native
 
-# pi to 60 decimals (OEIS A000796): a frequency's share of a turn is taken to nearest from its exact double value.
-_PI = Fraction(3141592653589793238462643383279502884197169399375105820974945, 10**60)
+# 1 / (2 pi) to 256 bits, from pi to 100 decimals (OEIS A000796).
+_PER_TURN = (10**100 << 255) // int("31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679")
 _STRIDES = ctypes.c_longlong * 3
 _BF16 = torch.bfloat16
-_WEIGHT = {torch.bfloat16: native.ATTN_WEIGHT_BF16, torch.float32: native.ATTN_WEIGHT_F32}
 _INDEX = {torch.int32: 0, torch.int64: 1}
 # The current stream's handle by device index, without a Stream object.
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -39,6 +36,12 @@ def _frequencies(rotary_dim: int, base: float) -> list[float]:
     if rotary_dim % 2 or not base > 0:
         raise ValueError("rotary_dim must be even and base positive")
     return [base ** (-2 * i / rotary_dim) for i in range(rotary_dim // 2)]
+
+
+def _turns(x: float) -> int:
+    """x / (2 pi) in 2^-64 turns, to nearest, whole turns dropped: the angle of position p is then p times it, mod 2^64."""
+    n, d = x.as_integer_ratio()  # d is a power of two
+    return ((n * _PER_TURN >> d.bit_length() - 1 + 256 - 65) + 1 >> 1) % 2**64
 
 
 class Rotary:
@@ -61,9 +64,8 @@ class Rotary:
         self.rotary_dim = 2 * len(f)
         self.interleaved = bool(interleaved)
         self.factor = float(factor)
-        turns = [round(Fraction(x) / (2 * _PI) * 2**64) % 2**64 for x in f]
+        turns = [_turns(x) for x in f]
         self._c = native.AttnRope((ctypes.c_ulonglong * 64)(*turns), self.rotary_dim, int(self.interleaved), self.factor)
-        self._workspace_bytes = {}
 
     @classmethod
     def from_base(cls, rotary_dim: int, base: float = 10000.0, stretch: float = 1.0, interleaved: bool = False):
@@ -97,6 +99,8 @@ class Rotary:
         """attn_rope_t for a call on tensors of `device`."""
         if self.rotary_dim > D:
             raise ValueError(f"{self.rotary_dim} elements are rotated, and a head has {D}")
+        if positions is None and q_norm is None and k_norm is None and not first:
+            return self._c  # never changed
         c = native.AttnRope.from_buffer_copy(self._c)
         c.first = first
         if positions is not None:
@@ -114,30 +118,15 @@ class Rotary:
             c.position_stride = positions.stride(0) if len(shape) == 2 and shape[0] > 1 else 0
         if q_norm is not None or k_norm is not None:
             c.eps = eps
-            formats = set()
-            for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-                if w is None:
-                    continue
-                if w.device != device or w.dtype not in _WEIGHT or tuple(w.shape) != (D,) or not w.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous bf16 or fp32 tensor [{D}] on {device}")
-                formats.add(_WEIGHT[w.dtype])
-            if len(formats) > 1:
-                raise ValueError("q_norm and k_norm must have one type")
-            c.weight_format = formats.pop()
-            c.q_weight = None if q_norm is None else q_norm.data_ptr()
-            c.k_weight = None if k_norm is None else k_norm.data_ptr()
+            dtype = (k_norm if q_norm is None else q_norm).dtype
+            if dtype is not _BF16 and dtype is not torch.float32:
+                raise ValueError(f"{'k_norm' if q_norm is None else 'q_norm'} must be bf16 or fp32")
+            c.weight_format = native.ATTN_WEIGHT_BF16 if dtype is _BF16 else native.ATTN_WEIGHT_F32
+            if q_norm is not None:
+                c.q_weight = _weight("q_norm", q_norm, dtype, D, device)
+            if k_norm is not None:
+                c.k_weight = _weight("k_norm", k_norm, dtype, D, device)
         return c
-
-    def _need(self, c, B, Hq, Hkv, S, D) -> int:
-        key = (bool(c.q_weight), bool(c.k_weight), B, Hq, Hkv, S, D)
-        need = self._workspace_bytes.get(key)
-        if need is None:
-            n = ctypes.c_ulonglong(0)
-            _ok(native.load().attn_rope_workspace(ctypes.byref(c), B, Hq, Hkv, S, D, ctypes.byref(n)), "attn_rope_workspace")
-            if len(self._workspace_bytes) > 256:
-                self._workspace_bytes.clear()
-            need = self._workspace_bytes[key] = n.value
-        return need
 
     # ------------------------------------------------------------------ calls
     def heads(self, qkv, q_heads: int, kv_heads: int, positions=None, first: int = 0, q_norm=None, k_norm=None,
@@ -153,120 +142,214 @@ class Rotary:
         of the first use, and a backward pass that meets it breaks the capture or ends the process.  A call
         that would is refused where that eager graph is of these functions (ValueError); let it go first,
         pass ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
-        _packed(qkv, q_heads, kv_heads)
+        x = _packed(qkv, q_heads, kv_heads)
         if torch.is_grad_enabled() and _any_grad(qkv, q_norm, k_norm):
-            return _functions()[0].apply(qkv, q_norm, k_norm, self, q_heads, kv_heads, positions, first, eps)
-        return self._heads(qkv, q_heads, kv_heads, positions, first, q_norm, k_norm, eps)
+            return _functions()[0].apply(qkv, q_norm, k_norm, self, x, positions, first, eps)
+        return self._heads(qkv, x, positions, first, q_norm, k_norm, eps)
 
     def rotate(self, q, k=None, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6):
         """q (and k), bf16 [B, H, S, D] of any strides of 16 bytes with D contiguous, normed and rotated as by
         ``heads``, in new contiguous tensors.  Gradients flow to q, k and the norms' weights."""
-        _rows("q", q)
-        if k is not None:
-            _rows("k", k, q)
-        elif k_norm is not None:
-            raise ValueError("k_norm without k")
+        x = _apart(q, k, k_norm)
         if torch.is_grad_enabled() and _any_grad(q, k, q_norm, k_norm):
-            out = _functions()[1].apply(q, k, q_norm, k_norm, self, positions, first, eps)
+            out = _functions()[1].apply(q, k, q_norm, k_norm, self, x, positions, first, eps)
         else:
-            out = self._rotate(q, k, positions, first, q_norm, k_norm, eps)
+            out = self._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
         return out if k is not None else out[0]
 
     def heads_backward(self, dq, dk, dv, qkv, q_heads: int, kv_heads: int, positions=None, first: int = 0, q_norm=None,
                        k_norm=None, eps: float = 1e-6, weight_grads: bool = True):
         """(dqkv, dq_norm, dk_norm) for upstream gradients of what ``heads`` returned with the same arguments.
         Without norms qkv's values are not read.  ``weight_grads=False`` leaves the norms' out (None)."""
-        B, S, W = _packed(qkv, q_heads, kv_heads)
-        D = W // (q_heads + 2 * kv_heads)
-        for name, t, H in (("dq", dq, q_heads), ("dk", dk, kv_heads), ("dv", dv, kv_heads)):
-            _upstream(name, t, (B, H, S, D), qkv.device)
-        with _on(qkv):
-            dqkv = torch.empty((B, S, W), dtype=_BF16, device=qkv.device)
-            got = self._backward((dq, dk, dv), _split(qkv, q_heads, kv_heads), _split(dqkv, q_heads, kv_heads), positions, first,
-                                 q_norm, k_norm, eps, weight_grads)
-        return (dqkv, *got)
+        x = _packed(qkv, q_heads, kv_heads)
+        for name, t, shape in (("dq", dq, x.q_shape), ("dk", dk, x.k_shape), ("dv", dv, x.k_shape)):
+            _upstream(name, t, shape, qkv.device)
+        return self._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads)
 
     def rotate_backward(self, dq, dk, q, k, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6,
                         weight_grads: bool = True):
         """(dq, dk, dq_norm, dk_norm): gradients of ``rotate``'s inputs, laid out as those are, for upstream
         ones of its outputs.  k and dk may be None together."""
-        _rows("q", q)
-        _upstream("dq", dq, tuple(q.shape), q.device)
+        x = _apart(q, k, k_norm)
         if (k is None) != (dk is None):
             raise ValueError("k and dk go together")
+        _upstream("dq", dq, x.q_shape, q.device)
         if k is not None:
-            _rows("k", k, q)
-            _upstream("dk", dk, tuple(k.shape), q.device)
-        elif k_norm is not None:
-            raise ValueError("k_norm without k")
-        with _on(q):
-            out = tuple(None if x is None else _like(x) for x in (q, k))
-            got = self._backward((dq, dk, None), (q, k, None), (*out, None), positions, first, q_norm, k_norm, eps, weight_grads)
-        return (*out, *got)
+            _upstream("dk", dk, x.k_shape, q.device)
+        return self._rotate_backward(dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads)
 
     # ------------------------------------------------------------------ the C calls
-    def _heads(self, qkv, Hq, Hkv, positions, first, q_norm, k_norm, eps):
-        B, S, W = qkv.shape
-        D = W // (Hq + 2 * Hkv)
-        c = self._plan(qkv.device, B, S, D, positions, first, q_norm, k_norm, eps)
-        with _on(qkv) as st:
-            q = torch.empty((B, Hq, S, D), dtype=_BF16, device=qkv.device)
-            k = torch.empty((B, Hkv, S, D), dtype=_BF16, device=qkv.device)
-            v = torch.empty((B, Hkv, S, D), dtype=_BF16, device=qkv.device)
-            _ok(native.load().attn_rope(c, _packed_heads(qkv, Hq, Hkv, D), _dense_heads(q, k, v), B, Hq, Hkv, S, D, st), "attn_rope")
+    def _heads(self, qkv, x, positions, first, q_norm, k_norm, eps):
+        c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        index = qkv.get_device()
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self._heads(qkv, x, positions, first, q_norm, k_norm, eps)
+        q, k, v = qkv.new_empty(x.q_shape), qkv.new_empty(x.k_shape), qkv.new_empty(x.k_shape)
+        rc = _lib().attn_rope(c, x.at(qkv), x.dense(q.data_ptr(), k.data_ptr(), v.data_ptr()), x.B, x.Hq, x.Hkv, x.S, x.D,
+                              _stream_handle(index))
+        if rc:
+            raise native.AttnError(rc, "attn_rope")
         return q, k, v
 
-    def _rotate(self, q, k, positions, first, q_norm, k_norm, eps):
-        B, Hq, S, D = q.shape
-        c = self._plan(q.device, B, S, D, positions, first, q_norm, k_norm, eps)
-        with _on(q) as st:
-            out = tuple(None if x is None else torch.empty(x.shape, dtype=_BF16, device=q.device) for x in (q, k))
-            _ok(native.load().attn_rope(c, _heads_of(q, k, None), _heads_of(*out, None), B, Hq, 1 if k is None else k.shape[1], S, D,
-                                        st), "attn_rope")
-        return out
+    def _rotate(self, q, k, x, positions, first, q_norm, k_norm, eps):
+        c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        index = q.get_device()
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
+        yq, yk = q.new_empty(x.q_shape), None if k is None else q.new_empty(x.k_shape)
+        rc = _lib().attn_rope(c, x.rows(q, k), x.dense(yq.data_ptr(), None if k is None else yk.data_ptr(), None), x.B, x.Hq, x.Hkv, x.S,
+                              x.D, _stream_handle(index))
+        if rc:
+            raise native.AttnError(rc, "attn_rope")
+        return yq, yk
 
-    def _backward(self, up, x, out, positions, first, q_norm, k_norm, eps, weight_grads):
-        """Fills `out` (q, k, v rows) from upstream gradients and the forward's rows; the weights' gradients."""
-        B, Hq, S, D = x[0].shape
-        Hkv = 1 if x[1] is None else x[1].shape[1]
-        c = self._plan(x[0].device, B, S, D, positions, first, q_norm, k_norm, eps)
-        st = _stream_handle(x[0].device.index)
-        dw = [None if w is None or not weight_grads else torch.empty_like(w) for w in (q_norm, k_norm)]
-        w, need = None, 0
-        if any(t is not None for t in dw):
-            need = self._need(c, B, Hq, Hkv, S, D)
-            w = torch.empty(need, dtype=torch.uint8, device=x[0].device)
-        up = [None if t is None else _aligned(t) for t in up]
-        normed = q_norm is not None or k_norm is not None
-        _ok(native.load().attn_rope_bwd(c, _heads_of(*up), _heads_of(*x) if normed else None, _heads_of(*out),
-                                        *(None if t is None else t.data_ptr() for t in dw), B, Hq, Hkv, S, D,
-                                        None if w is None else w.data_ptr(), need, st), "attn_rope_bwd")
-        return dw
+    def _heads_backward(self, dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads):
+        index = qkv.get_device()
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads)
+        dqkv = qkv.new_empty(qkv.shape)
+        return (dqkv, *self._backward(index, (dq, dk, dv), qkv, x, x.at(qkv), x.at_dense(dqkv), positions, first, q_norm, k_norm, eps,
+                                      weight_grads))
+
+    def _rotate_backward(self, dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads):
+        index = q.get_device()
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self._rotate_backward(dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads)
+        out = _like(q), None if k is None else _like(k)
+        return (*out, *self._backward(index, (dq, dk, None), q, x, x.rows(q, k), _heads_of(*out, None), positions, first, q_norm, k_norm,
+                                      eps, weight_grads))
+
+    def _backward(self, index, up, like, x, rows, out, positions, first, q_norm, k_norm, eps, weight_grads):
+        """Fills `out` from upstream gradients and the forward's rows; returns the weights' gradients."""
+        c = self._plan(like.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        dwq = dwk = w = None
+        need = 0
+        if weight_grads and (q_norm is not None or k_norm is not None):
+            need = x.need(c)
+            w = torch.empty(need, dtype=torch.uint8, device=like.device)
+            dwq = None if q_norm is None else torch.empty_like(q_norm)
+            dwk = None if k_norm is None else torch.empty_like(k_norm)
+        rc = _lib().attn_rope_bwd(c, x.upstream(*up), rows, out, None if dwq is None else dwq.data_ptr(),
+                                  None if dwk is None else dwk.data_ptr(), x.B, x.Hq, x.Hkv, x.S, x.D, None if w is None else w.data_ptr(),
+                                  need, _stream_handle(index))
+        if rc:
+            raise native.AttnError(rc, "attn_rope_bwd")
+        return dwq, dwk
 
 
-def _ok(rc, where):
-    if rc != native.ATTN_OK:
-        raise native.AttnError(rc, where)
+_library = None
 
 
-@contextlib.contextmanager
-def _switched(index):
-    with torch.cuda.device(index):
-        yield _stream_handle(index)
-
-
-def _on(x):
-    """x's device current; yields its current stream's handle."""
-    index = x.device.index
-    return contextlib.nullcontext(_stream_handle(index)) if _current_device() == index else _switched(index)
+def _lib():
+    global _library
+    if _library is None:
+        _library = native.load()
+    return _library
 
 
 def _any_grad(*tensors):
-    return any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
+
+
+def _weight(name, w, dtype, D, device):
+    if w.dtype is not dtype:
+        raise ValueError("q_norm and k_norm must have one type")
+    if w.device != device or w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor [{D}] on {device}")
+    return w.data_ptr()
+
+
+class _Sizes:
+    """What calls of one set of sizes and strides have in common: checked once, with the structs of the C calls but
+    for their addresses (a call fills a copy of its own)."""
+
+    def __init__(self, B, S, Hq, Hkv, D, strides):
+        self.B, self.S, self.Hq, self.Hkv, self.D = B, S, Hq, Hkv, D
+        self.q_shape, self.k_shape = (B, Hq, S, D), (B, Hkv, S, D)
+        self._in = native.AttnHeads(None, None, None, *(_STRIDES(*st) for st in strides))
+        self._dense = native.AttnHeads(None, None, None, *(_STRIDES(H * S * D, S * D, D) for H in (Hq, Hkv, Hkv)))
+        W = (Hq + 2 * Hkv) * D
+        self._packed = native.AttnHeads(None, None, None, *(_STRIDES(S * W, D, W) for _ in range(3)))
+        self._k_at, self._v_at = 2 * Hq * D, 2 * (Hq + Hkv) * D
+        self._need = {}
+
+    def _packed_at(self, c, p):
+        c = native.AttnHeads.from_buffer_copy(c)
+        c.q, c.k, c.v = p, p + self._k_at, p + self._v_at
+        return c
+
+    def at(self, qkv):
+        """The heads as they lie in qkv."""
+        return self._packed_at(self._in, qkv.data_ptr())
+
+    def at_dense(self, dqkv):
+        """The heads as they lie in a contiguous tensor of qkv's sizes."""
+        return self._packed_at(self._packed, dqkv.data_ptr())
+
+    def rows(self, q, k):
+        c = native.AttnHeads.from_buffer_copy(self._in)
+        c.q = q.data_ptr()
+        if k is not None:
+            c.k = k.data_ptr()
+        return c
+
+    def dense(self, q, k, v):
+        """Contiguous heads at these addresses."""
+        c = native.AttnHeads.from_buffer_copy(self._dense)
+        c.q, c.k, c.v = q, k, v
+        return c
+
+    def upstream(self, dq, dk, dv):
+        """attn_heads_t of upstream gradients, made dense where their strides or addresses do not fit (`held` keeps
+        those alive with it)."""
+        given = (dq, dk, dv)
+        at = [None if t is None else t.data_ptr() for t in given]
+        if all(t is None or (t.is_contiguous() and p % 16 == 0) for t, p in zip(given, at)):
+            return self.dense(*at)
+        held = [None if t is None else _aligned(t) for t in given]
+        c = _heads_of(*held)
+        c.held = held
+        return c
+
+    def need(self, c):
+        """Bytes of the backward's workspace."""
+        key = bool(c.q_weight), bool(c.k_weight)
+        need = self._need.get(key)
+        if need is None:
+            n = ctypes.c_ulonglong(0)
+            rc = _lib().attn_rope_workspace(c, self.B, self.Hq, self.Hkv, self.S, self.D, n)
+            if rc:
+                raise native.AttnError(rc, "attn_rope_workspace")
+            need = self._need[key] = n.value
+        return need
+
+
+_sizes: dict = {}  # _Sizes by the sizes and strides of a call
+
+
+def _kept(key, made):
+    if len(_sizes) >= 4096:
+        _sizes.clear()
+    _sizes[key] = made
+    return made
 
 
 def _packed(qkv, Hq, Hkv):
-    if not qkv.is_cuda or qkv.dtype is not _BF16 or qkv.dim() != 3:
+    """_Sizes of a projection's output, checked."""
+    if not qkv.is_cuda or qkv.dtype is not _BF16:
+        raise ValueError("qkv must be a bf16 CUDA tensor [B, S, (Hq + 2 Hkv) D]")
+    key = qkv.shape, qkv.stride(), Hq, Hkv
+    x = _sizes.get(key)
+    if x is not None:
+        return x
+    if qkv.dim() != 3:
         raise ValueError("qkv must be a bf16 CUDA tensor [B, S, (Hq + 2 Hkv) D]")
     B, S, W = qkv.shape
     if Hq < 1 or Hkv < 1 or W % (Hq + 2 * Hkv) or W // (Hq + 2 * Hkv) not in (64, 128):
@@ -275,22 +358,41 @@ def _packed(qkv, Hq, Hkv):
         raise ValueError("at least one sequence and one token are needed")
     if qkv.stride(2) != 1:
         raise ValueError("qkv's last dimension must be contiguous")
-    return B, S, W
+    D = W // (Hq + 2 * Hkv)
+    return _kept(key, _Sizes(B, S, Hq, Hkv, D, [(qkv.stride(0), D, qkv.stride(1))] * 3))
 
 
-def _rows(name, x, like=None):
-    if not x.is_cuda or x.dtype is not _BF16 or x.dim() != 4 or 0 in x.shape:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, S, D]")
-    if x.shape[3] not in (64, 128):
-        raise ValueError(f"heads of 64 or 128 elements are needed, got {x.shape[3]}")
-    if x.stride(3) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    if like is not None and (x.device != like.device or (x.shape[0], *x.shape[2:]) != (like.shape[0], *like.shape[2:])):
-        raise ValueError(f"{name} must be [{like.shape[0]}, H, {like.shape[2]}, {like.shape[3]}] on {like.device}")
+def _apart(q, k, k_norm):
+    """_Sizes of q and k (or None) by themselves, checked."""
+    if not q.is_cuda or q.dtype is not _BF16:
+        raise ValueError("q must be a bf16 CUDA tensor [B, H, S, D]")
+    if k is None:
+        if k_norm is not None:
+            raise ValueError("k_norm without k")
+    elif k.dtype is not _BF16 or k.device != q.device:
+        raise ValueError(f"k must be a bf16 tensor on {q.device}")
+    key = q.shape, q.stride(), None if k is None else (k.shape, k.stride())
+    x = _sizes.get(key)
+    if x is not None:
+        return x
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            continue
+        if t.dim() != 4 or 0 in t.shape:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, S, D]")
+        if t.shape[3] not in (64, 128):
+            raise ValueError(f"heads of 64 or 128 elements are needed, got {t.shape[3]}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        if (t.shape[0], t.shape[2], t.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
+            raise ValueError(f"{name} must be [{q.shape[0]}, H, {q.shape[2]}, {q.shape[3]}]")
+    B, Hq, S, D = q.shape
+    strides = [q.stride()[:3], (0, 0, 0) if k is None else k.stride()[:3], (0, 0, 0)]
+    return _kept(key, _Sizes(B, S, Hq, 1 if k is None else k.shape[1], D, strides))
 
 
 def _upstream(name, t, shape, device):
-    if t.device != device or t.dtype is not _BF16 or tuple(t.shape) != shape:
+    if t.device != device or t.dtype is not _BF16 or t.shape != shape:
         raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on {device}")
 
 
@@ -305,25 +407,7 @@ def _aligned(t):
 def _like(x):
     """A new tensor with x's order of dimensions in memory, D contiguous."""
     y = torch.empty_like(x)
-    return y if y.stride(3) == 1 else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-
-
-def _split(qkv, Hq, Hkv):
-    """q, k, v [B, H, S, D] as they lie in qkv."""
-    x = qkv.unflatten(2, (Hq + 2 * Hkv, -1)).transpose(1, 2)
-    return x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
-
-
-def _packed_heads(qkv, Hq, Hkv, D):
-    b, s, _ = qkv.stride()
-    at, st = qkv.data_ptr(), _STRIDES(b, D, s)
-    return native.AttnHeads(at, at + 2 * Hq * D, at + 2 * (Hq + Hkv) * D, st, st, st)
-
-
-def _dense_heads(q, k, v):
-    _, Hq, S, D = q.shape
-    qs, ks = _STRIDES(Hq * S * D, S * D, D), _STRIDES(k.shape[1] * S * D, S * D, D)
-    return native.AttnHeads(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, ks)
+    return y if y.stride(3) == 1 else x.new_empty(x.shape)
 
 
 def _heads_of(q, k, v):
@@ -333,28 +417,26 @@ def _heads_of(q, k, v):
     return native.AttnHeads(*pointers, *strides)
 
 
-# The live eager graphs of these functions by leaf (id): (leaf, node, stream), the first two as weak references.
+# Nodes of the eager calls whose graphs live, by id: (weak reference, stream).
 _live: dict = {}
 
 
 def _watch(ctx, leaves, index):
-    """Notes an eager call's leaves, or refuses a captured one that shares a leaf with an eager graph of another stream."""
-    leaves = [t for t in leaves if t is not None and t.requires_grad and t.is_leaf]
-    if not leaves:
+    """Notes an eager call, or refuses a captured one that shares a leaf with an eager graph of another stream."""
+    st = _stream_handle(index)
+    if not torch.cuda.is_current_stream_capturing():
+        key = id(ctx)
+        _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None)), st
         return
-    capturing, st = torch.cuda.is_current_stream_capturing(), _stream_handle(index)
-    for t in leaves:
-        held = [x for x in _live.get(id(t), ()) if x[0]() is t and x[1]() is not None]
-        if capturing:
-            if any(x[2] != st for x in held):
-                raise ValueError("an eager graph of the same leaf lives, whose backward node belongs to another stream: capturing "
-                                 "would break. Let it go first, pass leaf.detach().requires_grad_(), or capture the *_backward call")
-        else:
-            held.append((weakref.ref(t), weakref.ref(ctx), st))
-            if len(_live) > 4096:  # leaves that are gone
-                for key in [k for k, v in _live.items() if all(x[0]() is None or x[1]() is None for x in v)]:
-                    del _live[key]
-        _live[id(t)] = held
+    leaves = [t for t in leaves if t is not None and t.requires_grad and t.is_leaf]
+    for ref, of in list(_live.values()):
+        node = ref()
+        if node is None or of == st:
+            continue
+        held = [getattr(f, "variable", None) for f, _ in node.next_functions if f is not None]
+        if any(t is x for t in leaves for x in held):
+            raise ValueError("an eager graph of the same leaf lives, whose backward node belongs to another stream: capturing "
+                             "would break. Let it go first, pass leaf.detach().requires_grad_(), or capture the *_backward call")
 
 
 def _functions():
@@ -373,35 +455,35 @@ def _make_functions():
 
     class HeadsFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, qkv, q_norm, k_norm, rotary, Hq, Hkv, positions, first, eps):
-            _watch(ctx, (qkv, q_norm, k_norm), qkv.device.index)
+        def forward(ctx, qkv, q_norm, k_norm, rotary, x, positions, first, eps):
+            _watch(ctx, (qkv, q_norm, k_norm), qkv.get_device())
             ctx.save_for_backward(qkv, q_norm, k_norm, positions)
-            ctx.args = (rotary, Hq, Hkv, first, eps)
-            return rotary._heads(qkv, Hq, Hkv, positions, first, q_norm, k_norm, eps)
+            ctx.args = (rotary, x, first, eps)
+            return rotary._heads(qkv, x, positions, first, q_norm, k_norm, eps)
 
         @staticmethod
         @once
         def backward(ctx, dq, dk, dv):
             qkv, q_norm, k_norm, positions = ctx.saved_tensors
-            rotary, Hq, Hkv, first, eps = ctx.args
-            got = rotary.heads_backward(dq, dk, dv, qkv, Hq, Hkv, positions, first, q_norm, k_norm, eps, any(ctx.needs_input_grad[1:3]))
-            return (*got, None, None, None, None, None, None)
+            rotary, x, first, eps = ctx.args
+            got = rotary._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, any(ctx.needs_input_grad[1:3]))
+            return (*got, None, None, None, None, None)
 
     class RotateFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, q_norm, k_norm, rotary, positions, first, eps):
-            _watch(ctx, (q, k, q_norm, k_norm), q.device.index)
+        def forward(ctx, q, k, q_norm, k_norm, rotary, x, positions, first, eps):
+            _watch(ctx, (q, k, q_norm, k_norm), q.get_device())
             ctx.save_for_backward(q, k, q_norm, k_norm, positions)
-            ctx.args = (rotary, first, eps)
-            return rotary._rotate(q, k, positions, first, q_norm, k_norm, eps)
+            ctx.args = (rotary, x, first, eps)
+            return rotary._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
 
         @staticmethod
         @once
         def backward(ctx, dq, dk):
             q, k, q_norm, k_norm, positions = ctx.saved_tensors
-            rotary, first, eps = ctx.args
-            got = rotary.rotate_backward(dq, dk if k is not None else None, q, k, positions, first, q_norm, k_norm, eps,
-                                         any(ctx.needs_input_grad[2:4]))
-            return (*got, None, None, None, None)
+            rotary, x, first, eps = ctx.args
+            got = rotary._rotate_backward(dq, dk if k is not None else None, q, k, x, positions, first, q_norm, k_norm, eps,
+                                          any(ctx.needs_input_grad[2:4]))
+            return (*got, None, None, None, None, None)
 
     return HeadsFunction, RotateFunction

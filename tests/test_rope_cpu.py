@@ -312,7 +312,7 @@ def test_frequencies():
 def test_turns_are_exact():
     """Positions times the stored fractions, modulo a turn, against the angle in rationals."""
     from fractions import Fraction
-    from causal_scaled_dot_gb300.rotary import _PI
+    _PI = Fraction(31415926535897932384626433832795028841971693993751, 10**49)
     r = Rotary([1.0, 0.3, 1e-9, 7.5, -2.0, 1e-4, 0.0, 3.0])
     for p in (0, 1, 12345, 2**20 + 1, 2**31 - 1, -5):
         for f, t in zip(r.frequencies, r._c.turns):
