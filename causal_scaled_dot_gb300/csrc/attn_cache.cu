@@ -195,19 +195,23 @@ int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
 // q's heads a thread at most, and the units that their number comes down for (rope_plan).
 constexpr int kAppendPer = 8;
 constexpr long long kAppendUnits = 608;
-template <int D, bool kInter>
-int launch_append(int elements, CacheAppendParams& p, long long q_units, cudaStream_t st) {
-    const int threads = elements <= 64 * 32 ? 32 : elements <= 64 * 64 ? 64 : elements <= 64 * 128 ? 128 : 256;
-    const int per = 256 / threads;
-    p.write_blocks = (p.num_units + per - 1) / per;
+// Threads per unit that hold the largest unit's elements at 64 a thread.
+int append_threads(int elements) { return elements <= 64 * 32 ? 32 : elements <= 64 * 64 ? 64 : elements <= 64 * 128 ? 128 : 256; }
+template <int D, bool kInter, int kThreads>
+int launch_append(CacheAppendParams& p, long long q_units, cudaStream_t st) {
+    constexpr int kBlock = kAppendBlock<kThreads>, kPer = kBlock / kThreads;
+    p.write_blocks = (p.num_units + kPer - 1) / kPer;
     if (p.write_blocks + q_units > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
-    const int grid = p.write_blocks + (int)q_units;
+    return launch(attn_cache_append_kernel<D, kInter, kThreads>, p.write_blocks + (int)q_units, kBlock, 0, true, st, p);
+}
+template <int D, bool kInter>
+int launch_append(int threads, CacheAppendParams& p, long long q_units, cudaStream_t st) {
     switch (threads) {
-        case 32: return launch(attn_cache_append_kernel<D, kInter, 32>, grid, 256, 0, true, st, p);
-        case 64: return launch(attn_cache_append_kernel<D, kInter, 64>, grid, 256, 0, true, st, p);
-        case 128: return launch(attn_cache_append_kernel<D, kInter, 128>, grid, 256, 0, true, st, p);
-        default: return launch(attn_cache_append_kernel<D, kInter, 256>, grid, 256, 0, true, st, p);
+        case 32: return launch_append<D, kInter, 32>(p, q_units, st);
+        case 64: return launch_append<D, kInter, 64>(p, q_units, st);
+        case 128: return launch_append<D, kInter, 128>(p, q_units, st);
     }
+    return launch_append<D, kInter, D == 128 ? 256 : 128>(p, q_units, st);  // blocks of 128 tokens of 128 elements
 }
 
 }  // namespace
@@ -284,6 +288,8 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
         host::rope_meets(rope, cache->v, n, B, S, D) || host::rope_meets(rope, cache->k_scale, ns, B, S, D) ||
         host::rope_meets(rope, cache->v_scale, ns, B, S, D))
         return ATTN_ERR_INVALID_ARG;
+    const int bs = cache->block_size;
+    const int threads = append_threads((S < bs ? S : bs) * D);
     long long q_units = 0;
     if (q_out) {
         const size_t qb = (size_t)B * Hq * S * D * 2;
@@ -296,7 +302,7 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
         p.out.stride[0][0] = (long long)Hq * S * D;
         p.out.stride[0][1] = (long long)S * D;
         p.out.stride[0][2] = D;
-        p.plan = rope_plan((long long)B * S, Hq, 0, 0, D, kAppendPer, kAppendUnits);
+        p.plan = rope_plan((long long)B * S, Hq, 0, 0, D, threads > 128 ? threads : 128, kAppendPer, kAppendUnits);
         q_units = rope_tiles(p.plan) * rope_chunks(p.plan);
     }
     int sms = 0, device = -1;
@@ -306,18 +312,15 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
     host::fill_rope(rope, &p.r);
     p.new_lens = new_lens;
     p.S = S;
-    const int bs = cache->block_size;
     // as in attn_cache_write
     const long long touched = ((long long)S + bs - 2) / bs + 1;
     p.blocks_per_seq = (int)(touched < cache->max_blocks ? touched : cache->max_blocks);
     const long long units = (long long)B * Hkv * 2 * p.blocks_per_seq;
     if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
     p.num_units = (int)units;
-    const int elements = (S < bs ? S : bs) * D;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (D == 64)
-        return rope->interleaved ? launch_append<64, true>(elements, p, q_units, st) : launch_append<64, false>(elements, p, q_units, st);
-    return rope->interleaved ? launch_append<128, true>(elements, p, q_units, st) : launch_append<128, false>(elements, p, q_units, st);
+    if (D == 64) return rope->interleaved ? launch_append<64, true>(threads, p, q_units, st) : launch_append<64, false>(threads, p, q_units, st);
+    return rope->interleaved ? launch_append<128, true>(threads, p, q_units, st) : launch_append<128, false>(threads, p, q_units, st);
 }
 
 extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int first, int S, void* stream) {

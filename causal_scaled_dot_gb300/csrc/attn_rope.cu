@@ -19,7 +19,7 @@ using host::RowsBox;
 
 // Heads of a thread at most, and units (blocks) that its head count comes down for.
 constexpr int kPer = 8;
-constexpr long long kUnits = 1216;
+constexpr long long kUnits = 608;
 
 int check_sizes(int B, int Hq, int Hkv, int S, int D) {
     if (B < 1 || Hq < 1 || Hkv < 1 || S < 1) return ATTN_ERR_INVALID_ARG;
@@ -30,7 +30,7 @@ int check_sizes(int B, int Hq, int Hkv, int S, int D) {
 
 // The plan of a call: the split follows the sizes alone, not which of q, k and v are present.
 int plan_of(int B, int Hq, int Hkv, int S, int D, const bool (&present)[3], RopePlan* plan) {
-    *plan = rope_plan((long long)B * S, Hq, Hkv, Hkv, D, kPer, kUnits);
+    *plan = rope_plan((long long)B * S, Hq, Hkv, Hkv, D, kRopeThreads, kPer, kUnits);
     if (rope_tiles(*plan) * rope_chunks(*plan) > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     for (int i = 0; i < 3; ++i)
         if (!present[i]) plan->heads[i] = plan->chunks[i] = 0;

@@ -36,24 +36,32 @@ struct AppendPlace {
     }
 };
 
-// kThreads threads per unit, 256 / kThreads units per block; up to 4 shares of 16 elements a thread.
+// kThreads threads per unit, kBlock / kThreads units per block; up to 4 shares of 16 elements a thread.  Blocks that write
+// (much to compute) and blocks of q (much to load) alternate evenly, so that an SM has both at any time.
+template <int kThreads>
+constexpr int kAppendBlock = kThreads > 128 ? kThreads : 128;
 template <int D, bool kInter, int kThreads>
-__global__ void __launch_bounds__(256) attn_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
-    constexpr int kLanes = D / 16, kItems = 4;
-    __shared__ uint32_t warp_max[8];
+__global__ void __launch_bounds__(kAppendBlock<kThreads>, 512 / kAppendBlock<kThreads>)
+    attn_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
+    constexpr int kLanes = D / 16, kItems = 4, kBlock = kAppendBlock<kThreads>;
+    static_assert(kItems == kRopeDepth, "one ring serves both kinds of blocks");
+    __shared__ uint32_t warp_max[kBlock / 32];
+    __shared__ __align__(16) unsigned char smem[RopeRing<2, kRopeDepth, kBlock>::kBytes];
     ptx::launch_next();
     ptx::wait_previous();
-    if (blockIdx.x >= p.write_blocks) {
-        const unsigned int unit = blockIdx.x - p.write_blocks;
+    // of the first i + 1 blocks (i + 1) W / N write
+    const unsigned int before = (unsigned int)((unsigned long long)blockIdx.x * p.write_blocks / gridDim.x);
+    if ((unsigned int)((blockIdx.x + 1ull) * p.write_blocks / gridDim.x) == before) {
+        const unsigned int unit = blockIdx.x - before;
         if (p.r.weight[0])
-            rope_forward<D, kInter, true>(p.r, p.plan, unit, p.S, p.in, p.out, AppendPlace{p});
+            rope_forward<D, kInter, true, kBlock>(p.r, p.plan, unit, p.S, p.in, p.out, AppendPlace{p}, smem);
         else
-            rope_forward<D, kInter, false>(p.r, p.plan, unit, p.S, p.in, p.out, AppendPlace{p});
+            rope_forward<D, kInter, false, kBlock>(p.r, p.plan, unit, p.S, p.in, p.out, AppendPlace{p}, smem);
         return;
     }
     const CacheView& c = p.c;
     const int t = threadIdx.x % kThreads;
-    const int unit = blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+    const int unit = before * (kBlock / kThreads) + threadIdx.x / kThreads;
     bool active = unit < p.num_units, bad = false;
     const CacheRwUnit u = cache_rw_unit(active ? unit : 0, p.blocks_per_seq, c.Hkv, 2);
     const CacheSpan s = cache_span(c.seq_lens[u.b], p.new_lens ? p.new_lens[u.b] : p.S, c.max_blocks * c.block_size, p.S, &bad);
@@ -68,49 +76,64 @@ __global__ void __launch_bounds__(256) attn_cache_append_kernel(const __grid_con
     const int lane = t % kLanes, kind = u.is_v ? 2 : 1;
     const RopeLane l = rope_lane(lane, D, p.r.rot, kInter);
     const __nv_bfloat16* src = p.in.p[kind] + u.b * p.in.stride[kind][0] + u.h * p.in.stride[kind][1];
-    uint4 raw[kItems][2];
+    const RopeRing<2, kItems, kBlock> ring(smem);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int row = (t + i * kThreads) / kLanes;
-        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-            const uint4* x = reinterpret_cast<const uint4*>(src + (row0 + row) * p.in.stride[kind][2]);
-            raw[i][0] = __ldcs(x + l.a);
-            raw[i][1] = __ldcs(x + l.b);
-        }
+        const uint4* x = reinterpret_cast<const uint4*>(row < rows ? src + (row0 + row) * p.in.stride[kind][2] : p.in.p[kind]);
+        ring.fill(i, 0, x + l.a, row < rows);
+        ring.fill(i, 1, x + l.b, row < rows);
+        ptx::cp_async_commit();
     }
     const int block = active ? cache_block(entry, c.num_blocks, &bad) : -1;
     active = block >= 0;
     if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
-    if (kThreads == 32 && !active) return;  // whole warps: no barrier below
+    if (kThreads == 32 && !active) {  // whole warps: no barrier below
+        ptx::cp_async_wait<0>();
+        return;
+    }
     float* scale_at = active ? (u.is_v ? c.v_scale : c.k_scale) + (long long)block * c.Hkv + u.h : nullptr;
     const float s_old = active && slot0 > 0 ? *scale_at : 0.f;
     // A warp's threads may be of one unit only (kThreads >= 32): what follows is the same for all of them.
-    float x[kItems][16];
+    uint64_t x[kItems][8];
     float amax = 0.f;
     bool odd = false;  // this thread holds an infinity or NaN: those do not count
-    float w[16];
     const void* weight = u.is_v ? nullptr : p.r.weight[1];
-    if (weight) rope_weights(weight, p.r.weight_f32, l, w);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        if (i * kThreads >= rows * kLanes) break;
+        switch (i) {  // the copies of the items so far
+            case 0: ptx::cp_async_wait<3>(); break;
+            case 1: ptx::cp_async_wait<2>(); break;
+            case 2: ptx::cp_async_wait<1>(); break;
+            default: ptx::cp_async_wait<0>();
+        }
+        if (i * kThreads >= rows * kLanes) continue;
         const int row = (t + i * kThreads) / kLanes;
-        rope_unpack(raw[i][0], raw[i][1], x[i]);
+        rope_unpack(ring.at(i, 0), ring.at(i, 1), x[i]);
         if (!u.is_v) {
-            if (weight) rope_normed<kLanes>(x[i], w, p.r.eps);
-            if (l.turn_a || l.turn_b) {
-                const int at = row < rows ? row0 + row : row0;
-                RopeWaves<kInter> waves;
-                waves.at(p.r, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
-                waves.template turn<false>(x[i]);
+            const int at = row < rows ? row0 + row : row0;
+            RopeTurn<kInter> turn;
+            turn.template set<false>(p.r, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
+            if (weight) {
+                float down;
+                uint64_t w[8];
+                rope_weights(weight, p.r.weight_f32, l, w);
+                turn.weigh(w);
+                const float r = rope_norm<kLanes>(x[i], p.r.eps, &down);
+                turn.template turn<true>(x[i]);
+                rope_scale(x[i], r);
+            } else {
+                turn.template turn<false>(x[i]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float m = fabsf(x[i][j]);
-            odd = odd || !(m < INFINITY);
-            amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+        for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            ptx::f2_split(x[i][j], lo, hi);
+            lo = fabsf(lo);
+            hi = fabsf(hi);
+            odd = odd || !(lo < INFINITY) || !(hi < INFINITY);
+            amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
         }
     }
     uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
@@ -134,7 +157,8 @@ __global__ void __launch_bounds__(256) attn_cache_append_kernel(const __grid_con
         uint32_t code[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float lo = x[i][2 * j], hi = x[i][2 * j + 1];
+            float lo, hi;
+            ptx::f2_split(x[i][j], lo, hi);
             if (divide) {
                 lo = e4m3_divided(lo, s_new);
                 hi = e4m3_divided(hi, s_new);

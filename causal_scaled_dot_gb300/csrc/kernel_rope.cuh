@@ -45,15 +45,17 @@ struct RopePlace {
     }
 };
 template <int D, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_constant__ RopeFwdParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kNorm ? 5 : 7) attn_rope_kernel(const __grid_constant__ RopeFwdParams p) {
+    __shared__ __align__(16) unsigned char ring[RopeRing<2, kRopeDepth, kRopeThreads>::kBytes];
     ptx::launch_next();
     ptx::wait_previous();
-    rope_forward<D, kInter, kNorm>(p.r, p.plan, blockIdx.x, p.S, p.in, p.out, RopePlace{p});
+    rope_forward<D, kInter, kNorm, kRopeThreads>(p.r, p.plan, blockIdx.x, p.S, p.in, p.out, RopePlace{p}, ring);
 }
 
 template <int D, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) attn_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 6) attn_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
     constexpr int kLanes = D / 16, kWarps = kRopeThreads / 32;
+    __shared__ __align__(16) unsigned char smem[RopeRing<kNorm ? 4 : 2, kRopeDepth, kRopeThreads>::kBytes];
     __shared__ float part[kNorm ? kWarps * D : 1];
     ptx::launch_next();
     ptx::wait_previous();
@@ -64,69 +66,91 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_bwd_kernel(const __gri
     const bool copy = kind == 2;
     const void* weight = copy ? nullptr : p.r.weight[kind];
     const bool normed = kNorm && weight;
-    const __nv_bfloat16* up = p.up.p[kind] + t.b * p.up.stride[kind][0] + t.s * p.up.stride[kind][2];
-    const __nv_bfloat16* in = normed ? p.in.p[kind] + t.b * p.in.stride[kind][0] + t.s * p.in.stride[kind][2] : nullptr;
-    __nv_bfloat16* out = p.out.p[kind] ? p.out.p[kind] + t.b * p.out.stride[kind][0] + t.s * p.out.stride[kind][2] : nullptr;
-    RopeWaves<kInter> waves;
-    if (!copy) waves.at(p.r, l, lane, rope_position(p.r, t.b, t.s));
-    float w[16], dw[16];
+    const auto at = [&](const RopeRows& x) {
+        return reinterpret_cast<uint4*>(x.p[kind] + t.b * x.stride[kind][0] + t.s * x.stride[kind][2] + t.head * x.stride[kind][1]);
+    };
+    const uint4 *up = at(p.up), *in = normed ? at(p.in) : nullptr;
+    uint4* out = p.out.p[kind] ? at(p.out) : nullptr;
+    const long long up_step = p.plan.groups * p.up.stride[kind][1] / 8, in_step = p.plan.groups * p.in.stride[kind][1] / 8,
+                    out_step = p.plan.groups * p.out.stride[kind][1] / 8;
+    const int rows = there && t.head < t.end ? (t.end - t.head + p.plan.groups - 1) / p.plan.groups : 0;  // of this thread
+    const RopeRing<kNorm ? 4 : 2, kRopeDepth, kRopeThreads> ring(smem);
+    int next = 0;  // the row whose copies leave next
+    const auto fill = [&](int slot) {
+        const bool mine = next < rows;
+        const uint4* g = mine ? up : reinterpret_cast<const uint4*>(p.up.p[kind]);
+        ring.fill(slot, 0, g + l.a, mine);
+        ring.fill(slot, 1, g + l.b, mine);
+        if (normed) {
+            const uint4* x = mine ? in : reinterpret_cast<const uint4*>(p.in.p[kind]);
+            ring.fill(slot, 2, x + l.a, mine);
+            ring.fill(slot, 3, x + l.b, mine);
+            in += in_step;
+        }
+        ptx::cp_async_commit();
+        up += up_step;
+        ++next;
+    };
+#pragma unroll
+    for (int i = 0; i < kRopeDepth; ++i) fill(i);
+    RopeTurn<kInter> turn;
+    if (!copy) turn.template set<true>(p.r, l, lane, rope_position(p.r, t.b, t.s));
+    uint64_t w[8], dw[8];
     if (normed) rope_weights(weight, p.r.weight_f32, l, w);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dw[j] = 0.f;
+    for (int i = 0; i < 8; ++i) dw[i] = 0;
+#pragma unroll 1
     for (int i = 0; i < p.plan.per; ++i) {
-        const int h = t.head + i * p.plan.groups;
-        const bool mine = there && h < t.end;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a, xa = a, xb = a;
-        if (mine) {
-            const uint4* g = reinterpret_cast<const uint4*>(up + h * p.up.stride[kind][1]);
-            a = g[l.a];
-            b = g[l.b];
-            if (normed) {
-                const uint4* x = reinterpret_cast<const uint4*>(in + h * p.in.stride[kind][1]);
-                xa = x[l.a];
-                xb = x[l.b];
-            }
-        }
+        const int slot = i % kRopeDepth;
+        ptx::cp_async_wait<kRopeDepth - 1>();
+        uint4 a = ring.at(slot, 0), b = ring.at(slot, 1);
         if (!copy) {
-            float g[16];
+            uint64_t g[8];
             rope_unpack(a, b, g);
-            waves.template turn<true>(g);
-            if (normed) {
-                float x[16], down;
-                rope_unpack(xa, xb, x);
+            turn.template turn<false>(g);
+            if (normed) {  // rows that are not there have g = 0
+                uint64_t x[8];
+                float down;
+                rope_unpack(ring.at(slot, 2), ring.at(slot, 3), x);
                 const float r = rope_norm<kLanes>(x, p.r.eps, &down);
-                float dot = 0.f;
+                rope_scale(x, r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[j] *= r;
-                    const float d = g[j] * x[j];
-                    if (mine) dw[j] += d;
-                    dot = fmaf(d, w[j], dot);
+                for (int i = 0; i < 8; ++i) {
+                    dw[i] = ptx::fma2(g[i], x[i], dw[i]);
+                    g[i] = ptx::mul2(g[i], w[i]);
                 }
-                const float c = rope_row_sum<kLanes>(dot) * (1.f / D), rd = r * down;
+                const uint64_t c = rope_both(rope_row_sum<kLanes>(rope_dot(g, x)) * (-1.f / D));
 #pragma unroll
-                for (int j = 0; j < 16; ++j) g[j] = rd * fmaf(-x[j], c, g[j] * w[j]);
+                for (int i = 0; i < 8; ++i) g[i] = ptx::fma2(x[i], c, g[i]);
+                rope_scale(g, r * down);
             }
             rope_pack(g, a, b);
         }
-        if (mine && out) {
-            uint4* y = reinterpret_cast<uint4*>(out + h * p.out.stride[kind][1]);
-            y[l.a] = a;
-            y[l.b] = b;
+        if (out) {
+            if (i < rows) {
+                out[l.a] = a;
+                out[l.b] = b;
+            }
+            out += out_step;
         }
+        fill(slot);  // once the slot's values are out of it
     }
+    ptx::cp_async_wait<0>();
     if (!kNorm || !normed || !p.part[kind]) return;
     // The block's rows, in a fixed order: within a warp, then over the warps.
+    float sums[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ptx::f2_split(dw[i], sums[2 * i], sums[2 * i + 1]);
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
-        for (int i = kLanes; i < 32; i *= 2) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], i);
+        for (int i = kLanes; i < 32; i *= 2) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], i);
     if (threadIdx.x % 32 < kLanes) {
         float* to = part + threadIdx.x / 32 * D;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            to[8 * l.a + j] = dw[j];
-            to[8 * l.b + j] = dw[8 + j];
+            to[8 * l.a + j] = sums[j];
+            to[8 * l.b + j] = sums[8 + j];
         }
     }
     __syncthreads();
@@ -139,34 +163,45 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_bwd_kernel(const __gri
     }
 }
 
-// The sum of the units' parts of a weight's gradient, in a fixed order: 16 columns a block, 64 rows side by side.
+// The sum of the units' parts of a weight's gradient, in a fixed order: 16 columns a block, 128 rows side by side.
 struct RopeSumParams {
     const float* part[2];
     long long rows[2];
     void* out[2];  // null: not wanted
     int D, f32;
 };
-constexpr int kRopeSumThreads = 1024;
+constexpr int kRopeSumThreads = 512;
 __global__ void __launch_bounds__(kRopeSumThreads) attn_rope_sum_kernel(const __grid_constant__ RopeSumParams p) {
-    __shared__ float part[kRopeSumThreads];
+    constexpr int kSide = kRopeSumThreads / 4;  // rows side by side, four columns a thread
+    __shared__ float4 part[kRopeSumThreads / 32][4];
     ptx::launch_next();
     ptx::wait_previous();
-    const int blocks = p.D / 16, kind = blockIdx.x / blocks, column = (blockIdx.x - kind * blocks) * 16 + threadIdx.x % 16;
+    const int blocks = p.D / 16, kind = blockIdx.x / blocks, column = (blockIdx.x - kind * blocks) * 16 + threadIdx.x % 4 * 4;
     if (!p.out[kind]) return;
-    float sum = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](const float4& x) {
+        sum.x += x.x;
+        sum.y += x.y;
+        sum.z += x.z;
+        sum.w += x.w;
+    };
 #pragma unroll 8
-    for (long long i = threadIdx.x / 16; i < p.rows[kind]; i += kRopeSumThreads / 16) sum += p.part[kind][i * p.D + column];
-    part[threadIdx.x] = sum;
+    for (long long i = threadIdx.x / 4; i < p.rows[kind]; i += kSide) add(*reinterpret_cast<const float4*>(p.part[kind] + i * p.D + column));
+#pragma unroll
+    for (int i = 4; i < 32; i *= 2)
+        add(make_float4(__shfl_xor_sync(0xffffffffu, sum.x, i), __shfl_xor_sync(0xffffffffu, sum.y, i), __shfl_xor_sync(0xffffffffu, sum.z, i),
+                        __shfl_xor_sync(0xffffffffu, sum.w, i)));
+    if (threadIdx.x % 32 < 4) part[threadIdx.x / 32][threadIdx.x % 4] = sum;
     __syncthreads();
-    for (int n = kRopeSumThreads / 2; n >= 16; n /= 2) {
-        if (threadIdx.x < n) part[threadIdx.x] += part[threadIdx.x + n];
-        __syncthreads();
-    }
     if (threadIdx.x >= 16) return;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRopeSumThreads / 32; ++i) total += reinterpret_cast<const float*>(part[i])[threadIdx.x];
+    const int at = (blockIdx.x - kind * blocks) * 16 + threadIdx.x;
     if (p.f32)
-        static_cast<float*>(p.out[kind])[column] = part[threadIdx.x];
+        static_cast<float*>(p.out[kind])[at] = total;
     else
-        static_cast<__nv_bfloat16*>(p.out[kind])[column] = __float2bfloat16_rn(part[threadIdx.x]);
+        static_cast<__nv_bfloat16*>(p.out[kind])[at] = __float2bfloat16_rn(total);
 }
 
 }  // namespace attn

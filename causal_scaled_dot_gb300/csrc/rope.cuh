@@ -28,13 +28,38 @@ struct RopeRows {
     long long stride[3][3];   // batch, head, token, in elements
 };
 
-// m cos and m sin of position p and frequency F (2^-64 turns).  The product's upper half is the angle as a signed
-// fraction of half a turn; what it drops is below 2^-31 of one.
-__device__ __forceinline__ void rope_wave(long long p, unsigned long long F, float m, float& c, float& s) {
-    const unsigned long long t = (unsigned long long)p * F;
-    sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &s, &c);
-    c *= m;
-    s *= m;
+// m cos and m sin of position p and two frequencies (2^-64 turns), packed.  The product's upper half is the angle as a
+// signed fraction of a turn (what it drops is below 2^-32 of one); its two top bits, rounded, are the quadrant, and the
+// rest r, in -1/8 .. 1/8 turn, enters sin(2 pi r) = r S(r^2) and cos(2 pi r) = C(r^2): polynomials with the least largest
+// error there (exchange algorithm of Remez; 1e-9 and 3e-8, so fp32's own roundings are what is left, under 2^-22).
+// sincospif took a third of the backward's instructions.
+__device__ __forceinline__ void rope_wave2(long long p, unsigned long long F0, unsigned long long F1, uint64_t m, uint64_t& c, uint64_t& s) {
+    const uint32_t u0 = (uint32_t)((unsigned long long)p * F0 >> 32) + 0x20000000u;
+    const uint32_t u1 = (uint32_t)((unsigned long long)p * F1 >> 32) + 0x20000000u;
+    const auto both = [](float x) { return ptx::f2(x, x); };
+    const uint64_t r = ptx::mul2(ptx::f2((float)((int)(u0 & 0x3fffffffu) - 0x20000000), (float)((int)(u1 & 0x3fffffffu) - 0x20000000)),
+                                 both(2.3283064365386963e-10f));
+    const uint64_t y = ptx::mul2(r, r);
+    uint64_t cc = ptx::fma2(y, both(-83.66592125133988f), both(64.92322865171708f));
+    cc = ptx::fma2(y, cc, both(-19.739167263528856f));
+    cc = ptx::mul2(ptx::fma2(y, cc, both(1.f)), m);
+    uint64_t ss = ptx::fma2(y, both(-75.24283377371387f), both(81.58820665534085f));
+    ss = ptx::fma2(y, ss, both(-41.34162877037185f));
+    ss = ptx::fma2(y, ss, both(6.283185222149059f));
+    ss = ptx::mul2(ptx::mul2(ss, r), m);
+    float c0, c1, s0, s1;
+    ptx::f2_split(cc, c0, c1);
+    ptx::f2_split(ss, s0, s1);
+    // quadrants 0 .. 3: (c, s), (-s, c), (-c, -s), (s, -c)
+    const auto place = [](uint32_t u, float& c, float& s) {
+        const float x = u & 0x40000000u ? s : c, y = u & 0x40000000u ? c : s;
+        c = __uint_as_float(__float_as_uint(x) ^ ((u + 0x40000000u) & 0x80000000u));
+        s = __uint_as_float(__float_as_uint(y) ^ (u & 0x80000000u));
+    };
+    place(u0, c0, s0);
+    place(u1, c1, s1);
+    c = ptx::f2(c0, c1);
+    s = ptx::f2(s0, s1);
 }
 __device__ __forceinline__ long long rope_position(const RopeParams& r, long long b, long long s) {
     if (!r.positions) return r.first + s;
@@ -42,70 +67,119 @@ __device__ __forceinline__ long long rope_position(const RopeParams& r, long lon
     return r.positions_64 ? static_cast<const long long*>(r.positions)[i] : static_cast<const int*>(r.positions)[i];
 }
 
-// A lane's share of a row in fp32: x[0..7] its vector a, x[8..15] its vector b.
-__device__ __forceinline__ void rope_unpack(const uint4& a, const uint4& b, float (&x)[16]) {
+// A lane's share of a row in fp32, two elements a word: x[0..3] its vector a, x[4..7] its vector b.
+__device__ __forceinline__ void rope_unpack(const uint4& a, const uint4& b, uint64_t (&x)[8]) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = ptx::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void rope_pack(const float (&x)[16], uint4& a, uint4& b) {
-    a = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]), ptx::pack_bf16x2(x[4], x[5]),
-                   ptx::pack_bf16x2(x[6], x[7]));
-    b = make_uint4(ptx::pack_bf16x2(x[8], x[9]), ptx::pack_bf16x2(x[10], x[11]), ptx::pack_bf16x2(x[12], x[13]),
-                   ptx::pack_bf16x2(x[14], x[15]));
+__device__ __forceinline__ uint32_t rope_pack(uint64_t x) {
+    float lo, hi;
+    ptx::f2_split(x, lo, hi);
+    return ptx::pack_bf16x2(lo, hi);
 }
+__device__ __forceinline__ void rope_pack(const uint64_t (&x)[8], uint4& a, uint4& b) {
+    a = make_uint4(rope_pack(x[0]), rope_pack(x[1]), rope_pack(x[2]), rope_pack(x[3]));
+    b = make_uint4(rope_pack(x[4]), rope_pack(x[5]), rope_pack(x[6]), rope_pack(x[7]));
+}
+__device__ __forceinline__ uint64_t rope_both(float x) { return ptx::f2(x, x); }
+__device__ __forceinline__ uint64_t rope_swap(uint64_t x) {
+    float lo, hi;
+    ptx::f2_split(x, lo, hi);
+    return ptx::f2(hi, lo);
+}
+__device__ __forceinline__ uint64_t rope_negate(uint64_t x) { return x ^ 0x8000000080000000ull; }
 
-// The lane's 8 pairs: half layout (x[j], x[8 + j]); interleaved (x[2 j], x[2 j + 1]).
-template <bool kInter>
-struct RopeWaves {
-    float c[8], s[8];
-    bool turn_a, turn_b;
-    __device__ __forceinline__ void at(const RopeParams& r, const RopeLane& l, int lane, long long p) {
-        turn_a = l.turn_a;
-        turn_b = l.turn_b;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            c[j] = 1.f;
-            s[j] = 0.f;
-            const bool turn = kInter && j >= 4 ? turn_b : turn_a;
-            const int pair = kInter ? (j < 4 ? 4 * l.a + j : 4 * l.b + j - 4) : 8 * lane + j;
-            if (turn) rope_wave(p, r.turns[pair], r.factor, c[j], s[j]);
-        }
-    }
-    // Forward, or with `back` the transposed rotation.  Elements that are not rotated stay as they are, whatever they are.
-    template <bool kBack>
-    __device__ __forceinline__ void turn(float (&x)[16]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!(kInter && j >= 4 ? turn_b : turn_a)) continue;
-            const int i = kInter ? 2 * j : j, k = kInter ? 2 * j + 1 : 8 + j;
-            const float sn = kBack ? -s[j] : s[j], u = x[i], v = x[k];
-            x[i] = u * c[j] - v * sn;
-            x[k] = v * c[j] + u * sn;
-        }
-    }
-};
-
-// The lane's weights of a norm.
-__device__ __forceinline__ void rope_weights(const void* weight, int f32, const RopeLane& l, float (&w)[16]) {
+// The lane's weights of a norm, in the places of its elements.
+__device__ __forceinline__ void rope_weights(const void* weight, int f32, const RopeLane& l, uint64_t (&w)[8]) {
     if (f32) {
         const float4* p = static_cast<const float4*>(weight);
         const float4 q[4] = {p[2 * l.a], p[2 * l.a + 1], p[2 * l.b], p[2 * l.b + 1]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[4 * i] = q[i].x;
-            w[4 * i + 1] = q[i].y;
-            w[4 * i + 2] = q[i].z;
-            w[4 * i + 3] = q[i].w;
+            w[2 * i] = ptx::f2(q[i].x, q[i].y);
+            w[2 * i + 1] = ptx::f2(q[i].z, q[i].w);
         }
     } else {
         const uint4* p = static_cast<const uint4*>(weight);
         rope_unpack(p[l.a], p[l.b], w);
     }
 }
+
+// The rotation of a lane's elements as y = x p + z q, z their partners: the other vector in the half layout, the other of
+// the two in the interleaved one.  Of elements that are not rotated p is 1 and q not used.
+template <bool kInter>
+struct RopeTurn {
+    uint64_t p[8], q[8];
+    bool turn_a, turn_b;
+
+    // Position `at`; kBack: the transposed rotation.
+    template <bool kBack>
+    __device__ __forceinline__ void set(const RopeParams& r, const RopeLane& l, int lane, long long at) {
+        const uint64_t m = rope_both(r.factor);
+        turn_a = l.turn_a;
+        turn_b = l.turn_b;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = rope_both(1.f);
+            q[i] = 0;
+        }
+        if (kInter) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {  // pairs i and i + 1 of the lane, one in a word
+                if (!(i < 4 ? turn_a : turn_b)) continue;
+                const int pair = i < 4 ? 4 * l.a + i : 4 * l.b + i - 4;
+                uint64_t c, s;
+                rope_wave2(at, r.turns[pair], r.turns[pair + 1], m, c, s);
+                float c0, c1, s0, s1;
+                ptx::f2_split(c, c0, c1);
+                ptx::f2_split(s, s0, s1);
+                p[i] = rope_both(c0);
+                p[i + 1] = rope_both(c1);
+                q[i] = kBack ? ptx::f2(s0, -s0) : ptx::f2(-s0, s0);
+                q[i + 1] = kBack ? ptx::f2(s1, -s1) : ptx::f2(-s1, s1);
+            }
+        } else if (turn_a) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint64_t c, s;
+                rope_wave2(at, r.turns[8 * lane + 2 * i], r.turns[8 * lane + 2 * i + 1], m, c, s);
+                p[i] = p[i + 4] = c;
+                q[i] = kBack ? s : rope_negate(s);
+                q[i + 4] = kBack ? rope_negate(s) : s;
+            }
+        }
+    }
+    // With weights before the rotation: y = (x w) p + (z w') q.
+    __device__ __forceinline__ void weigh(const uint64_t (&w)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = ptx::mul2(p[i], w[i]);
+            q[i] = ptx::mul2(q[i], kInter ? rope_swap(w[i]) : w[i ^ 4]);
+        }
+    }
+    // y from x.  kWeighed: elements that are not rotated have weights too; else they stay as they are, whatever they are.
+    template <bool kWeighed>
+    __device__ __forceinline__ void turn(uint64_t (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // half layout: words i and i + 4 together
+            if (kInter) {
+                if (i < 4 ? turn_a : turn_b)
+                    x[i] = ptx::fma2(rope_swap(x[i]), q[i], ptx::mul2(x[i], p[i]));
+                else if (kWeighed)
+                    x[i] = ptx::mul2(x[i], p[i]);
+            } else if (i < 4) {
+                if (turn_a) {
+                    const uint64_t u = x[i], v = x[i + 4];
+                    x[i] = ptx::fma2(v, q[i], ptx::mul2(u, p[i]));
+                    x[i + 4] = ptx::fma2(u, q[i + 4], ptx::mul2(v, p[i + 4]));
+                } else if (kWeighed) {
+                    x[i] = ptx::mul2(x[i], p[i]);
+                    x[i + 4] = ptx::mul2(x[i + 4], p[i + 4]);
+                }
+            }
+    }
+};
 
 // Sum over a row's lanes (neighbouring, kLanes a power of two).
 template <int kLanes>
@@ -114,41 +188,37 @@ __device__ __forceinline__ float rope_row_sum(float x) {
     for (int i = 1; i < kLanes; i *= 2) x += __shfl_xor_sync(0xffffffffu, x, i);
     return x;
 }
-__device__ __forceinline__ float rope_squares(const float (&x)[16]) {
-    float a = 0.f, b = 0.f;
+// The sum of the products of a lane's elements.
+__device__ __forceinline__ float rope_dot(const uint64_t (&x)[8], const uint64_t (&y)[8]) {
+    uint64_t a = ptx::mul2(x[0], y[0]);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        a = fmaf(x[i], x[i], a);
-        b = fmaf(x[i + 1], x[i + 1], b);
-    }
-    return a + b;
+    for (int i = 1; i < 8; ++i) a = ptx::fma2(x[i], y[i], a);
+    float lo, hi;
+    ptx::f2_split(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ void rope_scale(uint64_t (&x)[8], float by) {
+    const uint64_t b = rope_both(by);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = ptx::mul2(x[i], b);
 }
 // r of a row.  bf16's largest values have squares beyond fp32: such a row's x (not its infinities) is taken 2^-72 times
 // smaller, where eps is nothing beside it, and *down is what r x is to be of x's own size.
 template <int kLanes>
-__device__ __forceinline__ float rope_norm(float (&x)[16], float eps, float* down) {
-    constexpr float kInv = 1.f / (16 * kLanes);
-    float ss = rope_row_sum<kLanes>(rope_squares(x));
+__device__ __forceinline__ float rope_norm(uint64_t (&x)[8], float eps, float* down) {
+    constexpr float kInv = 1.f / (16 * kLanes), kDown = 2.117582368135751e-22f;  // 2^-72
+    const float ss = rope_row_sum<kLanes>(rope_dot(x, x));
     *down = 1.f;
     const bool big = ss == INFINITY;
     if (__any_sync(0xffffffffu, big)) {
         if (big) {
-            *down = 2.117582368135751e-22f;  // 2^-72
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= 2.117582368135751e-22f;
+            *down = kDown;
+            rope_scale(x, kDown);
         }
-        const float again = rope_row_sum<kLanes>(rope_squares(x));
+        const float again = rope_row_sum<kLanes>(rope_dot(x, x));
         if (big) return rsqrtf(again * kInv);
     }
     return rsqrtf(fmaf(ss, kInv, eps));
-}
-
-template <int kLanes>
-__device__ __forceinline__ void rope_normed(float (&x)[16], const float (&w)[16], float eps) {
-    float down;
-    const float r = rope_norm<kLanes>(x, eps, &down);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
 }
 
 // The rows of a unit that one lane group takes: its token, and heads first, first + groups ... below `end`.
@@ -170,49 +240,95 @@ __device__ __forceinline__ bool rope_task(const RopePlan& p, unsigned int unit, 
     return there;
 }
 
+// A thread's rows on their way: kVectors vectors of a row at a time, kDepth rows ahead, in shared memory that only this
+// thread writes and reads, so nothing but its own copies is waited for.  Registers for as many rows would cost the warps
+// that hide the latency: with one row ahead in registers a norm's forward had 17 KB under way on an SM, where 45 are needed.
+template <int kVectors, int kDepth, int kThreads>
+struct RopeRing {
+    static constexpr int kBytes = kVectors * kDepth * kThreads * 16;
+    uint32_t base;
+    __device__ __forceinline__ explicit RopeRing(void* smem) : base(ptx::smem_addr(smem) + threadIdx.x * 16) {}
+    __device__ __forceinline__ void fill(int slot, int vector, const void* src, bool there) const {
+        ptx::cp_async_16(base + (slot * kVectors + vector) * kThreads * 16, src, there ? 16u : 0u);
+    }
+    __device__ __forceinline__ uint4 at(int slot, int vector) const {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(base + (slot * kVectors + vector) * kThreads * 16)
+                     : "memory");
+        return x;
+    }
+};
+constexpr int kRopeDepth = 4;
+
 // One unit of the forward.  `place(b, s, &position)`: where row s of sequence b stands, and whether it is one at all.  Every
 // lane of a warp goes through the same steps (rows that are not there are computed from zeros and not stored), as the
 // sums over a row's lanes ask for whole warps.
-template <int D, bool kInter, bool kNorm, typename Place>
+template <int D, bool kInter, bool kNorm, int kThreads, typename Place>
 __device__ __forceinline__ void rope_forward(const RopeParams& r, const RopePlan& plan, unsigned int unit, int S, const RopeRows& from,
-                                             const RopeRows& to, const Place& place) {
+                                             const RopeRows& to, const Place& place, void* smem) {
     constexpr int kLanes = D / 16;
+    const RopeRing<2, kRopeDepth, kThreads> ring(smem);
     RopeTask t;
     bool there = rope_task<D>(plan, unit, S, t);
     const int lane = threadIdx.x % kLanes, kind = t.kind;
     const RopeLane l = rope_lane(lane, D, r.rot, kInter);
     long long position;
     there = place(t.b, t.s, &position) && there;
-    const __nv_bfloat16* in = from.p[kind] + t.b * from.stride[kind][0] + t.s * from.stride[kind][2];
-    __nv_bfloat16* out = to.p[kind] + t.b * to.stride[kind][0] + t.s * to.stride[kind][2];
+    const __nv_bfloat16* base = from.p[kind] + t.b * from.stride[kind][0] + t.s * from.stride[kind][2];
+    const uint4* in = reinterpret_cast<const uint4*>(base + t.head * from.stride[kind][1]);
+    uint4* out = reinterpret_cast<uint4*>(to.p[kind] + t.b * to.stride[kind][0] + t.s * to.stride[kind][2] + t.head * to.stride[kind][1]);
+    const long long in_step = plan.groups * from.stride[kind][1] / 8, out_step = plan.groups * to.stride[kind][1] / 8;
+    const int rows = there && t.head < t.end ? (t.end - t.head + plan.groups - 1) / plan.groups : 0;  // of this thread
+    int next = 0;  // the row whose copy leaves next
+    const auto fill = [&](int slot) {
+        const bool mine = next < rows;
+        const uint4* x = mine ? in : reinterpret_cast<const uint4*>(from.p[kind]);
+        ring.fill(slot, 0, x + l.a, mine);
+        ring.fill(slot, 1, x + l.b, mine);
+        ptx::cp_async_commit();
+        in += in_step;
+        ++next;
+    };
+#pragma unroll
+    for (int i = 0; i < kRopeDepth; ++i) fill(i);
     const bool copy = kind == 2;
-    RopeWaves<kInter> waves;
-    if (!copy) waves.at(r, l, lane, position);
+    RopeTurn<kInter> turn;
     const void* weight = copy ? nullptr : r.weight[kind];
-    float w[16];
-    if (kNorm && weight) rope_weights(weight, r.weight_f32, l, w);
+    const bool normed = kNorm && weight;
+    if (!copy) {
+        uint64_t w[8];
+        if (normed) rope_weights(weight, r.weight_f32, l, w);
+        turn.template set<false>(r, l, lane, position);
+        if (normed) turn.weigh(w);
+    }
+#pragma unroll 1
     for (int i = 0; i < plan.per; ++i) {
-        const int h = t.head + i * plan.groups;
-        const bool mine = there && h < t.end;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (mine) {
-            const uint4* x = reinterpret_cast<const uint4*>(in + h * from.stride[kind][1]);
-            a = x[l.a];
-            b = x[l.b];
-        }
+        const int slot = i % kRopeDepth;
+        ptx::cp_async_wait<kRopeDepth - 1>();
+        uint4 a = ring.at(slot, 0), b = ring.at(slot, 1);
         if (!copy) {
-            float x[16];
+            uint64_t x[8];
             rope_unpack(a, b, x);
-            if (kNorm && weight) rope_normed<kLanes>(x, w, r.eps);
-            waves.template turn<false>(x);
+            if (normed) {
+                float down;
+                const float rr = rope_norm<kLanes>(x, r.eps, &down);
+                turn.template turn<true>(x);
+                rope_scale(x, rr);
+            } else {
+                turn.template turn<false>(x);
+            }
             rope_pack(x, a, b);
         }
-        if (mine) {
-            uint4* y = reinterpret_cast<uint4*>(out + h * to.stride[kind][1]);
-            y[l.a] = a;
-            y[l.b] = b;
+        if (i < rows) {
+            out[l.a] = a;
+            out[l.b] = b;
         }
+        out += out_step;
+        fill(slot);  // once the slot's values are out of it
     }
+    ptx::cp_async_wait<0>();
 }
 
 }  // namespace attn

@@ -12,7 +12,7 @@ namespace attn {
 
 // A row (one head of one token) is held by D / 16 lanes, two vectors of 8 elements each, so that both elements of every
 // pair are in one lane.
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // The vectors of lane `l` and whether they are rotated.  Half layout: rotated lanes hold vector l and the one rot / 2
 // elements further, element j of the one paired with element j of the other (pair 8 l + j); the rest of the head goes to
@@ -37,7 +37,7 @@ ROPE_HD RopeLane rope_lane(int l, int D, int rot, int interleaved) {
     return x;
 }
 
-// A block's rows: `tokens` (a power of two) by kRopeThreads / (D / 16) / tokens heads side by side, and up to `per` such
+// A block's rows: `tokens` (a power of two) by threads / (D / 16) / tokens heads side by side, and up to `per` such
 // groups of heads one after the other, all of one kind (q, k or v).  The units of a tile of tokens stand side by side.
 struct RopePlan {
     long long total;     // tokens, B * S
@@ -63,11 +63,11 @@ ROPE_HD RopeUnit rope_unit(const RopePlan& p, unsigned int unit) {
     return u;
 }
 
-// The plan for `total` tokens and these heads: `most` tokens side by side where there are so many, and as many heads a
+// The plan for `total` tokens, these heads and blocks of `threads`: as many tokens side by side as there are and fit, and as many heads a
 // thread as still give `units` units, `per` at most.
-ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int per, long long units) {
+ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int threads, int per, long long units) {
     RopePlan p;
-    const int rows = kRopeThreads / (D / 16);
+    const int rows = threads / (D / 16);
     p.total = total;
     p.tokens = 1;
     while (p.tokens < rows && p.tokens < total) p.tokens *= 2;

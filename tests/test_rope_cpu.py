@@ -228,7 +228,7 @@ int main(int argc, char** argv) {
         }
         return 0;
     }
-    const RopePlan p = rope_plan(atoll(argv[1]), atoi(argv[2]), atoi(argv[3]), atoi(argv[4]), atoi(argv[5]), atoi(argv[6]), atoll(argv[7]));
+    const RopePlan p = rope_plan(atoll(argv[1]), atoi(argv[2]), atoi(argv[3]), atoi(argv[4]), atoi(argv[5]), atoi(argv[6]), atoi(argv[7]), atoll(argv[8]));
     const long long units = rope_tiles(p) * rope_chunks(p);
     printf("%lld %d %d %d\n", units, p.tokens, p.groups, p.per);
     for (long long i = 0; i < units; ++i) {
@@ -276,11 +276,11 @@ def test_lanes_hold_every_element_once_and_pairs_together(plan_program, head, in
 
 @pytest.mark.parametrize("case", [(1, 2, 2, 2, 64), (1, 32, 8, 8, 128), (37, 12, 4, 4, 64), (64, 32, 8, 8, 128), (33, 5, 1, 0, 128),
                                   (1000, 7, 7, 7, 64), (4096, 16, 16, 16, 128), (3, 33, 1, 1, 128), (31, 40, 40, 0, 64)])
-@pytest.mark.parametrize("per,least", [(1, 1), (8, 1216), (5, 100), (16, 1)])
-def test_units_hold_every_row_once(plan_program, case, per, least):
+@pytest.mark.parametrize("threads,per,least", [(256, 1, 1), (128, 8, 1216), (256, 5, 100), (128, 16, 1)])
+def test_units_hold_every_row_once(plan_program, case, threads, per, least):
     total, Hq, Hk, Hv, head = case
-    (units, tokens, groups, heads), *listed = plan_program(total, Hq, Hk, Hv, head, per, least)
-    assert len(listed) == units and tokens * groups == 256 // (head // 16) and 1 <= heads <= per
+    (units, tokens, groups, heads), *listed = plan_program(total, Hq, Hk, Hv, head, threads, per, least)
+    assert len(listed) == units and tokens * groups == threads // (head // 16) and 1 <= heads <= per
     seen = np.zeros((total, 3, max(Hq, Hk, Hv)), int)
     for tile, kind, chunk in listed:
         H = (Hq, Hk, Hv)[kind]
