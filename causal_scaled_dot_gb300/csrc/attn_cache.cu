@@ -161,11 +161,20 @@ bool allow_smem() {
     return cudaFuncSetAttribute(attn_cache_fwd_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)CacheLayout<R>::kDynamicSmem) == cudaSuccess;
 }
+bool allow_append() {
+    // a unit of 128 tokens of 128 elements in kAppendThreads threads
+    const auto allow = [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, append_smem(128 * 128 / 16 / kAppendThreads)) ==
+               cudaSuccess;
+    };
+    return allow(attn_cache_append_kernel<64, false>) && allow(attn_cache_append_kernel<64, true>) &&
+           allow(attn_cache_append_kernel<128, false>) && allow(attn_cache_append_kernel<128, true>);
+}
 int setup_cache_kernels(int dev) {
     if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
     std::lock_guard<std::mutex> lock(g_cache_mutex);
     if (g_cache_ready[dev] == 0)
-        g_cache_ready[dev] = allow_smem<8>() && allow_smem<16>() && allow_smem<32>() &&
+        g_cache_ready[dev] = allow_smem<8>() && allow_smem<16>() && allow_smem<32>() && allow_append() &&
                                      cudaFuncSetAttribute(attn_cache_fwd_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                           (int)CacheWideLayout::kDynamicSmem) == cudaSuccess
                                  ? 1
@@ -195,23 +204,17 @@ int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
 // q's heads a thread at most, and the units that their number comes down for (rope_plan).
 constexpr int kAppendPer = 8;
 constexpr long long kAppendUnits = 608;
-// Threads per unit that hold the largest unit's elements at 64 a thread.
-int append_threads(int elements) { return elements <= 64 * 32 ? 32 : elements <= 64 * 64 ? 64 : elements <= 64 * 128 ? 128 : 256; }
-template <int D, bool kInter, int kThreads>
-int launch_append(CacheAppendParams& p, long long q_units, cudaStream_t st) {
-    constexpr int kBlock = kAppendBlock<kThreads>, kPer = kBlock / kThreads;
-    p.write_blocks = (p.num_units + kPer - 1) / kPer;
-    if (p.write_blocks + q_units > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
-    return launch(attn_cache_append_kernel<D, kInter, kThreads>, p.write_blocks + (int)q_units, kBlock, 0, true, st, p);
-}
+// Shares of 16 elements that a thread of a unit holds at most, before the unit gets twice the threads.
+constexpr int kAppendItems = 4;
 template <int D, bool kInter>
-int launch_append(int threads, CacheAppendParams& p, long long q_units, cudaStream_t st) {
-    switch (threads) {
-        case 32: return launch_append<D, kInter, 32>(p, q_units, st);
-        case 64: return launch_append<D, kInter, 64>(p, q_units, st);
-        case 128: return launch_append<D, kInter, 128>(p, q_units, st);
-    }
-    return launch_append<D, kInter, D == 128 ? 256 : 128>(p, q_units, st);  // blocks of 128 tokens of 128 elements
+int launch_append(CacheAppendParams& p, int rows, long long q_units, cudaStream_t st) {
+    const int shares = rows * (D / 16);
+    p.unit_shift = 5;
+    while (1 << p.unit_shift < kAppendThreads && shares > kAppendItems << p.unit_shift) ++p.unit_shift;
+    const int per = kAppendThreads >> p.unit_shift, items = (shares + (1 << p.unit_shift) - 1) >> p.unit_shift;
+    p.write_blocks = (p.num_units + per - 1) / per;
+    if (p.write_blocks + q_units > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    return launch(attn_cache_append_kernel<D, kInter>, p.write_blocks + (int)q_units, kAppendThreads, append_smem(items), true, st, p);
 }
 
 }  // namespace
@@ -289,7 +292,6 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
         host::rope_meets(rope, cache->v_scale, ns, B, S, D))
         return ATTN_ERR_INVALID_ARG;
     const int bs = cache->block_size;
-    const int threads = append_threads((S < bs ? S : bs) * D);
     long long q_units = 0;
     if (q_out) {
         const size_t qb = (size_t)B * Hq * S * D * 2;
@@ -302,12 +304,13 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
         p.out.stride[0][0] = (long long)Hq * S * D;
         p.out.stride[0][1] = (long long)S * D;
         p.out.stride[0][2] = D;
-        p.plan = rope_plan((long long)B * S, Hq, 0, 0, D, threads > 128 ? threads : 128, kAppendPer, kAppendUnits);
+        p.plan = rope_plan((long long)B * S, Hq, 0, 0, D, kAppendThreads, kAppendPer, kAppendUnits);
         q_units = rope_tiles(p.plan) * rope_chunks(p.plan);
     }
     int sms = 0, device = -1;
     unsigned int* status = nullptr;
     if ((rc = host::current_device(&sms, &status, &device)) != ATTN_OK) return rc;
+    if ((rc = setup_cache_kernels(device)) != ATTN_OK) return rc;
     p.c = view_of(cache, status);
     host::fill_rope(rope, &p.r);
     p.new_lens = new_lens;
@@ -319,8 +322,9 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
     if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
     p.num_units = (int)units;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (D == 64) return rope->interleaved ? launch_append<64, true>(threads, p, q_units, st) : launch_append<64, false>(threads, p, q_units, st);
-    return rope->interleaved ? launch_append<128, true>(threads, p, q_units, st) : launch_append<128, false>(threads, p, q_units, st);
+    const int rows = S < bs ? S : bs;  // of the largest unit
+    if (D == 64) return rope->interleaved ? launch_append<64, true>(p, rows, q_units, st) : launch_append<64, false>(p, rows, q_units, st);
+    return rope->interleaved ? launch_append<128, true>(p, rows, q_units, st) : launch_append<128, false>(p, rows, q_units, st);
 }
 
 extern "C" int attn_cache_read(const attn_cache_t* cache, void* k, void* v, int first, int S, void* stream) {

@@ -259,6 +259,17 @@ struct RopeRing {
                      : "memory");
         return x;
     }
+    // Two words of fp32 pairs in a vector's place.
+    __device__ __forceinline__ void put(int slot, int vector, uint64_t x, uint64_t y) const {
+        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(base + (slot * kVectors + vector) * kThreads * 16), "l"(x), "l"(y)
+                     : "memory");
+    }
+    __device__ __forceinline__ void get(int slot, int vector, uint64_t& x, uint64_t& y) const {
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                     : "=l"(x), "=l"(y)
+                     : "r"(base + (slot * kVectors + vector) * kThreads * 16)
+                     : "memory");
+    }
 };
 constexpr int kRopeDepth = 4;
 
