@@ -212,9 +212,10 @@ int launch_append(CacheAppendParams& p, int rows, long long q_units, cudaStream_
     p.unit_shift = 5;
     while (1 << p.unit_shift < kAppendThreads && shares > kAppendItems << p.unit_shift) ++p.unit_shift;
     const int per = kAppendThreads >> p.unit_shift, items = (shares + (1 << p.unit_shift) - 1) >> p.unit_shift;
-    p.write_blocks = (p.num_units + per - 1) / per;
-    if (p.write_blocks + q_units > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
-    return launch(attn_cache_append_kernel<D, kInter>, p.write_blocks + (int)q_units, kAppendThreads, append_smem(items), true, st, p);
+    const long long writes = (p.num_units + per - 1) / per, blocks = writes + q_units;
+    if (blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    p.write_share = (((unsigned long long)writes << 32) + blocks - 1) / blocks;
+    return launch(attn_cache_append_kernel<D, kInter>, (int)blocks, kAppendThreads, append_smem(items), true, st, p);
 }
 
 }  // namespace

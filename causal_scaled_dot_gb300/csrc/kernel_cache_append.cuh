@@ -21,7 +21,8 @@ struct CacheAppendParams {
     RopeRows in, out;   // q, k, v of the step; q rotated
     const int* new_lens;
     int S;
-    int blocks_per_seq, num_units, write_blocks;
+    int blocks_per_seq, num_units;
+    unsigned long long write_share;  // ceil(2^32 * writing blocks / blocks)
     int unit_shift;     // 2^unit_shift threads per unit: 32 .. kAppendThreads
     RopePlan plan;      // of q
 };
@@ -45,10 +46,18 @@ struct AppendPlace {
     }
 };
 
-// Four values' codes where one of them may be infinite (NaN then), or the scale is a caller's and no power of two.
-__device__ __noinline__ uint32_t append_codes_slow(float a, float b, float c, float d, float s, bool divide) {
-    const auto one = [&](float x) { return divide ? e4m3_divided(x, s) : fabsf(x) < INFINITY ? x / s : NAN; };
-    return e4m3_pair(one(a), one(b)) | e4m3_pair(one(c), one(d)) << 16;
+// A share's codes where one of its values may be infinite (NaN then), or the scale is a caller's and no power of two.
+__device__ __forceinline__ void append_codes_slow(const uint64_t (&x)[8], float s, bool divide, uint32_t (&code)[4]) {
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const auto one = [&](float y) { return divide ? e4m3_divided(y, s) : fabsf(y) < INFINITY ? y / s : NAN; };
+        float a, b, d, e;
+        ptx::f2_split(j == 0 ? x[0] : j == 1 ? x[2] : j == 2 ? x[4] : x[6], a, b);
+        ptx::f2_split(j == 0 ? x[1] : j == 1 ? x[3] : j == 2 ? x[5] : x[7], d, e);
+        const uint32_t four = e4m3_pair(one(a), one(b)) | e4m3_pair(one(d), one(e)) << 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) code[k] = k == j ? four : code[k];
+    }
 }
 __device__ __forceinline__ float append_largest(const uint64_t (&x)[8]) {
     float m = 0.f, lo, hi;
@@ -59,6 +68,25 @@ __device__ __forceinline__ float append_largest(const uint64_t (&x)[8]) {
     }
     return m;
 }
+__device__ __forceinline__ float append_largest_finite(const uint64_t (&x)[8]) {
+    float m = 0.f, lo, hi;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        ptx::f2_split(x[i], lo, hi);
+        m = ptx::max3(m, fabsf(lo) < INFINITY ? fabsf(lo) : 0.f, fabsf(hi) < INFINITY ? fabsf(hi) : 0.f);
+    }
+    return m;
+}
+// The largest finite magnitude of a thread's bf16 shares, as fp32 bits.
+__device__ __noinline__ uint32_t append_finite(RopeRing<4, 1, kAppendThreads> mine, int count) {
+    float m = 0.f;
+    for (int i = 0; i < count; ++i) {
+        uint64_t x[8];
+        rope_unpack(mine.at(i, 0), mine.at(i, 1), x);
+        m = fmaxf(m, append_largest_finite(x));
+    }
+    return __float_as_uint(m);
+}
 
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
@@ -67,10 +95,10 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
     extern __shared__ __align__(16) unsigned char smem[];
     ptx::launch_next();
     ptx::wait_previous();
-    // Blocks that write (much to compute) and blocks of q (much to load) alternate evenly: of the first i blocks i W / N
-    // write.
-    const unsigned int before = (unsigned int)((unsigned long long)blockIdx.x * p.write_blocks / gridDim.x);
-    if ((unsigned int)((blockIdx.x + 1ull) * p.write_blocks / gridDim.x) == before) {
+    // Blocks that write (much to compute) and blocks of q (much to load) alternate evenly: of the first i blocks
+    // i write_share / 2^32 write.
+    const unsigned int before = (unsigned int)(blockIdx.x * p.write_share >> 32);
+    if ((unsigned int)((blockIdx.x + 1) * p.write_share >> 32) == before) {
         rope_forward<D, kInter, true, kAppendThreads>(p.r, p.plan, blockIdx.x - before, p.S, p.in, p.out, AppendPlace{p}, smem);
         return;
     }
@@ -90,14 +118,16 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
     const int lane = t % kLanes, kind = u.is_v ? 2 : 1;
     const RopeLane l = rope_lane(lane, D, p.r.rot, kInter);
     const long long stride = p.in.stride[kind][2];
-    const __nv_bfloat16* src = p.in.p[kind] + u.b * p.in.stride[kind][0] + u.h * p.in.stride[kind][1] + row0 * stride;
+    const __nv_bfloat16* src = p.in.p[kind] + u.b * p.in.stride[kind][0] + u.h * p.in.stride[kind][1] + (row0 + t / kLanes) * stride;
     // The shares of this thread: rows first, first + step ...
-    const int first = t / kLanes, step = threads / kLanes, count = active ? (rows - first + step - 1) / step : 0;
+    const int first = t / kLanes, step_shift = p.unit_shift - (D == 128 ? 3 : 2), step = 1 << step_shift;
+    const int count = active ? (rows - first + step - 1) >> step_shift : 0;
     const RopeRing<4, 1, kAppendThreads> mine(smem);
     for (int i = 0; i < count; ++i) {
-        const uint4* x = reinterpret_cast<const uint4*>(src + (first + i * step) * stride);
+        const uint4* x = reinterpret_cast<const uint4*>(src);
         mine.fill(i, 0, x + l.a, true);
         mine.fill(i, 1, x + l.b, true);
+        src += stride << step_shift;
     }
     ptx::cp_async_commit();
     const int entry = active ? c.block_table[(long long)u.b * c.max_blocks + lb] : 0;
@@ -107,55 +137,67 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
     float* scale_at = active ? (u.is_v ? c.v_scale : c.k_scale) + (long long)block * c.Hkv + u.h : nullptr;
     const float s_old = active && slot0 > 0 ? *scale_at : 0.f;
 
-    const void* weight = u.is_v ? nullptr : p.r.weight[1];
-    float amax = 0.f;
+    uint32_t top = 0;  // the largest magnitude, as bits
     bool odd = false;  // this thread holds an infinity: those do not count, nor do NaN
-    // Whole warps stay together, as the sums over a row's lanes ask for: warps are of one unit, rows of neighbouring lanes.
-    const int most = active ? (rows + step - 1) / step : 0;
+    if (u.is_v) {
+        ptx::cp_async_wait<0>();
+        uint32_t two = 0;  // two elements an instruction, by their bits
 #pragma unroll 1
-    for (int i = 0; i < most; ++i) {
-        uint64_t x[8];
-        RopeTurn<kInter> turn;
-        const bool there = i < count;
-        const int at = row0 + (there ? first + i * step : 0);
-        if (!u.is_v) turn.template set<false>(p.r, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
-        if (i == 0) ptx::cp_async_wait<0>();
-        if (there) {
-            rope_unpack(mine.at(i, 0), mine.at(i, 1), x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0;
+        for (int i = 0; i < count; ++i) {
+            const uint4 a = mine.at(i, 0), b = mine.at(i, 1);
+            two = __vmaxu2(__vmaxu2(two, a.x & 0x7fff7fffu), __vmaxu2(a.y & 0x7fff7fffu, a.z & 0x7fff7fffu));
+            two = __vmaxu2(__vmaxu2(two, a.w & 0x7fff7fffu), __vmaxu2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu));
+            two = __vmaxu2(__vmaxu2(two, b.z & 0x7fff7fffu), b.w & 0x7fff7fffu);
         }
-        if (weight) {
-            float down;
-            uint64_t w[8];
-            rope_weights(weight, p.r.weight_f32, l, w);
-            turn.weigh(w);
-            const float r = rope_norm<kLanes>(x, p.r.eps, &down);
-            turn.template turn<true>(x);
-            rope_scale(x, r);
-        } else if (!u.is_v) {
-            turn.template turn<false>(x);
-        }
-        float m = append_largest(x);
-        if (m == INFINITY) {
+        top = max(two & 0xffffu, two >> 16) << 16;
+        if (top >= 0x7f800000u) {
             odd = true;
-            m = 0.f;
+            top = append_finite(mine, count);
+        }
+    } else {
+        const void* weight = p.r.weight[1];
+        float amax = 0.f;
+        // Whole warps stay together, as the sums over a row's lanes ask for: a warp is of one unit, a row of neighbouring lanes.
+        const int most = active ? (rows + step - 1) >> step_shift : 0;
+#pragma unroll 1
+        for (int i = 0; i < most; ++i) {
+            uint64_t x[8];
+            RopeTurn<kInter> turn;
+            const bool there = i < count;
+            const int at = row0 + (there ? first + i * step : 0);
+            turn.template set<false>(p.r, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
+            if (i == 0) ptx::cp_async_wait<0>();
+            if (there) {
+                rope_unpack(mine.at(i, 0), mine.at(i, 1), x);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                ptx::f2_split(x[j], lo, hi);
-                m = ptx::max3(m, fabsf(lo) < INFINITY ? fabsf(lo) : 0.f, fabsf(hi) < INFINITY ? fabsf(hi) : 0.f);
+                for (int j = 0; j < 8; ++j) x[j] = 0;
+            }
+            if (weight) {
+                float down;
+                uint64_t w[8];
+                rope_weights(weight, p.r.weight_f32, l, w);
+                const float r = rope_norm<kLanes>(x, p.r.eps, &down);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = ptx::mul2(x[j], w[j]);
+                rope_scale(x, r);
+            }
+            turn.template turn<false>(x);
+            float m = append_largest(x);
+            if (m == INFINITY) {
+                odd = true;
+                m = append_largest_finite(x);
+            }
+            amax = fmaxf(amax, m);
+            if (there) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine.put(i, j, x[2 * j], x[2 * j + 1]);
             }
         }
-        amax = fmaxf(amax, m);
-        if (there) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mine.put(i, j, x[2 * j], x[2 * j + 1]);
-        }
+        top = __float_as_uint(amax);
     }
     ptx::cp_async_wait<0>();
-    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    top = __reduce_max_sync(0xffffffffu, top);
     if (threads > 32) {
         if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
         __syncthreads();
@@ -172,24 +214,27 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
         uint32_t code[4];
+        uint64_t x[8];
+        if (u.is_v) {
+            rope_unpack(mine.at(i, 0), mine.at(i, 1), x);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint64_t x, y;
-            mine.get(i, j, x, y);
-            float a, b, d, e;
-            if (divide || odd) {
-                ptx::f2_split(x, a, b);
-                ptx::f2_split(y, d, e);
-                code[j] = append_codes_slow(a, b, d, e, s_new, divide);
-            } else {
-                ptx::f2_split(ptx::mul2(x, inv2), a, b);
-                ptx::f2_split(ptx::mul2(y, inv2), d, e);
+            for (int j = 0; j < 4; ++j) mine.get(i, j, x[2 * j], x[2 * j + 1]);
+        }
+        if (divide || odd) {
+            append_codes_slow(x, s_new, divide, code);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a, b, d, e;
+                ptx::f2_split(ptx::mul2(x[2 * j], inv2), a, b);
+                ptx::f2_split(ptx::mul2(x[2 * j + 1], inv2), d, e);
                 code[j] = e4m3_pair(a, b) | e4m3_pair(d, e) << 16;
             }
         }
-        unsigned char* to = dst + (long long)(i * step) * D;
-        *reinterpret_cast<uint2*>(to + 8 * l.a) = make_uint2(code[0], code[1]);
-        *reinterpret_cast<uint2*>(to + 8 * l.b) = make_uint2(code[2], code[3]);
+        *reinterpret_cast<uint2*>(dst + 8 * l.a) = make_uint2(code[0], code[1]);
+        *reinterpret_cast<uint2*>(dst + 8 * l.b) = make_uint2(code[2], code[3]);
+        dst += D << step_shift;
     }
     if (slot0 > 0 && s_new > s_old) {  // the block's earlier tokens move to the larger scale
         const float ratio = s_old * inv;

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 6) attn_rope_bwd_ker
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) sum += part[i * D + threadIdx.x];
         const RopeUnit u = rope_unit(p.plan, blockIdx.x);
-        p.part[kind][(u.tile * p.plan.chunks[kind] + u.chunk) * D + threadIdx.x] = sum;
+        p.part[kind][((long long)u.tile * p.plan.chunks[kind] + u.chunk) * D + threadIdx.x] = sum;
     }
 }
 

@@ -230,13 +230,14 @@ template <int D>
 __device__ __forceinline__ bool rope_task(const RopePlan& p, unsigned int unit, int S, RopeTask& t) {
     const RopeUnit u = rope_unit(p, unit);
     const int row = threadIdx.x / (D / 16), side = p.tokens == 1 ? row : row / p.tokens;
-    const long long token = u.tile * p.tokens + (row - side * p.tokens);
+    const unsigned int token = u.tile * p.tokens + (row - side * p.tokens);
     t.kind = u.kind;
     t.head = u.chunk * p.groups * p.per + side;
     t.end = min(p.heads[u.kind], (u.chunk + 1) * p.groups * p.per);
     const bool there = token < p.total;
-    t.b = there ? token / S : 0;
-    t.s = there ? token - t.b * S : 0;
+    const unsigned int b = there ? token / (unsigned int)S : 0;
+    t.b = b;
+    t.s = there ? token - b * (unsigned int)S : 0;
     return there;
 }
 

@@ -16,7 +16,8 @@ constexpr int kRopeThreads = 128;
 
 // The vectors of lane `l` and whether they are rotated.  Half layout: rotated lanes hold vector l and the one rot / 2
 // elements further, element j of the one paired with element j of the other (pair 8 l + j); the rest of the head goes to
-// the other lanes in order.  Interleaved: vectors l and l + D / 16, four pairs each (pairs 4 * vector + 0 .. 3).
+// the other lanes so that neighbouring lanes hold neighbouring vectors (two in a row a lane took 29 us where this takes 19,
+// for 33.5 M elements: half sectors).  Interleaved: vectors l and l + D / 16, four pairs each (pairs 4 * vector + 0 .. 3).
 struct RopeLane {
     int a, b;        // vectors, in units of 8 elements
     int turn_a, turn_b;
@@ -31,8 +32,8 @@ ROPE_HD RopeLane rope_lane(int l, int D, int rot, int interleaved) {
     } else {
         const int n = rot / 16;
         x.turn_a = x.turn_b = l < n;
-        x.a = l < n ? l : 2 * l;
-        x.b = l < n ? l + n : 2 * l + 1;
+        x.a = l < n ? l : l + n;
+        x.b = l < n ? l + n : l + D / 16;
     }
     return x;
 }
@@ -40,24 +41,24 @@ ROPE_HD RopeLane rope_lane(int l, int D, int rot, int interleaved) {
 // A block's rows: `tokens` (a power of two) by threads / (D / 16) / tokens heads side by side, and up to `per` such
 // groups of heads one after the other, all of one kind (q, k or v).  The units of a tile of tokens stand side by side.
 struct RopePlan {
-    long long total;     // tokens, B * S
+    unsigned int total;  // tokens, B * S < 2^31
     int tokens, groups;  // tokens and heads side by side
     int per;             // heads of a thread, at most
     int heads[3];        // of q, k and v; 0: absent
     int chunks[3];       // units of each kind in a tile of tokens
 };
 ROPE_HD int rope_chunks(const RopePlan& p) { return p.chunks[0] + p.chunks[1] + p.chunks[2]; }
-ROPE_HD long long rope_tiles(const RopePlan& p) { return (p.total + p.tokens - 1) / p.tokens; }
+ROPE_HD long long rope_tiles(const RopePlan& p) { return ((long long)p.total + p.tokens - 1) / p.tokens; }
 
 struct RopeUnit {
-    long long tile;
+    unsigned int tile;
     int kind, chunk;
 };
 ROPE_HD RopeUnit rope_unit(const RopePlan& p, unsigned int unit) {
     const unsigned int all = (unsigned int)rope_chunks(p);
     RopeUnit u;
     u.tile = unit / all;
-    u.chunk = (int)(unit - (unsigned int)u.tile * all);
+    u.chunk = (int)(unit - u.tile * all);
     u.kind = 0;
     while (u.chunk >= p.chunks[u.kind]) u.chunk -= p.chunks[u.kind++];
     return u;
@@ -68,7 +69,7 @@ ROPE_HD RopeUnit rope_unit(const RopePlan& p, unsigned int unit) {
 ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int threads, int per, long long units) {
     RopePlan p;
     const int rows = threads / (D / 16);
-    p.total = total;
+    p.total = (unsigned int)total;
     p.tokens = 1;
     while (p.tokens < rows && p.tokens < total) p.tokens *= 2;
     p.groups = rows / p.tokens;

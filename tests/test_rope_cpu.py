@@ -233,7 +233,7 @@ int main(int argc, char** argv) {
     printf("%lld %d %d %d\n", units, p.tokens, p.groups, p.per);
     for (long long i = 0; i < units; ++i) {
         const RopeUnit u = rope_unit(p, (unsigned)i);
-        printf("%lld %d %d\n", u.tile, u.kind, u.chunk);
+        printf("%u %d %d\n", u.tile, u.kind, u.chunk);
     }
 }
 """
