@@ -202,7 +202,7 @@ int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
 }
 
 // q's heads a thread at most, and the units that their number comes down for (rope_plan).
-constexpr int kAppendPer = 8;
+constexpr int kAppendPer = 16;
 constexpr long long kAppendUnits = 608;
 // Shares of 16 elements that a thread of a unit holds at most, before the unit gets twice the threads.
 constexpr int kAppendItems = 4;

@@ -28,38 +28,33 @@ struct RopeRows {
     long long stride[3][3];   // batch, head, token, in elements
 };
 
-// m cos and m sin of position p and two frequencies (2^-64 turns), packed.  The product's upper half is the angle as a
-// signed fraction of a turn (what it drops is below 2^-32 of one); its two top bits, rounded, are the quadrant, and the
-// rest r, in -1/8 .. 1/8 turn, enters sin(2 pi r) = r S(r^2) and cos(2 pi r) = C(r^2): polynomials with the least largest
-// error there (exchange algorithm of Remez; 1e-9 and 3e-8, so fp32's own roundings are what is left, under 2^-22).
-// sincospif took a third of the backward's instructions.
-__device__ __forceinline__ void rope_wave2(long long p, unsigned long long F0, unsigned long long F1, uint64_t m, uint64_t& c, uint64_t& s) {
-    const uint32_t u0 = (uint32_t)((unsigned long long)p * F0 >> 32) + 0x20000000u;
-    const uint32_t u1 = (uint32_t)((unsigned long long)p * F1 >> 32) + 0x20000000u;
+// cos and sin of position p and two frequencies (2^-64 turns), packed.  The product's upper half is the angle as a signed
+// fraction of a turn (what it drops is below 2^-32 of one).  Twice that, as an integer, is the rest x in -1/2 .. 1/2 half
+// turns, and both signs turn where its top bit differs from the angle's.  cos(pi x) = C(x^2) and sin(pi x) = x S(x^2) by
+// the polynomials with the least largest error there (exchange algorithm of Remez): 5e-8 and 3e-9, and with fp32's
+// roundings 2.0e-7 and 1.7e-7 over two million angles, under 2^-22.  sincospif took a third of the backward's instructions.
+__device__ __forceinline__ void rope_wave2(long long p, unsigned long long F0, unsigned long long F1, uint64_t& c, uint64_t& s) {
+    const uint32_t t0 = (uint32_t)((unsigned long long)p * F0 >> 32), t1 = (uint32_t)((unsigned long long)p * F1 >> 32);
     const auto both = [](float x) { return ptx::f2(x, x); };
-    const uint64_t r = ptx::mul2(ptx::f2((float)((int)(u0 & 0x3fffffffu) - 0x20000000), (float)((int)(u1 & 0x3fffffffu) - 0x20000000)),
-                                 both(2.3283064365386963e-10f));
-    const uint64_t y = ptx::mul2(r, r);
-    uint64_t cc = ptx::fma2(y, both(-83.66592125133988f), both(64.92322865171708f));
-    cc = ptx::fma2(y, cc, both(-19.739167263528856f));
-    cc = ptx::mul2(ptx::fma2(y, cc, both(1.f)), m);
-    uint64_t ss = ptx::fma2(y, both(-75.24283377371387f), both(81.58820665534085f));
-    ss = ptx::fma2(y, ss, both(-41.34162877037185f));
-    ss = ptx::fma2(y, ss, both(6.283185222149059f));
-    ss = ptx::mul2(ptx::mul2(ss, r), m);
-    float c0, c1, s0, s1;
-    ptx::f2_split(cc, c0, c1);
-    ptx::f2_split(ss, s0, s1);
-    // quadrants 0 .. 3: (c, s), (-s, c), (-c, -s), (s, -c)
-    const auto place = [](uint32_t u, float& c, float& s) {
-        const float x = u & 0x40000000u ? s : c, y = u & 0x40000000u ? c : s;
-        c = __uint_as_float(__float_as_uint(x) ^ ((u + 0x40000000u) & 0x80000000u));
-        s = __uint_as_float(__float_as_uint(y) ^ (u & 0x80000000u));
+    const uint64_t x = ptx::mul2(ptx::f2((float)(int)(t0 << 1), (float)(int)(t1 << 1)), both(2.3283064365386963e-10f));
+    const uint64_t y = ptx::mul2(x, x);
+    c = ptx::fma2(y, both(0.2200806587934494f), both(-1.3320938348770142f));
+    c = ptx::fma2(y, c, both(4.058451175689697f));
+    c = ptx::fma2(y, c, both(-4.934795379638672f));
+    c = ptx::fma2(y, c, both(1.f));
+    s = ptx::fma2(y, both(0.07722225040197372f), both(-0.5980464220046997f));
+    s = ptx::fma2(y, s, both(2.5500316619873047f));
+    s = ptx::fma2(y, s, both(-5.1677069664001465f));
+    s = ptx::fma2(y, s, both(3.141592502593994f));
+    s = ptx::mul2(s, x);
+    const uint32_t f0 = (t0 ^ t0 << 1) & 0x80000000u, f1 = (t1 ^ t1 << 1) & 0x80000000u;
+    const auto flip = [&](uint64_t v) {
+        float lo, hi;
+        ptx::f2_split(v, lo, hi);
+        return ptx::f2(__uint_as_float(__float_as_uint(lo) ^ f0), __uint_as_float(__float_as_uint(hi) ^ f1));
     };
-    place(u0, c0, s0);
-    place(u1, c1, s1);
-    c = ptx::f2(c0, c1);
-    s = ptx::f2(s0, s1);
+    c = flip(c);
+    s = flip(s);
 }
 __device__ __forceinline__ long long rope_position(const RopeParams& r, long long b, long long s) {
     if (!r.positions) return r.first + s;
@@ -116,7 +111,6 @@ struct RopeTurn {
     // Position `at`; kBack: the transposed rotation.
     template <bool kBack>
     __device__ __forceinline__ void set(const RopeParams& r, const RopeLane& l, int lane, long long at) {
-        const uint64_t m = rope_both(r.factor);
         turn_a = l.turn_a;
         turn_b = l.turn_b;
 #pragma unroll
@@ -130,7 +124,7 @@ struct RopeTurn {
                 if (!(i < 4 ? turn_a : turn_b)) continue;
                 const int pair = i < 4 ? 4 * l.a + i : 4 * l.b + i - 4;
                 uint64_t c, s;
-                rope_wave2(at, r.turns[pair], r.turns[pair + 1], m, c, s);
+                rope_wave2(at, r.turns[pair], r.turns[pair + 1], c, s);
                 float c0, c1, s0, s1;
                 ptx::f2_split(c, c0, c1);
                 ptx::f2_split(s, s0, s1);
@@ -143,10 +137,19 @@ struct RopeTurn {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint64_t c, s;
-                rope_wave2(at, r.turns[8 * lane + 2 * i], r.turns[8 * lane + 2 * i + 1], m, c, s);
+                rope_wave2(at, r.turns[8 * lane + 2 * i], r.turns[8 * lane + 2 * i + 1], c, s);
                 p[i] = p[i + 4] = c;
                 q[i] = kBack ? s : rope_negate(s);
                 q[i + 4] = kBack ? rope_negate(s) : s;
+            }
+        }
+        if (r.factor != 1.f) {
+            const uint64_t m = rope_both(r.factor);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!(i < 4 || !kInter ? turn_a : turn_b)) continue;
+                p[i] = ptx::mul2(p[i], m);
+                q[i] = ptx::mul2(q[i], m);
             }
         }
     }

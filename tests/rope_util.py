@@ -2,7 +2,7 @@
 library's arithmetic keeps.  Nothing here calls the library.
 
 Bounds.  The library computes in fp32 and rounds once to bf16 (half a step: 2^-8 of the value).  Its sines come from an
-angle held to 2^-25 half turns (the fraction of a turn as an fp32 number) and sincospi (2 ulp): 2^-22 each; the two
+angle held to 2^-25 half turns (the fraction of a turn as an fp32 number) and polynomials: 2^-22 each; the two
 products and the sum add three roundings of 2^-24; r = 1 / sqrt(mean x^2 + eps) sums D <= 128 squares in chains of at most
 8 + 3 additions, half of whose relative error counts, and rsqrt (2 ulp): under 2^-21, and two products after it.  In
 all, under 2^-19 of the magnitudes that meet in an element."""
