@@ -92,6 +92,7 @@ template <int D, bool kInter>
 __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
     constexpr int kLanes = D / 16;
     __shared__ uint32_t warp_max[kAppendThreads / 32];
+    __shared__ __align__(16) unsigned long long turns[64];
     extern __shared__ __align__(16) unsigned char smem[];
     ptx::launch_next();
     ptx::wait_previous();
@@ -102,6 +103,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
         rope_forward<D, kInter, true, kAppendThreads>(p.r, p.plan, blockIdx.x - before, p.S, p.in, p.out, AppendPlace{p}, smem);
         return;
     }
+    if (threadIdx.x < 64) turns[threadIdx.x] = p.r.turns[threadIdx.x];
+    __syncthreads();
     const CacheView& c = p.c;
     const int threads = 1 << p.unit_shift, t = threadIdx.x & (threads - 1);
     const int unit = (int)((before << 7 >> p.unit_shift) + (threadIdx.x >> p.unit_shift));
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
             RopeTurn<kInter> turn;
             const bool there = i < count;
             const int at = row0 + (there ? first + i * step : 0);
-            turn.template set<false>(p.r, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
+            turn.template set<false>(p.r, turns, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
             if (i == 0) ptx::cp_async_wait<0>();
             if (there) {
                 rope_unpack(mine.at(i, 0), mine.at(i, 1), x);

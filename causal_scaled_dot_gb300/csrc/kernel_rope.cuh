@@ -94,13 +94,13 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 6) attn_rope_bwd_ker
 #pragma unroll
     for (int i = 0; i < kRopeDepth; ++i) fill(i);
     RopeTurn<kInter> turn;
-    if (!copy) turn.template set<true>(p.r, l, lane, rope_position(p.r, t.b, t.s));
+    if (!copy) turn.template set<true>(p.r, p.r.turns, l, lane, rope_position(p.r, t.b, t.s));
     uint64_t w[8], dw[8];
     if (normed) rope_weights(weight, p.r.weight_f32, l, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[i] = 0;
 #pragma unroll 1
-    for (int i = 0; i < p.plan.per; ++i) {
+    for (int i = 0; i < t.most; ++i) {
         const int slot = i % kRopeDepth;
         ptx::cp_async_wait<kRopeDepth - 1>();
         uint4 a = ring.at(slot, 0), b = ring.at(slot, 1);

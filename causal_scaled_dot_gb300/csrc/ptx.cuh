@@ -499,10 +499,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float x0, float x1, float x2, fl
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// 16 bytes from global to shared memory without registers; bytes = 0 writes zeros and reads nothing.  A thread's copies
-// since its last commit are a group, and it sees them once at most kLeft later groups are under way.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes from global to shared memory without registers; `there` false writes zeros and reads nothing (a predicate: a
+// size in a register took 13 instructions a row more).  A thread's copies since its last commit are a group, and it sees
+// them once at most kLeft later groups are under way.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool there) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\tcp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst), "l"(src),
+                 "r"((uint32_t)there)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>

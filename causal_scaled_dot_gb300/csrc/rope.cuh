@@ -108,9 +108,10 @@ struct RopeTurn {
     uint64_t p[8], q[8];
     bool turn_a, turn_b;
 
-    // Position `at`; kBack: the transposed rotation.
+    // Position `at`; kBack: the transposed rotation.  `turns`: r.turns, or a copy of it where the lanes' reads, which a
+    // constant bank serves one after the other, come more often.
     template <bool kBack>
-    __device__ __forceinline__ void set(const RopeParams& r, const RopeLane& l, int lane, long long at) {
+    __device__ __forceinline__ void set(const RopeParams& r, const unsigned long long* turns, const RopeLane& l, int lane, long long at) {
         turn_a = l.turn_a;
         turn_b = l.turn_b;
 #pragma unroll
@@ -124,7 +125,7 @@ struct RopeTurn {
                 if (!(i < 4 ? turn_a : turn_b)) continue;
                 const int pair = i < 4 ? 4 * l.a + i : 4 * l.b + i - 4;
                 uint64_t c, s;
-                rope_wave2(at, r.turns[pair], r.turns[pair + 1], c, s);
+                rope_wave2(at, turns[pair], turns[pair + 1], c, s);
                 float c0, c1, s0, s1;
                 ptx::f2_split(c, c0, c1);
                 ptx::f2_split(s, s0, s1);
@@ -137,7 +138,7 @@ struct RopeTurn {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint64_t c, s;
-                rope_wave2(at, r.turns[8 * lane + 2 * i], r.turns[8 * lane + 2 * i + 1], c, s);
+                rope_wave2(at, turns[8 * lane + 2 * i], turns[8 * lane + 2 * i + 1], c, s);
                 p[i] = p[i + 4] = c;
                 q[i] = kBack ? s : rope_negate(s);
                 q[i + 4] = kBack ? rope_negate(s) : s;
@@ -228,6 +229,7 @@ __device__ __forceinline__ float rope_norm(uint64_t (&x)[8], float eps, float* d
 struct RopeTask {
     long long b, s;
     int kind, head, end;
+    int most;  // rows of the thread that has most of them, the same for the block
 };
 template <int D>
 __device__ __forceinline__ bool rope_task(const RopePlan& p, unsigned int unit, int S, RopeTask& t) {
@@ -237,6 +239,7 @@ __device__ __forceinline__ bool rope_task(const RopePlan& p, unsigned int unit, 
     t.kind = u.kind;
     t.head = u.chunk * p.groups * p.per + side;
     t.end = min(p.heads[u.kind], (u.chunk + 1) * p.groups * p.per);
+    t.most = (t.end - u.chunk * p.groups * p.per + p.groups - 1) / p.groups;
     const bool there = token < p.total;
     const unsigned int b = there ? token / (unsigned int)S : 0;
     t.b = b;
@@ -253,7 +256,7 @@ struct RopeRing {
     uint32_t base;
     __device__ __forceinline__ explicit RopeRing(void* smem) : base(ptx::smem_addr(smem) + threadIdx.x * 16) {}
     __device__ __forceinline__ void fill(int slot, int vector, const void* src, bool there) const {
-        ptx::cp_async_16(base + (slot * kVectors + vector) * kThreads * 16, src, there ? 16u : 0u);
+        ptx::cp_async_16(base + (slot * kVectors + vector) * kThreads * 16, src, there);
     }
     __device__ __forceinline__ uint4 at(int slot, int vector) const {
         uint4 x;
@@ -315,11 +318,11 @@ __device__ __forceinline__ void rope_forward(const RopeParams& r, const RopePlan
     if (!copy) {
         uint64_t w[8];
         if (normed) rope_weights(weight, r.weight_f32, l, w);
-        turn.template set<false>(r, l, lane, position);
+        turn.template set<false>(r, r.turns, l, lane, position);
         if (normed) turn.weigh(w);
     }
 #pragma unroll 1
-    for (int i = 0; i < plan.per; ++i) {
+    for (int i = 0; i < t.most; ++i) {
         const int slot = i % kRopeDepth;
         ptx::cp_async_wait<kRopeDepth - 1>();
         uint4 a = ring.at(slot, 0), b = ring.at(slot, 1);
