@@ -212,9 +212,10 @@ int launch_append(CacheAppendParams& p, int rows, long long q_units, cudaStream_
     p.unit_shift = 5;
     while (1 << p.unit_shift < kAppendThreads && shares > kAppendItems << p.unit_shift) ++p.unit_shift;
     const int per = kAppendThreads >> p.unit_shift, items = (shares + (1 << p.unit_shift) - 1) >> p.unit_shift;
-    const long long writes = (p.num_units + per - 1) / per, blocks = writes + q_units;
+    const long long writes = ((long long)p.num_units + per - 1) / per, blocks = 2 * writes + q_units;
     if (blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
-    p.write_share = (((unsigned long long)writes << 32) + blocks - 1) / blocks;
+    p.first_v = (unsigned int)(writes + q_units);
+    p.k_share = (((unsigned long long)writes << 32) + p.first_v - 1) / p.first_v;
     return launch(attn_cache_append_kernel<D, kInter>, (int)blocks, kAppendThreads, append_smem(items), true, st, p);
 }
 
@@ -319,8 +320,8 @@ extern "C" int attn_cache_append(const attn_cache_t* cache, const attn_rope_t* r
     // as in attn_cache_write
     const long long touched = ((long long)S + bs - 2) / bs + 1;
     p.blocks_per_seq = (int)(touched < cache->max_blocks ? touched : cache->max_blocks);
-    const long long units = (long long)B * Hkv * 2 * p.blocks_per_seq;
-    if (units > 0x7fffff00ll) return ATTN_ERR_UNSUPPORTED;
+    const long long units = (long long)B * Hkv * p.blocks_per_seq;
+    if (units > 0x3fffff00ll) return ATTN_ERR_UNSUPPORTED;
     p.num_units = (int)units;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rows = S < bs ? S : bs;  // of the largest unit

@@ -21,8 +21,10 @@ struct CacheAppendParams {
     RopeRows in, out;   // q, k, v of the step; q rotated
     const int* new_lens;
     int S;
-    int blocks_per_seq, num_units;
-    unsigned long long write_share;  // ceil(2^32 * writing blocks / blocks)
+    int blocks_per_seq;
+    int num_units;               // of K, and as many of V
+    unsigned int first_v;        // the first of V's blocks
+    unsigned long long k_share;  // ceil(2^32 * blocks of K / blocks of K and q)
     int unit_shift;     // 2^unit_shift threads per unit: 32 .. kAppendThreads
     RopePlan plan;      // of q
 };
@@ -96,20 +98,25 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
     extern __shared__ __align__(16) unsigned char smem[];
     ptx::launch_next();
     ptx::wait_previous();
-    // Blocks that write (much to compute) and blocks of q (much to load) alternate evenly: of the first i blocks
-    // i write_share / 2^32 write.
-    const unsigned int before = (unsigned int)(blockIdx.x * p.write_share >> 32);
-    if ((unsigned int)((blockIdx.x + 1) * p.write_share >> 32) == before) {
-        rope_forward<D, kInter, true, kAppendThreads>(p.r, p.plan, blockIdx.x - before, p.S, p.in, p.out, AppendPlace{p}, smem);
-        return;
+    // Blocks that write K (much to compute) and blocks of q (much to load) alternate evenly: of the first i blocks
+    // i k_share / 2^32 write K.  V's are quick and come last, so the launch ends evenly.
+    const bool is_v = blockIdx.x >= p.first_v;
+    unsigned int index = blockIdx.x - p.first_v;
+    if (!is_v) {
+        index = (unsigned int)(blockIdx.x * p.k_share >> 32);
+        if ((unsigned int)((blockIdx.x + 1) * p.k_share >> 32) == index) {
+            rope_forward<D, kInter, true, kAppendThreads>(p.r, p.plan, blockIdx.x - index, p.S, p.in, p.out, AppendPlace{p}, smem);
+            return;
+        }
     }
     if (threadIdx.x < 64) turns[threadIdx.x] = p.r.turns[threadIdx.x];
     __syncthreads();
     const CacheView& c = p.c;
     const int threads = 1 << p.unit_shift, t = threadIdx.x & (threads - 1);
-    const int unit = (int)((before << 7 >> p.unit_shift) + (threadIdx.x >> p.unit_shift));
+    const int unit = (int)(index * (kAppendThreads >> p.unit_shift) + (threadIdx.x >> p.unit_shift));
     bool active = unit < p.num_units, bad = false;
-    const CacheRwUnit u = cache_rw_unit(active ? unit : 0, p.blocks_per_seq, c.Hkv, 2);
+    CacheRwUnit u = cache_rw_unit(active ? unit : 0, p.blocks_per_seq, c.Hkv, 1);
+    u.is_v = is_v;
     const CacheSpan s = cache_span(c.seq_lens[u.b], p.new_lens ? p.new_lens[u.b] : p.S, c.max_blocks * c.block_size, p.S, &bad);
     const int begin = s.first < 0 ? 0 : s.first;       // first position written
     const int lb = (begin >> c.block_shift) + u.blk;   // this unit's block of the sequence
