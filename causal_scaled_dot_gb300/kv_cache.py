@@ -213,10 +213,11 @@ class KVCache:
         x = self._steps.get(key)
         if x is None:
             x = self._step(key, q, k, v)
-        S, Hq = x[0], x[1]
-        for name, t in (("k", k), ("v", v), ("q", q)):
-            if t is not None and (t.dtype is not _BF16 or t.device != self._device):
-                raise ValueError(f"{name} must be a bf16 tensor on {self._device}")
+        S, Hq, like = x
+        at = self._device
+        if k.dtype is not _BF16 or v.dtype is not _BF16 or k.device != at or v.device != at or (
+                q is not None and (q.dtype is not _BF16 or q.device != at)):
+            raise ValueError(f"k, v and q must be bf16 tensors on {at}")
         if q is None and (q_out is not None or q_norm is not None):
             raise ValueError("q_out and q_norm go with q")
         if q_out is not None:
@@ -227,7 +228,7 @@ class KVCache:
                     raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
         n = None if new_lens is None else self._counts("new_lens", new_lens)
         c = rotary._plan(self._device, B, S, D, positions, first, q_norm, k_norm, eps)
-        heads = native.AttnHeads.from_buffer_copy(x[2])
+        heads = native.AttnHeads.from_buffer_copy(like)
         heads.k, heads.v = k.data_ptr(), v.data_ptr()
         if q is not None:
             heads.q = q.data_ptr()

@@ -30,6 +30,7 @@ _INDEX = {torch.int32: 0, torch.int64: 1}
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
 def _frequencies(rotary_dim: int, base: float) -> list[float]:
@@ -143,18 +144,20 @@ class Rotary:
         that would is refused where that eager graph is of these functions (ValueError); let it go first,
         pass ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
         x = _packed(qkv, q_heads, kv_heads)
+        c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(qkv, q_norm, k_norm):
-            return _functions()[0].apply(qkv, q_norm, k_norm, self, x, positions, first, eps)
-        return self._heads(qkv, x, positions, first, q_norm, k_norm, eps)
+            return _functions()[0].apply(qkv, q_norm, k_norm, positions, self, x, c)
+        return self._heads(qkv, x, c)
 
     def rotate(self, q, k=None, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6):
         """q (and k), bf16 [B, H, S, D] of any strides of 16 bytes with D contiguous, normed and rotated as by
         ``heads``, in new contiguous tensors.  Gradients flow to q, k and the norms' weights."""
         x = _apart(q, k, k_norm)
+        c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(q, k, q_norm, k_norm):
-            out = _functions()[1].apply(q, k, q_norm, k_norm, self, x, positions, first, eps)
+            out = _functions()[1].apply(q, k, q_norm, k_norm, positions, self, x, c)
         else:
-            out = self._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
+            out = self._rotate(q, k, x, c)
         return out if k is not None else out[0]
 
     def heads_backward(self, dq, dk, dv, qkv, q_heads: int, kv_heads: int, positions=None, first: int = 0, q_norm=None,
@@ -164,7 +167,8 @@ class Rotary:
         x = _packed(qkv, q_heads, kv_heads)
         for name, t, shape in (("dq", dq, x.q_shape), ("dk", dk, x.k_shape), ("dv", dv, x.k_shape)):
             _upstream(name, t, shape, qkv.device)
-        return self._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads)
+        c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        return self._heads_backward(dq, dk, dv, qkv, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
 
     def rotate_backward(self, dq, dk, q, k, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6,
                         weight_grads: bool = True):
@@ -176,15 +180,15 @@ class Rotary:
         _upstream("dq", dq, x.q_shape, q.device)
         if k is not None:
             _upstream("dk", dk, x.k_shape, q.device)
-        return self._rotate_backward(dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads)
+        c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        return self._rotate_backward(dq, dk, q, k, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
 
     # ------------------------------------------------------------------ the C calls
-    def _heads(self, qkv, x, positions, first, q_norm, k_norm, eps):
-        c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+    def _heads(self, qkv, x, c):
         index = qkv.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._heads(qkv, x, positions, first, q_norm, k_norm, eps)
+                return self._heads(qkv, x, c)
         q, k, v = qkv.new_empty(x.q_shape), qkv.new_empty(x.k_shape), qkv.new_empty(x.k_shape)
         rc = _lib().attn_rope(c, x.at(qkv), x.dense(q.data_ptr(), k.data_ptr(), v.data_ptr()), x.B, x.Hq, x.Hkv, x.S, x.D,
                               _stream_handle(index))
@@ -192,12 +196,11 @@ class Rotary:
             raise native.AttnError(rc, "attn_rope")
         return q, k, v
 
-    def _rotate(self, q, k, x, positions, first, q_norm, k_norm, eps):
-        c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+    def _rotate(self, q, k, x, c):
         index = q.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
+                return self._rotate(q, k, x, c)
         yq, yk = q.new_empty(x.q_shape), None if k is None else q.new_empty(x.k_shape)
         rc = _lib().attn_rope(c, x.rows(q, k), x.dense(yq.data_ptr(), None if k is None else yk.data_ptr(), None), x.B, x.Hq, x.Hkv, x.S,
                               x.D, _stream_handle(index))
@@ -205,34 +208,33 @@ class Rotary:
             raise native.AttnError(rc, "attn_rope")
         return yq, yk
 
-    def _heads_backward(self, dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads):
+    def _heads_backward(self, dq, dk, dv, qkv, x, c, q_norm, k_norm):
         index = qkv.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, weight_grads)
+                return self._heads_backward(dq, dk, dv, qkv, x, c, q_norm, k_norm)
         dqkv = qkv.new_empty(qkv.shape)
-        return (dqkv, *self._backward(index, (dq, dk, dv), qkv, x, x.at(qkv), x.at_dense(dqkv), positions, first, q_norm, k_norm, eps,
-                                      weight_grads))
+        return (dqkv, *self._backward(index, (dq, dk, dv), qkv, x, x.at(qkv), x.at_dense(dqkv), c, q_norm, k_norm))
 
-    def _rotate_backward(self, dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads):
+    def _rotate_backward(self, dq, dk, q, k, x, c, q_norm, k_norm):
         index = q.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._rotate_backward(dq, dk, q, k, x, positions, first, q_norm, k_norm, eps, weight_grads)
+                return self._rotate_backward(dq, dk, q, k, x, c, q_norm, k_norm)
         out = _like(q), None if k is None else _like(k)
-        return (*out, *self._backward(index, (dq, dk, None), q, x, x.rows(q, k), _heads_of(*out, None), positions, first, q_norm, k_norm,
-                                      eps, weight_grads))
+        return (*out, *self._backward(index, (dq, dk, None), q, x, x.rows(q, k), _heads_of(*out, None), c, q_norm, k_norm))
 
-    def _backward(self, index, up, like, x, rows, out, positions, first, q_norm, k_norm, eps, weight_grads):
-        """Fills `out` from upstream gradients and the forward's rows; returns the weights' gradients."""
-        c = self._plan(like.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+    def _backward(self, index, up, like, x, rows, out, c, q_norm, k_norm):
+        """Fills `out` from upstream gradients and the forward's rows; returns the gradients of the weights given."""
         dwq = dwk = w = None
         need = 0
-        if weight_grads and (q_norm is not None or k_norm is not None):
+        if q_norm is not None or k_norm is not None:
             need = x.need(c)
-            w = torch.empty(need, dtype=torch.uint8, device=like.device)
-            dwq = None if q_norm is None else torch.empty_like(q_norm)
-            dwk = None if k_norm is None else torch.empty_like(k_norm)
+            w = like.new_empty((need + 1) // 2)  # elements of two bytes
+            if q_norm is not None:
+                dwq = torch.empty_like(q_norm)
+            if k_norm is not None:
+                dwk = torch.empty_like(k_norm)
         rc = _lib().attn_rope_bwd(c, x.upstream(*up), rows, out, None if dwq is None else dwq.data_ptr(),
                                   None if dwk is None else dwk.data_ptr(), x.B, x.Hq, x.Hkv, x.S, x.D, None if w is None else w.data_ptr(),
                                   need, _stream_handle(index))
@@ -424,7 +426,7 @@ _live: dict = {}
 def _watch(ctx, leaves, index):
     """Notes an eager call, or refuses a captured one that shares a leaf with an eager graph of another stream."""
     st = _stream_handle(index)
-    if not torch.cuda.is_current_stream_capturing():
+    if not _capturing():
         key = id(ctx)
         _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None)), st
         return
@@ -450,40 +452,48 @@ _FUNCTIONS = None
 
 
 def _make_functions():
-    """torch.autograd.Functions over the calls above."""
+    """torch.autograd.Functions over the calls above.  The plan of a forward call serves its backward: the tensors that it
+    points at are saved beside it."""
     once = torch.autograd.function.once_differentiable
+
+    def heads_backward(ctx, dq, dk, dv):
+        qkv, q_norm, k_norm, _ = ctx.saved_tensors
+        rotary, x, c = ctx.args
+        _, need_q, need_k, *_ = ctx.needs_input_grad
+        got = rotary._heads_backward(dq, dk, dv, qkv, x, c, q_norm if need_q else None, k_norm if need_k else None)
+        return (*got, None, None, None, None)
+
+    def rotate_backward(ctx, dq, dk):
+        q, k, q_norm, k_norm, _ = ctx.saved_tensors
+        rotary, x, c = ctx.args
+        _, _, need_q, need_k, *_ = ctx.needs_input_grad
+        got = rotary._rotate_backward(dq, dk if k is not None else None, q, k, x, c, q_norm if need_q else None, k_norm if need_k else None)
+        return (*got, None, None, None, None)
+
+    heads_once, rotate_once = once(heads_backward), once(rotate_backward)
 
     class HeadsFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, qkv, q_norm, k_norm, rotary, x, positions, first, eps):
+        def forward(ctx, qkv, q_norm, k_norm, positions, rotary, x, c):
             _watch(ctx, (qkv, q_norm, k_norm), qkv.get_device())
             ctx.save_for_backward(qkv, q_norm, k_norm, positions)
-            ctx.args = (rotary, x, first, eps)
-            return rotary._heads(qkv, x, positions, first, q_norm, k_norm, eps)
+            ctx.args = rotary, x, c
+            return rotary._heads(qkv, x, c)
 
         @staticmethod
-        @once
-        def backward(ctx, dq, dk, dv):
-            qkv, q_norm, k_norm, positions = ctx.saved_tensors
-            rotary, x, first, eps = ctx.args
-            got = rotary._heads_backward(dq, dk, dv, qkv, x, positions, first, q_norm, k_norm, eps, any(ctx.needs_input_grad[1:3]))
-            return (*got, None, None, None, None, None)
+        def backward(ctx, *up):  # `once` is for backward passes that are themselves recorded
+            return (heads_once if torch.is_grad_enabled() else heads_backward)(ctx, *up)
 
     class RotateFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, q_norm, k_norm, rotary, x, positions, first, eps):
+        def forward(ctx, q, k, q_norm, k_norm, positions, rotary, x, c):
             _watch(ctx, (q, k, q_norm, k_norm), q.get_device())
             ctx.save_for_backward(q, k, q_norm, k_norm, positions)
-            ctx.args = (rotary, x, first, eps)
-            return rotary._rotate(q, k, x, positions, first, q_norm, k_norm, eps)
+            ctx.args = rotary, x, c
+            return rotary._rotate(q, k, x, c)
 
         @staticmethod
-        @once
-        def backward(ctx, dq, dk):
-            q, k, q_norm, k_norm, positions = ctx.saved_tensors
-            rotary, x, first, eps = ctx.args
-            got = rotary._rotate_backward(dq, dk if k is not None else None, q, k, x, positions, first, q_norm, k_norm, eps,
-                                          any(ctx.needs_input_grad[2:4]))
-            return (*got, None, None, None, None, None)
+        def backward(ctx, *up):
+            return (rotate_once if torch.is_grad_enabled() else rotate_backward)(ctx, *up)
 
     return HeadsFunction, RotateFunction
