@@ -201,10 +201,12 @@ int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
     return launch(kernel, (p.num_units + per - 1) / per, 256, 0, true, st, p);
 }
 
-// q's heads a thread at most, and the units that their number comes down for (rope_plan).
+// q's heads a thread at most, and the units that their number comes down for (rope_plan).  2 x 4096 tokens of 32 + 8 + 8 heads
+// of 128 with norms: 37.4 us with 8, 35.1 with 16 and with 32.
 constexpr int kAppendPer = 16;
 constexpr long long kAppendUnits = 608;
-// Shares of 16 elements that a thread of a unit holds at most, before the unit gets twice the threads.
+// Shares of 16 elements that a thread of a unit holds at most, before the unit gets twice the threads: 2 x 4096 tokens as
+// above 35.2 us with 2, 35.1 with 4, 41.7 with 8.
 constexpr int kAppendItems = 4;
 template <int D, bool kInter>
 int launch_append(CacheAppendParams& p, int rows, long long q_units, cudaStream_t st) {
@@ -215,7 +217,7 @@ int launch_append(CacheAppendParams& p, int rows, long long q_units, cudaStream_
     const long long writes = ((long long)p.num_units + per - 1) / per, blocks = 2 * writes + q_units;
     if (blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     p.first_v = (unsigned int)(writes + q_units);
-    p.k_share = (((unsigned long long)writes << 32) + p.first_v - 1) / p.first_v;
+    p.k_share = append_share((unsigned int)writes, (unsigned int)q_units);
     return launch(attn_cache_append_kernel<D, kInter>, (int)blocks, kAppendThreads, append_smem(items), true, st, p);
 }
 

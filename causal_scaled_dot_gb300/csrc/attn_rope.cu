@@ -17,7 +17,10 @@ namespace {
 
 using host::RowsBox;
 
-// Heads of a thread at most, and units (blocks) that its head count comes down for.
+// Heads of a thread at most: 4 compute the sines twice as often (2 x 4096 tokens of 32 + 8 + 8 heads with norms, forward
+// and backward: 35.3 and 64 us, with 8 32.4 and 52.4, with 16 33.5 and 51.6), 16 leave less to go round (1 x 2048 tokens of 32
+// + 32 + 32: 18.0 and 19.7).  And the units (blocks) that this comes down for: with 304 and 1216 a backward of 3711 tokens of 12 +
+// 4 + 4 heads of 64 takes 10.3 and 12.4 us, with 608 9.1.
 constexpr int kPer = 8;
 constexpr long long kUnits = 608;
 
@@ -221,5 +224,5 @@ extern "C" int attn_rope_bwd(const attn_rope_t* rope, const attn_heads_t* grad, 
     sum.f32 = rope->weight_format == ATTN_WEIGHT_F32;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = dispatch<Backward>(p, D, rope->interleaved != 0, any_weight(rope), st)) != ATTN_OK || need == 0) return rc;
-    return launch(attn_rope_sum_kernel, 2 * D / 16, kRopeSumThreads, 0, true, st, sum);
+    return launch(attn_rope_sum_kernel, 2 * D / kRopeSumColumns, kRopeSumThreads, 0, true, st, sum);
 }

@@ -11,7 +11,8 @@
 namespace attn {
 
 // A row (one head of one token) is held by D / 16 lanes, two vectors of 8 elements each, so that both elements of every
-// pair are in one lane.
+// pair are in one lane.  Blocks of 256 threads leave more of the last wave empty: 1 x 2048 tokens of 32 + 32 + 32 heads with
+// norms 19.7 us, with 128 18.0.
 constexpr int kRopeThreads = 128;
 
 // The vectors of lane `l` and whether they are rotated.  Half layout: rotated lanes hold vector l and the one rot / 2
@@ -80,6 +81,19 @@ ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int t
         for (int i = 0; i < 3; ++i) p.chunks[i] = (p.heads[i] + p.groups * p.per - 1) / (p.groups * p.per);
         if (p.per == 1 || rope_tiles(p) * rope_chunks(p) >= units) return p;
     }
+}
+
+// The first blocks of an append: `ks` that write K among `qs` of q, evenly.  Of the first i of them i share / 2^32 write K.
+ROPE_HD unsigned long long append_share(unsigned int ks, unsigned int qs) {
+    const unsigned long long all = (unsigned long long)ks + qs;
+    return (((unsigned long long)ks << 32) + all - 1) / all;
+}
+// Whether block i is one that writes K, and which of its kind it is.
+ROPE_HD bool append_is_k(unsigned long long share, unsigned int i, unsigned int* index) {
+    const unsigned int before = (unsigned int)(i * share >> 32);
+    const bool k = (unsigned int)((i + 1ull) * share >> 32) != before;
+    *index = k ? before : i - before;
+    return k;
 }
 
 }  // namespace attn

@@ -33,9 +33,9 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
-def _frequencies(rotary_dim: int, base: float) -> list[float]:
-    if rotary_dim % 2 or not base > 0:
-        raise ValueError("rotary_dim must be even and base positive")
+def _frequencies(rotary_dim: int, base: float, stretch: float) -> list[float]:
+    if rotary_dim % 2 or not base > 0 or not stretch > 0:
+        raise ValueError("rotary_dim must be even, base and stretch positive")
     return [base ** (-2 * i / rotary_dim) for i in range(rotary_dim // 2)]
 
 
@@ -68,17 +68,25 @@ class Rotary:
         turns = [_turns(x) for x in f]
         self._c = native.AttnRope((ctypes.c_ulonglong * 64)(*turns), self.rotary_dim, int(self.interleaved), self.factor)
 
+    def __reduce__(self):  # the struct of the C calls is made again
+        return type(self), (self.frequencies, self.interleaved, self.factor)
+
+    def __repr__(self):
+        return f"Rotary({self.rotary_dim} elements, {'neighbouring' if self.interleaved else 'half-way'} pairs, factor {self.factor:g})"
+
     @classmethod
     def from_base(cls, rotary_dim: int, base: float = 10000.0, stretch: float = 1.0, interleaved: bool = False):
         """frequencies[i] = base^(-2i / rotary_dim) / stretch: a stretch of s puts s positions where one was."""
-        return cls([f / stretch for f in _frequencies(rotary_dim, base)], interleaved)
+        return cls([f / stretch for f in _frequencies(rotary_dim, base, stretch)], interleaved)
 
     @classmethod
     def raised_base(cls, rotary_dim: int, stretch: float, base: float = 10000.0, interleaved: bool = False):
         """The base raised so that the slowest pair is stretched by ``stretch`` and the fastest stays."""
         if rotary_dim < 4:
             raise ValueError("rotary_dim must be 4 or more")
-        return cls(_frequencies(rotary_dim, base * stretch ** (rotary_dim / (rotary_dim - 2))), interleaved)
+        if not stretch > 0:
+            raise ValueError("stretch must be positive")
+        return cls(_frequencies(rotary_dim, base * stretch ** (rotary_dim / (rotary_dim - 2)), 1.0), interleaved)
 
     @classmethod
     def by_parts(cls, rotary_dim: int, stretch: float, original_length: float, base: float = 10000.0, slow: float = 1.0,
@@ -90,7 +98,7 @@ class Rotary:
         if not fast > slow:
             raise ValueError("fast must be larger than slow")
         out = []
-        for f in _frequencies(rotary_dim, base):
+        for f in _frequencies(rotary_dim, base, stretch):
             keep = min(max((original_length * f / math.tau - slow) / (fast - slow), 0.0), 1.0)
             out.append(f * (keep + (1 - keep) / stretch))
         return cls(out, interleaved, 0.1 * math.log(stretch) + 1 if factor is None else factor)

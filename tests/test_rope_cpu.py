@@ -220,6 +220,15 @@ PLAN = r"""
 #include <cstdlib>
 using namespace attn;
 int main(int argc, char** argv) {
+    if (argc == 3) {  // blocks of K and of q: which is which
+        const unsigned ks = atoi(argv[1]), qs = atoi(argv[2]);
+        for (unsigned i = 0; i < ks + qs; ++i) {
+            unsigned index;
+            const int k = append_is_k(append_share(ks, qs), i, &index);
+            printf("%d %u\n", k, index);
+        }
+        return 0;
+    }
     if (argc == 4) {  // D rot interleaved: each lane's vectors
         const int D = atoi(argv[1]);
         for (int l = 0; l < D / 16; ++l) {
@@ -293,6 +302,14 @@ def test_units_hold_every_row_once(plan_program, case, threads, per, least):
         assert (seen[:, kind, :H] == 1).all() and (seen[:, kind, H:] == 0).all()
 
 
+@pytest.mark.parametrize("ks,qs", [(1, 0), (7, 0), (1, 1), (1, 1000), (1000, 1), (512, 1024), (1024, 512), (333, 1000), (999, 1001), (40000, 7)])
+def test_an_appends_blocks_are_each_there_once(plan_program, ks, qs):
+    got = plan_program(ks, qs)
+    assert [i for k, i in got if k] == list(range(ks)) and [i for k, i in got if not k] == list(range(qs))
+    done = np.cumsum([k for k, _ in got])
+    assert (np.abs(done - np.arange(1, ks + qs + 1) * ks / (ks + qs)) <= 1 + 1e-6).all()  # evenly
+
+
 # ------------------------------------------------------------------ frequencies
 def test_frequencies():
     assert Rotary.from_base(64).frequencies == tuple(10000.0 ** (-i / 32) for i in range(32))
@@ -307,6 +324,15 @@ def test_frequencies():
     assert Rotary.by_parts(64, 4, 4096, factor=1.0).factor == 1.0
     assert Rotary([]).rotary_dim == 0
     assert Rotary(torch.ones(8)).rotary_dim == 16
+
+
+def test_a_plan_is_copied_and_pickled():
+    """As part of a model that is."""
+    import copy
+    import pickle
+    r = Rotary.by_parts(64, 4, 2048, interleaved=True)
+    for other in (copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert bytes(other._c) == bytes(r._c) and other.frequencies == r.frequencies and repr(other) == repr(r)
 
 
 def test_turns_are_exact():
@@ -326,6 +352,7 @@ def test_turns_are_exact():
     lambda: Rotary([1.0] * 7), lambda: Rotary([1.0] * 3, interleaved=True), lambda: Rotary([1.0] * 72),
     lambda: Rotary([float("nan")] * 8), lambda: Rotary([1.0] * 8, factor=float("inf")), lambda: Rotary.from_base(63),
     lambda: Rotary.from_base(64, base=0.0), lambda: Rotary.raised_base(2, 4.0), lambda: Rotary.by_parts(64, 4, 4096, slow=3, fast=3),
+    lambda: Rotary.from_base(64, stretch=0.0), lambda: Rotary.raised_base(64, -1.0), lambda: Rotary.by_parts(64, -4, 4096),
 ])
 def test_bad_frequencies_are_refused(call):
     with pytest.raises(ValueError):
