@@ -390,3 +390,61 @@ def test_offsets_past_32_bits():
     assert torch.equal(a, b)
     for p, q in zip(far.read(140), near_.read(140)):
         assert torch.equal(p, q)
+
+
+def test_two_streams_at_once():
+    """Appends to two caches that run side by side."""
+    D, Hq, Hkv = 64, 4, 2
+    r, w = Rotary.from_base(D), [t.cuda() for t in weights(D, torch.float32)]
+    sets = []
+    for i in range(2):
+        c, _ = make(3, Hkv, D, 32, 400, seed=i)
+        ref, _ = make(3, Hkv, D, 32, 400, seed=i)
+        for x in (c, ref):
+            set_lens(x, [300, 17, 211])
+        sets.append((c, ref, projected(3, 211, Hq, Hkv, D, 40 + i), ints([211, 17, 100])))
+    call = lambda c, x, n: c.append(x[1], x[2], r, q=x[0], new_lens=n, q_norm=w[0], k_norm=w[1])  # noqa: E731
+    # rows past a sequence's own are left unspecified in a new tensor: compare those that are there
+    want = [call(ref, x, n) for _, ref, x, n in sets]
+    torch.cuda.synchronize()
+    got, streams = [None, None], [torch.cuda.Stream() for _ in sets]
+    for _ in range(10):
+        for i, (c, _, x, n) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i] = call(c, x, n)
+    torch.cuda.synchronize()
+    for i, (c, ref, _, n) in enumerate(sets):
+        for b, m in enumerate(n.tolist()):
+            assert torch.equal(got[i][b, :, :m], want[i][b, :, :m])
+        assert torch.equal(c.k.view(torch.uint8), ref.k.view(torch.uint8)) and torch.equal(c.v.view(torch.uint8), ref.v.view(torch.uint8))
+
+
+def test_the_same_tokens_again():
+    """An append that is made twice leaves what the first one left."""
+    D = 64
+    c, table = make(2, 2, D, 16, 100, seed=3)
+    r = Rotary.from_base(D)
+    e = Expected(c)
+    e.append(table, [40, 21], [40, 21], *projected(2, 40, 2, 2, D, 1), r, None, None)
+    x = projected(2, 30, 2, 2, D, 2)
+    set_lens(c, [70, 51])
+    c.append(x[1], x[2], r)
+    once = [t.clone() for t in (c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale.nan_to_num(-1), c.v_scale.nan_to_num(-1))]
+    c.append(x[1], x[2], r, check_status=True)
+    for a, b in zip((c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale.nan_to_num(-1), c.v_scale.nan_to_num(-1)), once):
+        assert torch.equal(a, b)
+
+
+def test_gradients_are_refused_and_no_grad_is_taken():
+    D = 64
+    c, _ = make(1, 1, D, 16, 32, seed=3)
+    c.seq_lens.fill_(3)
+    q, k, v = projected(1, 3, 1, 1, D, 1)
+    w = torch.ones(D, device="cuda", requires_grad=True)
+    r = Rotary.from_base(D)
+    with pytest.raises(ValueError, match="gradient"):
+        c.append(k.requires_grad_() if k.is_leaf else k.detach().requires_grad_(), v, r)
+    with pytest.raises(ValueError, match="k_norm"):
+        c.append(k.detach(), v, r, k_norm=w)
+    with torch.no_grad():
+        c.append(k, v, r, k_norm=w, check_status=True)

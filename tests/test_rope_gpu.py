@@ -564,3 +564,83 @@ def test_offsets_past_32_bits():
 def test_many_tokens_of_one_head():
     """More rows than one wave of blocks holds, odd counts."""
     check_heads(Rotary.from_base(64), 7, 1771, 1, 1, 64, torch.float32)
+
+
+def test_rows_past_32_bits_of_elements():
+    """More than 2^31 elements in the input, the outputs and the gradient: rows at both ends and in the middle."""
+    B, S, Hq, Hkv, D = 1, 270_001, 64, 1, 128
+    r, w = Rotary.from_base(D), [t.cuda() for t in weights(D, torch.float32)]
+    at = [0, 1, 131_072, 262_143, 262_145, S - 1]
+    few = rows((1, len(at), (Hq + 2 * Hkv) * D), 5).cuda()
+    x = torch.zeros((B, S, (Hq + 2 * Hkv) * D), dtype=torch.bfloat16, device="cuda")
+    x[:, at] = few
+    positions = torch.tensor(at, device="cuda")
+    got, want = r.heads(x, Hq, Hkv, q_norm=w[0], k_norm=w[1]), r.heads(few, Hq, Hkv, positions=positions, q_norm=w[0], k_norm=w[1])
+    for a, b in zip(got, want):
+        assert torch.equal(a[:, :, at], b)
+    up = [torch.zeros_like(t) for t in got]
+    few_up = [rows(t.shape, 6 + i).cuda() for i, t in enumerate(want)]
+    for t, u in zip(up, few_up):
+        t[:, :, at] = u
+    dx, dwq, dwk = r.heads_backward(*up, x, Hq, Hkv, q_norm=w[0], k_norm=w[1])
+    want = r.heads_backward(*few_up, few, Hq, Hkv, positions=positions, q_norm=w[0], k_norm=w[1])
+    assert torch.equal(dx[:, at], want[0]) and not dx[:, 2:1000].any()
+    for a, b in zip((dwq, dwk), want[1:]):  # the same terms in another order
+        assert float((a - b).abs().max()) <= 2.0 ** -17 * float(b.abs().max()) * len(at) * Hq
+
+
+def test_two_threads_at_once():
+    """Calls of one plan from two threads, each on a stream of its own."""
+    import threading
+    r = Rotary.by_parts(64, 4, 128)
+    w = [t.cuda() for t in weights(64, torch.bfloat16)]
+    xs = [rows((2, 64 + 3 * i, 6 * 64), 80 + i).cuda() for i in range(2)]
+    call = lambda x: (*r.heads(x, 2, 2, q_norm=w[0], k_norm=w[1]), *r.heads_backward(*r.heads(x, 2, 2), x, 2, 2, q_norm=w[0], k_norm=w[1]))  # noqa: E731
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(100):
+                if not all(torch.equal(a, b) for a, b in zip(call(xs[i]), want[i])):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+
+
+def test_rotate_backward_without_weight_gradients():
+    r, w = Rotary.from_base(64), [t.cuda() for t in weights(64, torch.float32)]
+    q, k = rows((2, 3, 20, 64), 1).cuda(), rows((2, 1, 20, 64), 2).cuda()
+    dq, dk = rows(q.shape, 3).cuda(), rows(k.shape, 4).cuda()
+    full = r.rotate_backward(dq, dk, q, k, q_norm=w[0], k_norm=w[1])
+    bare = r.rotate_backward(dq, dk, q, k, q_norm=w[0], k_norm=w[1], weight_grads=False)
+    assert torch.equal(full[0], bare[0]) and torch.equal(full[1], bare[1]) and bare[2] is None and bare[3] is None
+
+
+def test_frozen_weights_under_autograd():
+    """A norm's weight that needs no gradient gets none, the other does."""
+    r, x = Rotary.from_base(64), rows((1, 30, 4 * 64), 2).cuda().requires_grad_()
+    w = [t.cuda() for t in weights(64, torch.float32)]
+    w[1].requires_grad_()
+    out = r.heads(x, 2, 1, q_norm=w[0], k_norm=w[1])
+    up = [rows(t.shape, 5).cuda() for t in out]
+    dx, dwk = torch.autograd.grad(out, (x, w[1]), up)
+    want = r.heads_backward(*up, x.detach(), 2, 1, q_norm=w[0], k_norm=w[1].detach())
+    assert torch.equal(dx, want[0]) and torch.equal(dwk, want[2]) and w[0].grad is None
+
+
+def test_inputs_changed_before_the_backward_are_noticed():
+    r, x = Rotary.from_base(64), rows((1, 30, 4 * 64), 2).cuda()
+    w = weights(64, torch.float32)[0].cuda().requires_grad_()
+    at = torch.arange(30, device="cuda")
+    q = r.heads(x, 2, 1, positions=at, q_norm=w)[0]
+    at.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        q.float().sum().backward()
