@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 6) attn_rope_bwd_ker
     const void* weight = copy ? nullptr : p.r.weight[kind];
     const bool normed = kNorm && weight;
     const auto at = [&](const RopeRows& x) {
-        return reinterpret_cast<uint4*>(x.p[kind] + t.b * x.stride[kind][0] + t.s * x.stride[kind][2] + t.head * x.stride[kind][1]);
+        return reinterpret_cast<uint4*>(x.p[kind] + t.b * x.stride[kind][0] + t.s * x.stride[kind][2] + (unsigned int)t.head * x.stride[kind][1]);
     };
     const uint4 *up = at(p.up), *in = normed ? at(p.in) : nullptr;
     uint4* out = p.out.p[kind] ? at(p.out) : nullptr;
     const long long up_step = p.plan.groups * p.up.stride[kind][1] / 8, in_step = p.plan.groups * p.in.stride[kind][1] / 8,
                     out_step = p.plan.groups * p.out.stride[kind][1] / 8;
-    const int rows = there && t.head < t.end ? (t.end - t.head + p.plan.groups - 1) / p.plan.groups : 0;  // of this thread
+    const int rows = there && t.head < t.end ? (t.end - t.head + p.plan.groups - 1) >> p.plan.group_shift : 0;  // of this thread
     const RopeRing<kNorm ? 4 : 2, kRopeDepth, kRopeThreads> ring(smem);
     int next = 0;  // the row whose copies leave next
     const auto fill = [&](int slot) {

@@ -227,23 +227,23 @@ __device__ __forceinline__ float rope_norm(uint64_t (&x)[8], float eps, float* d
 
 // The rows of a unit that one lane group takes: its token, and heads first, first + groups ... below `end`.
 struct RopeTask {
-    long long b, s;
+    unsigned int b, s;
     int kind, head, end;
     int most;  // rows of the thread that has most of them, the same for the block
 };
 template <int D>
 __device__ __forceinline__ bool rope_task(const RopePlan& p, unsigned int unit, int S, RopeTask& t) {
     const RopeUnit u = rope_unit(p, unit);
-    const int row = threadIdx.x / (D / 16), side = p.tokens == 1 ? row : row / p.tokens;
-    const unsigned int token = u.tile * p.tokens + (row - side * p.tokens);
+    const int row = threadIdx.x / (D / 16), side = row >> p.token_shift;
+    const unsigned int token = (u.tile << p.token_shift) + (row & (p.tokens - 1));
     t.kind = u.kind;
-    t.head = u.chunk * p.groups * p.per + side;
-    t.end = min(p.heads[u.kind], (u.chunk + 1) * p.groups * p.per);
-    t.most = (t.end - u.chunk * p.groups * p.per + p.groups - 1) / p.groups;
+    const int most = p.per << p.group_shift, begin = u.chunk * most;
+    t.head = begin + side;
+    t.end = min(p.heads[u.kind], begin + most);
+    t.most = (t.end - begin + p.groups - 1) >> p.group_shift;
     const bool there = token < p.total;
-    const unsigned int b = there ? token / (unsigned int)S : 0;
-    t.b = b;
-    t.s = there ? token - b * (unsigned int)S : 0;
+    t.b = there ? token / (unsigned int)S : 0;
+    t.s = there ? token - t.b * (unsigned int)S : 0;
     return there;
 }
 
@@ -297,10 +297,10 @@ __device__ __forceinline__ void rope_forward(const RopeParams& r, const RopePlan
     long long position;
     there = place(t.b, t.s, &position) && there;
     const __nv_bfloat16* base = from.p[kind] + t.b * from.stride[kind][0] + t.s * from.stride[kind][2];
-    const uint4* in = reinterpret_cast<const uint4*>(base + t.head * from.stride[kind][1]);
-    uint4* out = reinterpret_cast<uint4*>(to.p[kind] + t.b * to.stride[kind][0] + t.s * to.stride[kind][2] + t.head * to.stride[kind][1]);
+    const uint4* in = reinterpret_cast<const uint4*>(base + (unsigned int)t.head * from.stride[kind][1]);
+    uint4* out = reinterpret_cast<uint4*>(to.p[kind] + t.b * to.stride[kind][0] + t.s * to.stride[kind][2] + (unsigned int)t.head * to.stride[kind][1]);
     const long long in_step = plan.groups * from.stride[kind][1] / 8, out_step = plan.groups * to.stride[kind][1] / 8;
-    const int rows = there && t.head < t.end ? (t.end - t.head + plan.groups - 1) / plan.groups : 0;  // of this thread
+    const int rows = there && t.head < t.end ? (t.end - t.head + plan.groups - 1) >> plan.group_shift : 0;  // of this thread
     int next = 0;  // the row whose copy leaves next
     const auto fill = [&](int slot) {
         const bool mine = next < rows;

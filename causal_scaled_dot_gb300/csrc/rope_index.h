@@ -43,7 +43,8 @@ ROPE_HD RopeLane rope_lane(int l, int D, int rot, int interleaved) {
 // groups of heads one after the other, all of one kind (q, k or v).  The units of a tile of tokens stand side by side.
 struct RopePlan {
     unsigned int total;  // tokens, B * S < 2^31
-    int tokens, groups;  // tokens and heads side by side
+    int tokens, groups;  // tokens and heads side by side, powers of two
+    int token_shift, group_shift;
     int per;             // heads of a thread, at most
     int heads[3];        // of q, k and v; 0: absent
     int chunks[3];       // units of each kind in a tile of tokens
@@ -72,8 +73,14 @@ ROPE_HD RopePlan rope_plan(long long total, int Hq, int Hk, int Hv, int D, int t
     const int rows = threads / (D / 16);
     p.total = (unsigned int)total;
     p.tokens = 1;
-    while (p.tokens < rows && p.tokens < total) p.tokens *= 2;
+    p.token_shift = 0;
+    while (p.tokens < rows && p.tokens < total) {
+        p.tokens *= 2;
+        ++p.token_shift;
+    }
     p.groups = rows / p.tokens;
+    p.group_shift = 0;
+    while (1 << p.group_shift < p.groups) ++p.group_shift;
     p.heads[0] = Hq;
     p.heads[1] = Hk;
     p.heads[2] = Hv;
