@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
     const int lane = t % kLanes, kind = u.is_v ? 2 : 1;
     const RopeLane l = rope_lane(lane, D, p.r.rot, kInter);
     const long long stride = p.in.stride[kind][2];
-    const __nv_bfloat16* src = p.in.p[kind] + u.b * p.in.stride[kind][0] + u.h * p.in.stride[kind][1] + (row0 + t / kLanes) * stride;
+    const __nv_bfloat16* src = p.in.p[kind] + (unsigned int)u.b * p.in.stride[kind][0] + (unsigned int)u.h * p.in.stride[kind][1] +
+                               (unsigned int)(active ? row0 + t / kLanes : 0) * stride;
     // The shares of this thread: rows first, first + step ...
     const int first = t / kLanes, step_shift = p.unit_shift - (D == 128 ? 3 : 2), step = 1 << step_shift;
     const int count = active ? (rows - first + step - 1) >> step_shift : 0;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
         src += stride << step_shift;
     }
     ptx::cp_async_commit();
-    const int entry = active ? c.block_table[(long long)u.b * c.max_blocks + lb] : 0;
+    const int entry = active ? c.block_table[(unsigned int)u.b * (unsigned long long)(unsigned int)c.max_blocks + (unsigned int)lb] : 0;
     const int block = active ? cache_block(entry, c.num_blocks, &bad) : -1;
     active = block >= 0;
     if (bad && t == 0) atomicOr(c.status, kStatusBadCache);
