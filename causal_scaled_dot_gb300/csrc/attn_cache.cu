@@ -19,7 +19,6 @@
 #include "kernel_cache_wide.cuh"
 #include "launch.h"
 #include "rope_check.h"
-#include "rows.h"
 
 namespace attn {
 namespace {

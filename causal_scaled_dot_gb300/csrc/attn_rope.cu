@@ -51,7 +51,7 @@ int rows_of(const attn_heads_t* x, int kind, int B, int H, int S, int D, RowsBox
         if (box->n[i] == 1) continue;
         if (st[i] < 0) return ATTN_ERR_INVALID_ARG;
         if (st[i] % 8) return ATTN_ERR_MISALIGNED;
-        if (st[i] > (1ll << 40)) return ATTN_ERR_UNSUPPORTED;
+        if (st[i] > (1ll << 46) / (box->n[i] - 1)) return ATTN_ERR_UNSUPPORTED;  // 2^47 bytes from the first to the last
         box->stride[i] = st[i];
     }
     return ATTN_OK;

@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ptx_stream.cuh"
 #include "rope.cuh"
 #include "rope_index.h"
 
@@ -141,30 +142,32 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 6) attn_rope_bwd_ker
         fill(slot);  // once the slot's values are out of it
     }
     ptx::cp_async_wait<0>();
-    if (!kNorm || !normed || !p.part[kind]) return;
-    // The block's rows, in a fixed order: within a warp, then over the warps.
-    float sums[16];
+    if constexpr (kNorm) {
+        if (!normed || !p.part[kind]) return;
+        // The block's rows, in a fixed order: within a warp, then over the warps.
+        float sums[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ptx::f2_split(dw[i], sums[2 * i], sums[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) ptx::f2_split(dw[i], sums[2 * i], sums[2 * i + 1]);
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 16; ++j)
 #pragma unroll
-        for (int i = kLanes; i < 32; i *= 2) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], i);
-    if (threadIdx.x % 32 < kLanes) {
-        float* to = part + threadIdx.x / 32 * D;
+            for (int i = kLanes; i < 32; i *= 2) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], i);
+        if (threadIdx.x % 32 < kLanes) {
+            float* to = part + threadIdx.x / 32 * D;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            to[8 * l.a + j] = sums[j];
-            to[8 * l.b + j] = sums[8 + j];
+            for (int j = 0; j < 8; ++j) {
+                to[8 * l.a + j] = sums[j];
+                to[8 * l.b + j] = sums[8 + j];
+            }
         }
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float sum = 0.f;
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum += part[i * D + threadIdx.x];
-        const RopeUnit u = rope_unit(p.plan, blockIdx.x);
-        p.part[kind][((long long)u.tile * p.plan.chunks[kind] + u.chunk) * D + threadIdx.x] = sum;
+            for (int i = 0; i < kWarps; ++i) sum += part[i * D + threadIdx.x];
+            const RopeUnit u = rope_unit(p.plan, blockIdx.x);
+            p.part[kind][((long long)u.tile * p.plan.chunks[kind] + u.chunk) * D + threadIdx.x] = sum;
+        }
     }
 }
 

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ptx_stream.cuh"
 
 namespace attn {
 namespace ptx {

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ptx_stream.cuh"
 #include "rope_index.h"
 
 namespace attn {

@@ -106,7 +106,8 @@ def test_null_rope_is_refused(call):
     (dict(x=dense(), y=dense()), ATTN_ERR_INVALID_ARG),
     (dict(x=packed(T + 8)), ATTN_ERR_MISALIGNED), (dict(y=dense(2 * T + 2, 3 * T, 4 * T)), ATTN_ERR_MISALIGNED),
     (dict(x=packed(T, W=1028)), ATTN_ERR_MISALIGNED), (dict(x=dense(T, 6 * T, 7 * T, q_strides=(-8, 0, 0))), ATTN_ERR_INVALID_ARG),
-    (dict(x=dense(T, 6 * T, 7 * T, v_strides=(1 << 41, 0, 0))), ATTN_ERR_UNSUPPORTED),
+    (dict(x=dense(T, 6 * T, 7 * T, v_strides=(1 << 47, 0, 0))), ATTN_ERR_UNSUPPORTED),
+    (dict(x=dense(T, 6 * T, 7 * T, k_strides=(0, 0, 1 << 45))), ATTN_ERR_UNSUPPORTED),  # ten tokens
     (dict(y=dense(2 * T, 2 * T, 4 * T)), ATTN_ERR_INVALID_ARG),               # outputs share
     (dict(y=dense(T, 3 * T, 4 * T)), ATTN_ERR_INVALID_ARG),                   # over the input, of another layout
     (dict(y=dense(2 * T, 3 * T, T - 1024)), ATTN_ERR_INVALID_ARG),
