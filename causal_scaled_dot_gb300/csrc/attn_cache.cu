@@ -201,9 +201,10 @@ int launch_rw(K kernel, int threads, const P& p, cudaStream_t st) {
 }
 
 // q's heads a thread at most, and the units that their number comes down for (rope_plan).  2 x 4096 tokens of 32 + 8 + 8 heads
-// of 128 with norms: 37.4 us with 8, 35.1 with 16 and with 32.
+// of 128 with norms: 37.4 us with 8, 35.1 with 16 and with 32.  8 x 64 tokens of them 7.3 us with 152 units, 6.7 with 304, 8.7 with
+// 608; 256 single tokens 6.1, 6.9 and 6.9.
 constexpr int kAppendPer = 16;
-constexpr long long kAppendUnits = 608;
+constexpr long long kAppendUnits = 304;
 // Shares of 16 elements that a thread of a unit holds at most, before the unit gets twice the threads: 2 x 4096 tokens as
 // above 35.2 us with 2, 35.1 with 4, 41.7 with 8.
 constexpr int kAppendItems = 4;

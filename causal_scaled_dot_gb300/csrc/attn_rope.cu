@@ -19,10 +19,12 @@ using host::RowsBox;
 
 // Heads of a thread at most: 4 compute the sines twice as often (2 x 4096 tokens of 32 + 8 + 8 heads with norms, forward
 // and backward: 35.3 and 64 us, with 8 32.4 and 52.4, with 16 33.5 and 51.6), 16 leave less to go round (1 x 2048 tokens of 32
-// + 32 + 32: 18.0 and 19.7).  And the units (blocks) that this comes down for: with 304 and 1216 a backward of 3711 tokens of 12 +
-// 4 + 4 heads of 64 takes 10.3 and 12.4 us, with 608 9.1.
+// + 32 + 32: 18.0 and 19.7).
+// And the units (blocks) that this comes down for, forward / backward with norms: 300 tokens of 32 + 8 + 8 heads of 128 take 5.1
+// / 8.4 us with 152, 4.4 / 7.6 with 304, 5.3 / 9.5 with 608; 3 x 1237 of 12 + 4 + 4 heads of 64 6.5 / 10.9, 6.5 / 10.9 and 5.8 /
+// 10.9.
 constexpr int kPer = 8;
-constexpr long long kUnits = 608;
+constexpr long long kUnits = 304;
 
 int check_sizes(int B, int Hq, int Hkv, int S, int D) {
     if (B < 1 || Hq < 1 || Hkv < 1 || S < 1) return ATTN_ERR_INVALID_ARG;

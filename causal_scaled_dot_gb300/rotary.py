@@ -154,7 +154,7 @@ class Rotary:
         x = _packed(qkv, q_heads, kv_heads)
         c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(qkv, q_norm, k_norm):
-            return _functions()[0].apply(qkv, q_norm, k_norm, positions, self, x, c)
+            return _functions()[0].apply(qkv, q_norm, k_norm, positions, self, x, c, (q_heads, kv_heads, first, eps))
         return self._heads(qkv, x, c)
 
     def rotate(self, q, k=None, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6):
@@ -163,7 +163,7 @@ class Rotary:
         x = _apart(q, k, k_norm)
         c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(q, k, q_norm, k_norm):
-            out = _functions()[1].apply(q, k, q_norm, k_norm, positions, self, x, c)
+            out = _functions()[1].apply(q, k, q_norm, k_norm, positions, self, x, c, (first, eps))
         else:
             out = self._rotate(q, k, x, c)
         return out if k is not None else out[0]
@@ -176,7 +176,8 @@ class Rotary:
         for name, t, shape in (("dq", dq, x.q_shape), ("dk", dk, x.k_shape), ("dv", dv, x.k_shape)):
             _upstream(name, t, shape, qkv.device)
         c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
-        return self._heads_backward(dq, dk, dv, qkv, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
+        rows = None if q_norm is None and k_norm is None else x.at(qkv)
+        return self._heads_backward(dq, dk, dv, rows, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
 
     def rotate_backward(self, dq, dk, q, k, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6,
                         weight_grads: bool = True):
@@ -189,7 +190,8 @@ class Rotary:
         if k is not None:
             _upstream("dk", dk, x.k_shape, q.device)
         c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
-        return self._rotate_backward(dq, dk, q, k, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
+        rows = None if q_norm is None and k_norm is None else x.rows(q, k)
+        return self._rotate_backward(dq, dk, rows, x, c, *((q_norm, k_norm) if weight_grads else (None, None)))
 
     # ------------------------------------------------------------------ the C calls
     def _heads(self, qkv, x, c):
@@ -216,29 +218,31 @@ class Rotary:
             raise native.AttnError(rc, "attn_rope")
         return yq, yk
 
-    def _heads_backward(self, dq, dk, dv, qkv, x, c, q_norm, k_norm):
-        index = qkv.get_device()
+    # `rows`: the forward's, where they have norms; None without any.
+    def _heads_backward(self, dq, dk, dv, rows, x, c, q_norm, k_norm):
+        index = dq.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._heads_backward(dq, dk, dv, qkv, x, c, q_norm, k_norm)
-        dqkv = qkv.new_empty(qkv.shape)
-        return (dqkv, *self._backward(index, (dq, dk, dv), qkv, x, x.at(qkv), x.at_dense(dqkv), c, q_norm, k_norm))
+                return self._heads_backward(dq, dk, dv, rows, x, c, q_norm, k_norm)
+        dqkv = dq.new_empty(x.qkv_shape)
+        return (dqkv, *self._backward(index, (dq, dk, dv), x, rows, x.at_dense(dqkv), c, q_norm, k_norm))
 
-    def _rotate_backward(self, dq, dk, q, k, x, c, q_norm, k_norm):
-        index = q.get_device()
+    def _rotate_backward(self, dq, dk, rows, x, c, q_norm, k_norm):
+        index = dq.get_device()
         if _current_device() != index:
             with torch.cuda.device(index):
-                return self._rotate_backward(dq, dk, q, k, x, c, q_norm, k_norm)
-        out = _like(q), None if k is None else _like(k)
-        return (*out, *self._backward(index, (dq, dk, None), q, x, x.rows(q, k), _heads_of(*out, None), c, q_norm, k_norm))
+                return self._rotate_backward(dq, dk, rows, x, c, q_norm, k_norm)
+        sq, sk = x.grad_strides()
+        out = dq.new_empty_strided(x.q_shape, sq), None if dk is None else dq.new_empty_strided(x.k_shape, sk)
+        return (*out, *self._backward(index, (dq, dk, None), x, rows, _heads_of(*out, None), c, q_norm, k_norm))
 
-    def _backward(self, index, up, like, x, rows, out, c, q_norm, k_norm):
+    def _backward(self, index, up, x, rows, out, c, q_norm, k_norm):
         """Fills `out` from upstream gradients and the forward's rows; returns the gradients of the weights given."""
         dwq = dwk = w = None
         need = 0
         if q_norm is not None or k_norm is not None:
             need = x.need(c)
-            w = like.new_empty((need + 1) // 2)  # elements of two bytes
+            w = up[0].new_empty((need + 1) // 2)  # elements of two bytes
             if q_norm is not None:
                 dwq = torch.empty_like(q_norm)
             if k_norm is not None:
@@ -282,7 +286,8 @@ class _Sizes:
 
     def __init__(self, B, S, Hq, Hkv, D, strides):
         self.B, self.S, self.Hq, self.Hkv, self.D = B, S, Hq, Hkv, D
-        self.q_shape, self.k_shape = (B, Hq, S, D), (B, Hkv, S, D)
+        self.q_shape, self.k_shape, self.qkv_shape = (B, Hq, S, D), (B, Hkv, S, D), (B, S, (Hq + 2 * Hkv) * D)
+        self._strides, self._grad_strides = strides, None
         self._in = native.AttnHeads(None, None, None, *(_STRIDES(*st) for st in strides))
         self._dense = native.AttnHeads(None, None, None, *(_STRIDES(H * S * D, S * D, D) for H in (Hq, Hkv, Hkv)))
         W = (Hq + 2 * Hkv) * D
@@ -315,6 +320,15 @@ class _Sizes:
         c = native.AttnHeads.from_buffer_copy(self._dense)
         c.q, c.k, c.v = q, k, v
         return c
+
+    def grad_strides(self):
+        """Strides of new tensors with the order of q's and k's dimensions in memory, D contiguous."""
+        if self._grad_strides is None:
+            def like(shape, stride):
+                y = torch.empty_like(torch.empty_strided(shape, (*stride, 1), device="meta"))
+                return y.stride() if y.stride(3) == 1 else torch.empty(shape, device="meta").stride()
+            self._grad_strides = like(self.q_shape, self._strides[0]), like(self.k_shape, self._strides[1])
+        return self._grad_strides
 
     def upstream(self, dq, dk, dv):
         """attn_heads_t of upstream gradients, made dense where their strides or addresses do not fit (`held` keeps
@@ -402,7 +416,7 @@ def _apart(q, k, k_norm):
 
 
 def _upstream(name, t, shape, device):
-    if t.device != device or t.dtype is not _BF16 or t.shape != shape:
+    if t is None or t.device != device or t.dtype is not _BF16 or t.shape != shape:
         raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on {device}")
 
 
@@ -412,12 +426,6 @@ def _aligned(t):
         return t
     t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
-
-
-def _like(x):
-    """A new tensor with x's order of dimensions in memory, D contiguous."""
-    y = torch.empty_like(x)
-    return y if y.stride(3) == 1 else x.new_empty(x.shape)
 
 
 def _heads_of(q, k, v):
@@ -460,32 +468,40 @@ _FUNCTIONS = None
 
 
 def _make_functions():
-    """torch.autograd.Functions over the calls above.  The plan of a forward call serves its backward: the tensors that it
-    points at are saved beside it."""
+    """torch.autograd.Functions over the calls above.  What is saved is q and k, or qkv, only where they have norms; a
+    backward takes sizes, strides and addresses from what it gets back, which hooks may have moved."""
     once = torch.autograd.function.once_differentiable
 
     def heads_backward(ctx, dq, dk, dv):
-        qkv, q_norm, k_norm, _ = ctx.saved_tensors
-        rotary, x, c = ctx.args
+        qkv, q_norm, k_norm, positions = ctx.saved_tensors
+        rotary, x, (Hq, Hkv, first, eps) = ctx.args
         _, need_q, need_k, *_ = ctx.needs_input_grad
-        got = rotary._heads_backward(dq, dk, dv, qkv, x, c, q_norm if need_q else None, k_norm if need_k else None)
-        return (*got, None, None, None, None)
+        rows = None
+        if qkv is not None:
+            x = _packed(qkv, Hq, Hkv)
+            rows = x.at(qkv)
+        c = rotary._plan(dq.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        got = rotary._heads_backward(dq, dk, dv, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
+        return (*got, None, None, None, None, None)
 
     def rotate_backward(ctx, dq, dk):
-        q, k, q_norm, k_norm, _ = ctx.saved_tensors
-        rotary, x, c = ctx.args
+        q, k, q_norm, k_norm, positions = ctx.saved_tensors
+        rotary, x, (first, eps), has_k = ctx.args
         _, _, need_q, need_k, *_ = ctx.needs_input_grad
-        got = rotary._rotate_backward(dq, dk if k is not None else None, q, k, x, c, q_norm if need_q else None, k_norm if need_k else None)
-        return (*got, None, None, None, None)
+        rows = None if q is None else _apart(q, k, k_norm).rows(q, k)
+        c = rotary._plan(dq.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
+        got = rotary._rotate_backward(dq, dk if has_k else None, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
+        return (*got, None, None, None, None, None)
 
     heads_once, rotate_once = once(heads_backward), once(rotate_backward)
 
     class HeadsFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, qkv, q_norm, k_norm, positions, rotary, x, c):
+        def forward(ctx, qkv, q_norm, k_norm, positions, rotary, x, c, args):
             _watch(ctx, (qkv, q_norm, k_norm), qkv.get_device())
-            ctx.save_for_backward(qkv, q_norm, k_norm, positions)
-            ctx.args = rotary, x, c
+            normed = q_norm is not None or k_norm is not None
+            ctx.save_for_backward(qkv if normed else None, q_norm, k_norm, positions)
+            ctx.args = rotary, x, args
             return rotary._heads(qkv, x, c)
 
         @staticmethod
@@ -494,10 +510,11 @@ def _make_functions():
 
     class RotateFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, q_norm, k_norm, positions, rotary, x, c):
+        def forward(ctx, q, k, q_norm, k_norm, positions, rotary, x, c, args):
             _watch(ctx, (q, k, q_norm, k_norm), q.get_device())
-            ctx.save_for_backward(q, k, q_norm, k_norm, positions)
-            ctx.args = rotary, x, c
+            normed = q_norm is not None or k_norm is not None
+            ctx.save_for_backward(*((q, k) if normed else (None, None)), q_norm, k_norm, positions)
+            ctx.args = rotary, x, args, k is not None
             return rotary._rotate(q, k, x, c)
 
         @staticmethod

@@ -431,6 +431,8 @@ def test_rows_are_checked():
         r.rotate_backward(Fake((2, 4, 6, 64)), None, q, None)
     with pytest.raises(ValueError, match="together"):
         r.rotate_backward(q, q, q, None)
+    with pytest.raises(ValueError, match="dk"):
+        r.heads_backward(Fake((2, 2, 5, 64)), None, Fake((2, 1, 5, 64)), Fake((2, 5, 4 * 64)), 2, 1)
     with pytest.raises(ValueError, match="dv"):
         r.heads_backward(Fake((2, 2, 5, 64)), Fake((2, 1, 5, 64)), Fake((2, 2, 5, 64)), Fake((2, 5, 4 * 64)), 2, 1)
 

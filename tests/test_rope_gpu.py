@@ -644,3 +644,38 @@ def test_inputs_changed_before_the_backward_are_noticed():
     at.add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         q.float().sum().backward()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_saved_tensors_that_move(norm):
+    """Hooks that keep what is saved elsewhere and bring it back as another tensor, dense where it was a view, while the
+    positions of the forward are gone."""
+    r = Rotary.from_base(64)
+    wide = rows((3, 40, 9 * 64), 2).cuda()
+    w = [t.cuda().requires_grad_() for t in weights(64, torch.float32)] if norm else [None, None]
+    up = [rows((3, H, 40, 64), 5 + H).cuda() for H in (2, 1, 1)]
+
+    def step():
+        x = wide.clone().requires_grad_()
+        view = x[:, :, 64:320]
+        q, k, v = r.heads(view, 2, 1, positions=torch.arange(40, device="cuda") * 3, q_norm=w[0], k_norm=w[1])
+        h = view.unflatten(2, (4, 64)).transpose(1, 2)
+        q2, k2 = r.rotate(h[:, :2], h[:, 2:3], positions=torch.arange(40, device="cuda") + 7, q_norm=w[0], k_norm=w[1])
+        torch.full((1 << 16,), -1, dtype=torch.int64, device="cuda")  # where the positions were
+        return torch.autograd.grad((q, k, v, q2, k2), [x, *(t for t in w if norm)], (*up, up[0], up[1]))
+
+    want = step()
+    with torch.autograd.graph.save_on_cpu():
+        got = step()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_what_is_kept_for_the_backward():
+    """Without norms the projection's output is not."""
+    r, x = Rotary.from_base(64), rows((1, 30, 4 * 64), 2).cuda().requires_grad_()
+    h = x.unflatten(2, (4, 64)).transpose(1, 2)
+    kept = lambda out: [t for t in out[0].grad_fn.saved_tensors if t is not None]  # noqa: E731
+    assert kept(r.heads(x, 2, 1)) == [] and kept(r.rotate(h[:, :2], h[:, 2:3])) == []
+    w = torch.ones(64, device="cuda")
+    assert len(kept(r.heads(x, 2, 1, q_norm=w))) == 2 and len(kept(r.rotate(h[:, :2], h[:, 2:3], k_norm=w))) == 3
