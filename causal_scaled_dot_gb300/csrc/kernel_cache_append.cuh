@@ -9,7 +9,7 @@
 // by the rotation's plan, have much to load, those of K much to compute: they alternate evenly, and V's, which are quick,
 // come last, so that the launch ends evenly (37.8 us with K and V in one order with q, 35.1 so).
 // Bound by the bytes, 2 in and 1 out per element of K and V, 2 and 2 of q, and for long prompts by the latency of K's units
-// too: 20 warps an SM, issuing in 55 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 35.1 us,
+// too: 20 warps an SM, issuing in 55 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 35.0 us,
 // 5.3 TB/s; one token of 64 sequences 4.0 us, of one 3.0.
 #pragma once
 

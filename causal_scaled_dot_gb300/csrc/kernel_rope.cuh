@@ -11,8 +11,8 @@
 // Bound by the bytes: each element is read once and written once, from and to any layout of rows.  A lane holds both
 // elements of each of its pairs, two vectors of 16 bytes, and keeps its token for all of its heads, so the sines are
 // computed once for up to 8 rows.  What it took to come near the bytes was enough of them under way (RopeRing) and few
-// instructions a row (two elements each).  4 x 4096 tokens of 48 heads of 128, 403 MB: 60.3 us, 6.7 TB/s, where the
-// measured copy has 6.8; with norms 2 x 4096 of 32 + 8 + 8: forward 32.4 us for 201 MB, backward 46.6 for 285, and 52.5
+// instructions a row (two elements each).  4 x 4096 tokens of 48 heads of 128, 403 MB: 60.0 us, 6.7 TB/s, where the
+// measured copy has 6.8; with norms 2 x 4096 of 32 + 8 + 8: forward 32.3 us for 201 MB, backward 45.7 for 285, and 52.0
 // with the weights' gradients, which a second kernel adds up.
 #pragma once
 
