@@ -9,8 +9,8 @@
 // by the rotation's plan, have much to load, those of K much to compute: they alternate evenly, and V's, which are quick,
 // come last, so that the launch ends evenly (37.8 us with K and V in one order with q, 35.1 so).
 // Bound by the bytes, 2 in and 1 out per element of K and V, 2 and 2 of q, and for long prompts by the latency of K's units
-// too: 20 warps an SM, issuing in 55 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 35.0 us,
-// 5.3 TB/s; one token of 64 sequences 4.0 us, of one 3.0.
+// too: 20 warps an SM, issuing in 55 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 34.4 us,
+// 5.4 TB/s; one token of 64 sequences 4.0 us, of one 2.9.
 #pragma once
 
 #include "cache_index.h"
@@ -94,7 +94,8 @@ __device__ __noinline__ uint32_t append_finite(RopeRing<4, 1, kAppendThreads> mi
     return __float_as_uint(m);
 }
 
-// Five blocks an SM: with 4 the prompt above takes 37.4 us, with 6, which do without 80 bytes of registers, 37.8.
+// Five blocks an SM: with 6 the prompt above takes 33.2 us, but one token of 64 sequences 4.4, and 512 of 2 9.4 where 5 take 8.7;
+// with 4 (and twice the registers for the sines) it took 37.4 where 5 took 35.1.
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
     constexpr int kLanes = D / 16;
@@ -173,10 +174,10 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
 #pragma unroll 1
         for (int i = 0; i < most; ++i) {
             uint64_t x[8];
-            RopeTurn<kInter> turn;
             const bool there = i < count;
             const int at = row0 + (there ? first + i * step : 0);
-            turn.template set<false>(p.r, turns, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
+            RopeWaves<kInter> waves;
+            waves.set(p.r, turns, l, lane, p.r.positions ? rope_position(p.r, u.b, at) : p.r.first + s.first + at);
             if (i == 0) ptx::cp_async_wait<0>();
             if (there) {
                 rope_unpack(mine.at(i, 0), mine.at(i, 1), x);
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
                 for (int j = 0; j < 8; ++j) x[j] = ptx::mul2(x[j], w[j]);
                 rope_scale(x, r);
             }
-            turn.template turn<false>(x);
+            waves.turn(l, x);
             float m = append_largest(x);
             if (m == INFINITY) {
                 odd = true;

@@ -186,6 +186,42 @@ struct RopeTurn {
     }
 };
 
+// The sines of one row's pairs, two in a word, for a row that is the only one of its token: half of RopeTurn's registers.
+template <bool kInter>
+struct RopeWaves {
+    uint64_t c[4], s[4];
+
+    __device__ __forceinline__ void set(const RopeParams& r, const unsigned long long* turns, const RopeLane& l, int lane, long long at) {
+        const uint64_t m = rope_both(r.factor);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!(kInter && i >= 2 ? l.turn_b : l.turn_a)) continue;
+            const int pair = !kInter ? 8 * lane + 2 * i : i < 2 ? 4 * l.a + 2 * i : 4 * l.b + 2 * i - 4;
+            rope_wave2(at, turns[pair], turns[pair + 1], c[i], s[i]);
+            c[i] = ptx::mul2(c[i], m);
+            s[i] = ptx::mul2(s[i], m);
+        }
+    }
+    // The forward rotation; elements that are not rotated stay as they are.
+    __device__ __forceinline__ void turn(const RopeLane& l, uint64_t (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!(kInter && i >= 2 ? l.turn_b : l.turn_a)) continue;
+            if (kInter) {
+                float c0, c1, s0, s1;
+                ptx::f2_split(c[i], c0, c1);
+                ptx::f2_split(s[i], s0, s1);
+                x[2 * i] = ptx::fma2(rope_swap(x[2 * i]), ptx::f2(-s0, s0), ptx::mul2(x[2 * i], rope_both(c0)));
+                x[2 * i + 1] = ptx::fma2(rope_swap(x[2 * i + 1]), ptx::f2(-s1, s1), ptx::mul2(x[2 * i + 1], rope_both(c1)));
+            } else {
+                const uint64_t u = x[i], v = x[i + 4];
+                x[i] = ptx::fma2(v, rope_negate(s[i]), ptx::mul2(u, c[i]));
+                x[i + 4] = ptx::fma2(u, s[i], ptx::mul2(v, c[i]));
+            }
+        }
+    }
+};
+
 // Sum over a row's lanes (neighbouring, kLanes a power of two).
 template <int kLanes>
 __device__ __forceinline__ float rope_row_sum(float x) {
