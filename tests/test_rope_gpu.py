@@ -679,3 +679,31 @@ def test_what_is_kept_for_the_backward():
     assert kept(r.heads(x, 2, 1)) == [] and kept(r.rotate(h[:, :2], h[:, 2:3])) == []
     w = torch.ones(64, device="cuda")
     assert len(kept(r.heads(x, 2, 1, q_norm=w))) == 2 and len(kept(r.rotate(h[:, :2], h[:, 2:3], k_norm=w))) == 3
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "qk", "qv", "kv", "qkv"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_c_calls_of_some_tensors(which, packed):
+    """Any of q, k and v, from a projection's output to new tensors or in place, and the gradients of the same ones."""
+    from causal_scaled_dot_gb300.native import AttnHeads
+    r, lib = Rotary.from_base(32), native.load()
+    B, S, Hq, Hkv, D = 2, 45, 3, 2, 64
+    x = rows((B, S, 7 * D), 3).cuda()
+    w = [t.cuda() for t in weights(D, torch.bfloat16)]
+    want = r.heads(x, Hq, Hkv, q_norm=w[0], k_norm=w[1])
+    c = r._plan(x.device, B, S, D, None, 0, *w, EPS)
+    split_ = lambda t: (lambda h: (h[:, :Hq], h[:, Hq:Hq + Hkv], h[:, Hq + Hkv:]))(t.unflatten(2, (7, D)).transpose(1, 2))  # noqa: E731
+    some = lambda ts: c_heads(*(t if n in which else None for n, t in zip("qkv", ts)))  # noqa: E731
+    st = torch.cuda.current_stream().cuda_stream
+    held = x.clone()
+    to = split_(held) if packed else tuple(torch.full_like(t, 7.0) for t in want)
+    assert lib.attn_rope(c, some(split_(held)), some(to), B, Hq, Hkv, S, D, st) == 0
+    for n, got, ref, was in zip("qkv", to, want, split_(x)):
+        assert torch.equal(got, ref if n in which else was if packed else torch.full_like(ref, 7.0))
+    up = [rows(t.shape, 8).cuda() for t in want]
+    dx = r.heads_backward(*up, x, Hq, Hkv, q_norm=w[0], k_norm=w[1], weight_grads=False)[0]
+    out = torch.full_like(x, 7.0)
+    assert isinstance(some(up), AttnHeads)
+    assert lib.attn_rope_bwd(c, some(up), some(split_(x)), some(split_(out)), None, None, B, Hq, Hkv, S, D, None, 0, st) == 0
+    for n, got, ref in zip("qkv", split_(out), split_(dx)):
+        assert torch.equal(got, ref if n in which else torch.full_like(ref, 7.0))
