@@ -471,3 +471,63 @@ def test_definitions_agree_with_differences(interleaved, weight):
     q, k = rng.normal(size=(1, 1, 1, 64)), rng.normal(size=(1, 1, 1, 64))
     score = lambda i, j: float((rope_util.turn(q, [[i]], r) * rope_util.turn(k, [[j]], r)).sum())  # noqa: E731
     assert score(7, 3) == pytest.approx(score(1007, 1003), abs=1e-9) and score(7, 3) != pytest.approx(score(7, 4), abs=1e-3)
+
+
+ROWS = r"""
+#include "rows.h"
+#include <cstdio>
+#include <cstdlib>
+#include <set>
+using namespace attn::host;
+static unsigned long long state = 12345;
+static int below(int n) { state = state * 6364136223846793005ull + 1442695040888963407ull; return (int)((state >> 33) % n); }
+static std::multiset<long long> elements(const RowsBox& x) {
+    std::multiset<long long> all;
+    for (int b = 0; b < x.n[0]; ++b)
+        for (int h = 0; h < x.n[1]; ++h)
+            for (int s = 0; s < x.n[2]; ++s)
+                for (int d = 0; d < x.D; d += 8)  // strides and addresses are multiples of 8 elements
+                    all.insert((long long)(size_t)x.p / 2 + b * x.stride[0] + h * x.stride[1] + s * x.stride[2] + d);
+    return all;
+}
+int main() {
+    int apart = 0, told_apart = 0, distinct = 0, told_distinct = 0;
+    for (int i = 0; i < 20000; ++i) {
+        RowsBox box[2];
+        const int common = below(2), D = 16;  // half of the pairs: views of one tensor
+        long long st[3] = {8ll * below(200), 8ll * below(20), 8ll * below(60)};
+        for (int k = 0; k < 2; ++k) {
+            box[k] = RowsBox{(const void*)(size_t)(4096 + 16 * below(300)), {1 + below(3), 1 + below(3), 1 + below(4)}, {0, 0, 0}, D};
+            for (int d = 0; d < 3; ++d)
+                if (box[k].n[d] > 1) box[k].stride[d] = common ? st[d] : 8ll * below(d == 0 ? 200 : 40);
+        }
+        const auto a = elements(box[0]), b = elements(box[1]);
+        const std::set<long long> only(a.begin(), a.end());
+        bool share = false;
+        for (long long e : b) share = share || only.count(e);
+        const bool once = only.size() == a.size();
+        if (rows_apart(box[0], box[1]) && share) { printf("apart %d\n", i); return 1; }
+        if (rows_apart(box[0], box[1]) != rows_apart(box[1], box[0])) { printf("order %d\n", i); return 1; }
+        if (rows_distinct(box[0]) && !once) { printf("distinct %d\n", i); return 1; }
+        apart += !share;
+        told_apart += rows_apart(box[0], box[1]);
+        distinct += once;
+        told_distinct += rows_distinct(box[0]);
+    }
+    printf("%d %d %d %d\n", apart, told_apart, distinct, told_distinct);
+}
+"""
+
+
+def test_shared_elements_are_never_overlooked(tmp_path):
+    """Random strided tensors against their elements one by one: what is called apart shares none, what is called
+    distinct has each once, and few that would do are refused."""
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
+    (tmp_path / "rows.cpp").write_text(ROWS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "causal_scaled_dot_gb300", "csrc"), "-o", str(tmp_path / "rows"),
+                    str(tmp_path / "rows.cpp")], check=True)
+    r = subprocess.run([str(tmp_path / "rows")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    apart, told_apart, distinct, told_distinct = map(int, r.stdout.split())
+    assert told_apart > 0.5 * apart and told_distinct > 0.5 * distinct, r.stdout
