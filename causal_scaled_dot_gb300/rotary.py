@@ -147,10 +147,11 @@ class Rotary:
         Gradients flow to qkv and the norms' weights.  Runs with qkv's device current, on its current stream.
 
         Captured into a graph, a step with its backward pass must not share leaves (qkv or weights that are
-        nobody's result) with an eager graph that still lives: torch keeps one node per leaf, on the stream
-        of the first use, and a backward pass that meets it breaks the capture or ends the process.  A call
-        that would is refused where that eager graph is of these functions (ValueError); let it go first,
-        pass ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
+        nobody's result) with an eager graph of the default stream that still lives: torch keeps one node per
+        leaf, on the stream of the first use, and a backward pass that meets one of the default stream, which
+        cannot be captured, breaks the capture or ends the process.  A call that would is refused where that
+        eager graph is of these functions (ValueError); let it go first, warm up on another stream, pass
+        ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
         x = _packed(qkv, q_heads, kv_heads)
         c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(qkv, q_norm, k_norm):
@@ -435,26 +436,27 @@ def _heads_of(q, k, v):
     return native.AttnHeads(*pointers, *strides)
 
 
-# Nodes of the eager calls whose graphs live, by id: (weak reference, stream).
+# Nodes of the eager calls on a default stream whose graphs live, by id, as weak references.
 _live: dict = {}
 
 
 def _watch(ctx, leaves, index):
-    """Notes an eager call, or refuses a captured one that shares a leaf with an eager graph of another stream."""
-    st = _stream_handle(index)
+    """Notes an eager call on the default stream, or refuses a captured one that shares a leaf with such a call's graph."""
     if not _capturing():
-        key = id(ctx)
-        _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None)), st
+        if _stream_handle(index) == 0:
+            key = id(ctx)
+            _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None))
         return
     leaves = [t for t in leaves if t is not None and t.requires_grad and t.is_leaf]
-    for ref, of in list(_live.values()):
+    for ref in list(_live.values()):
         node = ref()
-        if node is None or of == st:
+        if node is None:
             continue
         held = [getattr(f, "variable", None) for f, _ in node.next_functions if f is not None]
         if any(t is x for t in leaves for x in held):
-            raise ValueError("an eager graph of the same leaf lives, whose backward node belongs to another stream: capturing "
-                             "would break. Let it go first, pass leaf.detach().requires_grad_(), or capture the *_backward call")
+            raise ValueError("an eager graph of the same leaf lives, whose backward node belongs to the default stream: capturing "
+                             "would break. Let it go first, warm up on another stream, pass leaf.detach().requires_grad_(), or "
+                             "capture the *_backward call")
 
 
 def _functions():

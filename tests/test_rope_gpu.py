@@ -707,3 +707,45 @@ def test_c_calls_of_some_tensors(which, packed):
     assert lib.attn_rope_bwd(c, some(up), some(split_(x)), some(split_(out)), None, None, B, Hq, Hkv, S, D, None, 0, st) == 0
     for n, got, ref in zip("qkv", split_(out), split_(dx)):
         assert torch.equal(got, ref if n in which else torch.full_like(ref, 7.0))
+
+
+def test_captured_after_a_warm_up_whose_results_live():
+    """The usual way: a few steps on a side stream, whose last results are still held, then the capture of a whole step with
+    .backward() into the leaves' gradients."""
+    r, D, S = Rotary.from_base(64), 64, 96
+    x = rows((1, S, 4 * D), 2).cuda()
+    w = [t.cuda().requires_grad_() for t in weights(D, torch.float32)]
+
+    def step():
+        q, k, v = r.heads(x, 2, 1, q_norm=w[0], k_norm=w[1])
+        o = native.attention_trainable(q, k, v)
+        (o.float() ** 2).sum().backward()
+        return q, k, v, o
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            for t in w:
+                t.grad = None
+            held = step()
+    torch.cuda.current_stream().wait_stream(s)
+    for t in w:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    grads = [t.grad for t in w]
+    for i in range(2):
+        x.copy_(rows(x.shape, 30 + i).cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        alias = [t.detach().requires_grad_() for t in w]
+        q, k, v = r.heads(x, 2, 1, q_norm=alias[0], k_norm=alias[1])
+        o = native.attention_trainable(q, k, v)
+        want = torch.autograd.grad((o.float() ** 2).sum(), alias)
+        assert torch.equal(got[3], o)
+        for a, b in zip(grads, want):
+            assert torch.equal(a, b)
+        del q, k, v, o
+    assert all(t.isfinite().all() for t in held)
