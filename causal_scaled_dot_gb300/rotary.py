@@ -149,7 +149,7 @@ class Rotary:
         Captured into a graph, a step with its backward pass must not share leaves (qkv or weights that are
         nobody's result) with an eager graph of the default stream that still lives: torch keeps one node per
         leaf, on the stream of the first use, and a backward pass that meets one of the default stream, which
-        cannot be captured, breaks the capture or ends the process.  A call that would is refused where that
+        cannot be captured, breaks the capture or ends the process.  The backward pass is refused where that
         eager graph is of these functions (ValueError); let it go first, warm up on another stream, pass
         ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
         x = _packed(qkv, q_heads, kv_heads)
@@ -440,20 +440,25 @@ def _heads_of(q, k, v):
 _live: dict = {}
 
 
-def _watch(ctx, leaves, index):
-    """Notes an eager call on the default stream, or refuses a captured one that shares a leaf with such a call's graph."""
-    if not _capturing():
-        if _stream_handle(index) == 0:
-            key = id(ctx)
-            _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None))
+def _watch(ctx, index):
+    """Notes an eager forward on the default stream."""
+    if _stream_handle(index) == 0 and not _capturing():
+        key = id(ctx)
+        _live[key] = weakref.ref(ctx, lambda _: _live.pop(key, None))
+
+
+def _leaves(node):
+    return [f.variable for f, _ in node.next_functions if f is not None and hasattr(f, "variable")]
+
+
+def _check(ctx):
+    """Refuses a captured backward whose leaves an eager graph of the default stream holds."""
+    if not _live or not _capturing():
         return
-    leaves = [t for t in leaves if t is not None and t.requires_grad and t.is_leaf]
+    mine = _leaves(ctx)
     for ref in list(_live.values()):
         node = ref()
-        if node is None:
-            continue
-        held = [getattr(f, "variable", None) for f, _ in node.next_functions if f is not None]
-        if any(t is x for t in leaves for x in held):
+        if node is not None and any(t is x for t in mine for x in _leaves(node)):
             raise ValueError("an eager graph of the same leaf lives, whose backward node belongs to the default stream: capturing "
                              "would break. Let it go first, warm up on another stream, pass leaf.detach().requires_grad_(), or "
                              "capture the *_backward call")
@@ -475,6 +480,7 @@ def _make_functions():
     once = torch.autograd.function.once_differentiable
 
     def heads_backward(ctx, dq, dk, dv):
+        _check(ctx)
         qkv, q_norm, k_norm, positions = ctx.saved_tensors
         rotary, x, (Hq, Hkv, first, eps) = ctx.args
         _, need_q, need_k, *_ = ctx.needs_input_grad
@@ -487,6 +493,7 @@ def _make_functions():
         return (*got, None, None, None, None, None)
 
     def rotate_backward(ctx, dq, dk):
+        _check(ctx)
         q, k, q_norm, k_norm, positions = ctx.saved_tensors
         rotary, x, (first, eps), has_k = ctx.args
         _, _, need_q, need_k, *_ = ctx.needs_input_grad
@@ -500,7 +507,7 @@ def _make_functions():
     class HeadsFunction(torch.autograd.Function):
         @staticmethod
         def forward(ctx, qkv, q_norm, k_norm, positions, rotary, x, c, args):
-            _watch(ctx, (qkv, q_norm, k_norm), qkv.get_device())
+            _watch(ctx, qkv.get_device())
             normed = q_norm is not None or k_norm is not None
             ctx.save_for_backward(qkv if normed else None, q_norm, k_norm, positions)
             ctx.args = rotary, x, args
@@ -513,7 +520,7 @@ def _make_functions():
     class RotateFunction(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, q_norm, k_norm, positions, rotary, x, c, args):
-            _watch(ctx, (q, k, q_norm, k_norm), q.get_device())
+            _watch(ctx, q.get_device())
             normed = q_norm is not None or k_norm is not None
             ctx.save_for_backward(*((q, k) if normed else (None, None)), q_norm, k_norm, positions)
             ctx.args = rotary, x, args, k is not None

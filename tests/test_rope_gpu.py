@@ -486,16 +486,23 @@ def test_captured_step():
 
 
 def test_captured_while_an_eager_graph_lives():
-    """Through autograd that is refused before anything is captured; the backward call itself is captured and replayed."""
+    """Through autograd the backward is refused, the forward captured; the backward call itself is captured and replayed."""
     r, x = Rotary.from_base(64), rows((1, 50, 4 * 64), 2).cuda()
     w = weights(64, torch.float32)[0].cuda().requires_grad_()
     eager = r.heads(x, 2, 1, q_norm=w)
     up = [rows(t.shape, 5).cuda() for t in eager]
-    for call in (lambda: r.heads(x, 2, 1, q_norm=w), lambda: r.rotate(x.unflatten(2, (4, 64)).transpose(1, 2), q_norm=w)):
+    for call in (lambda: r.heads(x, 2, 1, q_norm=w), lambda: (r.rotate(x.unflatten(2, (4, 64)).transpose(1, 2), q_norm=w),)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        graph.replay()
+        assert torch.equal(out[0][:, :2], eager[0])
+        del out
         graph = torch.cuda.CUDAGraph()
         with pytest.raises(ValueError, match="eager graph"):
             with torch.cuda.graph(graph):
-                call()
+                torch.autograd.grad(call()[0].float().sum(), w)
+        torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = r.heads_backward(*up, x, 2, 1, q_norm=w.detach())
