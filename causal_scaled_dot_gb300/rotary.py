@@ -20,6 +20,7 @@ import weakref
 import torch
 
 from . import native
+from .autograd import tied
 
 # 1 / (2 pi) to 256 bits, from pi to 100 decimals (OEIS A000796).
 _PER_TURN = (10**100 << 255) // int("31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679")
@@ -144,7 +145,8 @@ class Rotary:
         q's heads, then k's, then v's; strides of 16 bytes with the last dimension contiguous), q and k
         normed where ``q_norm`` / ``k_norm`` ([D], bf16 or fp32) are given, and rotated.  Row s of sequence b
         stands at ``positions[b, s]`` (int32 or int64 [B, S] or [S] on the device), or at first + s.
-        Gradients flow to qkv and the norms' weights.  Runs with qkv's device current, on its current stream.
+        Gradients flow to qkv and the norms' weights, once: a gradient made with ``create_graph=True`` raises where
+        it is differentiated again (RuntimeError).  Runs with qkv's device current, on its current stream.
 
         Captured into a graph, a step with its backward pass must not share leaves (qkv or weights that are
         nobody's result) with an eager graph of the default stream that still lives: torch keeps one node per
@@ -476,12 +478,12 @@ _FUNCTIONS = None
 
 def _make_functions():
     """torch.autograd.Functions over the calls above.  What is saved is q and k, or qkv, only where they have norms; a
-    backward takes sizes, strides and addresses from what it gets back, which hooks may have moved."""
-    once = torch.autograd.function.once_differentiable
+    backward takes sizes, strides and addresses from what it gets back, which hooks may have moved.  In a backward that is
+    itself recorded each gradient is tied to what it depends on, and cannot be differentiated again."""
 
-    def heads_backward(ctx, dq, dk, dv):
+    def heads_backward(ctx, saved, dq, dk, dv):
         _check(ctx)
-        qkv, q_norm, k_norm, positions = ctx.saved_tensors
+        qkv, q_norm, k_norm, positions = saved
         rotary, x, (Hq, Hkv, first, eps) = ctx.args
         _, need_q, need_k, *_ = ctx.needs_input_grad
         rows = None
@@ -489,20 +491,16 @@ def _make_functions():
             x = _packed(qkv, Hq, Hkv)
             rows = x.at(qkv)
         c = rotary._plan(dq.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
-        got = rotary._heads_backward(dq, dk, dv, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
-        return (*got, None, None, None, None, None)
+        return rotary._heads_backward(dq, dk, dv, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
 
-    def rotate_backward(ctx, dq, dk):
+    def rotate_backward(ctx, saved, dq, dk):
         _check(ctx)
-        q, k, q_norm, k_norm, positions = ctx.saved_tensors
+        q, k, q_norm, k_norm, positions = saved
         rotary, x, (first, eps), has_k = ctx.args
         _, _, need_q, need_k, *_ = ctx.needs_input_grad
         rows = None if q is None else _apart(q, k, k_norm).rows(q, k)
         c = rotary._plan(dq.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
-        got = rotary._rotate_backward(dq, dk if has_k else None, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
-        return (*got, None, None, None, None, None)
-
-    heads_once, rotate_once = once(heads_backward), once(rotate_backward)
+        return rotary._rotate_backward(dq, dk if has_k else None, rows, x, c, q_norm if need_q else None, k_norm if need_k else None)
 
     class HeadsFunction(torch.autograd.Function):
         @staticmethod
@@ -514,8 +512,16 @@ def _make_functions():
             return rotary._heads(qkv, x, c)
 
         @staticmethod
-        def backward(ctx, *up):  # `once` is for backward passes that are themselves recorded
-            return (heads_once if torch.is_grad_enabled() else heads_backward)(ctx, *up)
+        def backward(ctx, dq, dk, dv):
+            saved = ctx.saved_tensors  # once: hooks may make them anew each time, or refuse to
+            if torch.is_grad_enabled():
+                qkv, q_norm, k_norm, _ = saved
+                with torch.no_grad():
+                    dqkv, dq_norm, dk_norm = heads_backward(ctx, saved, dq, dk, dv)
+                got = tied(dqkv, dq, dk, dv, qkv, q_norm, k_norm), tied(dq_norm, dq, qkv), tied(dk_norm, dk, qkv)
+            else:
+                got = heads_backward(ctx, saved, dq, dk, dv)
+            return (*got, None, None, None, None, None)
 
     class RotateFunction(torch.autograd.Function):
         @staticmethod
@@ -527,7 +533,17 @@ def _make_functions():
             return rotary._rotate(q, k, x, c)
 
         @staticmethod
-        def backward(ctx, *up):
-            return (rotate_once if torch.is_grad_enabled() else rotate_backward)(ctx, *up)
+        def backward(ctx, dq, dk):
+            saved = ctx.saved_tensors
+            if torch.is_grad_enabled():
+                q, k, q_norm, k_norm, _ = saved
+                with torch.no_grad():
+                    gq, gk, dq_norm, dk_norm = rotate_backward(ctx, saved, dq, dk)
+                of_q = () if q_norm is None else (q, q_norm)  # without a norm a gradient depends on the upstream one alone
+                of_k = () if k_norm is None else (k, k_norm)
+                got = tied(gq, dq, *of_q), tied(gk, dk, *of_k), tied(dq_norm, dq, q), tied(dk_norm, dk, k)
+            else:
+                got = rotate_backward(ctx, saved, dq, dk)
+            return (*got, None, None, None, None, None)
 
     return HeadsFunction, RotateFunction
