@@ -548,6 +548,8 @@ def _attention_function():
     library's entry points (argument marshalling only)."""
     import torch
 
+    from .autograd import tied
+
     class AttentionFunction(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, v, causal, scale, block_mask, keep_bits, dropout_p, seed, offset,
@@ -587,6 +589,8 @@ def _attention_function():
                             st)
                 if check_status:
                     attn_sync_status(st)
+            if torch.is_grad_enabled():  # a recorded backward
+                dq, dk, dv = tied(dq, dout, q, k, v), tied(dk, dout, q, k, v), tied(dv, dout, q, k)
             return dq, dk, dv, None, None, None, None, None, None, None, None
 
     return AttentionFunction
@@ -603,6 +607,8 @@ def attention_trainable(q, k, v, causal: bool = True, scale: float | None = None
     on its current stream.  q [B,Hq,S,D], k/v [B,Hkv,S,D] bf16 CUDA tensors;
     block_mask uint8 [1 or Hq, nt, nt]; keep_bits uint8 [1 or Hq, S, 16*nt];
     dropout combines with either or both.  Every tensor must be on q's device.
+    A gradient made with ``create_graph=True`` raises where it is differentiated
+    again (RuntimeError).
     ``check_status=True`` reads the per-device status word after each pass (as
     ``attention`` does) and raises AttnError on a device-side timeout."""
     global _ATTENTION_FUNCTION
