@@ -23,6 +23,7 @@ import math
 import torch
 
 from . import native
+from .autograd import refuse_tangents
 from .rotary import _heads_of
 
 _DIMS3 = ctypes.c_longlong * 3
@@ -141,8 +142,10 @@ class KVCache:
         if not strided:
             if not contiguous:
                 raise ValueError(f"{name} must be contiguous")
-        elif x.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
+        else:
+            if x.requires_grad and torch.is_grad_enabled():
+                raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
+            refuse_tangents(x)
         return shape[2], None if contiguous else _strides(name, x)
 
     def _counts(self, name, t):
@@ -226,6 +229,7 @@ class KVCache:
             for name, t in (("k", k), ("v", v), ("q", q), ("q_norm", q_norm), ("k_norm", k_norm)):
                 if t is not None and t.requires_grad:
                     raise ValueError(f"{name} requires a gradient, and none flows through an 8-bit cache: detach it")
+        refuse_tangents(k, v, q, q_norm, k_norm)
         n = None if new_lens is None else self._counts("new_lens", new_lens)
         c = rotary._plan(self._device, B, S, D, positions, first, q_norm, k_norm, eps)
         heads = native.AttnHeads.from_buffer_copy(like)

@@ -20,7 +20,7 @@ import weakref
 import torch
 
 from . import native
-from .autograd import tied
+from .autograd import refuse_tangents, tied
 
 # 1 / (2 pi) to 256 bits, from pi to 100 decimals (OEIS A000796).
 _PER_TURN = (10**100 << 255) // int("31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679")
@@ -146,7 +146,8 @@ class Rotary:
         normed where ``q_norm`` / ``k_norm`` ([D], bf16 or fp32) are given, and rotated.  Row s of sequence b
         stands at ``positions[b, s]`` (int32 or int64 [B, S] or [S] on the device), or at first + s.
         Gradients flow to qkv and the norms' weights, once: a gradient made with ``create_graph=True`` raises where
-        it is differentiated again (RuntimeError).  Runs with qkv's device current, on its current stream.
+        it is differentiated again (RuntimeError).  Forward-mode tangents are refused (ValueError).  Runs with
+        qkv's device current, on its current stream.
 
         Captured into a graph, a step with its backward pass must not share leaves (qkv or weights that are
         nobody's result) with an eager graph of the default stream that still lives: torch keeps one node per
@@ -155,6 +156,7 @@ class Rotary:
         eager graph is of these functions (ValueError); let it go first, warm up on another stream, pass
         ``leaf.detach().requires_grad_()``, or capture ``heads_backward``, which needs no autograd."""
         x = _packed(qkv, q_heads, kv_heads)
+        refuse_tangents(qkv, q_norm, k_norm)
         c = self._plan(qkv.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(qkv, q_norm, k_norm):
             return _functions()[0].apply(qkv, q_norm, k_norm, positions, self, x, c, (q_heads, kv_heads, first, eps))
@@ -164,6 +166,7 @@ class Rotary:
         """q (and k), bf16 [B, H, S, D] of any strides of 16 bytes with D contiguous, normed and rotated as by
         ``heads``, in new contiguous tensors.  Gradients flow to q, k and the norms' weights."""
         x = _apart(q, k, k_norm)
+        refuse_tangents(q, k, q_norm, k_norm)
         c = self._plan(q.device, x.B, x.S, x.D, positions, first, q_norm, k_norm, eps)
         if torch.is_grad_enabled() and _any_grad(q, k, q_norm, k_norm):
             out = _functions()[1].apply(q, k, q_norm, k_norm, positions, self, x, c, (first, eps))
@@ -174,7 +177,8 @@ class Rotary:
     def heads_backward(self, dq, dk, dv, qkv, q_heads: int, kv_heads: int, positions=None, first: int = 0, q_norm=None,
                        k_norm=None, eps: float = 1e-6, weight_grads: bool = True):
         """(dqkv, dq_norm, dk_norm) for upstream gradients of what ``heads`` returned with the same arguments.
-        Without norms qkv's values are not read.  ``weight_grads=False`` leaves the norms' out (None)."""
+        Without norms qkv's values are not read.  ``weight_grads=False`` leaves the norms' out (None).  Outside
+        autograd: nothing is recorded, whatever the arguments require."""
         x = _packed(qkv, q_heads, kv_heads)
         for name, t, shape in (("dq", dq, x.q_shape), ("dk", dk, x.k_shape), ("dv", dv, x.k_shape)):
             _upstream(name, t, shape, qkv.device)
@@ -185,7 +189,7 @@ class Rotary:
     def rotate_backward(self, dq, dk, q, k, positions=None, first: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6,
                         weight_grads: bool = True):
         """(dq, dk, dq_norm, dk_norm): gradients of ``rotate``'s inputs, laid out as those are, for upstream
-        ones of its outputs.  k and dk may be None together."""
+        ones of its outputs.  k and dk may be None together.  Outside autograd, as ``heads_backward``."""
         x = _apart(q, k, k_norm)
         if (k is None) != (dk is None):
             raise ValueError("k and dk go together")

@@ -1,8 +1,9 @@
 """Gradients made outside autograd, tied to what they were made from (causal_scaled_dot_gb300/autograd.py)."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
-from causal_scaled_dot_gb300.autograd import tied
+from causal_scaled_dot_gb300.autograd import refuse_tangents, tied
 
 
 class Cube(torch.autograd.Function):
@@ -62,3 +63,13 @@ def test_first_order_is_as_it_was():
     assert torch.equal(x.grad, 2 * want[0]) and torch.equal(w.grad, 2 * want[1])
     with torch.no_grad():
         x.grad.zero_()
+
+
+def test_tangents_are_refused():
+    t = torch.ones(3)
+    refuse_tangents(t, None)
+    with forward_ad.dual_level():
+        refuse_tangents(t, None)
+        with pytest.raises(ValueError, match="tangent"):
+            refuse_tangents(t, None, forward_ad.make_dual(t, t))
+    refuse_tangents(t)
