@@ -243,23 +243,23 @@ __device__ __forceinline__ void rope_scale(uint64_t (&x)[8], float by) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = ptx::mul2(x[i], b);
 }
-// r of a row.  bf16's largest values have squares beyond fp32: such a row's x (not its infinities) is taken 2^-72 times
-// smaller, where eps is nothing beside it, and *down is what r x is to be of x's own size.
+// r of a row.  bf16's largest values have squares beyond fp32: where mean(x^2) + eps is infinite the row's x (not its
+// infinities) is taken 2^-72 times smaller and eps 2^-144 times, and *down is what r x is to be of x's own size.
 template <int kLanes>
 __device__ __forceinline__ float rope_norm(uint64_t (&x)[8], float eps, float* down) {
     constexpr float kInv = 1.f / (16 * kLanes), kDown = 2.117582368135751e-22f;  // 2^-72
-    const float ss = rope_row_sum<kLanes>(rope_dot(x, x));
+    const float mean = fmaf(rope_row_sum<kLanes>(rope_dot(x, x)), kInv, eps);
     *down = 1.f;
-    const bool big = ss == INFINITY;
+    const bool big = mean == INFINITY;
     if (__any_sync(0xffffffffu, big)) {
         if (big) {
             *down = kDown;
             rope_scale(x, kDown);
         }
         const float again = rope_row_sum<kLanes>(rope_dot(x, x));
-        if (big) return rsqrtf(again * kInv);
+        if (big) return rsqrtf(fmaf(again, kInv, eps * kDown * kDown));
     }
-    return rsqrtf(fmaf(ss, kInv, eps));
+    return rsqrtf(mean);
 }
 
 // The rows of a unit that one lane group takes: its token, and heads first, first + groups ... below `end`.
