@@ -9,8 +9,9 @@
 // by the rotation's plan, have much to load, those of K much to compute: they alternate evenly, and V's, which are quick,
 // come last, so that the launch ends evenly (37.8 us with K and V in one order with q, 35.1 so).
 // Bound by the bytes, 2 in and 1 out per element of K and V, 2 and 2 of q, and for long prompts by the latency of K's units
-// too: 20 warps an SM, issuing in 55 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 34.4 us,
-// 5.4 TB/s; one token of 64 sequences 4.0 us, of one 2.9.
+// too: 20 warps an SM, issuing in 54 % of the cycles.  2 x 4096 tokens of 32 + 8 + 8 heads of 128 with norms, 185 MB: 34.4 us,
+// 5.4 TB/s; one token of 64 sequences 4.0 us, of one 2.9, while the blocks' scales hold.  A step in which they rise passes
+// over the blocks' earlier tokens, at the end of this kernel: for those 64 sequences up to 6 us more with blocks of 64, 16 with 128.
 #pragma once
 
 #include "cache_index.h"
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) attn_cache_append_kernel(co
         *reinterpret_cast<uint2*>(dst + 8 * l.b) = make_uint2(code[2], code[3]);
         dst += D << step_shift;
     }
-    if (slot0 > 0 && s_new > s_old) {  // the block's earlier tokens move to the larger scale
+    if (slot0 > 0 && s_new > s_old) {  // the block's earlier tokens move to the larger scale, a round of memory latency a vector
         const float ratio = s_old * inv;
         uint2* had = reinterpret_cast<uint2*>((u.is_v ? c.v : c.k) + cache_offset(block, u.h, 0, c.Hkv, c.block_size, D));
         for (int v = t; v < slot0 * (D / 8); v += threads) {

@@ -32,8 +32,8 @@ struct RopeRows {
 // cos and sin of position p and two frequencies (2^-64 turns), packed.  The product's upper half is the angle as a signed
 // fraction of a turn (what it drops is below 2^-32 of one).  Twice that, as an integer, is the rest x in -1/2 .. 1/2 half
 // turns, and both signs turn where its top bit differs from the angle's.  cos(pi x) = C(x^2) and sin(pi x) = x S(x^2) by
-// the polynomials with the least largest error there (exchange algorithm of Remez): 5e-8 and 3e-9, and with fp32's
-// roundings 2.0e-7 and 1.7e-7 over two million angles, under 2^-22.
+// the polynomials with the least largest error there (exchange algorithm of Remez): 7.7e-8 and 4.8e-8 with coefficients
+// rounded to fp32, and with the other roundings 2.0e-7 and 1.7e-7 over two million angles, under 2^-22.
 __device__ __forceinline__ void rope_wave2(long long p, unsigned long long F0, unsigned long long F1, uint64_t& c, uint64_t& s) {
     const uint32_t t0 = (uint32_t)((unsigned long long)p * F0 >> 32), t1 = (uint32_t)((unsigned long long)p * F1 >> 32);
     const auto both = [](float x) { return ptx::f2(x, x); };

@@ -52,8 +52,8 @@ class Rotary:
     (i, i + len(frequencies)), or neighbours (2i, 2i + 1) when ``interleaved``; the rest of the head stays.
     No frequencies: no rotation (norms and the change of layout remain).
 
-    Angles are exact at any position (the frequencies are held as 64-bit fractions of a turn); there is no
-    table and no longest position.  A Rotary holds no device memory, so it serves every device."""
+    The frequencies are held as 64-bit fractions of a turn, and there is no table: cos and sin of position p
+    are within 2^-22 + abs(p) 2^-62.  A Rotary holds no device memory, so it serves every device."""
 
     def __init__(self, frequencies, interleaved: bool = False, factor: float = 1.0):
         f = [float(x) for x in (frequencies.tolist() if hasattr(frequencies, "tolist") else frequencies)]

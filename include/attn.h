@@ -352,7 +352,8 @@ enum { ATTN_WEIGHT_BF16 = 0, ATTN_WEIGHT_F32 = 1 };
  * k, as attn_rope, attn_rope_bwd and attn_cache_append take them.  A row x is
  * one head of one token, D elements at position p.
  *   Norm (where the weight w is given): u_d = x_d w_d / sqrt(mean(x^2) + eps),
- *   over the whole head; else u = x.
+ *   over the whole head; else u = x.  (x w comes before the division: weights of
+ *   2^64 and more can carry it past fp32.)
  *   Rotation: pair i < rotary_dim / 2 of elements (a, b) turns by p f_i radians
  *       y_a = factor (u_a cos - u_b sin),   y_b = factor (u_b cos + u_a sin);
  *   the pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) when `interleaved`;
@@ -360,7 +361,9 @@ enum { ATTN_WEIGHT_BF16 = 0, ATTN_WEIGHT_F32 = 1 };
  * Everything in fp32, rounded once at the end.
  *
  *   turns        f_i / (2 pi) as a fraction of 2^64, to nearest (whole turns per
- *                position drop out): the angle is then exact to |p| 2^-65 turns.
+ *                position drop out): p f_i is then right to |p| 2^-65 turns, of
+ *                which the leading 32 bits are taken: cos and sin are within
+ *                2^-22 + |p| 2^-62.
  *                Entries from rotary_dim / 2 on are not read.
  *   rotary_dim   0 .. D, a multiple of 16, or of 8 when interleaved (else
  *                ATTN_ERR_UNSUPPORTED); 0: no rotation.
